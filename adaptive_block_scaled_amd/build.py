@@ -27,7 +27,8 @@ LIB = os.path.join(HERE, "libif4.so")
 SAN_LIB = os.path.join(HERE, "libif4_san.so")
 CLANGXX = "/opt/rocm/llvm/bin/clang++"
 
-SOURCES = ["api.cpp", "quantize.hip", "dequantize.hip", "gemm.hip", "ifn.hip"]
+SOURCES = ["api.cpp", "quantize.hip", "dequantize.hip", "gemm.hip", "ifn.hip",
+           "kv_cache.hip", "kv_attention.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -2,9 +2,12 @@
 // Validation runs before any HIP call, so a bad argument never enqueues work.
 #include "../../include/if4.h"
 
+#include <math.h>
 #include <stdint.h>
 
+#include "../../include/if4_kv.h"
 #include "if4_internal.h"
+#include "kv_internal.h"
 
 namespace {
 
@@ -42,6 +45,54 @@ int check_quantize_t(const void* x, int x_dtype, int64_t rows, int64_t cols, int
     if (!x || !codes || !scales) return IF4_ERR_NULL;
     if (!aligned(x, elem_size(x_dtype)) || !aligned(codes, 8)) return IF4_ERR_ALIGN;
     return IF4_OK;
+}
+
+// Largest sizes of the KV cache's entry points: row and key indices are 32-bit
+// in the kernels, kv heads are a grid dimension.
+constexpr int64_t kMaxIndex = (int64_t)1 << 30;
+constexpr int64_t kMaxKvHeads = 65535;
+
+int check_cache(const if4_kv_cache& c) {
+    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return IF4_ERR_SHAPE;
+    if (c.page_size <= 0 || c.page_size % 16 != 0 || c.page_size > kMaxIndex) return IF4_ERR_SHAPE;
+    if (c.pages < 0 || c.pages > kMaxIndex) return IF4_ERR_SHAPE;
+    if (c.kv_heads <= 0 || c.kv_heads > kMaxKvHeads) return IF4_ERR_SHAPE;
+    if (c.k_exp < -kMaxExp || c.k_exp > kMaxExp || c.v_exp < -kMaxExp || c.v_exp > kMaxExp)
+        return IF4_ERR_RANGE;
+    return IF4_OK;
+}
+
+int check_cache_pointers(const if4_kv_cache& c) {
+    if (c.pages == 0) return IF4_OK;
+    if (!c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales) return IF4_ERR_NULL;
+    if (!aligned(c.k_codes, 16) || !aligned(c.k_scales, 16) || !aligned(c.v_codes, 16) ||
+        !aligned(c.v_scales, 16))
+        return IF4_ERR_ALIGN;
+    return IF4_OK;
+}
+
+int check_attention(const if4_kv_cache* cache, const if4_kv_attention_args* a) {
+    if (!cache || !a) return IF4_ERR_NULL;
+    const int st = check_cache(*cache);
+    if (st != IF4_OK) return st;
+    if (a->batch < 0 || a->total_q < 0 || a->max_q < 0 || a->max_len < 0 || a->table_stride < 0)
+        return IF4_ERR_SHAPE;
+    if (a->heads <= 0 || a->heads % cache->kv_heads != 0) return IF4_ERR_SHAPE;
+    const int64_t group = a->heads / cache->kv_heads;
+    if (a->total_q > kMaxIndex / group || a->batch > kMaxIndex / cache->kv_heads ||
+        a->table_stride > kMaxIndex)
+        return IF4_ERR_SHAPE;
+    if (a->window < 0 || a->sinks < 0 || (!a->causal && (a->window || a->sinks)))
+        return IF4_ERR_RANGE;
+    if (!isfinite(a->scale) || a->scale < 0.0f) return IF4_ERR_RANGE;
+    return IF4_OK;
+}
+
+// No sequence can have more rows than there are.
+if4_kv_attention_args bounded(const if4_kv_attention_args& a) {
+    if4_kv_attention_args r = a;
+    if (r.max_q > r.total_q) r.max_q = r.total_q;
+    return r;
 }
 
 }  // namespace
@@ -153,6 +204,76 @@ int if4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_exp,
         return IF4_ERR_ALIGN;
     return hip_status(if4::launch_gemm(a_codes, a_scales, a_exp, w_codes, w_scales, w_exp, M,
                                        N, K, c, ldc, (hipStream_t)stream));
+}
+
+int if4_kv_append(const if4_kv_cache* cache, const void* k, const void* v, int dtype,
+                  int64_t tokens, int64_t k_stride_token, int64_t k_stride_head,
+                  int64_t v_stride_token, int64_t v_stride_head, const int64_t* slots, int mode,
+                  void* stream) {
+    if (!cache) return IF4_ERR_NULL;
+    if (dtype != IF4_F32 && dtype != IF4_BF16) return IF4_ERR_DTYPE;
+    if (mode < IF4_MODE_ADAPTIVE || mode > IF4_MODE_FORCE_INT4) return IF4_ERR_DTYPE;
+    int st = check_cache(*cache);
+    if (st != IF4_OK) return st;
+    if (tokens < 0) return IF4_ERR_SHAPE;
+    if (tokens == 0) return IF4_OK;
+    if (!k || !v || !slots) return IF4_ERR_NULL;
+    st = check_cache_pointers(*cache);
+    if (st != IF4_OK) return st;
+    const int64_t strides[4] = {k_stride_token, k_stride_head, v_stride_token, v_stride_head};
+    for (int64_t s : strides)
+        if (s * elem_size(dtype) % 16 != 0) return IF4_ERR_ALIGN;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return IF4_ERR_ALIGN;
+    if (cache->pages == 0) return IF4_OK;
+    return hip_status(if4::launch_kv_append(*cache, k, v, dtype == IF4_BF16, tokens, strides, slots,
+                                            mode, (hipStream_t)stream));
+}
+
+int if4_kv_read(const if4_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k, void* v,
+                int dtype, void* stream) {
+    if (!cache) return IF4_ERR_NULL;
+    if (dtype != IF4_F32 && dtype != IF4_BF16) return IF4_ERR_DTYPE;
+    int st = check_cache(*cache);
+    if (st != IF4_OK) return st;
+    if (tokens < 0) return IF4_ERR_SHAPE;
+    if (tokens == 0) return IF4_OK;
+    if (!k || !v || !slots) return IF4_ERR_NULL;
+    st = check_cache_pointers(*cache);
+    if (st != IF4_OK) return st;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return IF4_ERR_ALIGN;
+    return hip_status(if4::launch_kv_read(*cache, slots, tokens, k, v, dtype == IF4_BF16,
+                                          (hipStream_t)stream));
+}
+
+int64_t if4_kv_attention_workspace(const if4_kv_cache* cache, const if4_kv_attention_args* args) {
+    const int st = check_attention(cache, args);
+    if (st != IF4_OK) return -st;
+    const if4_kv_attention_args a = bounded(*args);
+    if (a.batch == 0 || a.max_q == 0) return 0;
+    return if4::kv_attention_workspace(*cache, a);
+}
+
+int if4_kv_attention(const if4_kv_cache* cache, const if4_kv_attention_args* args, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+    int st = check_attention(cache, args);
+    if (st != IF4_OK) return st;
+    const if4_kv_attention_args a = bounded(*args);
+    if (a.batch == 0 || a.max_q == 0) return IF4_OK;
+    if (!a.q || !a.out || !a.seq_lens || !a.q_starts) return IF4_ERR_NULL;
+    if (a.table_stride > 0 && !a.page_table) return IF4_ERR_NULL;
+    st = check_cache_pointers(*cache);
+    if (st != IF4_OK) return st;
+    if (!aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.page_table, 4) ||
+        !aligned(a.seq_lens, 4) || !aligned(a.q_starts, 4))
+        return IF4_ERR_ALIGN;
+    if (a.q_stride_token % 8 || a.q_stride_head % 8 || a.out_stride_token % 8 ||
+        a.out_stride_head % 8)
+        return IF4_ERR_ALIGN;
+    const int64_t need = if4::kv_attention_workspace(*cache, a);
+    if (need > 0 && !workspace) return IF4_ERR_NULL;
+    if (need > workspace_bytes) return IF4_ERR_SHAPE;
+    if (!aligned(workspace, 16)) return IF4_ERR_ALIGN;
+    return hip_status(if4::launch_kv_attention(*cache, a, workspace, (hipStream_t)stream));
 }
 
 }  // extern "C"

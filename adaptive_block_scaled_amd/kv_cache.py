@@ -1,0 +1,231 @@
+"""Paged KV cache in IF4 and the attention that reads it: the Python binding of
+include/if4_kv.h.
+
+A cache is four uint8 tensors (KVCache): `pages` pages of `page_size` tokens,
+K and V quantized to IF4 in groups of 16 along the head dimension, 4.5 bits
+per value.  `append` quantizes new tokens into slots (page * page_size +
+offset), `read` gives slots back as bf16 or fp32, `attention` attends from the
+newest tokens of a batch of sequences, each with its row of a page table.
+
+As in the rest of the binding, arguments are checked and marshalled here and
+all work runs in the HIP kernels of libif4.so, on torch's current stream.
+"""
+import ctypes
+import math
+from typing import NamedTuple
+
+import torch
+
+from .if4 import GROUP, MODE_ADAPTIVE, _check, _dtype_code, _need, _stream, lib
+
+EXPORTS = ("if4_kv_append", "if4_kv_read", "if4_kv_attention", "if4_kv_attention_workspace")
+HEAD_DIMS = (64, 128, 256)
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("k_exp", ctypes.c_int32), ("v_exp", ctypes.c_int32)]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("q_stride_token", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+                ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("seq_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("total_q", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("max_q", ctypes.c_int64), ("max_len", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("sinks", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int32)]
+
+
+def _declare():
+    vp, i64, ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    cache, args = ctypes.POINTER(_Cache), ctypes.POINTER(_Attention)
+    lib.if4_kv_append.restype = ci
+    lib.if4_kv_append.argtypes = [cache, vp, vp, ci, i64, i64, i64, i64, i64, vp, ci, vp]
+    lib.if4_kv_read.restype = ci
+    lib.if4_kv_read.argtypes = [cache, vp, i64, vp, vp, ci, vp]
+    lib.if4_kv_attention.restype = ci
+    lib.if4_kv_attention.argtypes = [cache, args, vp, i64, vp]
+    lib.if4_kv_attention_workspace.restype = i64
+    lib.if4_kv_attention_workspace.argtypes = [cache, args]
+
+
+_declare()
+
+
+class KVCache(NamedTuple):
+    """The tensors of a cache (uint8, contiguous; layouts in include/if4_kv.h)."""
+    k_codes: torch.Tensor   # [pages, kv_heads, page_size, D/2]
+    k_scales: torch.Tensor  # [pages, kv_heads, page_size, D/16]
+    v_codes: torch.Tensor   # [pages, kv_heads, page_size/16, 16, 16, D/32]
+    v_scales: torch.Tensor  # [pages, kv_heads, page_size/16, D/16, 16]
+
+
+def empty(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> KVCache:
+    """A cache of zeros (every slot reads as zeros)."""
+    if head_dim not in HEAD_DIMS:
+        raise ValueError(f"head_dim must be one of {HEAD_DIMS}, not {head_dim}")
+    if page_size <= 0 or page_size % 16:
+        raise ValueError(f"page_size must be a multiple of 16, not {page_size}")
+    return KVCache(*(torch.zeros(shape, dtype=torch.uint8, device=device)
+                     for shape in _shapes(pages, page_size, kv_heads, head_dim)))
+
+
+def _shapes(pages, page_size, kv_heads, head_dim):
+    tiles = page_size // 16
+    return ((pages, kv_heads, page_size, head_dim // 2),
+            (pages, kv_heads, page_size, head_dim // GROUP),
+            (pages, kv_heads, tiles, 16, 16, head_dim // 32),
+            (pages, kv_heads, tiles, head_dim // GROUP, 16))
+
+
+def _cache(cache: KVCache, k_exp: int, v_exp: int):
+    kc = cache.k_codes
+    if not isinstance(kc, torch.Tensor) or not kc.is_cuda or kc.dim() != 4:
+        raise ValueError("k_codes must be a CUDA tensor [pages, kv_heads, page_size, D/2]")
+    pages, kv_heads, page_size, half = kc.shape
+    if 2 * half not in HEAD_DIMS:
+        raise ValueError(f"head_dim must be one of {HEAD_DIMS}, not {2 * half}")
+    if page_size <= 0 or page_size % 16:
+        raise ValueError(f"page_size must be a multiple of 16, not {page_size}")
+    for t, name, shape in zip(cache, KVCache._fields, _shapes(pages, page_size, kv_heads, 2 * half)):
+        _need(t, name, shape, torch.uint8, kc.device)
+    return _Cache(kc.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
+                  cache.v_scales.data_ptr(), pages, page_size, kv_heads, 2 * half, int(k_exp),
+                  int(v_exp))
+
+
+def _vectors(t, name, shape, dtype, device):
+    """A [tokens, heads, D] tensor with unit stride along D and free others."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dim")
+
+
+def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_exp: int = 0,
+           v_exp: int = 0, mode: int = MODE_ADAPTIVE) -> KVCache:
+    """Quantize k and v ([tokens, kv_heads, D], fp32 or bf16, unit stride along
+    D, other strides multiples of 16 bytes: slices of a fused projection are
+    fine) into the cache's slots (int64 [tokens], all different; a slot outside
+    the cache is skipped).  Returns the cache, which is written in place."""
+    c = _cache(cache, k_exp, v_exp)
+    dev = cache.k_codes.device
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a 3-D tensor [tokens, kv_heads, D]")
+    shape = (k.shape[0], c.kv_heads, c.head_dim)
+    _vectors(k, "k", shape, k.dtype, dev)
+    _vectors(v, "v", shape, k.dtype, dev)
+    _need(slots, "slots", (shape[0],), torch.int64, dev)
+    st = lib.if4_kv_append(c, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), shape[0],
+                           k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr(),
+                           int(mode), _stream(dev))
+    _check("if4_kv_append", st)
+    return cache
+
+
+def read(cache: KVCache, slots: torch.Tensor, k_exp: int = 0, v_exp: int = 0,
+         dtype=torch.bfloat16, out=None):
+    """Values of the cache's slots (int64 [tokens]): (k, v), each [tokens,
+    kv_heads, D] of `dtype` (bf16 or fp32).  A slot outside the cache reads as
+    zeros.  `out` may pass preallocated (k, v)."""
+    c = _cache(cache, k_exp, v_exp)
+    dev = cache.k_codes.device
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D tensor")
+    _need(slots, "slots", tuple(slots.shape), torch.int64, dev)
+    shape = (slots.shape[0], c.kv_heads, c.head_dim)
+    if out is None:
+        k, v = torch.empty((2, *shape), dtype=dtype, device=dev).unbind(0)
+    else:
+        k, v = out
+        _need(k, "k", shape, k.dtype, dev)
+        _need(v, "v", shape, k.dtype, dev)
+    st = lib.if4_kv_read(c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+                         _dtype_code(k.dtype), _stream(dev))
+    _check("if4_kv_read", st)
+    return k, v
+
+
+def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+              q_starts: torch.Tensor, *, max_q: int, max_len=None, scale=None, k_exp: int = 0,
+              v_exp: int = 0, causal: bool = True, window: int = 0, sinks: int = 0, out=None,
+              workspace=None) -> torch.Tensor:
+    """Attention of the newest tokens of a batch of sequences over the cache.
+
+    q [total_q, heads, D] bf16 (unit stride along D) holds the sequences'
+    newest tokens one after another, sequence b in rows q_starts[b] ..
+    q_starts[b + 1] - 1 (int32 [batch + 1]); seq_lens (int32 [batch]) counts
+    the tokens that each has in the cache, these included; page_table (int32
+    [batch, pages of the longest]) names their pages.  max_q: the most rows of
+    any sequence.  max_len: about how long the longest is (default: what the
+    page table has room for); it only steers how the work is split.
+
+    A row at position p sees key j iff j <= p (causal) and, with a window, j >
+    p - window or j < sinks.  Rows that see no key give zeros.  scale defaults
+    to 1/sqrt(D).  Returns [total_q, heads, D] bf16; `out` may pass it
+    preallocated, `workspace` a uint8 tensor of workspace_bytes()."""
+    c = _cache(cache, k_exp, v_exp)
+    dev = cache.k_codes.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a 3-D tensor [total_q, heads, D]")
+    total, heads, dim = q.shape
+    _vectors(q, "q", (total, heads, c.head_dim), torch.bfloat16, dev)
+    if heads == 0 or heads % c.kv_heads:
+        raise ValueError(f"heads ({heads}) must be a multiple of kv_heads ({c.kv_heads})")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a 2-D tensor [batch, pages]")
+    batch, width = page_table.shape
+    _need(page_table, "page_table", (batch, width), torch.int32, dev)
+    _need(seq_lens, "seq_lens", (batch,), torch.int32, dev)
+    _need(q_starts, "q_starts", (batch + 1,), torch.int32, dev)
+    scale = dim ** -0.5 if scale is None else float(scale)
+    if not (math.isfinite(scale) and scale >= 0):
+        raise ValueError("scale must be finite and not negative")
+    if window < 0 or sinks < 0 or (not causal and (window or sinks)):
+        raise ValueError("window and sinks must not be negative, and need causal")
+    if out is None:
+        out = torch.empty((total, heads, dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _vectors(out, "out", (total, heads, dim), torch.bfloat16, dev)
+    a = _Attention(q.data_ptr(), out.data_ptr(), q.stride(0), q.stride(1), out.stride(0),
+                   out.stride(1), page_table.data_ptr(), width, seq_lens.data_ptr(),
+                   q_starts.data_ptr(), batch, total, heads, int(max_q),
+                   width * c.page_size if max_len is None else int(max_len), int(window),
+                   int(sinks), scale, int(bool(causal)))
+    need = lib.if4_kv_attention_workspace(c, a)
+    if need < 0:
+        _check("if4_kv_attention", -need)
+    if workspace is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        ws = workspace
+        if not isinstance(ws, torch.Tensor) or ws.device != dev or ws.dtype != torch.uint8 or \
+                not ws.is_contiguous() or ws.numel() < need:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
+    st = lib.if4_kv_attention(c, a, ws.data_ptr() if ws is not None else None,
+                              ws.numel() if ws is not None else 0, _stream(dev))
+    _check("if4_kv_attention", st)
+    return out
+
+
+def workspace_bytes(cache: KVCache, *, total_q: int, heads: int, batch: int, max_q: int,
+                    max_len: int, window: int = 0, sinks: int = 0) -> int:
+    """Bytes that attention() needs for these sizes: a program that captures
+    calls in a graph, or makes many, allocates them once."""
+    c = _cache(cache, 0, 0)
+    a = _Attention(batch=batch, total_q=total_q, heads=heads, max_q=max_q, max_len=max_len,
+                   window=window, sinks=sinks, scale=1.0, causal=1)
+    need = lib.if4_kv_attention_workspace(c, a)
+    if need < 0:
+        _check("if4_kv_attention_workspace", -need)
+    return need
