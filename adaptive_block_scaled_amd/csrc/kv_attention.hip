@@ -25,6 +25,7 @@ namespace if4 {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -142,6 +143,27 @@ __device__ __forceinline__ float q_value(float x, int e) {
                                                 : __uint_as_float(0x7FC00000u);
 }
 
+// Largest magnitude of 8 bf16 values, and their operand.
+__device__ __forceinline__ float largest(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        a = __builtin_fmaxf(a, __uint_as_float((w[j] << 16) & 0x7FFFFFFFu));
+        a = __builtin_fmaxf(a, __uint_as_float(w[j] & 0x7FFF0000u));
+    }
+    return a;
+}
+__device__ __forceinline__ half8 q_operand(const uint4& v, int e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        h[j] = pack_half(q_value(__uint_as_float(w[j] << 16), e),
+                         q_value(__uint_as_float(w[j] & 0xFFFF0000u), e));
+    return __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
+}
+
 // ---------------------------------------------------------------------------
 // Few rows (a decode step, short chunks): tiles of 16 * kBlocks rows.
 //
@@ -203,7 +225,7 @@ struct FewRows {
 };
 
 template <int D, int kBlocks>
-__global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 3 : 1) few_rows_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) few_rows_kernel(const Args p) {
     constexpr int kRows = 16 * kBlocks, kPad = D + 4, M = D / 16;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint2* const tables = reinterpret_cast<uint2*>(smem);
@@ -249,27 +271,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 3 : 1) fe
 #pragma unroll
         for (int i = 0; i < D / 32; i++) {
             raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                a = __builtin_fmaxf(a, __uint_as_float((w[j] << 16) & 0x7FFFFFFFu));
-                a = __builtin_fmaxf(a, __uint_as_float(w[j] & 0x7FFF0000u));
-            }
+            a = __builtin_fmaxf(a, largest(raw[i]));
         }
         a = __builtin_fmaxf(a, __shfl_xor(a, 16));
         a = __builtin_fmaxf(a, __shfl_xor(a, 32));
         const int e = row_exponent(a);
 #pragma unroll
-        for (int i = 0; i < D / 32; i++) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            uint4 h;
-            uint32_t* hw = &h.x;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                hw[j] = pack_half(q_value(__uint_as_float(w[j] << 16), e),
-                                  q_value(__uint_as_float(w[j] & 0xFFFF0000u), e));
-            q[nr][i] = __builtin_bit_cast(half8, h);
-        }
+        for (int i = 0; i < D / 32; i++) q[nr][i] = q_operand(raw[i], e);
         factor[nr] = score_factor(p, e);
         const int pos = s.pos0 + t;
         see_hi[nr] = p.causal && pos < s.len - 1 ? pos : s.len - 1;
@@ -468,6 +476,335 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 3 : 1) fe
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows (chunks of prompt): tiles of 128 * kBlocks rows, 4 waves of
+// 32 * kBlocks rows each.
+//
+// The four waves share K and V: each decodes one 16-token cache tile of every
+// 64 keys into double-buffered LDS tiles in the order of the operands of
+// v_mfma_f32_32x32x16_f16, so that every operand is one contiguous 1 KB
+// ds_read_b128 and every ds_write covers whole banks.
+//
+// Operand order.  K, block of 32 keys, step t: lane (key, half h) holds word
+// 2t + h (8 dims) of its key.  V, 16 keys, block b of 32 rows: row r is dim
+// M (r % 16) + 2b + r / 16 with M = D/16 (the pieces of the cache's V are rows
+// apart), lane (row, h) holds keys 4h .. 4h + 3 and 8 + 4h .. 11 + 4h: the
+// order in which S^T's accumulators hold the probabilities.
+//
+// Steps of 32 keys are pipelined: while the matrix cores compute the scores of
+// step k + 1, the VALU turns those of step k into probabilities, and while
+// they add step k to O, it decodes the next tile.
+template <int D>
+struct ManyRows {
+    static constexpr int kTile = 64 * D * 2;  // bytes of K or V of 64 keys
+    static constexpr int kFlags = kScaleTableBytes + 4 * kTile;
+    static constexpr int kLds = kFlags + 2 * kWaves * 4;
+};
+
+// Workgroup barrier that orders LDS only: global loads in flight (the codes
+// of the next tiles) are not waited for.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <int D, int kBlocks>
+__global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
+    constexpr int kRows = 128 * kBlocks, T = D / 16, B = D / 32, M = D / 16;
+    constexpr int kTile = ManyRows<D>::kTile;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    uint2* const tables = reinterpret_cast<uint2*>(smem);
+    uint8_t* const k_lds = smem + kScaleTableBytes;
+    uint8_t* const v_lds = k_lds + 2 * kTile;
+    uint32_t* const flags = reinterpret_cast<uint32_t*>(smem + ManyRows<D>::kFlags);
+
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // (sequence, kv head) fastest, as for few rows; the last row tiles, which
+    // see the most keys, first
+    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
+    const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
+    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+
+    const Sequence s = sequence_of(p, b);
+    const int row0 = row_tile * kRows, rows = s.rows * p.group;
+    if (row0 >= rows) return;
+    fill_scale_tables(tables, tid, kThreads);
+
+    const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
+    const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
+    const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, 64);
+    const int per = (units.n + p.splits - 1) / p.splits;
+    const int begin = split * per;
+    const int end = begin + per < units.n ? begin + per : units.n;
+
+    half8 q[kBlocks][T];
+    float factor[kBlocks], m[kBlocks], l[kBlocks];
+    int see_hi[kBlocks], see_lo[kBlocks];
+    f32x16 o[B][kBlocks], x[2][kBlocks];
+#pragma unroll
+    for (int nr = 0; nr < kBlocks; nr++) {
+        const int r = row0 + 32 * (kBlocks * wave + nr) + (lane & 31);
+        const int rc = r < rows ? r : rows - 1;
+        const int t = rc / p.group, g = rc - t * p.group;
+        const uint16_t* src = p.q + (s.first_row + t) * p.q_st +
+                              (int64_t)(head * p.group + g) * p.q_sh + half * 8;
+        uint4 raw[T];
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < T; i++) {
+            raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
+            a = __builtin_fmaxf(a, largest(raw[i]));
+        }
+        a = __builtin_fmaxf(a, __shfl_xor(a, 32));
+        const int e = row_exponent(a);
+#pragma unroll
+        for (int i = 0; i < T; i++) q[nr][i] = q_operand(raw[i], e);
+        factor[nr] = score_factor(p, e);
+        const int pos = s.pos0 + t;
+        see_hi[nr] = p.causal && pos < s.len - 1 ? pos : s.len - 1;
+        see_lo[nr] = p.window ? pos - p.window : -1;
+        m[nr] = kLowest;
+        l[nr] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < B; d++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) o[d][nr][i] = 0.0f;
+    }
+
+    // this lane's codes of its wave's cache tile: K (key lane % 16, quarter
+    // lane / 16 of D), V (piece lane % 16, tokens 4 quarter ..); V's quarters
+    // are dealt so that each half wave writes whole 16-byte pieces
+    const int kq = lane >> 4, vq = (kq & 1) * 2 + (kq >> 1);
+    const uint32_t k_at = (lane & 15) * (D / 2) + kq * (D / 8);
+    const uint32_t v_at = (lane & 15) * (D / 2) + vq * (D / 8);
+    const uint32_t ks_at = (lane & 15) * (D / 16) + kq * (D / 64);
+    const uint32_t vs_at = (lane & 15) * D / 256 * 16 + vq * 4;
+    uint8_t* const k_to = k_lds + ((wave >> 1) * T + kq * (D / 64)) * 1024 +
+                          (16 * (wave & 1) + (lane & 15)) * 16;
+    uint8_t* const v_to =
+        v_lds + wave * B * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8;
+
+    uint32_t kw[D / 32], vw[D / 32], ks, vs;
+    auto load_k = [&](int i) {
+        const int u = units(i < end ? i : end - 1);
+        const int64_t at = cache_tile(p, s, head, 4 * u + wave);
+        UnitCodes<D>::words(p.k_codes + at * (8 * D) + k_at, kw);
+        const uint8_t* src = p.k_scales + at * D + ks_at;
+        if constexpr (D == 64)
+            ks = *src;
+        else if constexpr (D == 128)
+            ks = *reinterpret_cast<const uint16_t*>(src);
+        else
+            ks = *reinterpret_cast<const uint32_t*>(src);
+    };
+    auto load_v = [&](int i) {
+        const int u = units(i < end ? i : end - 1);
+        const int64_t at = cache_tile(p, s, head, 4 * u + wave);
+        UnitCodes<D>::words(p.v_codes + at * (8 * D) + v_at, vw);
+        vs = *reinterpret_cast<const uint32_t*>(p.v_scales + at * D + vs_at);
+    };
+    auto decode_k = [&](int buf) {
+#pragma unroll
+        for (int w = 0; w < D / 32; w++) {
+            const GroupScale sc = k_scale(tables, (ks >> (8 * (w / 2))) & 0xFFu);
+            *reinterpret_cast<half8*>(k_to + buf * kTile + (w >> 1) * 1024 + (w & 1) * 512) =
+                decode_k_word(kw[w], sc);
+        }
+    };
+    auto decode_v = [&](int buf) {
+        uint32_t out[M][2];
+        decode_v_piece<D>(vw, vs, tables, out);
+#pragma unroll
+        for (int d = 0; d < M; d++)
+            *reinterpret_cast<uint2*>(v_to + buf * kTile + (d >> 1) * 1024 + (d & 1) * 256) =
+                make_uint2(out[d][0], out[d][1]);
+        const uint64_t bad = __builtin_amdgcn_ballot_w64(nan_bytes(vs) != 0);
+        if (lane == 0) flags[buf * kWaves + wave] = bad != 0;
+    };
+    // scores of 32 keys
+    auto scores = [&](f32x16 (&to)[kBlocks], int buf, int kb) {
+        const uint8_t* src = k_lds + buf * kTile + kb * T * 1024 + lane * 16;
+#pragma unroll
+        for (int nr = 0; nr < kBlocks; nr++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) to[nr][i] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; t++) {
+            const half8 a = *reinterpret_cast<const half8*>(src + t * 1024);
+#pragma unroll
+            for (int nr = 0; nr < kBlocks; nr++)
+                to[nr] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[nr][t], to[nr], 0, 0, 0);
+        }
+    };
+    // hides what a row does not see, and raises m where it has to
+    auto settle = [&](f32x16 (&sc)[kBlocks], int key0) {
+        const bool all = key0 + 32 <= s.len && (!p.causal || key0 + 31 <= pos_lo) &&
+                         (!p.window || key0 > pos_hi - p.window || key0 + 32 <= p.sinks);
+        if (!all) {
+#pragma unroll
+            for (int nr = 0; nr < kBlocks; nr++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int key = key0 + 8 * (i >> 2) + 4 * half + (i & 3);
+                    const bool seen = key <= see_hi[nr] && (key > see_lo[nr] || key < p.sinks);
+                    sc[nr][i] = seen ? sc[nr][i] : -__builtin_inff();
+                }
+        }
+        float top[kBlocks];
+        bool raise = false;
+#pragma unroll
+        for (int nr = 0; nr < kBlocks; nr++) {
+            top[nr] = sc[nr][0];
+#pragma unroll
+            for (int i = 1; i < 16; i++) top[nr] = __builtin_fmaxf(top[nr], sc[nr][i]);
+            top[nr] *= factor[nr];
+            raise |= top[nr] > m[nr] + kSlack;
+        }
+        if (__builtin_amdgcn_ballot_w64(raise) != 0) {
+#pragma unroll
+            for (int nr = 0; nr < kBlocks; nr++) {
+                float t = __builtin_fmaxf(top[nr], m[nr]);
+                t = __builtin_fmaxf(t, __shfl_xor(t, 32));
+                const float alpha = __builtin_amdgcn_exp2f(m[nr] - t);
+                m[nr] = t;
+                l[nr] *= alpha;
+#pragma unroll
+                for (int d = 0; d < B; d++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) o[d][nr][i] *= alpha;
+            }
+        }
+    };
+    uint4 prob[kBlocks][2];
+    auto probabilities = [&](f32x16 (&sc)[kBlocks]) {
+#pragma unroll
+        for (int nr = 0; nr < kBlocks; nr++) {
+            float e[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nr][i], factor[nr], -m[nr]));
+                l[nr] += e[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                prob[nr][i] =
+                    make_uint4(pack_half(e[8 * i], e[8 * i + 1]), pack_half(e[8 * i + 2], e[8 * i + 3]),
+                               pack_half(e[8 * i + 4], e[8 * i + 5]),
+                               pack_half(e[8 * i + 6], e[8 * i + 7]));
+        }
+    };
+    auto accumulate = [&](int buf, int kb) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int d = 0; d < B; d++) {
+                const half8 a = *reinterpret_cast<const half8*>(
+                    v_lds + buf * kTile + ((2 * kb + i) * B + d) * 1024 + lane * 16);
+#pragma unroll
+                for (int nr = 0; nr < kBlocks; nr++)
+                    o[d][nr] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        a, __builtin_bit_cast(half8, prob[nr][i]), o[d][nr], 0, 0, 0);
+            }
+    };
+    // NaN values of V (decoded as zeros) of a 64-key tile: into the rows that
+    // see them
+    auto poison = [&](int u) {
+#pragma unroll 1
+        for (int j = 0; j < 4 * T; j++) {  // 16-token tile j / T, group j % T
+            const int64_t at = cache_tile(p, s, head, 4 * u + j / T);
+            const uint8_t* src = p.v_scales + at * D + (j % T) * 16;
+#pragma unroll 1
+            for (int t = 0; t < 16; t++) {
+                if ((src[t] & 0x7F) != 0x7F) continue;
+                const int key = 64 * u + 16 * (j / T) + t;
+#pragma unroll
+                for (int nr = 0; nr < kBlocks; nr++) {
+                    const bool seen = key <= see_hi[nr] && (key > see_lo[nr] || key < p.sinks);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
+                        const bool hit = seen && piece * M / 16 == j % T;
+#pragma unroll
+                        for (int d = 0; d < B; d++)
+                            o[d][nr][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][nr][i];
+                    }
+                }
+            }
+        }
+    };
+
+    __syncthreads();
+    if (begin < end) {
+        load_k(begin);
+        load_v(begin);
+        decode_k(0);
+        load_k(begin + 1);
+        decode_v(0);
+        load_v(begin + 1);
+        lds_barrier();
+        scores(x[0], 0, 0);
+        settle(x[0], 64 * units(begin));
+#pragma unroll 1
+        for (int i = begin; i < end; i++) {
+            const int buf = (i - begin) & 1, u = units(i);
+            // keys 0 .. 31 of the tile
+            scores(x[1], buf, 1);
+            probabilities(x[0]);
+            accumulate(buf, 0);
+            decode_k(buf ^ 1);
+            load_k(i + 2);
+            settle(x[1], 64 * u + 32);
+            lds_barrier();
+            // keys 32 .. 63
+            scores(x[0], buf ^ 1, 0);
+            probabilities(x[1]);
+            accumulate(buf, 1);
+            const uint4 f = *reinterpret_cast<const uint4*>(flags + buf * kWaves);
+            if (__builtin_amdgcn_readfirstlane((f.x | f.y) | (f.z | f.w)) != 0) poison(u);
+            decode_v(buf ^ 1);
+            load_v(i + 2);
+            if (i + 1 < end) settle(x[0], 64 * units(i + 1));
+            lds_barrier();
+        }
+    }
+
+#pragma unroll
+    for (int nr = 0; nr < kBlocks; nr++) {
+        l[nr] += __shfl_xor(l[nr], 32);
+        const int r = row0 + 32 * (kBlocks * wave + nr) + (lane & 31);
+        if (r >= rows) continue;
+        const int t = r / p.group, g = r - t * p.group;
+        const int64_t row = s.first_row + t, hd = head * p.group + g;
+        if (p.splits == 1) {
+            const float f = l[nr] == 0.0f ? 0.0f : p.v_mul / l[nr];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh +
+                                                            piece * M);
+#pragma unroll
+                for (int d = 0; d < B; d++)
+                    dst[d] = pack_bf16(o[d][nr][i] * f, o[d][nr][i + 8] * f);
+            }
+        } else {
+            const int64_t at = split * p.rows_all + row * p.heads + hd;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
+                f32x2* dst = reinterpret_cast<f32x2*>(p.part_o + at * D + piece * M);
+#pragma unroll
+                for (int d = 0; d < B; d++) dst[d] = f32x2{o[d][nr][i], o[d][nr][i + 8]};
+            }
+            if (half == 0) {
+                p.part_ml[2 * at] = m[nr];
+                p.part_ml[2 * at + 1] = l[nr];
+            }
+        }
+    }
+}
+
 // Joins the splits of every row: one wave per row, lane l the dims l D/64 ..
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
@@ -504,7 +841,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
 // ---------------------------------------------------------------------------
 // Host side: which kernel, how many splits.
 struct Plan {
-    int blocks;  // row blocks of 16 per tile
+    bool many;
+    int blocks;  // row blocks of a tile (few rows) or of a wave (many rows)
     int row_tiles;
     int splits;
     int64_t ws_o, ws_ml;  // bytes
@@ -513,15 +851,25 @@ struct Plan {
 Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     Plan pl;
     const int64_t group = a.heads / c.kv_heads, rows = a.max_q * group;
-    pl.blocks = rows <= 16 || c.head_dim == 256 ? 1 : 2;
-    pl.row_tiles = (int)((rows + 16 * pl.blocks - 1) / (16 * pl.blocks));
-    // Splits of the keys: enough workgroups to fill 256 CUs a few times over,
-    // and at least one unit for each wave of a split.
+    pl.many = rows > 32;
+    int tile;
+    if (pl.many) {
+        pl.blocks = c.head_dim == 256 || rows <= 128 ? 1 : 2;
+        tile = 128 * pl.blocks;
+    } else {
+        pl.blocks = rows <= 16 || c.head_dim == 256 ? 1 : 2;
+        tile = 16 * pl.blocks;
+    }
+    pl.row_tiles = (int)((rows + tile - 1) / tile);
+    // Splits of the keys: enough workgroups to fill 256 CUs a few times over
+    // (twice where a workgroup fills a CU's registers), each with at least one
+    // unit of keys for each of its waves.
     int64_t keys = a.max_len;
     if (a.window && a.window + a.sinks + a.max_q < keys) keys = a.window + a.sinks + a.max_q;
     const int64_t base = a.batch * c.kv_heads * pl.row_tiles;
-    const int64_t most = (keys + kUnit * kWaves - 1) / (kUnit * kWaves);
-    int64_t s = base > 0 ? 1024 / base : 1;
+    const int64_t unit = pl.many ? 256 : kUnit * kWaves;
+    const int64_t most = (keys + unit - 1) / unit;
+    int64_t s = base > 0 ? (pl.many ? 512 : 1024) / base : 1;
     s = s > most ? most : s;
     pl.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
     const int64_t rows_all = a.total_q * a.heads;
@@ -530,18 +878,16 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     return pl;
 }
 
-template <int D, int kBlocks>
-hipError_t few_rows(const Args& p, hipStream_t stream) {
-    constexpr int lds = FewRows<D, kBlocks>::kLds;
-    const void* f = (const void*)few_rows_kernel<D, kBlocks>;
+template <int D>
+hipError_t launch(void (*kernel)(Args), int lds, const Args& p, hipStream_t stream) {
     if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        const hipError_t e = hipFuncSetAttribute((const void*)kernel,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
     const int64_t grid = (int64_t)p.batch_heads * p.row_tiles * p.splits;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((few_rows_kernel<D, kBlocks>), dim3((unsigned)grid), dim3(kThreads), lds,
-                       stream, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t joins = (p.rows_all + kWaves - 1) / kWaves;
@@ -553,9 +899,12 @@ hipError_t few_rows(const Args& p, hipStream_t stream) {
 template <int D>
 hipError_t dispatch(const Args& p, const Plan& pl, hipStream_t stream) {
     if constexpr (D < 256) {
-        if (pl.blocks == 2) return few_rows<D, 2>(p, stream);
+        if (pl.blocks == 2)
+            return pl.many ? launch<D>(many_rows_kernel<D, 2>, ManyRows<D>::kLds, p, stream)
+                           : launch<D>(few_rows_kernel<D, 2>, FewRows<D, 2>::kLds, p, stream);
     }
-    return few_rows<D, 1>(p, stream);
+    return pl.many ? launch<D>(many_rows_kernel<D, 1>, ManyRows<D>::kLds, p, stream)
+                   : launch<D>(few_rows_kernel<D, 1>, FewRows<D, 1>::kLds, p, stream);
 }
 
 int clamp_int(int64_t v) { return (int)(v > 0x3FFFFFFF ? 0x3FFFFFFF : v); }
