@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from .if4 import GROUP, MODE_ADAPTIVE, _check, _dtype_code, _need, _stream, lib
+from .if4 import GROUP, MODE_ADAPTIVE, _check, _dtype_code, _need, lib
 
 EXPORTS = ("if4_kv_append", "if4_kv_read", "if4_kv_attention", "if4_kv_attention_workspace")
 HEAD_DIMS = (64, 128, 256)
@@ -40,6 +40,10 @@ class _Attention(ctypes.Structure):
                 ("max_q", ctypes.c_int64), ("max_len", ctypes.c_int64),
                 ("window", ctypes.c_int64), ("sinks", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("causal", ctypes.c_int32)]
+
+
+# torch.cuda.current_stream(device).cuda_stream without the Stream object
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _declare():
@@ -84,8 +88,17 @@ def _shapes(pages, page_size, kv_heads, head_dim):
             (pages, kv_heads, tiles, head_dim // GROUP, 16))
 
 
+def _is(t, shape, dtype, index) -> bool:
+    """Whether t is a contiguous tensor of this shape and type on CUDA device
+    `index`: the check of a call that is in order.  It costs a third of a
+    microsecond; only one that fails goes on to _need, which says what is
+    wrong."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and
+            t.shape == shape and t.is_contiguous())
+
+
 def _cache(cache: KVCache, k_exp: int, v_exp: int):
-    kc = cache.k_codes
+    kc, ks, vc, vs = cache
     if not isinstance(kc, torch.Tensor) or not kc.is_cuda or kc.dim() != 4:
         raise ValueError("k_codes must be a CUDA tensor [pages, kv_heads, page_size, D/2]")
     pages, kv_heads, page_size, half = kc.shape
@@ -93,23 +106,31 @@ def _cache(cache: KVCache, k_exp: int, v_exp: int):
         raise ValueError(f"head_dim must be one of {HEAD_DIMS}, not {2 * half}")
     if page_size <= 0 or page_size % 16:
         raise ValueError(f"page_size must be a multiple of 16, not {page_size}")
-    for t, name, shape in zip(cache, KVCache._fields, _shapes(pages, page_size, kv_heads, 2 * half)):
-        _need(t, name, shape, torch.uint8, kc.device)
-    return _Cache(kc.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
-                  cache.v_scales.data_ptr(), pages, page_size, kv_heads, 2 * half, int(k_exp),
-                  int(v_exp))
+    u8, index = torch.uint8, kc.get_device()
+    shapes = _shapes(pages, page_size, kv_heads, 2 * half)
+    if not (_is(kc, shapes[0], u8, index) and _is(ks, shapes[1], u8, index) and
+            _is(vc, shapes[2], u8, index) and _is(vs, shapes[3], u8, index)):
+        for t, name, shape in zip(cache, KVCache._fields, shapes):
+            _need(t, name, shape, u8, kc.device)
+    return _Cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page_size,
+                  kv_heads, 2 * half, int(k_exp), int(v_exp)), index
 
 
-def _vectors(t, name, shape, dtype, device):
+def _vectors(t, name, shape, dtype, index):
     """A [tokens, heads, D] tensor with unit stride along D and free others."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.stride(2) != 1:
         raise ValueError(f"{name} must have unit stride along its last dim")
+
+
+def _plain(t, name, shape, dtype, index):
+    if not _is(t, shape, dtype, index):
+        _need(t, name, shape, dtype, torch.device("cuda", index))
 
 
 def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_exp: int = 0,
@@ -118,18 +139,18 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     D, other strides multiples of 16 bytes: slices of a fused projection are
     fine) into the cache's slots (int64 [tokens], all different; a slot outside
     the cache is skipped).  Returns the cache, which is written in place."""
-    c = _cache(cache, k_exp, v_exp)
-    dev = cache.k_codes.device
+    c, index = _cache(cache, k_exp, v_exp)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a 3-D tensor [tokens, kv_heads, D]")
     shape = (k.shape[0], c.kv_heads, c.head_dim)
-    _vectors(k, "k", shape, k.dtype, dev)
-    _vectors(v, "v", shape, k.dtype, dev)
-    _need(slots, "slots", (shape[0],), torch.int64, dev)
-    st = lib.if4_kv_append(c, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), shape[0],
-                           k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr(),
-                           int(mode), _stream(dev))
-    _check("if4_kv_append", st)
+    _vectors(k, "k", shape, k.dtype, index)
+    _vectors(v, "v", shape, k.dtype, index)
+    _plain(slots, "slots", shape[:1], torch.int64, index)
+    (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
+    st = lib.if4_kv_append(c, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), shape[0], kt, kh,
+                           vt, vh, slots.data_ptr(), int(mode), _raw_stream(index))
+    if st:
+        _check("if4_kv_append", st)
     return cache
 
 
@@ -138,21 +159,24 @@ def read(cache: KVCache, slots: torch.Tensor, k_exp: int = 0, v_exp: int = 0,
     """Values of the cache's slots (int64 [tokens]): (k, v), each [tokens,
     kv_heads, D] of `dtype` (bf16 or fp32).  A slot outside the cache reads as
     zeros.  `out` may pass preallocated (k, v)."""
-    c = _cache(cache, k_exp, v_exp)
-    dev = cache.k_codes.device
+    c, index = _cache(cache, k_exp, v_exp)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D tensor")
-    _need(slots, "slots", tuple(slots.shape), torch.int64, dev)
+    _plain(slots, "slots", slots.shape, torch.int64, index)
     shape = (slots.shape[0], c.kv_heads, c.head_dim)
     if out is None:
-        k, v = torch.empty((2, *shape), dtype=dtype, device=dev).unbind(0)
+        k = torch.empty(shape, dtype=dtype, device=slots.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
-        _need(k, "k", shape, k.dtype, dev)
-        _need(v, "v", shape, k.dtype, dev)
+        if not isinstance(k, torch.Tensor):
+            raise ValueError("out must be two tensors (k, v)")
+        _plain(k, "k", shape, k.dtype, index)
+        _plain(v, "v", shape, k.dtype, index)
     st = lib.if4_kv_read(c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-                         _dtype_code(k.dtype), _stream(dev))
-    _check("if4_kv_read", st)
+                         _dtype_code(k.dtype), _raw_stream(index))
+    if st:
+        _check("if4_kv_read", st)
     return k, v
 
 
@@ -174,47 +198,47 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_len
     p - window or j < sinks.  Rows that see no key give zeros.  scale defaults
     to 1/sqrt(D).  Returns [total_q, heads, D] bf16; `out` may pass it
     preallocated, `workspace` a uint8 tensor of workspace_bytes()."""
-    c = _cache(cache, k_exp, v_exp)
-    dev = cache.k_codes.device
+    c, index = _cache(cache, k_exp, v_exp)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D tensor [total_q, heads, D]")
-    total, heads, dim = q.shape
-    _vectors(q, "q", (total, heads, c.head_dim), torch.bfloat16, dev)
+    shape = total, heads, dim = q.shape
+    _vectors(q, "q", (total, heads, c.head_dim), torch.bfloat16, index)
     if heads == 0 or heads % c.kv_heads:
         raise ValueError(f"heads ({heads}) must be a multiple of kv_heads ({c.kv_heads})")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a 2-D tensor [batch, pages]")
     batch, width = page_table.shape
-    _need(page_table, "page_table", (batch, width), torch.int32, dev)
-    _need(seq_lens, "seq_lens", (batch,), torch.int32, dev)
-    _need(q_starts, "q_starts", (batch + 1,), torch.int32, dev)
+    _plain(page_table, "page_table", (batch, width), torch.int32, index)
+    _plain(seq_lens, "seq_lens", (batch,), torch.int32, index)
+    _plain(q_starts, "q_starts", (batch + 1,), torch.int32, index)
     scale = dim ** -0.5 if scale is None else float(scale)
-    if not (math.isfinite(scale) and scale >= 0):
+    if not 0 <= scale < math.inf:
         raise ValueError("scale must be finite and not negative")
     if window < 0 or sinks < 0 or (not causal and (window or sinks)):
         raise ValueError("window and sinks must not be negative, and need causal")
     if out is None:
-        out = torch.empty((total, heads, dim), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     else:
-        _vectors(out, "out", (total, heads, dim), torch.bfloat16, dev)
-    a = _Attention(q.data_ptr(), out.data_ptr(), q.stride(0), q.stride(1), out.stride(0),
-                   out.stride(1), page_table.data_ptr(), width, seq_lens.data_ptr(),
-                   q_starts.data_ptr(), batch, total, heads, int(max_q),
+        _vectors(out, "out", shape, torch.bfloat16, index)
+    (qt, qh, _), (ot, oh, _) = q.stride(), out.stride()
+    a = _Attention(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, page_table.data_ptr(), width,
+                   seq_lens.data_ptr(), q_starts.data_ptr(), batch, total, heads, int(max_q),
                    width * c.page_size if max_len is None else int(max_len), int(window),
-                   int(sinks), scale, int(bool(causal)))
+                   int(sinks), scale, 1 if causal else 0)
     need = lib.if4_kv_attention_workspace(c, a)
     if need < 0:
         _check("if4_kv_attention", -need)
-    if workspace is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    else:
-        ws = workspace
-        if not isinstance(ws, torch.Tensor) or ws.device != dev or ws.dtype != torch.uint8 or \
-                not ws.is_contiguous() or ws.numel() < need:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
-    st = lib.if4_kv_attention(c, a, ws.data_ptr() if ws is not None else None,
-                              ws.numel() if ws is not None else 0, _stream(dev))
-    _check("if4_kv_attention", st)
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or \
+                workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+                workspace.numel() < need:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {q.device}")
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = lib.if4_kv_attention(c, a, workspace.data_ptr() if need else None, need,
+                              _raw_stream(index))
+    if st:
+        _check("if4_kv_attention", st)
     return out
 
 
@@ -222,7 +246,7 @@ def workspace_bytes(cache: KVCache, *, total_q: int, heads: int, batch: int, max
                     max_len: int, window: int = 0, sinks: int = 0) -> int:
     """Bytes that attention() needs for these sizes: a program that captures
     calls in a graph, or makes many, allocates them once."""
-    c = _cache(cache, 0, 0)
+    c, _ = _cache(cache, 0, 0)
     a = _Attention(batch=batch, total_q=total_q, heads=heads, max_q=max_q, max_len=max_len,
                    window=window, sinks=sinks, scale=1.0, causal=1)
     need = lib.if4_kv_attention_workspace(c, a)
