@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "if4_internal.h"
 #include "kv_internal.h"
 #include "kv_operand.h"
@@ -44,7 +46,7 @@ struct Args {
     int64_t table_stride;
     float *part_o, *part_ml;  // splits > 1: [splits][total_q * heads][D], [..][2]
     int64_t rows_all;         // total_q * heads
-    int total_q, pages, kv_heads, heads, group, batch_heads, row_tiles, splits;
+    int total_q, pages, kv_heads, heads, group, batch_heads, row_tiles, splits, split_units;
     int causal, window, sinks;
     // 16-token tiles per page, and its reciprocal: n / d = n * magic >> shift
     uint32_t page_tiles, page_magic;
@@ -102,15 +104,56 @@ __device__ __forceinline__ KeyUnits key_units(const Args& p, int len, int lo, in
     return u;
 }
 
+// Units that a split takes.  By the length hint, the same for every sequence,
+// so that workgroups take equally long and a short sequence has fewer of
+// them, unless this one is too long for that.
+__device__ __forceinline__ int units_per_split(const Args& p, int n) {
+    const int own = (n + p.splits - 1) / p.splits;
+    return own > p.split_units ? own : p.split_units;
+}
+
+// A split without keys: its rows' sums are zero, which the join skips.
+__device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int head, int row0,
+                                           int last_row) {
+    const int split = blockIdx.x / (p.batch_heads * p.row_tiles);
+    for (int r = row0 + threadIdx.x; r <= last_row; r += kThreads) {
+        const int t = r / p.group, g = r - t * p.group;
+        const int64_t at = split * p.rows_all + (int64_t)(s.first_row + t) * p.heads +
+                           head * p.group + g;
+        *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, 0.0f};
+    }
+}
+
 // Cache tile (16 tokens) of one kv head that holds keys 16 n .. 16 n + 15 of
-// a sequence; n past its last key gives some valid tile.
-__device__ __forceinline__ int64_t cache_tile(const Args& p, const Sequence& s, int head, int n) {
+// a sequence; n past its last key gives some valid tile.  Made in two steps,
+// so that the page table's entry can be on its way long before its use.
+struct TileRef {
+    int page;
+    uint32_t rest;  // tile in the page
+};
+__device__ __forceinline__ TileRef tile_ref(const Args& p, const Sequence& s, int n) {
     const int last = s.len > 0 ? (s.len - 1) >> 4 : 0;
     const uint32_t m = (uint32_t)(n < last ? n : last);
     const uint32_t i = (uint32_t)((uint64_t)m * p.page_magic >> p.page_shift);
-    int page = s.table[i];
-    page = page < 0 ? 0 : page >= p.pages ? p.pages - 1 : page;
-    return ((int64_t)page * p.kv_heads + head) * p.page_tiles + (m - i * p.page_tiles);
+    return {s.table[i], m - i * p.page_tiles};
+}
+__device__ __forceinline__ int64_t cache_tile(const Args& p, int head, TileRef r) {
+    const int page = r.page < 0 ? 0 : r.page >= p.pages ? p.pages - 1 : r.page;
+    return ((int64_t)page * p.kv_heads + head) * p.page_tiles + r.rest;
+}
+
+// 4, as a value that the compiler cannot fold (see high_bytes).
+__device__ __forceinline__ uint32_t opaque_four(const Args& p) {
+    return 4u + ((uint32_t)p.total_q >> 31);
+}
+
+// f(0), f(1) .. f(n - 1) with constants.
+template <int n, int i = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (i < n) {
+        f(std::integral_constant<int, i>{});
+        each<n, i + 1>(f);
+    }
 }
 
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
@@ -195,37 +238,46 @@ struct UnitCodes {
             }
         }
     }
-    __device__ __forceinline__ void load(const Args& p, const Sequence& s, int head, int unit,
-                                         int lane) {
+    __device__ __forceinline__ void load_k(const Args& p, const int64_t (&at)[2], int lane) {
         const uint32_t code = (lane & 15) * (D / 2) + (lane >> 4) * (D / 8);
-        const uint32_t ksc = (lane & 15) * (D / 16) + (lane >> 4) * (D / 64);
-        const uint32_t vsc = (lane & 15) * D / 256 * 16 + (lane >> 4) * 4;
+        const uint32_t scale = (lane & 15) * (D / 16) + (lane >> 4) * (D / 64);
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            const int64_t at = cache_tile(p, s, head, 2 * unit + t);
-            words(p.k_codes + at * (8 * D) + code, k[t]);
-            words(p.v_codes + at * (8 * D) + code, v[t]);
-            const uint8_t* kp = p.k_scales + at * D + ksc;
+            words(p.k_codes + at[t] * (8 * D) + code, k[t]);
+            const uint8_t* src = p.k_scales + at[t] * D + scale;
             if constexpr (D == 64)
-                ks[t] = *kp;
+                ks[t] = *src;
             else if constexpr (D == 128)
-                ks[t] = *reinterpret_cast<const uint16_t*>(kp);
+                ks[t] = *reinterpret_cast<const uint16_t*>(src);
             else
-                ks[t] = *reinterpret_cast<const uint32_t*>(kp);
-            vs[t] = *reinterpret_cast<const uint32_t*>(p.v_scales + at * D + vsc);
+                ks[t] = *reinterpret_cast<const uint32_t*>(src);
+        }
+    }
+    __device__ __forceinline__ void load_v(const Args& p, const int64_t (&at)[2], int lane) {
+        const uint32_t code = (lane & 15) * (D / 2) + (lane >> 4) * (D / 8);
+        const uint32_t scale = (lane & 15) * D / 256 * 16 + (lane >> 4) * 4;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            words(p.v_codes + at[t] * (8 * D) + code, v[t]);
+            vs[t] = *reinterpret_cast<const uint32_t*>(p.v_scales + at[t] * D + scale);
         }
     }
 };
 
 template <int D, int kBlocks>
 struct FewRows {
+    // Waves per SIMD that the registers are held to: single-token calls are
+    // bound by the latency of their loads (64 sequences of 3-12k keys: 154 us
+    // with two, 145 with three, 144 with four; 16 rows at D = 128 use 128
+    // registers).
+    static constexpr int kOccupancy = D * kBlocks <= 128 ? 4 : 2;
     static constexpr int kRows = 16 * kBlocks;
     static constexpr int kPad = D + 4;
     static constexpr int kLds = kScaleTableBytes + kWaves * 16 * kPad * 4 + 2 * kWaves * kRows * 4;
 };
 
 template <int D, int kBlocks>
-__global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) few_rows_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) few_rows_kernel(const Args p) {
     constexpr int kRows = 16 * kBlocks, kPad = D + 4, M = D / 16;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint2* const tables = reinterpret_cast<uint2*>(smem);
@@ -245,14 +297,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) fe
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * p.group;
     if (row0 >= rows) return;
-    fill_scale_tables(tables, tid, kThreads);
-
+    const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
     const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, kUnit);
-    const int per = (units.n + p.splits - 1) / p.splits;
+    const int per = units_per_split(p, units.n);
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
+    if (p.splits > 1 && begin >= end) {
+        mark_empty(p, s, head, row0, last_row);
+        return;
+    }
+    fill_scale_tables(tables, tid, kThreads);
 
     // this lane's row of each block, its q as operands, and what it sees:
     // keys <= see_hi that are > see_lo or < sinks
@@ -295,7 +351,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) fe
     }
     __syncthreads();
 
-    auto compute = [&](const UnitCodes<D>& c, int unit) {
+    UnitCodes<D> c;
+    // one unit; `next`: the cache tiles whose codes are asked for as soon as
+    // this unit's are decoded
+    auto compute = [&](int unit, const int64_t (&next)[2]) {
         const int key0 = unit * kUnit;
         f32x4 acc[2][kBlocks];
 #pragma unroll
@@ -303,15 +362,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) fe
 #pragma unroll
             for (int nr = 0; nr < kBlocks; nr++) acc[t][nr] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < D / 32; i++) {
-                const GroupScale sc = k_scale(tables, (c.ks[t] >> (8 * (i / 2))) & 0xFFu);
-                const half8 a = decode_k_word(c.k[t][i], sc);
+            for (int i = 0; i < D / 32; i += 2) {
+                half8 a[2];
+                decode_k_group(c.k[t][i], c.k[t][i + 1],
+                               k_scale(tables, (c.ks[t] >> (4 * i)) & 0xFFu), four, a[0], a[1]);
 #pragma unroll
-                for (int nr = 0; nr < kBlocks; nr++)
-                    acc[t][nr] =
-                        __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[nr][i], acc[t][nr], 0, 0, 0);
+                for (int j = 0; j < 2; j++)
+#pragma unroll
+                    for (int nr = 0; nr < kBlocks; nr++)
+                        acc[t][nr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            a[j], q[nr][i + j], acc[t][nr], 0, 0, 0);
             }
         }
+        c.load_k(p, next, lane);
         // does every row of the tile see every key of the unit?
         const bool all = key0 + kUnit <= s.len && (!p.causal || key0 + kUnit - 1 <= pos_lo) &&
                          (!p.window || key0 > pos_hi - p.window || key0 + kUnit <= p.sinks);
@@ -354,23 +417,26 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) fe
             prob[nr] = make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]),
                                   pack_half(x[4], x[5]), pack_half(x[6], x[7]));
         }
-        uint32_t v0[M][2], v1[M][2];
-        decode_v_piece<D>(c.v[0], c.vs[0], tables, v0);
-        decode_v_piece<D>(c.v[1], c.vs[1], tables, v1);
+        VPiece<D> v[2];
 #pragma unroll
-        for (int d = 0; d < M; d++) {
-            const half8 a =
-                __builtin_bit_cast(half8, make_uint4(v0[d][0], v0[d][1], v1[d][0], v1[d][1]));
+        for (int t = 0; t < 2; t++) v[t].unpack(c.v[t], c.vs[t], tables, four);
+        const uint32_t vs[2] = {c.vs[0], c.vs[1]};
+        c.load_v(p, next, lane);
+        each<M>([&](auto dim) {
+            constexpr int d = decltype(dim)::value;
+            const half8 a = __builtin_bit_cast(
+                half8, make_uint4(v[0].template pair<d, 0>(), v[0].template pair<d, 1>(),
+                                  v[1].template pair<d, 0>(), v[1].template pair<d, 1>()));
 #pragma unroll
             for (int nr = 0; nr < kBlocks; nr++)
                 o[d][nr] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                     a, __builtin_bit_cast(half8, prob[nr]), o[d][nr], 0, 0, 0);
-        }
+        });
         // NaN values of V (decoded as zeros): into the rows that see them
-        if (__builtin_amdgcn_ballot_w64((nan_bytes(c.vs[0]) | nan_bytes(c.vs[1])) != 0) != 0) {
+        if (__builtin_amdgcn_ballot_w64((nan_bytes(vs[0]) | nan_bytes(vs[1])) != 0) != 0) {
 #pragma unroll 1
             for (int j = 0; j < 8; j++) {
-                const uint32_t byte = ((j >> 2 ? c.vs[1] : c.vs[0]) >> (8 * (j & 3))) & 0x7Fu;
+                const uint32_t byte = ((j >> 2 ? vs[1] : vs[0]) >> (8 * (j & 3))) & 0x7Fu;
                 const uint64_t bad = __builtin_amdgcn_ballot_w64(byte == 0x7Fu);
 #pragma unroll 1
                 for (int quarter = 0; quarter < 4; quarter++) {
@@ -393,23 +459,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) fe
         }
     };
 
-    // two register sets in turn: the next unit's codes are on their way while
-    // one is computed, and no loaded value is copied (that would wait for it)
     int i = begin + wave;
     if (i < end) {
-        UnitCodes<D> c0, c1;
-        c0.load(p, s, head, units(i), lane);
-        while (true) {
-            const int n1 = i + kWaves < end ? i + kWaves : i;
-            c1.load(p, s, head, units(n1), lane);
-            compute(c0, units(i));
-            i += kWaves;
-            if (i >= end) break;
-            const int n2 = i + kWaves < end ? i + kWaves : i;
-            c0.load(p, s, head, units(n2), lane);
-            compute(c1, units(i));
-            i += kWaves;
-            if (i >= end) break;
+        const auto refs = [&](int j, TileRef (&r)[2]) {
+            const int u = units(j < end ? j : end - 1);
+            r[0] = tile_ref(p, s, 2 * u);
+            r[1] = tile_ref(p, s, 2 * u + 1);
+        };
+        const auto tiles = [&](const TileRef (&r)[2], int64_t (&at)[2]) {
+            at[0] = cache_tile(p, head, r[0]);
+            at[1] = cache_tile(p, head, r[1]);
+        };
+        TileRef r[2];
+        int64_t at[2];
+        refs(i, r);
+        tiles(r, at);
+        c.load_k(p, at, lane);
+        c.load_v(p, at, lane);
+        refs(i + kWaves, r);
+#pragma unroll 1
+        for (; i < end; i += kWaves) {
+            tiles(r, at);
+            refs(i + 2 * kWaves, r);
+            compute(units(i), at);
         }
     }
 
@@ -530,14 +602,18 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * p.group;
     if (row0 >= rows) return;
-    fill_scale_tables(tables, tid, kThreads);
-
+    const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
     const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, 64);
-    const int per = (units.n + p.splits - 1) / p.splits;
+    const int per = units_per_split(p, units.n);
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
+    if (p.splits > 1 && begin >= end) {
+        mark_empty(p, s, head, row0, last_row);
+        return;
+    }
+    fill_scale_tables(tables, tid, kThreads);
 
     half8 q[kBlocks][T];
     float factor[kBlocks], m[kBlocks], l[kBlocks];
@@ -589,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
     uint32_t kw[D / 32], vw[D / 32], ks, vs;
     auto load_k = [&](int i) {
         const int u = units(i < end ? i : end - 1);
-        const int64_t at = cache_tile(p, s, head, 4 * u + wave);
+        const int64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + wave));
         UnitCodes<D>::words(p.k_codes + at * (8 * D) + k_at, kw);
         const uint8_t* src = p.k_scales + at * D + ks_at;
         if constexpr (D == 64)
@@ -601,25 +677,29 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
     };
     auto load_v = [&](int i) {
         const int u = units(i < end ? i : end - 1);
-        const int64_t at = cache_tile(p, s, head, 4 * u + wave);
+        const int64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + wave));
         UnitCodes<D>::words(p.v_codes + at * (8 * D) + v_at, vw);
         vs = *reinterpret_cast<const uint32_t*>(p.v_scales + at * D + vs_at);
     };
     auto decode_k = [&](int buf) {
 #pragma unroll
-        for (int w = 0; w < D / 32; w++) {
-            const GroupScale sc = k_scale(tables, (ks >> (8 * (w / 2))) & 0xFFu);
-            *reinterpret_cast<half8*>(k_to + buf * kTile + (w >> 1) * 1024 + (w & 1) * 512) =
-                decode_k_word(kw[w], sc);
+        for (int w = 0; w < D / 32; w += 2) {
+            half8 a[2];
+            decode_k_group(kw[w], kw[w + 1], k_scale(tables, (ks >> (4 * w)) & 0xFFu), four, a[0],
+                           a[1]);
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                *reinterpret_cast<half8*>(k_to + buf * kTile + (w >> 1) * 1024 + j * 512) = a[j];
         }
     };
     auto decode_v = [&](int buf) {
-        uint32_t out[M][2];
-        decode_v_piece<D>(vw, vs, tables, out);
-#pragma unroll
-        for (int d = 0; d < M; d++)
+        VPiece<D> v;
+        v.unpack(vw, vs, tables, four);
+        each<M>([&](auto dim) {
+            constexpr int d = decltype(dim)::value;
             *reinterpret_cast<uint2*>(v_to + buf * kTile + (d >> 1) * 1024 + (d & 1) * 256) =
-                make_uint2(out[d][0], out[d][1]);
+                make_uint2(v.template pair<d, 0>(), v.template pair<d, 1>());
+        });
         const uint64_t bad = __builtin_amdgcn_ballot_w64(nan_bytes(vs) != 0);
         if (lane == 0) flags[buf * kWaves + wave] = bad != 0;
     };
@@ -713,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
     auto poison = [&](int u) {
 #pragma unroll 1
         for (int j = 0; j < 4 * T; j++) {  // 16-token tile j / T, group j % T
-            const int64_t at = cache_tile(p, s, head, 4 * u + j / T);
+            const int64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + j / T));
             const uint8_t* src = p.v_scales + at * D + (j % T) * 16;
 #pragma unroll 1
             for (int t = 0; t < 16; t++) {
@@ -805,36 +885,80 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
     }
 }
 
-// Joins the splits of every row: one wave per row, lane l the dims l D/64 ..
+// Joins the splits of one row per workgroup.  All waves read every split's m
+// and l at once, lane = split mod 64; then D/4 lanes read one split's
+// O as 16 bytes each, the workgroup 1024 / D splits side by side, so that the
+// whole row is a handful of independent loads.  (One wave per row with a loop
+// over the splits took 19 us for 33 splits, nearly all of it waiting.)
+constexpr int kMaxSplits = 128;
+constexpr int64_t kMaxKeys = (int64_t)1 << 30;  // of a length hint
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
-    const int64_t at = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (at >= p.rows_all) return;
-    constexpr int E = D / 64;
-    float top = kLowest;
-    for (int i = 0; i < p.splits; i++)
-        top = __builtin_fmaxf(top, p.part_ml[2 * (i * p.rows_all + at)]);
-    float sum = 0.0f, acc[E];
+    constexpr int kLanes = D / 4, kSide = kThreads / kLanes, kRounds = kMaxSplits / kSide;
+    __shared__ float weights[kMaxSplits];
+    __shared__ __attribute__((aligned(16))) float sums[kThreads * 4];
+    const int64_t at = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, side = tid / kLanes, d = tid % kLanes;
+    constexpr int kPer = kMaxSplits / 64;
+    f32x2 ml[kPer];
 #pragma unroll
-    for (int d = 0; d < E; d++) acc[d] = 0.0f;
-    for (int i = 0; i < p.splits; i++) {
-        const int64_t a = i * p.rows_all + at;
-        const float f = __builtin_amdgcn_exp2f(p.part_ml[2 * a] - top);
-        sum = __builtin_fmaf(f, p.part_ml[2 * a + 1], sum);
-#pragma unroll
-        for (int d = 0; d < E; d++)
-            acc[d] = __builtin_fmaf(f, p.part_o[a * D + lane * E + d], acc[d]);
+    for (int j = 0; j < kPer; j++) {
+        const int i = lane + 64 * j;
+        ml[j] = *reinterpret_cast<const f32x2*>(
+            p.part_ml + 2 * ((i < p.splits ? i : 0) * p.rows_all + at));
     }
-    const float f = sum == 0.0f ? 0.0f : p.v_mul / sum;
-    const int64_t row = at / p.heads, hd = at - row * p.heads;
-    uint16_t* dst = p.out + row * p.o_st + hd * p.o_sh + lane * E;
-    if constexpr (E == 1) {
-        dst[0] = (uint16_t)pack_bf16(acc[0] * f, 0.0f);
-    } else {
+    f32x4 part[kRounds];
 #pragma unroll
-        for (int d = 0; d < E; d += 2)
-            *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(acc[d] * f, acc[d + 1] * f);
+    for (int i = 0; i < kRounds; i++) {
+        const int split = i * kSide + side;
+        if (i * kSide < p.splits)
+            part[i] = *reinterpret_cast<const f32x4*>(
+                p.part_o + ((split < p.splits ? split : 0) * p.rows_all + at) * D + 4 * d);
+    }
+    uint64_t used[kPer];
+    float top = ml[0][0], sum = 0.0f;
+#pragma unroll
+    for (int j = 1; j < kPer; j++) top = __builtin_fmaxf(top, ml[j][0]);
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, i));
+#pragma unroll
+    for (int j = 0; j < kPer; j++) {
+        // zero also for splits without keys, whose O is not there
+        const bool in = lane + 64 * j < p.splits && ml[j][1] != 0.0f;
+        const float w = in ? __builtin_amdgcn_exp2f(ml[j][0] - top) : 0.0f;
+        sum += in ? w * ml[j][1] : 0.0f;
+        used[j] = __builtin_amdgcn_ballot_w64(in);
+        if (tid < 64) weights[lane + 64 * j] = w;
+    }
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) sum += __shfl_xor(sum, i);
+    __syncthreads();
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kRounds; i++) {
+        if (i * kSide < p.splits) {
+            const int split = i * kSide + side;
+            const float f = weights[split];
+            const bool in = used[i * kSide / 64] >> (split & 63) & 1;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                acc[j] = in ? __builtin_fmaf(f, part[i][j], acc[j]) : acc[j];
+        }
+    }
+    *reinterpret_cast<f32x4*>(sums + 4 * tid) = acc;
+    __syncthreads();
+    if (tid < kLanes) {
+#pragma unroll
+        for (int i = 1; i < kSide; i++) {
+            const f32x4 o = *reinterpret_cast<const f32x4*>(sums + 4 * (i * kLanes + tid));
+#pragma unroll
+            for (int j = 0; j < 4; j++) acc[j] += o[j];
+        }
+        const float f = sum == 0.0f ? 0.0f : p.v_mul / sum;
+        const int64_t row = at / p.heads, hd = at - row * p.heads;
+        *reinterpret_cast<uint2*>(p.out + row * p.o_st + hd * p.o_sh + 4 * tid) =
+            make_uint2(pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f));
     }
 }
 
@@ -844,7 +968,7 @@ struct Plan {
     bool many;
     int blocks;  // row blocks of a tile (few rows) or of a wave (many rows)
     int row_tiles;
-    int splits;
+    int splits, split_units;
     int64_t ws_o, ws_ml;  // bytes
 };
 
@@ -866,12 +990,19 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     // unit of keys for each of its waves.
     int64_t keys = a.max_len;
     if (a.window && a.window + a.sinks + a.max_q < keys) keys = a.window + a.sinks + a.max_q;
+    keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t base = a.batch * c.kv_heads * pl.row_tiles;
-    const int64_t unit = pl.many ? 256 : kUnit * kWaves;
-    const int64_t most = (keys + unit - 1) / unit;
-    int64_t s = base > 0 ? (pl.many ? 512 : 1024) / base : 1;
+    const int64_t unit = pl.many ? 64 : kUnit, least = pl.many ? 256 : kUnit * kWaves;
+    const int64_t most = (keys + least - 1) / least;
+    int64_t s = base > 0 ? (pl.many ? 512 : 3072) / base : 1;
     s = s > most ? most : s;
-    pl.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+    const int64_t units = (keys + unit - 1) / unit;
+    pl.split_units = (int)((units + s - 1) / s);
+    // whole rounds of the waves, and no split that the hint leaves empty
+    if (!pl.many && s > 1) pl.split_units = (pl.split_units + kWaves - 1) / kWaves * kWaves;
+    if (s > 1) s = (units + pl.split_units - 1) / pl.split_units;
+    pl.splits = (int)s;
     const int64_t rows_all = a.total_q * a.heads;
     pl.ws_o = pl.splits > 1 ? pl.splits * rows_all * c.head_dim * 4 : 0;
     pl.ws_ml = pl.splits > 1 ? pl.splits * rows_all * 8 : 0;
@@ -890,9 +1021,8 @@ hipError_t launch(void (*kernel)(Args), int lds, const Args& p, hipStream_t stre
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t joins = (p.rows_all + kWaves - 1) / kWaves;
-    if (joins > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)joins), dim3(kThreads), 0, stream, p);
+    if (p.rows_all > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)p.rows_all), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -945,6 +1075,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.batch_heads = (int)(a.batch * c.kv_heads);
     p.row_tiles = pl.row_tiles;
     p.splits = pl.splits;
+    p.split_units = pl.split_units;
     p.causal = a.causal != 0;
     p.window = clamp_int(a.window);
     p.sinks = clamp_int(a.sinks);

@@ -65,12 +65,21 @@ __device__ __forceinline__ GroupScale v_scale(const uint2* tables, uint32_t byte
 
 constexpr uint32_t kLoNibbles = 0x0F0F0F0Fu;
 
-// fp16 high bytes of the even (he) and odd (ho) elements of 8 nibbles.
-__device__ __forceinline__ void high_bytes(uint32_t w, uint32_t shifted, uint32_t masked,
-                                           uint32_t& he, uint32_t& ho) {
-    const uint32_t sign = w ^ masked;  // bits 3 and 7 of each byte
-    he = bit_select(shifted, sign << 4, kLoNibbles);
-    ho = bit_select(shifted >> 4, sign, kLoNibbles);
+// fp16 high bytes of the even (he) and odd (ho) elements of two words of 8
+// nibbles, whose magnitudes `shifted` already holds at their places.  The
+// shifts by 4 are 64-bit ones, single instructions on gfx950: what they carry
+// from word to word lands in masked-off bits.  `four` is 4, kept opaque
+// (a constant amount is split into 32-bit shifts).
+__device__ __forceinline__ void high_bytes(const uint32_t (&w)[2], const uint32_t (&masked)[2],
+                                           uint64_t shifted, uint32_t four, uint32_t (&he)[2],
+                                           uint32_t (&ho)[2]) {
+    const uint32_t g0 = w[0] ^ masked[0], g1 = w[1] ^ masked[1];  // bits 3 and 7 of each byte
+    const uint64_t low = shifted >> four;
+    const uint64_t up = ((uint64_t)g1 << 32 | g0) << four;
+    he[0] = bit_select((uint32_t)shifted, (uint32_t)up, kLoNibbles);
+    he[1] = bit_select((uint32_t)(shifted >> 32), (uint32_t)(up >> 32), kLoNibbles);
+    ho[0] = bit_select((uint32_t)low, g0, kLoNibbles);
+    ho[1] = bit_select((uint32_t)(low >> 32), g1, kLoNibbles);
 }
 
 // byte i of lo and byte j of hi as the high bytes of a pair of fp16 numbers
@@ -79,67 +88,84 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t hi, uint32_t lo) {
     return __builtin_amdgcn_perm(hi, lo, 0x040C000Cu + ((uint32_t)j << 24) + ((uint32_t)i << 8));
 }
 
-// K: 8 consecutive elements of one group as one operand.
-__device__ __forceinline__ half8 decode_k_word(uint32_t w, GroupScale s) {
-    const uint32_t m = w & 0x77777777u;
-    uint32_t he, ho;
-    high_bytes(w, m << (s.sh2 & 31u), m, he, ho);
-    uint4 r;
-    r.x = pk_mul(pair_of<0, 0>(ho, he), s.sig2);
-    r.y = pk_mul(pair_of<1, 1>(ho, he), s.sig2);
-    r.z = pk_mul(pair_of<2, 2>(ho, he), s.sig2);
-    r.w = pk_mul(pair_of<3, 3>(ho, he), s.sig2);
-    return __builtin_bit_cast(half8, r);
+// K: one group (two words) as two operands of 8 consecutive elements.
+__device__ __forceinline__ void decode_k_group(uint32_t w0, uint32_t w1, GroupScale s,
+                                               uint32_t four, half8& a, half8& b) {
+    const uint32_t w[2] = {w0, w1}, m[2] = {w0 & 0x77777777u, w1 & 0x77777777u};
+    uint32_t he[2], ho[2];
+    high_bytes(w, m, ((uint64_t)m[1] << 32 | m[0]) << (s.sh2 & 63u), four, he, ho);
+    uint4 r[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        r[i].x = pk_mul(pair_of<0, 0>(ho[i], he[i]), s.sig2);
+        r[i].y = pk_mul(pair_of<1, 1>(ho[i], he[i]), s.sig2);
+        r[i].z = pk_mul(pair_of<2, 2>(ho[i], he[i]), s.sig2);
+        r[i].w = pk_mul(pair_of<3, 3>(ho[i], he[i]), s.sig2);
+    }
+    a = __builtin_bit_cast(half8, r[0]);
+    b = __builtin_bit_cast(half8, r[1]);
 }
 
-// V: one piece (D/16 dims) of four consecutive tokens, words as they lie in
-// the cache and the tokens' four scale bytes in one word.  out[d][0] holds dim
-// d of tokens 0 and 1, out[d][1] of tokens 2 and 3: pairs of tokens come out
-// of the same v_perm that K spends on pairs of dims, so V needs no transposition.
+// V: one piece (D/16 dims) of four consecutive tokens.  Split in two, so that
+// the codes' registers are free for the next loads before the operands exist:
+// first the fp16 high bytes and the multipliers of token pairs, then any
+// dim's operand half.  A pair of tokens comes out of the same v_perm that K
+// spends on a pair of dims, so V needs no transposition.
 template <int D>
-__device__ __forceinline__ void decode_v_piece(const uint32_t (&w)[D / 32], uint32_t scales,
-                                               const uint2* tables, uint32_t (&out)[D / 16][2]) {
-    GroupScale s[4];
+struct VPiece {
+    static constexpr int kWords = D / 32;   // even and odd bytes, one word each
+    uint32_t he[kWords], ho[kWords];
+    uint32_t sig[2];                        // tokens 0 and 1, tokens 2 and 3
+
+    // w: words as they lie in the cache; scales: the tokens' four scale bytes
+    __device__ __forceinline__ void unpack(const uint32_t (&w)[D / 32], uint32_t scales,
+                                           const uint2* tables, uint32_t four) {
+        GroupScale s[4];
 #pragma unroll
-    for (int t = 0; t < 4; t++) s[t] = v_scale(tables, (scales >> (8 * t)) & 0xFFu);
+        for (int t = 0; t < 4; t++) s[t] = v_scale(tables, (scales >> (8 * t)) & 0xFFu);
 #pragma unroll
-    for (int p = 0; p < 2; p++) {  // tokens 2p, 2p + 1
-        const uint32_t sig = bit_select(s[2 * p].sig2, s[2 * p + 1].sig2, 0xFFFFu);
-        if constexpr (D == 64) {
-            // both tokens' 4 nibbles share a word
-            typedef uint16_t us2 __attribute__((ext_vector_type(2)));
-            const uint32_t sh = bit_select(s[2 * p].sh2, s[2 * p + 1].sh2, 0xFFFFu);
-            const uint32_t m = w[p] & 0x77777777u;
-            const uint32_t ms = __builtin_bit_cast(
-                uint32_t, (us2)(__builtin_bit_cast(us2, m) << __builtin_bit_cast(us2, sh)));
-            uint32_t he, ho;
-            high_bytes(w[p], ms, m, he, ho);
-            out[0][p] = pk_mul(__builtin_amdgcn_perm(he, he, 0x020C000Cu), sig);
-            out[1][p] = pk_mul(__builtin_amdgcn_perm(ho, ho, 0x020C000Cu), sig);
-            out[2][p] = pk_mul(__builtin_amdgcn_perm(he, he, 0x030C010Cu), sig);
-            out[3][p] = pk_mul(__builtin_amdgcn_perm(ho, ho, 0x030C010Cu), sig);
-        } else {
-            constexpr int W = D / 128;  // words per token
+        for (int p = 0; p < 2; p++) sig[p] = bit_select(s[2 * p].sig2, s[2 * p + 1].sig2, 0xFFFFu);
 #pragma unroll
-            for (int k = 0; k < W; k++) {
-                uint32_t he[2], ho[2];
+        for (int i = 0; i < kWords / 2; i++) {
+            const uint32_t x[2] = {w[2 * i], w[2 * i + 1]};
+            const uint32_t m[2] = {x[0] & 0x77777777u, x[1] & 0x77777777u};
+            uint32_t sh[2];
+            if constexpr (D == 64) {
+                // a word holds two tokens' 4 nibbles: 16-bit shifts
+                typedef uint16_t us2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    const uint32_t x = w[(2 * p + t) * W + k], m = x & 0x77777777u;
-                    high_bytes(x, m << (s[2 * p + t].sh2 & 31u), m, he[t], ho[t]);
+                for (int j = 0; j < 2; j++) {
+                    const uint32_t by = bit_select(s[2 * j].sh2, s[2 * j + 1].sh2, 0xFFFFu);
+                    sh[j] = __builtin_bit_cast(uint32_t, (us2)(__builtin_bit_cast(us2, m[j])
+                                                               << __builtin_bit_cast(us2, by)));
                 }
-                out[8 * k + 0][p] = pk_mul(pair_of<0, 0>(he[1], he[0]), sig);
-                out[8 * k + 1][p] = pk_mul(pair_of<0, 0>(ho[1], ho[0]), sig);
-                out[8 * k + 2][p] = pk_mul(pair_of<1, 1>(he[1], he[0]), sig);
-                out[8 * k + 3][p] = pk_mul(pair_of<1, 1>(ho[1], ho[0]), sig);
-                out[8 * k + 4][p] = pk_mul(pair_of<2, 2>(he[1], he[0]), sig);
-                out[8 * k + 5][p] = pk_mul(pair_of<2, 2>(ho[1], ho[0]), sig);
-                out[8 * k + 6][p] = pk_mul(pair_of<3, 3>(he[1], he[0]), sig);
-                out[8 * k + 7][p] = pk_mul(pair_of<3, 3>(ho[1], ho[0]), sig);
+            } else {
+                constexpr int per = D / 128;  // words per token
+                sh[0] = m[0] << (s[2 * i / per].sh2 & 31u);
+                sh[1] = m[1] << (s[(2 * i + 1) / per].sh2 & 31u);
             }
+            uint32_t e[2], o[2];
+            high_bytes(x, m, (uint64_t)sh[1] << 32 | sh[0], four, e, o);
+            he[2 * i] = e[0];
+            he[2 * i + 1] = e[1];
+            ho[2 * i] = o[0];
+            ho[2 * i + 1] = o[1];
         }
     }
-}
+    // dim d of tokens 2p and 2p + 1
+    template <int d, int p>
+    __device__ __forceinline__ uint32_t pair() const {
+        const uint32_t* const src = d & 1 ? ho : he;
+        if constexpr (D == 64) {
+            constexpr int b = d / 2;
+            return pk_mul(__builtin_amdgcn_perm(src[p], src[p], 0x020C000Cu + b * 0x01000100u),
+                          sig[p]);
+        } else {
+            constexpr int per = D / 128, k = d / 8, b = d % 8 / 2;
+            return pk_mul(pair_of<b, b>(src[(2 * p + 1) * per + k], src[2 * p * per + k]), sig[p]);
+        }
+    }
+};
 
 // Whether any of four scale bytes is NaN.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t scales) {
