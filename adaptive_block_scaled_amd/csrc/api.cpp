@@ -57,6 +57,8 @@ int check_cache(const if4_kv_cache& c) {
     if (c.page_size <= 0 || c.page_size % 16 != 0 || c.page_size > kMaxIndex) return IF4_ERR_SHAPE;
     if (c.pages < 0 || c.pages > kMaxIndex) return IF4_ERR_SHAPE;
     if (c.kv_heads <= 0 || c.kv_heads > kMaxKvHeads) return IF4_ERR_SHAPE;
+    // tiles of 16 tokens and one kv head: their index is 31 bits in the kernels
+    if (c.pages > 0 && c.page_size / 16 * c.kv_heads > 0x7FFFFFFF / c.pages) return IF4_ERR_SHAPE;
     if (c.k_exp < -kMaxExp || c.k_exp > kMaxExp || c.v_exp < -kMaxExp || c.v_exp > kMaxExp)
         return IF4_ERR_RANGE;
     return IF4_OK;

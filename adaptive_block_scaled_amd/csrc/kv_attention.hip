@@ -31,11 +31,16 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
+// (lambdas that hold a kernel's state have to be inlined, whatever their size)
+#define KV_INLINE __attribute__((always_inline))
+
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kUnit = 32;             // keys that a wave takes at once
 constexpr float kLowest = -3.0e38f;   // running maximum before any key
 constexpr float kSlack = 8.0f;        // how far scores may exceed it
+constexpr int kMaxLen = 0x3FFFFF00;   // keys of a sequence
+constexpr int kHidden = 0x3FFFFF80;   // first key of a step that no row sees
 
 struct Args {
     const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
@@ -70,7 +75,8 @@ __device__ __forceinline__ Sequence sequence_of(const Args& p, int b) {
     q1 = q1 < q0 ? q0 : q1 > p.total_q ? p.total_q : q1;
     s.first_row = q0;
     s.rows = q1 - q0;
-    const int64_t room = p.table_stride * p.page_tiles * 16;
+    int64_t room = p.table_stride * p.page_tiles * 16;
+    room = room < kMaxLen ? room : kMaxLen;
     const int64_t len = p.seq_lens[b];
     s.len = (int)(len < 0 ? 0 : len > room ? room : len);
     s.pos0 = s.len - s.rows;
@@ -116,13 +122,28 @@ __device__ __forceinline__ int units_per_split(const Args& p, int n) {
 __device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int head, int row0,
                                            int last_row) {
     const int split = blockIdx.x / (p.batch_heads * p.row_tiles);
-    for (int r = row0 + threadIdx.x; r <= last_row; r += kThreads) {
+    for (int r = row0 + threadIdx.x; r <= last_row; r += blockDim.x) {
         const int t = r / p.group, g = r - t * p.group;
         const int64_t at = split * p.rows_all + (int64_t)(s.first_row + t) * p.heads +
                            head * p.group + g;
         *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, 0.0f};
     }
 }
+
+// First keys of the steps of `step` keys that every row of a tile sees whole:
+// at most `hi`, and at least `lo` or at most `sink`.
+struct WholeSteps {
+    int lo, hi, sink;
+    __device__ __forceinline__ WholeSteps(const Args& p, int len, int pos_lo, int pos_hi, int step) {
+        const int n = p.causal && pos_lo + 1 < len ? pos_lo + 1 : len;
+        hi = n - step;
+        lo = p.window ? pos_hi - p.window + 1 : -1;
+        sink = p.sinks - step;
+    }
+    __device__ __forceinline__ bool operator()(int key0) const {
+        return (key0 <= hi) & ((key0 >= lo) | (key0 <= sink));
+    }
+};
 
 // Cache tile (16 tokens) of one kv head that holds keys 16 n .. 16 n + 15 of
 // a sequence; n past its last key gives some valid tile.  Made in two steps,
@@ -131,15 +152,25 @@ struct TileRef {
     int page;
     uint32_t rest;  // tile in the page
 };
-__device__ __forceinline__ TileRef tile_ref(const Args& p, const Sequence& s, int n) {
+// (page: its place in the sequence's row of the table)
+__device__ __forceinline__ TileRef tile_ref_of(const Args& p, const Sequence& s, int n) {
     const int last = s.len > 0 ? (s.len - 1) >> 4 : 0;
     const uint32_t m = (uint32_t)(n < last ? n : last);
     const uint32_t i = (uint32_t)((uint64_t)m * p.page_magic >> p.page_shift);
-    return {s.table[i], m - i * p.page_tiles};
+    return {(int)i, m - i * p.page_tiles};
 }
-__device__ __forceinline__ int64_t cache_tile(const Args& p, int head, TileRef r) {
-    const int page = r.page < 0 ? 0 : r.page >= p.pages ? p.pages - 1 : r.page;
-    return ((int64_t)page * p.kv_heads + head) * p.page_tiles + r.rest;
+__device__ __forceinline__ TileRef tile_ref(const Args& p, const Sequence& s, int n) {
+    const TileRef r = tile_ref_of(p, s, n);
+    // (constant address space: a scalar load, whatever stores are around)
+    typedef const __attribute__((address_space(4))) int32_t* Table;
+    return {((Table)(uintptr_t)s.table)[r.page], r.rest};
+}
+// (all tiles of a cache, pages x kv heads x tiles of a page, fit 31 bits)
+__device__ __forceinline__ uint32_t cache_tile(const Args& p, int head, TileRef r) {
+    const int last = p.pages - 1;
+    int page = r.page < last ? r.page : last;
+    page = page > 0 ? page : 0;
+    return (uint32_t)(page * p.kv_heads + head) * p.page_tiles + r.rest;
 }
 
 // 4, as a value that the compiler cannot fold (see high_bytes).
@@ -185,6 +216,19 @@ __device__ __forceinline__ float q_value(float x, int e) {
     return __builtin_fabsf(x) <= 3.40282347e38f ? __builtin_ldexpf(x, -e)
                                                 : __uint_as_float(0x7FC00000u);
 }
+
+// Token, row of q and query head of tile row r (the last row's past the end).
+struct RowPlace {
+    int token;
+    int64_t row, head;
+    __device__ __forceinline__ RowPlace(const Args& p, const Sequence& s, int kv_head, int r,
+                                        int rows) {
+        const int rc = r < rows ? r : rows - 1;
+        token = rc / p.group;
+        row = s.first_row + token;
+        head = kv_head * p.group + (rc - token * p.group);
+    }
+};
 
 // Largest magnitude of 8 bf16 values, and their operand.
 __device__ __forceinline__ float largest(const uint4& v) {
@@ -238,13 +282,13 @@ struct UnitCodes {
             }
         }
     }
-    __device__ __forceinline__ void load_k(const Args& p, const int64_t (&at)[2], int lane) {
+    __device__ __forceinline__ void load_k(const Args& p, const uint32_t (&at)[2], int lane) {
         const uint32_t code = (lane & 15) * (D / 2) + (lane >> 4) * (D / 8);
         const uint32_t scale = (lane & 15) * (D / 16) + (lane >> 4) * (D / 64);
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            words(p.k_codes + at[t] * (8 * D) + code, k[t]);
-            const uint8_t* src = p.k_scales + at[t] * D + scale;
+            words(p.k_codes + (uint64_t)at[t] * (8 * D) + code, k[t]);
+            const uint8_t* src = p.k_scales + (uint64_t)at[t] * D + scale;
             if constexpr (D == 64)
                 ks[t] = *src;
             else if constexpr (D == 128)
@@ -253,13 +297,13 @@ struct UnitCodes {
                 ks[t] = *reinterpret_cast<const uint32_t*>(src);
         }
     }
-    __device__ __forceinline__ void load_v(const Args& p, const int64_t (&at)[2], int lane) {
+    __device__ __forceinline__ void load_v(const Args& p, const uint32_t (&at)[2], int lane) {
         const uint32_t code = (lane & 15) * (D / 2) + (lane >> 4) * (D / 8);
         const uint32_t scale = (lane & 15) * D / 256 * 16 + (lane >> 4) * 4;
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            words(p.v_codes + at[t] * (8 * D) + code, v[t]);
-            vs[t] = *reinterpret_cast<const uint32_t*>(p.v_scales + at[t] * D + scale);
+            words(p.v_codes + (uint64_t)at[t] * (8 * D) + code, v[t]);
+            vs[t] = *reinterpret_cast<const uint32_t*>(p.v_scales + (uint64_t)at[t] * D + scale);
         }
     }
 };
@@ -354,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) f
     UnitCodes<D> c;
     // one unit; `next`: the cache tiles whose codes are asked for as soon as
     // this unit's are decoded
-    auto compute = [&](int unit, const int64_t (&next)[2]) {
+    auto compute = [&](int unit, const uint32_t (&next)[2]) {
         const int key0 = unit * kUnit;
         f32x4 acc[2][kBlocks];
 #pragma unroll
@@ -363,9 +407,10 @@ __global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) f
             for (int nr = 0; nr < kBlocks; nr++) acc[t][nr] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < D / 32; i += 2) {
-                half8 a[2];
-                decode_k_group(c.k[t][i], c.k[t][i + 1],
-                               k_scale(tables, (c.ks[t] >> (4 * i)) & 0xFFu), four, a[0], a[1]);
+                KGroup group;
+                group.unpack(c.k[t][i], c.k[t][i + 1],
+                             k_scale(tables, (c.ks[t] >> (4 * i)) & 0xFFu), four);
+                const half8 a[2] = {group.operand<0>(), group.operand<1>()};
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
@@ -419,7 +464,11 @@ __global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) f
         }
         VPiece<D> v[2];
 #pragma unroll
-        for (int t = 0; t < 2; t++) v[t].unpack(c.v[t], c.vs[t], tables, four);
+        for (int t = 0; t < 2; t++) {
+            GroupScale sc[4];
+            VPiece<D>::look_up(tables, c.vs[t], sc);
+            v[t].unpack(c.v[t], sc, four);
+        }
         const uint32_t vs[2] = {c.vs[0], c.vs[1]};
         c.load_v(p, next, lane);
         each<M>([&](auto dim) {
@@ -466,12 +515,12 @@ __global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) f
             r[0] = tile_ref(p, s, 2 * u);
             r[1] = tile_ref(p, s, 2 * u + 1);
         };
-        const auto tiles = [&](const TileRef (&r)[2], int64_t (&at)[2]) {
+        const auto tiles = [&](const TileRef (&r)[2], uint32_t (&at)[2]) {
             at[0] = cache_tile(p, head, r[0]);
             at[1] = cache_tile(p, head, r[1]);
         };
         TileRef r[2];
-        int64_t at[2];
+        uint32_t at[2];
         refs(i, r);
         tiles(r, at);
         c.load_k(p, at, lane);
@@ -582,7 +631,7 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 template <int D, int kBlocks>
-__global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) many_rows_kernel(const Args p) {
     constexpr int kRows = 128 * kBlocks, T = D / 16, B = D / 32, M = D / 16;
     constexpr int kTile = ManyRows<D>::kTile;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -618,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
     half8 q[kBlocks][T];
     float factor[kBlocks], m[kBlocks], l[kBlocks];
     int see_hi[kBlocks], see_lo[kBlocks];
+    uint32_t poisoned[kBlocks];  // groups of O that are NaN
     f32x16 o[B][kBlocks], x[2][kBlocks];
 #pragma unroll
     for (int nr = 0; nr < kBlocks; nr++) {
@@ -643,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
         see_lo[nr] = p.window ? pos - p.window : -1;
         m[nr] = kLowest;
         l[nr] = 0.0f;
+        poisoned[nr] = 0;
 #pragma unroll
         for (int d = 0; d < B; d++)
 #pragma unroll
@@ -663,9 +714,21 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
         v_lds + wave * B * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8;
 
     uint32_t kw[D / 32], vw[D / 32], ks, vs;
-    auto load_k = [&](int i) {
-        const int u = units(i < end ? i : end - 1);
-        const int64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + wave));
+    // Page table entries of 64 tiles at a time, a lane each: the next ones are
+    // there long before their use, and reading one is a v_readlane (scalar loads
+    // would share, and drain, the counter of the LDS reads in flight).
+    int pages_now, pages_next;
+    auto load_pages = [&](int i) {
+        i += lane;
+        return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + wave).page;
+    };
+    auto tile_at = [&](int i) {
+        const int j = i < end ? i : end - 1;
+        TileRef r = tile_ref_of(p, s, 4 * units(j) + wave);
+        r.page = __builtin_amdgcn_readlane(pages_now, (j - begin) & 63);
+        return cache_tile(p, head, r);
+    };
+    auto load_k = [&](uint64_t at) {
         UnitCodes<D>::words(p.k_codes + at * (8 * D) + k_at, kw);
         const uint8_t* src = p.k_scales + at * D + ks_at;
         if constexpr (D == 64)
@@ -675,18 +738,16 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
         else
             ks = *reinterpret_cast<const uint32_t*>(src);
     };
-    auto load_v = [&](int i) {
-        const int u = units(i < end ? i : end - 1);
-        const int64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + wave));
+    auto load_v = [&](uint64_t at) {
         UnitCodes<D>::words(p.v_codes + at * (8 * D) + v_at, vw);
         vs = *reinterpret_cast<const uint32_t*>(p.v_scales + at * D + vs_at);
     };
     auto decode_k = [&](int buf) {
 #pragma unroll
         for (int w = 0; w < D / 32; w += 2) {
-            half8 a[2];
-            decode_k_group(kw[w], kw[w + 1], k_scale(tables, (ks >> (4 * w)) & 0xFFu), four, a[0],
-                           a[1]);
+            KGroup group;
+            group.unpack(kw[w], kw[w + 1], k_scale(tables, (ks >> (4 * w)) & 0xFFu), four);
+            const half8 a[2] = {group.operand<0>(), group.operand<1>()};
 #pragma unroll
             for (int j = 0; j < 2; j++)
                 *reinterpret_cast<half8*>(k_to + buf * kTile + (w >> 1) * 1024 + j * 512) = a[j];
@@ -694,7 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
     };
     auto decode_v = [&](int buf) {
         VPiece<D> v;
-        v.unpack(vw, vs, tables, four);
+        GroupScale sc[4];
+        VPiece<D>::look_up(tables, vs, sc);
+        v.unpack(vw, sc, four);
         each<M>([&](auto dim) {
             constexpr int d = decltype(dim)::value;
             *reinterpret_cast<uint2*>(v_to + buf * kTile + (d >> 1) * 1024 + (d & 1) * 256) =
@@ -718,10 +781,26 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
                 to[nr] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[nr][t], to[nr], 0, 0, 0);
         }
     };
-    // hides what a row does not see, and raises m where it has to
+    // Scores above m by more than the slack, or keys that some row does not
+    // see: then keys are hidden and m is raised.  Everything but the first
+    // look at the scores is behind one branch, which few steps take.
+    float top[kBlocks];
+    auto largest_scores = [&](const f32x16 (&sc)[kBlocks]) {
+#pragma unroll
+        for (int nr = 0; nr < kBlocks; nr++) {
+            top[nr] = sc[nr][0];
+#pragma unroll
+            for (int i = 1; i < 16; i++) top[nr] = __builtin_fmaxf(top[nr], sc[nr][i]);
+            top[nr] *= factor[nr];
+        }
+    };
     auto settle = [&](f32x16 (&sc)[kBlocks], int key0) {
         const bool all = key0 + 32 <= s.len && (!p.causal || key0 + 31 <= pos_lo) &&
                          (!p.window || key0 > pos_hi - p.window || key0 + 32 <= p.sinks);
+        bool raise = !all;
+#pragma unroll
+        for (int nr = 0; nr < kBlocks; nr++) raise |= top[nr] > m[nr] + kSlack;
+        if (__builtin_amdgcn_ballot_w64(raise) == 0) return;
         if (!all) {
 #pragma unroll
             for (int nr = 0; nr < kBlocks; nr++)
@@ -731,30 +810,20 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
                     const bool seen = key <= see_hi[nr] && (key > see_lo[nr] || key < p.sinks);
                     sc[nr][i] = seen ? sc[nr][i] : -__builtin_inff();
                 }
+            largest_scores(sc);
         }
-        float top[kBlocks];
-        bool raise = false;
 #pragma unroll
         for (int nr = 0; nr < kBlocks; nr++) {
-            top[nr] = sc[nr][0];
+            float t = __builtin_fmaxf(top[nr], m[nr]);
+            t = __builtin_fmaxf(t, __shfl_xor(t, 32));
+            t = t > m[nr] + kSlack ? t : m[nr];
+            const float alpha = __builtin_amdgcn_exp2f(m[nr] - t);
+            m[nr] = t;
+            l[nr] *= alpha;
 #pragma unroll
-            for (int i = 1; i < 16; i++) top[nr] = __builtin_fmaxf(top[nr], sc[nr][i]);
-            top[nr] *= factor[nr];
-            raise |= top[nr] > m[nr] + kSlack;
-        }
-        if (__builtin_amdgcn_ballot_w64(raise) != 0) {
+            for (int d = 0; d < B; d++)
 #pragma unroll
-            for (int nr = 0; nr < kBlocks; nr++) {
-                float t = __builtin_fmaxf(top[nr], m[nr]);
-                t = __builtin_fmaxf(t, __shfl_xor(t, 32));
-                const float alpha = __builtin_amdgcn_exp2f(m[nr] - t);
-                m[nr] = t;
-                l[nr] *= alpha;
-#pragma unroll
-                for (int d = 0; d < B; d++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) o[d][nr][i] *= alpha;
-            }
+                for (int i = 0; i < 16; i++) o[d][nr][i] *= alpha;
         }
     };
     uint4 prob[kBlocks][2];
@@ -788,28 +857,21 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
                         a, __builtin_bit_cast(half8, prob[nr][i]), o[d][nr], 0, 0, 0);
             }
     };
-    // NaN values of V (decoded as zeros) of a 64-key tile: into the rows that
-    // see them
+    // NaN values of V (decoded as zeros) of a 64-key tile: the groups that turn
+    // NaN in the rows that see them
     auto poison = [&](int u) {
 #pragma unroll 1
         for (int j = 0; j < 4 * T; j++) {  // 16-token tile j / T, group j % T
-            const int64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + j / T));
+            const uint64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + j / T));
             const uint8_t* src = p.v_scales + at * D + (j % T) * 16;
 #pragma unroll 1
             for (int t = 0; t < 16; t++) {
-                if ((src[t] & 0x7F) != 0x7F) continue;
                 const int key = 64 * u + 16 * (j / T) + t;
+                const bool bad = (src[t] & 0x7F) == 0x7F;
 #pragma unroll
                 for (int nr = 0; nr < kBlocks; nr++) {
                     const bool seen = key <= see_hi[nr] && (key > see_lo[nr] || key < p.sinks);
-#pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
-                        const bool hit = seen && piece * M / 16 == j % T;
-#pragma unroll
-                        for (int d = 0; d < B; d++)
-                            o[d][nr][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][nr][i];
-                    }
+                    poisoned[nr] |= (uint32_t)(bad && seen) << (j % T);
                 }
             }
         }
@@ -817,34 +879,46 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
 
     __syncthreads();
     if (begin < end) {
-        load_k(begin);
-        load_v(begin);
+        pages_now = load_pages(begin);
+        uint32_t at = tile_at(begin);
+        load_k(at);
+        load_v(at);
         decode_k(0);
-        load_k(begin + 1);
+        at = tile_at(begin + 1);
+        load_k(at);
         decode_v(0);
-        load_v(begin + 1);
+        load_v(at);
+        pages_next = load_pages(begin + 64);
         lds_barrier();
         scores(x[0], 0, 0);
+        largest_scores(x[0]);
         settle(x[0], 64 * units(begin));
 #pragma unroll 1
         for (int i = begin; i < end; i++) {
             const int buf = (i - begin) & 1, u = units(i);
+            if (((i + 2 - begin) & 63) == 0) {
+                pages_now = pages_next;
+                pages_next = load_pages(i + 66);
+            }
+            at = tile_at(i + 2);
             // keys 0 .. 31 of the tile
             scores(x[1], buf, 1);
             probabilities(x[0]);
             accumulate(buf, 0);
             decode_k(buf ^ 1);
-            load_k(i + 2);
+            load_k(at);
+            largest_scores(x[1]);
             settle(x[1], 64 * u + 32);
             lds_barrier();
             // keys 32 .. 63
+            const uint4 f = *reinterpret_cast<const uint4*>(flags + buf * kWaves);
             scores(x[0], buf ^ 1, 0);
             probabilities(x[1]);
             accumulate(buf, 1);
-            const uint4 f = *reinterpret_cast<const uint4*>(flags + buf * kWaves);
-            if (__builtin_amdgcn_readfirstlane((f.x | f.y) | (f.z | f.w)) != 0) poison(u);
             decode_v(buf ^ 1);
-            load_v(i + 2);
+            load_v(at);
+            largest_scores(x[0]);
+            if (__builtin_amdgcn_readfirstlane((f.x | f.y) | (f.z | f.w)) != 0) poison(u);
             if (i + 1 < end) settle(x[0], 64 * units(i + 1));
             lds_barrier();
         }
@@ -855,6 +929,14 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
         l[nr] += __shfl_xor(l[nr], 32);
         const int r = row0 + 32 * (kBlocks * wave + nr) + (lane & 31);
         if (r >= rows) continue;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
+            const bool hit = poisoned[nr] >> (piece * M / 16) & 1;
+#pragma unroll
+            for (int d = 0; d < B; d++)
+                o[d][nr][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][nr][i];
+        }
         const int t = r / p.group, g = r - t * p.group;
         const int64_t row = s.first_row + t, hd = head * p.group + g;
         if (p.splits == 1) {
@@ -883,6 +965,395 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const Args p) {
             }
         }
     }
+}
+
+// ---------------------------------------------------------------------------
+// Prompts (more than 128 rows, D <= 128): tiles of 256 rows, 8 waves of 32.
+//
+// Two waves share a SIMD, wave w and w + 4, and take turns: while one issues
+// the products of a step (A: scores of step k + 1, O of step k, 512 cycles of
+// matrix core), the other does the VALU work of its step (B: probabilities of
+// step k + 1, its share of the decode, 500-600 cycles), with a barrier between
+// the phases.  Waves 4-7 run one phase behind, and the matrix cores and the
+// VALU are both busy all the time.  With c = 64-key tile, phases of waves 0-3:
+// A(2c) = 4c, B(2c) = 4c + 1, ..; of waves 4-7 one later.
+//   * waves 4-7 decode K of tile c + 2 in their two B of tile c (phases 4c + 2
+//     and 4c + 4): K of tile c, in the same buffer, was last read in B(2c - 1),
+//     phase 4c; K of tile c + 2 is first read in B(2c + 2), phase 4c + 5.
+//   * waves 0-3 decode V of tile c + 1 in theirs (4c + 1 and 4c + 3): V of tile
+//     c - 1, in the same buffer, was last read in A(2c - 1) of waves 4-7, phase
+//     4c - 1; V of tile c + 1 is first read in A(2c + 2), phase 4c + 4.
+// Operands and their order are those of many_rows_kernel.
+constexpr int kPairWaves = 8, kPairThreads = 64 * kPairWaves;
+
+//
+// Both halves of a workgroup run this, each in code of its own from beginning to
+// end (kLate: waves 4-7): with shared ends around two loops the register
+// allocator spilled 21 registers; apart they need 218 of 256.
+template <int D, bool kLate>
+__device__ __forceinline__ void prompt_rows(const Args& p) {
+    constexpr int kRows = 256, T = D / 16, B = D / 32, M = D / 16;
+    constexpr int kTile = ManyRows<D>::kTile;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    uint2* const tables = reinterpret_cast<uint2*>(smem);
+    uint8_t* const k_lds = smem + kScaleTableBytes;
+    uint8_t* const v_lds = k_lds + 2 * kTile;
+    uint32_t* const flags = reinterpret_cast<uint32_t*>(smem + ManyRows<D>::kFlags);
+
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int unit16 = wave & 3;  // which 16 keys of a tile it decodes
+    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
+    const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
+    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+
+    const Sequence s = sequence_of(p, b);
+    const int row0 = row_tile * kRows, rows = s.rows * p.group;
+    if (row0 >= rows) return;
+    const uint32_t four = opaque_four(p);
+    const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
+    const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
+    const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, 64);
+    const WholeSteps whole(p, s.len, pos_lo, pos_hi, 32);
+    const int per = units_per_split(p, units.n);
+    const int begin = split * per;
+    const int end = begin + per < units.n ? begin + per : units.n;
+    if (p.splits > 1 && begin >= end) {
+        mark_empty(p, s, head, row0, last_row);
+        return;
+    }
+    fill_scale_tables(tables, tid, kPairThreads);
+
+    half8 q[T];
+    float factor, m = kLowest, l = 0.0f;
+    int pos;
+    {
+        const RowPlace at(p, s, head, row0 + 32 * wave + (lane & 31), rows);
+        pos = s.pos0 + at.token;
+        const uint16_t* src = p.q + at.row * p.q_st + at.head * p.q_sh + half * 8;
+        uint4 raw[T];
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < T; i++) {
+            raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
+            a = __builtin_fmaxf(a, largest(raw[i]));
+        }
+        a = __builtin_fmaxf(a, __shfl_xor(a, 32));
+        const int e = row_exponent(a);
+#pragma unroll
+        for (int i = 0; i < T; i++) q[i] = q_operand(raw[i], e);
+        factor = score_factor(p, e);
+    }
+    auto sees = [&](int key) KV_INLINE {
+        return (key <= pos || !p.causal) & (key < s.len) &
+               (!p.window || key > pos - p.window || key < p.sinks);
+    };
+    uint32_t poisoned = 0;  // groups of O that are NaN
+    f32x16 o[B], x;
+#pragma unroll
+    for (int d = 0; d < B; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
+
+    // this lane's codes of the 16 keys that its wave decodes
+    const int kq = lane >> 4, vq = (kq & 1) * 2 + (kq >> 1);
+    const uint32_t code_at = (lane & 15) * (D / 2) + (kLate ? kq : vq) * (D / 8);
+    const uint32_t scale_at = kLate ? (lane & 15) * (D / 16) + kq * (D / 64)
+                                   : (lane & 15) * D / 256 * 16 + vq * 4;
+    const uint8_t* const codes = kLate ? p.k_codes : p.v_codes;
+    const uint8_t* const scales = kLate ? p.k_scales : p.v_scales;
+    uint8_t* const k_to = k_lds + ((unit16 >> 1) * T + kq * (D / 64)) * 1024 +
+                          (16 * (unit16 & 1) + (lane & 15)) * 16;
+    uint8_t* const v_to =
+        v_lds + unit16 * B * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8;
+
+    uint32_t w[D / 32], sc;
+    bool bad = false;  // a NaN among the scales of w (V)
+    auto load = [&](uint64_t at) KV_INLINE {
+        UnitCodes<D>::words(codes + at * (8 * D) + code_at, w);
+        const uint8_t* src = scales + at * D + scale_at;
+        if constexpr (!kLate)
+            sc = *reinterpret_cast<const uint32_t*>(src);
+        else if constexpr (D == 64)
+            sc = *src;
+        else
+            sc = *reinterpret_cast<const uint16_t*>(src);
+    };
+    auto ref = [&](int i) KV_INLINE { return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + unit16); };
+    // The scales of the codes in w, looked up one phase before their decode.
+    GroupScale look[4];
+    auto look_up = [&]() KV_INLINE {
+        if constexpr (kLate) {
+#pragma unroll
+            for (int i = 0; i < D / 64; i++) look[i] = k_scale(tables, (sc >> (8 * i)) & 0xFFu);
+        } else {
+            VPiece<D>::look_up(tables, sc, look);
+            bad = __builtin_amdgcn_ballot_w64(nan_bytes(sc) != 0) != 0;
+        }
+    };
+    // Decode of w (one 16-token tile), in 2 T slices that go between the products
+    // of an A phase: the bits first, then operand by operand.
+    KGroup kg[D / 64];
+    VPiece<D> vp;
+    auto decode = [&](int buf, auto slice_c) KV_INLINE {
+        constexpr int n = decltype(slice_c)::value;
+        if constexpr (n < T) {
+            if constexpr (n % 2 == 1 && n / 2 < D / 64) {
+                if constexpr (kLate)
+                    kg[n / 2].unpack(w[n - 1], w[n], look[n / 2], four);
+                else
+                    vp.template unpack_words<n / 2>(w, look, four);
+            }
+            if constexpr (!kLate && n == 0)
+                flags[buf * kWaves + unit16] = bad;  // (every lane the same)
+        } else if constexpr (!kLate) {
+            constexpr int d = n - T;
+            *reinterpret_cast<uint2*>(v_to + buf * kTile + (d >> 1) * 1024 + (d & 1) * 256) =
+                make_uint2(vp.template pair<d, 0>(), vp.template pair<d, 1>());
+        } else if constexpr (n % 2 == 0) {
+            constexpr int i = (n - T) / 2;  // operand of 8 elements
+            *reinterpret_cast<half8*>(k_to + buf * kTile + (i / 2) * 1024 + (i % 2) * 512) =
+                kg[i / 2].template operand<i % 2>();
+        }
+    };
+    half8 ka[T];
+    auto read_k = [&](int buf, int kb) KV_INLINE {
+        const uint8_t* src = k_lds + buf * kTile + kb * T * 1024 + lane * 16;
+#pragma unroll
+        for (int t = 0; t < T; t++) ka[t] = *reinterpret_cast<const half8*>(src + t * 1024);
+    };
+    uint4 prob[2];
+    // Largest score of this lane, in parts that go between products.
+    float part[6], top;
+    auto largest_part = [&](auto part_c) KV_INLINE {
+        constexpr int j = decltype(part_c)::value;
+        if constexpr (j < 3) {
+#pragma unroll
+            for (int i = 2 * j; i < 2 * j + 2 && i < 5; i++)
+                part[i] = __builtin_fmaxf(__builtin_fmaxf(x[3 * i], x[3 * i + 1]), x[3 * i + 2]);
+        } else if constexpr (j == 3) {
+            part[5] = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), x[15]);
+            part[2] = __builtin_fmaxf(__builtin_fmaxf(part[2], part[3]), part[4]);
+        } else {
+            top = __builtin_fmaxf(part[2], part[5]) * factor;
+        }
+    };
+    // The products of an A phase: scores of the step whose K is in ka, then V's
+    // operands of keys 32 kb .. of a tile times the probabilities.  V's operands
+    // are asked for one beside each product of the first half, the next step's K
+    // (tile buffer k_buf, half k_half) beside those of the second; the largest
+    // score is taken once the scores are there; f(slice) is the work that goes
+    // behind each product.
+    auto products = [&](int buf, int kb, int k_buf, int k_half, auto&& f) KV_INLINE {
+        const uint8_t* src = v_lds + buf * kTile + 2 * kb * B * 1024 + lane * 16;
+        const uint8_t* k_src = k_lds + k_buf * kTile + k_half * T * 1024 + lane * 16;
+        half8 va[T];
+        each<T>([&](auto t_c) KV_INLINE {
+            constexpr int t = decltype(t_c)::value;
+            if constexpr (t == 0) {
+                f32x16 zero;
+#pragma unroll
+                for (int i = 0; i < 16; i++) zero[i] = 0.0f;
+                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[0], q[0], zero, 0, 0, 0);
+            } else {
+                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[t], q[t], x, 0, 0, 0);
+            }
+            va[t] = *reinterpret_cast<const half8*>(src + t * 1024);
+            f(t_c);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        each<T>([&](auto n_c) KV_INLINE {
+            constexpr int n = decltype(n_c)::value;
+            o[n % B] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                va[n], __builtin_bit_cast(half8, prob[n / B]), o[n % B], 0, 0, 0);
+            ka[n] = *reinterpret_cast<const half8*>(k_src + n * 1024);
+            f(std::integral_constant<int, T + n>{});
+            if constexpr (T == 8 && n >= 3) {
+                largest_part(std::integral_constant<int, n - 3>{});
+            } else if constexpr (T == 4 && n == 2) {
+                each<3>(largest_part);
+            } else if constexpr (T == 4 && n == 3) {
+                largest_part(std::integral_constant<int, 3>{});
+                largest_part(std::integral_constant<int, 4>{});
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    auto scores = [&]() KV_INLINE {
+#pragma unroll
+        for (int i = 0; i < 16; i++) x[i] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; t++)
+            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[t], q[t], x, 0, 0, 0);
+    };
+    // NaN values of V (decoded as zeros) of a 64-key tile: the groups that turn
+    // NaN in the rows that see them
+    auto poison = [&](int u) KV_INLINE {
+#pragma unroll 1
+        for (int j = 0; j < 4 * T; j++) {  // 16-token tile j / T, group j % T
+            const uint64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + j / T));
+            const uint8_t* src = p.v_scales + at * D + (j % T) * 16;
+#pragma unroll 1
+            for (int t = 0; t < 16; t++) {
+                const int key = 64 * u + 16 * (j / T) + t;
+                poisoned |= (uint32_t)((src[t] & 0x7F) == 0x7F && sees(key)) << (j % T);
+            }
+        }
+    };
+
+    // What few steps need, behind one branch: keys that some row does not see
+    // are hidden, m is raised where a score exceeds it by more than the slack,
+    // and NaN values of V are noted.
+    auto settle = [&](int key0, uint32_t nan_tile, int u) KV_INLINE {
+        const bool all = whole(key0);
+        if (all & (__builtin_amdgcn_ballot_w64((top > m + kSlack) | (nan_tile != 0)) == 0)) return;
+        if (nan_tile != 0) poison(u);
+        if (!all) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                const int key = key0 + 8 * (i >> 2) + 4 * half + (i & 3);
+                x[i] = sees(key) ? x[i] : -__builtin_inff();
+            }
+            each<5>(largest_part);
+        }
+        if (__builtin_amdgcn_ballot_w64(top > m + kSlack) == 0) return;
+        const float raised = __builtin_fmaxf(top, m);
+        const float both = __builtin_fmaxf(raised, __shfl_xor(raised, 32));
+        const float alpha = __builtin_amdgcn_exp2f(m - both);
+        m = both;
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < B; d++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) o[d][i] *= alpha;
+    };
+    auto probabilities = [&]() KV_INLINE {
+        float e[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], factor, -m));
+        uint32_t h[8];
+        float sum[2] = {l, 0.0f};  // two short chains
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            h[i] = pack_half(e[2 * i], e[2 * i + 1]);
+            // l sums what the second product sees, the fp16 probabilities
+            sum[i & 1] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, h[i]),
+                                                __builtin_bit_cast(half2v, 0x3C003C00u),
+                                                sum[i & 1], false);
+        }
+        l = sum[0] + sum[1];
+        prob[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        prob[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    };
+
+    __syncthreads();
+    if (begin < end) {
+        // K of tiles 0 and 1, V of tile 0, probabilities of step 0
+        load(cache_tile(p, head, ref(begin)));
+        const auto decode_tile = [&](int buf) KV_INLINE {
+            look_up();
+            each<2 * T>([&](auto n) KV_INLINE { decode(buf, n); });
+        };
+        decode_tile(0);
+        load(cache_tile(p, head, ref(begin + 1)));
+        if constexpr (kLate) {
+            decode_tile(1);
+            load(cache_tile(p, head, ref(begin + 2)));
+        }
+        const int ahead = kLate ? 3 : 2;  // the tile whose codes are loaded next
+        TileRef next = ref(begin + ahead);
+        lds_barrier();
+        read_k(0, 0);
+        scores();
+        each<5>(largest_part);
+        settle(64 * units(begin), 0, 0);
+        probabilities();
+        read_k(0, 1);
+        look_up();
+        if constexpr (kLate) lds_barrier();
+#pragma unroll 1
+        for (int i = begin; i < end; i++) {
+            const int buf = (i - begin) & 1, u = units(i);
+            const uint32_t at = cache_tile(p, head, next);
+            next = ref(i + 1 + ahead);
+            // A(2c), B(2c)
+            uint4 f;
+            uint32_t nan_tile;
+            __builtin_amdgcn_s_setprio(1);
+            products(buf, 0, buf ^ 1, 0, [&](auto n) KV_INLINE {
+                if constexpr (decltype(n)::value == 0)
+                    f = *reinterpret_cast<const uint4*>(flags + buf * kWaves);
+                if constexpr (decltype(n)::value == 2) nan_tile = (f.x | f.y) | (f.z | f.w);
+                decode(kLate ? buf : buf ^ 1, n);
+                if constexpr (decltype(n)::value == T) load(at);
+            });
+            __builtin_amdgcn_s_setprio(0);
+            lds_barrier();
+            settle(64 * u + 32, nan_tile, u);
+            probabilities();
+            lds_barrier();
+            // A(2c + 1), B(2c + 1)
+            __builtin_amdgcn_s_setprio(1);
+            products(buf, 1, buf ^ 1, 1, [](auto) {});
+            __builtin_amdgcn_s_setprio(0);
+            lds_barrier();
+            settle(i + 1 < end ? 64 * units(i + 1) : kHidden, 0, 0);
+            probabilities();
+            look_up();
+            lds_barrier();
+        }
+        if constexpr (!kLate) lds_barrier();
+    }
+
+    l += __shfl_xor(l, 32);
+    // the row's place again, from a lane number that the compiler takes for
+    // another one: kept across the loop it would cost registers
+    int lane_again = lane;
+    asm volatile("" : "+v"(lane_again));
+    const int r = row0 + 32 * wave + (lane_again & 31);
+    if (r >= rows) return;
+    const RowPlace place(p, s, head, r, rows);
+    const int64_t row = place.row, hd = place.head;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
+        const bool hit = poisoned >> (piece * M / 16) & 1;
+#pragma unroll
+        for (int d = 0; d < B; d++) o[d][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][i];
+    }
+    if (p.splits == 1) {
+        const float f = l == 0.0f ? 0.0f : p.v_mul / l;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
+            uint32_t* dst =
+                reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh + piece * M);
+#pragma unroll
+            for (int d = 0; d < B; d++) dst[d] = pack_bf16(o[d][i] * f, o[d][i + 8] * f);
+        }
+    } else {
+        const int64_t at = split * p.rows_all + row * p.heads + hd;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
+            f32x2* dst = reinterpret_cast<f32x2*>(p.part_o + at * D + piece * M);
+#pragma unroll
+            for (int d = 0; d < B; d++) dst[d] = f32x2{o[d][i], o[d][i + 8]};
+        }
+        if (half == 0) {
+            p.part_ml[2 * at] = m;
+            p.part_ml[2 * at + 1] = l;
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPairThreads, 2) prompt_kernel(const Args p) {
+    if (threadIdx.x >= kPairThreads / 2)
+        prompt_rows<D, true>(p);
+    else
+        prompt_rows<D, false>(p);
 }
 
 // Joins the splits of one row per workgroup.  All waves read every split's m
@@ -965,8 +1436,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
 // ---------------------------------------------------------------------------
 // Host side: which kernel, how many splits.
 struct Plan {
-    bool many;
-    int blocks;  // row blocks of a tile (few rows) or of a wave (many rows)
+    enum Kind { kFew, kMany, kPrompt } kind;
+    int blocks;  // row blocks of 16 of a tile (few rows)
     int row_tiles;
     int splits, split_units;
     int64_t ws_o, ws_ml;  // bytes
@@ -975,15 +1446,13 @@ struct Plan {
 Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     Plan pl;
     const int64_t group = a.heads / c.kv_heads, rows = a.max_q * group;
-    pl.many = rows > 32;
-    int tile;
-    if (pl.many) {
-        pl.blocks = c.head_dim == 256 || rows <= 128 ? 1 : 2;
-        tile = 128 * pl.blocks;
-    } else {
-        pl.blocks = rows <= 16 || c.head_dim == 256 ? 1 : 2;
-        tile = 16 * pl.blocks;
-    }
+    pl.kind = rows <= 32 ? Plan::kFew
+              : c.head_dim <= 128 && rows > 128 ? Plan::kPrompt
+                                         : Plan::kMany;
+    pl.blocks = rows <= 16 || c.head_dim == 256 ? 1 : 2;
+    const int tile = pl.kind == Plan::kFew    ? 16 * pl.blocks
+                     : pl.kind == Plan::kMany ? 128
+                                              : 256;
     pl.row_tiles = (int)((rows + tile - 1) / tile);
     // Splits of the keys: enough workgroups to fill 256 CUs a few times over
     // (twice where a workgroup fills a CU's registers), each with at least one
@@ -992,15 +1461,16 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     if (a.window && a.window + a.sinks + a.max_q < keys) keys = a.window + a.sinks + a.max_q;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t base = a.batch * c.kv_heads * pl.row_tiles;
-    const int64_t unit = pl.many ? 64 : kUnit, least = pl.many ? 256 : kUnit * kWaves;
+    const bool few = pl.kind == Plan::kFew;
+    const int64_t unit = few ? kUnit : 64, least = few ? kUnit * kWaves : 256;
     const int64_t most = (keys + least - 1) / least;
-    int64_t s = base > 0 ? (pl.many ? 512 : 3072) / base : 1;
+    int64_t s = base > 0 ? (few ? 3072 : 512) / base : 1;
     s = s > most ? most : s;
     s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
     const int64_t units = (keys + unit - 1) / unit;
     pl.split_units = (int)((units + s - 1) / s);
     // whole rounds of the waves, and no split that the hint leaves empty
-    if (!pl.many && s > 1) pl.split_units = (pl.split_units + kWaves - 1) / kWaves * kWaves;
+    if (few && s > 1) pl.split_units = (pl.split_units + kWaves - 1) / kWaves * kWaves;
     if (s > 1) s = (units + pl.split_units - 1) / pl.split_units;
     pl.splits = (int)s;
     const int64_t rows_all = a.total_q * a.heads;
@@ -1010,7 +1480,7 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
 }
 
 template <int D>
-hipError_t launch(void (*kernel)(Args), int lds, const Args& p, hipStream_t stream) {
+hipError_t launch(void (*kernel)(Args), int threads, int lds, const Args& p, hipStream_t stream) {
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kernel,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -1018,7 +1488,7 @@ hipError_t launch(void (*kernel)(Args), int lds, const Args& p, hipStream_t stre
     }
     const int64_t grid = (int64_t)p.batch_heads * p.row_tiles * p.splits;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), lds, stream, p);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     if (p.rows_all > 0x7FFFFFFF) return hipErrorInvalidValue;
@@ -1028,13 +1498,15 @@ hipError_t launch(void (*kernel)(Args), int lds, const Args& p, hipStream_t stre
 
 template <int D>
 hipError_t dispatch(const Args& p, const Plan& pl, hipStream_t stream) {
-    if constexpr (D < 256) {
-        if (pl.blocks == 2)
-            return pl.many ? launch<D>(many_rows_kernel<D, 2>, ManyRows<D>::kLds, p, stream)
-                           : launch<D>(few_rows_kernel<D, 2>, FewRows<D, 2>::kLds, p, stream);
+    if constexpr (D <= 128) {
+        if (pl.kind == Plan::kPrompt)
+            return launch<D>(prompt_kernel<D>, kPairThreads, ManyRows<D>::kLds, p, stream);
+        if (pl.kind == Plan::kFew && pl.blocks == 2)
+            return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, p, stream);
     }
-    return pl.many ? launch<D>(many_rows_kernel<D, 1>, ManyRows<D>::kLds, p, stream)
-                   : launch<D>(few_rows_kernel<D, 1>, FewRows<D, 1>::kLds, p, stream);
+    if (pl.kind == Plan::kFew)
+        return launch<D>(few_rows_kernel<D, 1>, kThreads, FewRows<D, 1>::kLds, p, stream);
+    return launch<D>(many_rows_kernel<D, 1>, kThreads, ManyRows<D>::kLds, p, stream);
 }
 
 int clamp_int(int64_t v) { return (int)(v > 0x3FFFFFFF ? 0x3FFFFFFF : v); }

@@ -88,23 +88,23 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t hi, uint32_t lo) {
     return __builtin_amdgcn_perm(hi, lo, 0x040C000Cu + ((uint32_t)j << 24) + ((uint32_t)i << 8));
 }
 
-// K: one group (two words) as two operands of 8 consecutive elements.
-__device__ __forceinline__ void decode_k_group(uint32_t w0, uint32_t w1, GroupScale s,
-                                               uint32_t four, half8& a, half8& b) {
-    const uint32_t w[2] = {w0, w1}, m[2] = {w0 & 0x77777777u, w1 & 0x77777777u};
-    uint32_t he[2], ho[2];
-    high_bytes(w, m, ((uint64_t)m[1] << 32 | m[0]) << (s.sh2 & 63u), four, he, ho);
-    uint4 r[2];
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        r[i].x = pk_mul(pair_of<0, 0>(ho[i], he[i]), s.sig2);
-        r[i].y = pk_mul(pair_of<1, 1>(ho[i], he[i]), s.sig2);
-        r[i].z = pk_mul(pair_of<2, 2>(ho[i], he[i]), s.sig2);
-        r[i].w = pk_mul(pair_of<3, 3>(ho[i], he[i]), s.sig2);
+// K: one group (two words), unpacked to fp16 high bytes first, then either half
+// as an operand of 8 consecutive elements.
+struct KGroup {
+    uint32_t he[2], ho[2], sig;
+    __device__ __forceinline__ void unpack(uint32_t w0, uint32_t w1, GroupScale s, uint32_t four) {
+        const uint32_t w[2] = {w0, w1}, m[2] = {w0 & 0x77777777u, w1 & 0x77777777u};
+        high_bytes(w, m, ((uint64_t)m[1] << 32 | m[0]) << (s.sh2 & 63u), four, he, ho);
+        sig = s.sig2;
     }
-    a = __builtin_bit_cast(half8, r[0]);
-    b = __builtin_bit_cast(half8, r[1]);
-}
+    template <int i>
+    __device__ __forceinline__ half8 operand() const {
+        return __builtin_bit_cast(half8, make_uint4(pk_mul(pair_of<0, 0>(ho[i], he[i]), sig),
+                                                    pk_mul(pair_of<1, 1>(ho[i], he[i]), sig),
+                                                    pk_mul(pair_of<2, 2>(ho[i], he[i]), sig),
+                                                    pk_mul(pair_of<3, 3>(ho[i], he[i]), sig)));
+    }
+};
 
 // V: one piece (D/16 dims) of four consecutive tokens.  Split in two, so that
 // the codes' registers are free for the next loads before the operands exist:
@@ -117,16 +117,35 @@ struct VPiece {
     uint32_t he[kWords], ho[kWords];
     uint32_t sig[2];                        // tokens 0 and 1, tokens 2 and 3
 
-    // w: words as they lie in the cache; scales: the tokens' four scale bytes
-    __device__ __forceinline__ void unpack(const uint32_t (&w)[D / 32], uint32_t scales,
-                                           const uint2* tables, uint32_t four) {
-        GroupScale s[4];
+    // The four tokens' scales, from their four scale bytes.
+    __device__ static __forceinline__ void look_up(const uint2* tables, uint32_t scales,
+                                                   GroupScale (&s)[4]) {
 #pragma unroll
         for (int t = 0; t < 4; t++) s[t] = v_scale(tables, (scales >> (8 * t)) & 0xFFu);
+    }
+    // w: words as they lie in the cache
+    __device__ __forceinline__ void unpack(const uint32_t (&w)[D / 32], const GroupScale (&s)[4],
+                                           uint32_t four) {
+        each_word_pair<0>(w, s, four);
+    }
+    template <int i>
+    __device__ __forceinline__ void each_word_pair(const uint32_t (&w)[D / 32],
+                                                   const GroupScale (&s)[4], uint32_t four) {
+        if constexpr (i < kWords / 2) {
+            unpack_words<i>(w, s, four);
+            each_word_pair<i + 1>(w, s, four);
+        }
+    }
+    // words 2i and 2i + 1; the multipliers with the first
+    template <int i>
+    __device__ __forceinline__ void unpack_words(const uint32_t (&w)[D / 32],
+                                                 const GroupScale (&s)[4], uint32_t four) {
+        if constexpr (i == 0) {
 #pragma unroll
-        for (int p = 0; p < 2; p++) sig[p] = bit_select(s[2 * p].sig2, s[2 * p + 1].sig2, 0xFFFFu);
-#pragma unroll
-        for (int i = 0; i < kWords / 2; i++) {
+            for (int p = 0; p < 2; p++)
+                sig[p] = bit_select(s[2 * p].sig2, s[2 * p + 1].sig2, 0xFFFFu);
+        }
+        {
             const uint32_t x[2] = {w[2 * i], w[2 * i + 1]};
             const uint32_t m[2] = {x[0] & 0x77777777u, x[1] & 0x77777777u};
             uint32_t sh[2];
