@@ -23,6 +23,9 @@
 #include "kv_internal.h"
 #include "kv_operand.h"
 
+#ifndef MANYT
+#define MANYT 768
+#endif
 namespace if4 {
 namespace {
 
@@ -120,8 +123,7 @@ __device__ __forceinline__ int units_per_split(const Args& p, int n) {
 
 // A split without keys: its rows' sums are zero, which the join skips.
 __device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int head, int row0,
-                                           int last_row) {
-    const int split = blockIdx.x / (p.batch_heads * p.row_tiles);
+                                           int last_row, int split) {
     for (int r = row0 + threadIdx.x; r <= last_row; r += blockDim.x) {
         const int t = r / p.group, g = r - t * p.group;
         const int64_t at = split * p.rows_all + (int64_t)(s.first_row + t) * p.heads +
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) f
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
     if (p.splits > 1 && begin >= end) {
-        mark_empty(p, s, head, row0, last_row);
+        mark_empty(p, s, head, row0, last_row, split);
         return;
     }
     fill_scale_tables(tables, tid, kThreads);
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
     if (p.splits > 1 && begin >= end) {
-        mark_empty(p, s, head, row0, last_row);
+        mark_empty(p, s, head, row0, last_row, split);
         return;
     }
     fill_scale_tables(tables, tid, kThreads);
@@ -714,20 +716,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
         v_lds + wave * B * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8;
 
     uint32_t kw[D / 32], vw[D / 32], ks, vs;
-    // Page table entries of 64 tiles at a time, a lane each: the next ones are
-    // there long before their use, and reading one is a v_readlane (scalar loads
-    // would share, and drain, the counter of the LDS reads in flight).
-    int pages_now, pages_next;
-    auto load_pages = [&](int i) {
-        i += lane;
-        return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + wave).page;
-    };
-    auto tile_at = [&](int i) {
-        const int j = i < end ? i : end - 1;
-        TileRef r = tile_ref_of(p, s, 4 * units(j) + wave);
-        r.page = __builtin_amdgcn_readlane(pages_now, (j - begin) & 63);
-        return cache_tile(p, head, r);
-    };
+    auto ref = [&](int i) { return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + wave); };
     auto load_k = [&](uint64_t at) {
         UnitCodes<D>::words(p.k_codes + at * (8 * D) + k_at, kw);
         const uint8_t* src = p.k_scales + at * D + ks_at;
@@ -781,27 +770,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
                 to[nr] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[nr][t], to[nr], 0, 0, 0);
         }
     };
-    // Scores above m by more than the slack, or keys that some row does not
-    // see: then keys are hidden and m is raised.  Everything but the first
-    // look at the scores is behind one branch, which few steps take.
-    float top[kBlocks];
-    auto largest_scores = [&](const f32x16 (&sc)[kBlocks]) {
-#pragma unroll
-        for (int nr = 0; nr < kBlocks; nr++) {
-            top[nr] = sc[nr][0];
-#pragma unroll
-            for (int i = 1; i < 16; i++) top[nr] = __builtin_fmaxf(top[nr], sc[nr][i]);
-            top[nr] *= factor[nr];
-        }
-    };
+    // hides what a row does not see, and raises m where it has to
+    const WholeSteps whole(p, s.len, pos_lo, pos_hi, 32);
     auto settle = [&](f32x16 (&sc)[kBlocks], int key0) {
-        const bool all = key0 + 32 <= s.len && (!p.causal || key0 + 31 <= pos_lo) &&
-                         (!p.window || key0 > pos_hi - p.window || key0 + 32 <= p.sinks);
-        bool raise = !all;
-#pragma unroll
-        for (int nr = 0; nr < kBlocks; nr++) raise |= top[nr] > m[nr] + kSlack;
-        if (__builtin_amdgcn_ballot_w64(raise) == 0) return;
-        if (!all) {
+        if (!whole(key0)) {
 #pragma unroll
             for (int nr = 0; nr < kBlocks; nr++)
 #pragma unroll
@@ -810,13 +782,22 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
                     const bool seen = key <= see_hi[nr] && (key > see_lo[nr] || key < p.sinks);
                     sc[nr][i] = seen ? sc[nr][i] : -__builtin_inff();
                 }
-            largest_scores(sc);
         }
+        float top[kBlocks];
+        bool raise = false;
+#pragma unroll
+        for (int nr = 0; nr < kBlocks; nr++) {
+            top[nr] = sc[nr][0];
+#pragma unroll
+            for (int i = 1; i < 16; i++) top[nr] = __builtin_fmaxf(top[nr], sc[nr][i]);
+            top[nr] *= factor[nr];
+            raise |= top[nr] > m[nr] + kSlack;
+        }
+        if (__builtin_amdgcn_ballot_w64(raise) == 0) return;
 #pragma unroll
         for (int nr = 0; nr < kBlocks; nr++) {
             float t = __builtin_fmaxf(top[nr], m[nr]);
             t = __builtin_fmaxf(t, __shfl_xor(t, 32));
-            t = t > m[nr] + kSlack ? t : m[nr];
             const float alpha = __builtin_amdgcn_exp2f(m[nr] - t);
             m[nr] = t;
             l[nr] *= alpha;
@@ -879,35 +860,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
 
     __syncthreads();
     if (begin < end) {
-        pages_now = load_pages(begin);
-        uint32_t at = tile_at(begin);
+        uint32_t at = cache_tile(p, head, ref(begin));
         load_k(at);
         load_v(at);
         decode_k(0);
-        at = tile_at(begin + 1);
+        at = cache_tile(p, head, ref(begin + 1));
         load_k(at);
         decode_v(0);
         load_v(at);
-        pages_next = load_pages(begin + 64);
+        TileRef next = ref(begin + 2);
         lds_barrier();
         scores(x[0], 0, 0);
-        largest_scores(x[0]);
         settle(x[0], 64 * units(begin));
 #pragma unroll 1
         for (int i = begin; i < end; i++) {
             const int buf = (i - begin) & 1, u = units(i);
-            if (((i + 2 - begin) & 63) == 0) {
-                pages_now = pages_next;
-                pages_next = load_pages(i + 66);
-            }
-            at = tile_at(i + 2);
+            at = cache_tile(p, head, next);
+            next = ref(i + 3);
             // keys 0 .. 31 of the tile
             scores(x[1], buf, 1);
             probabilities(x[0]);
             accumulate(buf, 0);
             decode_k(buf ^ 1);
             load_k(at);
-            largest_scores(x[1]);
             settle(x[1], 64 * u + 32);
             lds_barrier();
             // keys 32 .. 63
@@ -917,7 +892,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
             accumulate(buf, 1);
             decode_v(buf ^ 1);
             load_v(at);
-            largest_scores(x[0]);
             if (__builtin_amdgcn_readfirstlane((f.x | f.y) | (f.z | f.w)) != 0) poison(u);
             if (i + 1 < end) settle(x[0], 64 * units(i + 1));
             lds_barrier();
@@ -968,42 +942,57 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
 }
 
 // ---------------------------------------------------------------------------
-// Prompts (more than 128 rows, D <= 128): tiles of 256 rows, 8 waves of 32.
+// Prompts (more than 128 rows): tiles of 256 rows, 8 waves of 32.
 //
 // Two waves share a SIMD, wave w and w + 4, and take turns: while one issues
 // the products of a step (A: scores of step k + 1, O of step k, 512 cycles of
-// matrix core), the other does the VALU work of its step (B: probabilities of
-// step k + 1, its share of the decode, 500-600 cycles), with a barrier between
-// the phases.  Waves 4-7 run one phase behind, and the matrix cores and the
-// VALU are both busy all the time.  With c = 64-key tile, phases of waves 0-3:
+// matrix core at D = 128), the other does the VALU work of its step (B:
+// probabilities of step k + 1), with a barrier between the phases; waves 4-7 run
+// one phase behind.  Each wave decodes a quarter of a K or V tile in one of its
+// A phases, between the products.  With c = 64-key tile, phases of waves 0-3:
 // A(2c) = 4c, B(2c) = 4c + 1, ..; of waves 4-7 one later.
-//   * waves 4-7 decode K of tile c + 2 in their two B of tile c (phases 4c + 2
-//     and 4c + 4): K of tile c, in the same buffer, was last read in B(2c - 1),
-//     phase 4c; K of tile c + 2 is first read in B(2c + 2), phase 4c + 5.
-//   * waves 0-3 decode V of tile c + 1 in theirs (4c + 1 and 4c + 3): V of tile
-//     c - 1, in the same buffer, was last read in A(2c - 1) of waves 4-7, phase
-//     4c - 1; V of tile c + 1 is first read in A(2c + 2), phase 4c + 4.
+//   * waves 0-3 decode V of tile c + 1 in A(2c), phase 4c.  V of tile c - 1, in
+//     the same buffer, was last read in A(2c - 1) of waves 4-7, phase 4c - 1; V of
+//     tile c + 1 is first read in A(2c + 2), phase 4c + 4.
+//   * waves 4-7 decode K of tile c + 2 in A(2c + 1), phase 4c + 3.  K of tile c,
+//     in the same buffer, was last read (as step 2c + 1) in A(2c) of waves 4-7,
+//     phase 4c + 1; K of tile c + 2 is first read in A(2c + 2), phase 4c + 4.
 // Operands and their order are those of many_rows_kernel.
+//
+// At D = 256 one wave's registers do not hold Q, O and the operands in flight:
+// two workgroups take half of O's dims each (kHalves), the words of 8 dims of
+// every V piece that have their number, and both compute the scores.
 constexpr int kPairWaves = 8, kPairThreads = 64 * kPairWaves;
 
-//
+template <int D>
+struct PromptTile {
+    static constexpr int kV = D == 256 ? 128 : D;  // dims of O in one workgroup
+    static constexpr int kHalves = D / kV;
+    static constexpr int kKBytes = 64 * D * 2, kVBytes = 64 * kV * 2;
+    static constexpr int kFlags = kScaleTableBytes + 2 * (kKBytes + kVBytes);
+    static constexpr int kLds = kFlags + 2 * kWaves * 4;
+};
+
 // Both halves of a workgroup run this, each in code of its own from beginning to
 // end (kLate: waves 4-7): with shared ends around two loops the register
-// allocator spilled 21 registers; apart they need 218 of 256.
+// allocator spilled 21 registers at D = 128; apart they need 210 of 256.
 template <int D, bool kLate>
 __device__ __forceinline__ void prompt_rows(const Args& p) {
-    constexpr int kRows = 256, T = D / 16, B = D / 32, M = D / 16;
-    constexpr int kTile = ManyRows<D>::kTile;
+    typedef PromptTile<D> Tile;
+    // products of a step: T for the scores, P = 2 B for O; M dims of a V piece
+    constexpr int kRows = 256, T = D / 16, DV = Tile::kV, B = DV / 32, P = 2 * B, M = DV / 16;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint2* const tables = reinterpret_cast<uint2*>(smem);
     uint8_t* const k_lds = smem + kScaleTableBytes;
-    uint8_t* const v_lds = k_lds + 2 * kTile;
-    uint32_t* const flags = reinterpret_cast<uint32_t*>(smem + ManyRows<D>::kFlags);
+    uint8_t* const v_lds = k_lds + 2 * Tile::kKBytes;
+    uint32_t* const flags = reinterpret_cast<uint32_t*>(smem + Tile::kFlags);
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int unit16 = wave & 3;  // which 16 keys of a tile it decodes
-    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
+    const int bh = blockIdx.x % p.batch_heads;
+    const int part_of_o = blockIdx.x / p.batch_heads % Tile::kHalves;
+    const int rest = blockIdx.x / (p.batch_heads * Tile::kHalves);
     const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
@@ -1019,7 +1008,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
     if (p.splits > 1 && begin >= end) {
-        mark_empty(p, s, head, row0, last_row);
+        mark_empty(p, s, head, row0, last_row, split);
         return;
     }
     fill_scale_tables(tables, tid, kPairThreads);
@@ -1067,12 +1056,19 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     uint8_t* const v_to =
         v_lds + unit16 * B * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8;
 
-    uint32_t w[D / 32], sc;
+    uint32_t w[kLate ? D / 32 : DV / 32], sc;
     bool bad = false;  // a NaN among the scales of w (V)
     auto load = [&](uint64_t at) KV_INLINE {
-        UnitCodes<D>::words(codes + at * (8 * D) + code_at, w);
-        const uint8_t* src = scales + at * D + scale_at;
-        if constexpr (!kLate)
+        const uint8_t* src = codes + at * (8 * D) + code_at;
+        if constexpr (kLate || D == DV) {
+            UnitCodes<D>::words(src, w);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; t++)  // one of the two words of each token
+                w[t] = *reinterpret_cast<const uint32_t*>(src + 4 * part_of_o + 8 * t);
+        }
+        src = scales + at * D + scale_at;
+        if constexpr (!kLate || D == 256)
             sc = *reinterpret_cast<const uint32_t*>(src);
         else if constexpr (D == 64)
             sc = *src;
@@ -1087,40 +1083,37 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 #pragma unroll
             for (int i = 0; i < D / 64; i++) look[i] = k_scale(tables, (sc >> (8 * i)) & 0xFFu);
         } else {
-            VPiece<D>::look_up(tables, sc, look);
+            VPiece<DV>::look_up(tables, sc, look);
             bad = __builtin_amdgcn_ballot_w64(nan_bytes(sc) != 0) != 0;
         }
     };
-    // Decode of w (one 16-token tile), in 2 T slices that go between the products
-    // of an A phase: the bits first, then operand by operand.
+    // Decode of w (one 16-token tile), in T + P slices that go between the
+    // products of an A phase: the bits first, then operand by operand.
     KGroup kg[D / 64];
-    VPiece<D> vp;
+    VPiece<DV> vp;
     auto decode = [&](int buf, auto slice_c) KV_INLINE {
         constexpr int n = decltype(slice_c)::value;
         if constexpr (n < T) {
-            if constexpr (n % 2 == 1 && n / 2 < D / 64) {
-                if constexpr (kLate)
-                    kg[n / 2].unpack(w[n - 1], w[n], look[n / 2], four);
-                else
-                    vp.template unpack_words<n / 2>(w, look, four);
-            }
+            if constexpr (kLate && n % 2 == 1 && n / 2 < D / 64)
+                kg[n / 2].unpack(w[n - 1], w[n], look[n / 2], four);
+            if constexpr (!kLate && n % 2 == 1 && n / 2 < DV / 64)
+                vp.template unpack_words<n / 2>(w, look, four);
             if constexpr (!kLate && n == 0)
                 flags[buf * kWaves + unit16] = bad;  // (every lane the same)
         } else if constexpr (!kLate) {
             constexpr int d = n - T;
-            *reinterpret_cast<uint2*>(v_to + buf * kTile + (d >> 1) * 1024 + (d & 1) * 256) =
+            *reinterpret_cast<uint2*>(v_to + buf * Tile::kVBytes + (d >> 1) * 1024 + (d & 1) * 256) =
                 make_uint2(vp.template pair<d, 0>(), vp.template pair<d, 1>());
-        } else if constexpr (n % 2 == 0) {
-            constexpr int i = (n - T) / 2;  // operand of 8 elements
-            *reinterpret_cast<half8*>(k_to + buf * kTile + (i / 2) * 1024 + (i % 2) * 512) =
+        } else if constexpr ((n - T) % (P / (D / 32)) == 0) {
+            constexpr int i = (n - T) / (P / (D / 32));  // operand of 8 elements
+            *reinterpret_cast<half8*>(k_to + buf * Tile::kKBytes + (i / 2) * 1024 + (i % 2) * 512) =
                 kg[i / 2].template operand<i % 2>();
         }
     };
-    half8 ka[T];
-    auto read_k = [&](int buf, int kb) KV_INLINE {
-        const uint8_t* src = k_lds + buf * kTile + kb * T * 1024 + lane * 16;
-#pragma unroll
-        for (int t = 0; t < T; t++) ka[t] = *reinterpret_cast<const half8*>(src + t * 1024);
+    half8 ka[P];  // K's operands, P ahead
+    auto read_k = [&](int buf, int kb, int t) KV_INLINE {
+        return *reinterpret_cast<const half8*>(k_lds + buf * Tile::kKBytes + (kb * T + t) * 1024 +
+                                               lane * 16);
     };
     uint4 prob[2];
     // Largest score of this lane, in parts that go between products.
@@ -1138,16 +1131,15 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
             top = __builtin_fmaxf(part[2], part[5]) * factor;
         }
     };
-    // The products of an A phase: scores of the step whose K is in ka, then V's
-    // operands of keys 32 kb .. of a tile times the probabilities.  V's operands
-    // are asked for one beside each product of the first half, the next step's K
-    // (tile buffer k_buf, half k_half) beside those of the second; the largest
-    // score is taken once the scores are there; f(slice) is the work that goes
-    // behind each product.
+    // The products of an A phase: scores of the step whose first P operands of K
+    // are in ka (the others lie at `more`), then V's operands of keys 32 kb .. of a
+    // tile times the probabilities.  Beside each product one operand is asked for,
+    // P products ahead of its use: the rest of K, V, the first of the next
+    // step's K (tile buffer k_buf, half k_half).  The largest score is taken once
+    // the scores are there; f(slice) is the work that goes behind each product.
     auto products = [&](int buf, int kb, int k_buf, int k_half, auto&& f) KV_INLINE {
-        const uint8_t* src = v_lds + buf * kTile + 2 * kb * B * 1024 + lane * 16;
-        const uint8_t* k_src = k_lds + k_buf * kTile + k_half * T * 1024 + lane * 16;
-        half8 va[T];
+        const uint8_t* src = v_lds + buf * Tile::kVBytes + 2 * kb * B * 1024 + lane * 16;
+        half8 va[P];
         each<T>([&](auto t_c) KV_INLINE {
             constexpr int t = decltype(t_c)::value;
             if constexpr (t == 0) {
@@ -1156,41 +1148,37 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
                 for (int i = 0; i < 16; i++) zero[i] = 0.0f;
                 x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[0], q[0], zero, 0, 0, 0);
             } else {
-                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[t], q[t], x, 0, 0, 0);
+                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[t % P], q[t], x, 0, 0, 0);
             }
-            va[t] = *reinterpret_cast<const half8*>(src + t * 1024);
+            if constexpr (t < T - P)  // the same step's, the other half of this tile or the next's
+                ka[t] = read_k(kb == 0 ? buf : k_buf, 1 - kb, t + P);
+            else
+                va[t - (T - P)] = *reinterpret_cast<const half8*>(src + (t - (T - P)) * 1024);
             f(t_c);
             __builtin_amdgcn_sched_barrier(0);
         });
-        each<T>([&](auto n_c) KV_INLINE {
+        each<P>([&](auto n_c) KV_INLINE {
             constexpr int n = decltype(n_c)::value;
             o[n % B] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
                 va[n], __builtin_bit_cast(half8, prob[n / B]), o[n % B], 0, 0, 0);
-            ka[n] = *reinterpret_cast<const half8*>(k_src + n * 1024);
+            ka[n] = read_k(k_buf, k_half, n);
             f(std::integral_constant<int, T + n>{});
-            if constexpr (T == 8 && n >= 3) {
+            if constexpr (P == 8 && n >= 3) {
                 largest_part(std::integral_constant<int, n - 3>{});
-            } else if constexpr (T == 4 && n == 2) {
+            } else if constexpr (P == 4 && n == 2) {
                 each<3>(largest_part);
-            } else if constexpr (T == 4 && n == 3) {
+            } else if constexpr (P == 4 && n == 3) {
                 largest_part(std::integral_constant<int, 3>{});
                 largest_part(std::integral_constant<int, 4>{});
             }
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    auto scores = [&]() KV_INLINE {
-#pragma unroll
-        for (int i = 0; i < 16; i++) x[i] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < T; t++)
-            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[t], q[t], x, 0, 0, 0);
-    };
     // NaN values of V (decoded as zeros) of a 64-key tile: the groups that turn
     // NaN in the rows that see them
     auto poison = [&](int u) KV_INLINE {
 #pragma unroll 1
-        for (int j = 0; j < 4 * T; j++) {  // 16-token tile j / T, group j % T
+        for (int j = 0; j < 4 * T; j++) {  // 16-token tile j / T, group j % T (T = D / 16)
             const uint64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + j / T));
             const uint8_t* src = p.v_scales + at * D + (j % T) * 16;
 #pragma unroll 1
@@ -1250,27 +1238,31 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     __syncthreads();
     if (begin < end) {
         // K of tiles 0 and 1, V of tile 0, probabilities of step 0
-        load(cache_tile(p, head, ref(begin)));
         const auto decode_tile = [&](int buf) KV_INLINE {
             look_up();
-            each<2 * T>([&](auto n) KV_INLINE { decode(buf, n); });
+            each<T + P>([&](auto n) KV_INLINE { decode(buf, n); });
         };
+        load(cache_tile(p, head, ref(begin)));
         decode_tile(0);
         load(cache_tile(p, head, ref(begin + 1)));
         if constexpr (kLate) {
             decode_tile(1);
             load(cache_tile(p, head, ref(begin + 2)));
         }
-        const int ahead = kLate ? 3 : 2;  // the tile whose codes are loaded next
+        constexpr int ahead = kLate ? 3 : 2;  // the tile whose codes are loaded next
         TileRef next = ref(begin + ahead);
         lds_barrier();
-        read_k(0, 0);
-        scores();
+#pragma unroll
+        for (int i = 0; i < 16; i++) x[i] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; t++)
+            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(read_k(0, 0, t), q[t], x, 0, 0, 0);
         each<5>(largest_part);
         settle(64 * units(begin), 0, 0);
         probabilities();
-        read_k(0, 1);
-        look_up();
+#pragma unroll
+        for (int n = 0; n < P; n++) ka[n] = read_k(0, 1, n);
+        if constexpr (!kLate) look_up();
         if constexpr (kLate) lds_barrier();
 #pragma unroll 1
         for (int i = begin; i < end; i++) {
@@ -1285,22 +1277,26 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
                 if constexpr (decltype(n)::value == 0)
                     f = *reinterpret_cast<const uint4*>(flags + buf * kWaves);
                 if constexpr (decltype(n)::value == 2) nan_tile = (f.x | f.y) | (f.z | f.w);
-                decode(kLate ? buf : buf ^ 1, n);
-                if constexpr (decltype(n)::value == T) load(at);
+                if constexpr (!kLate) decode(buf ^ 1, n);
+                if constexpr (!kLate && decltype(n)::value == T) load(at);
             });
             __builtin_amdgcn_s_setprio(0);
             lds_barrier();
             settle(64 * u + 32, nan_tile, u);
             probabilities();
+            if constexpr (kLate) look_up();
             lds_barrier();
             // A(2c + 1), B(2c + 1)
             __builtin_amdgcn_s_setprio(1);
-            products(buf, 1, buf ^ 1, 1, [](auto) {});
+            products(buf, 1, buf ^ 1, 1, [&](auto n) KV_INLINE {
+                if constexpr (kLate) decode(buf, n);
+                if constexpr (kLate && decltype(n)::value == T) load(at);
+            });
             __builtin_amdgcn_s_setprio(0);
             lds_barrier();
             settle(i + 1 < end ? 64 * units(i + 1) : kHidden, 0, 0);
             probabilities();
-            look_up();
+            if constexpr (!kLate) look_up();
             lds_barrier();
         }
         if constexpr (!kLate) lds_barrier();
@@ -1318,7 +1314,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 #pragma unroll
     for (int i = 0; i < 16; i++) {
         const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
-        const bool hit = poisoned >> (piece * M / 16) & 1;
+        const bool hit = poisoned >> (piece * D / 256) & 1;
 #pragma unroll
         for (int d = 0; d < B; d++) o[d][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][i];
     }
@@ -1328,7 +1324,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
         for (int i = 0; i < 8; i++) {
             const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
             uint32_t* dst =
-                reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh + piece * M);
+                reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh + piece * (D / 16) + part_of_o * M);
 #pragma unroll
             for (int d = 0; d < B; d++) dst[d] = pack_bf16(o[d][i] * f, o[d][i + 8] * f);
         }
@@ -1337,11 +1333,11 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
-            f32x2* dst = reinterpret_cast<f32x2*>(p.part_o + at * D + piece * M);
+            f32x2* dst = reinterpret_cast<f32x2*>(p.part_o + at * D + piece * (D / 16) + part_of_o * M);
 #pragma unroll
             for (int d = 0; d < B; d++) dst[d] = f32x2{o[d][i], o[d][i + 8]};
         }
-        if (half == 0) {
+        if (half == 0 && part_of_o == 0) {
             p.part_ml[2 * at] = m;
             p.part_ml[2 * at + 1] = l;
         }
@@ -1447,8 +1443,8 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     Plan pl;
     const int64_t group = a.heads / c.kv_heads, rows = a.max_q * group;
     pl.kind = rows <= 32 ? Plan::kFew
-              : c.head_dim <= 128 && rows > 128 ? Plan::kPrompt
-                                         : Plan::kMany;
+              : rows > 128 || c.head_dim == 256 ? Plan::kPrompt
+                                                : Plan::kMany;
     pl.blocks = rows <= 16 || c.head_dim == 256 ? 1 : 2;
     const int tile = pl.kind == Plan::kFew    ? 16 * pl.blocks
                      : pl.kind == Plan::kMany ? 128
@@ -1460,11 +1456,15 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     int64_t keys = a.max_len;
     if (a.window && a.window + a.sinks + a.max_q < keys) keys = a.window + a.sinks + a.max_q;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
-    const int64_t base = a.batch * c.kv_heads * pl.row_tiles;
+    // row tiles that hold rows: at most one per sequence is not full
+    int64_t tiles = a.total_q * group / tile + a.batch;
+    tiles = tiles < a.batch * pl.row_tiles ? tiles : a.batch * pl.row_tiles;
+    const int64_t base = c.kv_heads * tiles * (pl.kind == Plan::kPrompt && c.head_dim == 256 ? 2 : 1);
     const bool few = pl.kind == Plan::kFew;
     const int64_t unit = few ? kUnit : 64, least = few ? kUnit * kWaves : 256;
     const int64_t most = (keys + least - 1) / least;
-    int64_t s = base > 0 ? (few ? 3072 : 512) / base : 1;
+    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? MANYT : 512;
+    int64_t s = base > 0 ? target / base : 1;
     s = s > most ? most : s;
     s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
     const int64_t units = (keys + unit - 1) / unit;
@@ -1480,13 +1480,14 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
 }
 
 template <int D>
-hipError_t launch(void (*kernel)(Args), int threads, int lds, const Args& p, hipStream_t stream) {
+hipError_t launch(void (*kernel)(Args), int threads, int lds, int parts, const Args& p,
+                  hipStream_t stream) {
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kernel,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    const int64_t grid = (int64_t)p.batch_heads * p.row_tiles * p.splits;
+    const int64_t grid = (int64_t)p.batch_heads * p.row_tiles * p.splits * parts;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, stream, p);
     hipError_t e = hipGetLastError();
@@ -1498,15 +1499,16 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, const Args& p, hip
 
 template <int D>
 hipError_t dispatch(const Args& p, const Plan& pl, hipStream_t stream) {
+    if (pl.kind == Plan::kPrompt)
+        return launch<D>(prompt_kernel<D>, kPairThreads, PromptTile<D>::kLds, PromptTile<D>::kHalves,
+                         p, stream);
     if constexpr (D <= 128) {
-        if (pl.kind == Plan::kPrompt)
-            return launch<D>(prompt_kernel<D>, kPairThreads, ManyRows<D>::kLds, p, stream);
-        if (pl.kind == Plan::kFew && pl.blocks == 2)
-            return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, p, stream);
+        if (pl.kind == Plan::kMany)
+            return launch<D>(many_rows_kernel<D, 1>, kThreads, ManyRows<D>::kLds, 1, p, stream);
+        if (pl.blocks == 2)
+            return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, 1, p, stream);
     }
-    if (pl.kind == Plan::kFew)
-        return launch<D>(few_rows_kernel<D, 1>, kThreads, FewRows<D, 1>::kLds, p, stream);
-    return launch<D>(many_rows_kernel<D, 1>, kThreads, ManyRows<D>::kLds, p, stream);
+    return launch<D>(few_rows_kernel<D, 1>, kThreads, FewRows<D, 1>::kLds, 1, p, stream);
 }
 
 int clamp_int(int64_t v) { return (int)(v > 0x3FFFFFFF ? 0x3FFFFFFF : v); }
