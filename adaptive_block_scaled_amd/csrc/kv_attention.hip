@@ -23,6 +23,9 @@
 #include "kv_internal.h"
 #include "kv_operand.h"
 
+#ifndef PROMPTT
+#define PROMPTT 512
+#endif
 #ifndef MANYT
 #define MANYT 768
 #endif
@@ -1345,7 +1348,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPairThreads, 2) prompt_kernel(const Args p) {
+__global__ void __launch_bounds__(kPairThreads, D == 64 ? 4 : 2) prompt_kernel(const Args p) {
     if (threadIdx.x >= kPairThreads / 2)
         prompt_rows<D, true>(p);
     else
@@ -1429,6 +1432,67 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
     }
 }
 
+// The same for at most kFewSplits splits: one wave per row, no LDS.
+constexpr int kFewSplits = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) join_few_kernel(const Args p) {
+    constexpr int kLanes = D / 4, kSide = 64 / kLanes, kRounds = kFewSplits / kSide;
+    const int64_t at = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, side = lane / kLanes, d = lane % kLanes;
+    if (at >= p.rows_all) return;
+    f32x2 ml[kFewSplits];
+#pragma unroll
+    for (int i = 0; i < kFewSplits; i++)
+        ml[i] = *reinterpret_cast<const f32x2*>(
+            p.part_ml + 2 * ((i < p.splits ? i : 0) * p.rows_all + at));
+    f32x4 part[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; i++) {
+        const int split = i * kSide + side;
+        if (i * kSide < p.splits)
+            part[i] = *reinterpret_cast<const f32x4*>(
+                p.part_o + ((split < p.splits ? split : 0) * p.rows_all + at) * D + 4 * d);
+    }
+    float top = ml[0][0], sum = 0.0f;
+#pragma unroll
+    for (int i = 1; i < kFewSplits; i++) top = __builtin_fmaxf(top, ml[i][0]);
+    float w[kFewSplits];
+#pragma unroll
+    for (int i = 0; i < kFewSplits; i++) {
+        // zero also for splits without keys, whose O is not there
+        const bool in = i < p.splits && ml[i][1] != 0.0f;
+        w[i] = in ? __builtin_amdgcn_exp2f(ml[i][0] - top) : 0.0f;
+        sum += in ? w[i] * ml[i][1] : 0.0f;
+        ml[i][1] = in ? 1.0f : 0.0f;
+    }
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kRounds; i++) {
+        if (i * kSide < p.splits) {
+            float f = w[i * kSide], in = ml[i * kSide][1];
+#pragma unroll
+            for (int j = 1; j < kSide; j++) {
+                f = side == j ? w[i * kSide + j] : f;
+                in = side == j ? ml[i * kSide + j][1] : in;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                acc[j] = in != 0.0f ? __builtin_fmaf(f, part[i][j], acc[j]) : acc[j];
+        }
+    }
+#pragma unroll
+    for (int i = kLanes; i < 64; i *= 2)
+#pragma unroll
+        for (int j = 0; j < 4; j++) acc[j] += __shfl_xor(acc[j], i);
+    if (side == 0) {
+        const float f = sum == 0.0f ? 0.0f : p.v_mul / sum;
+        const int64_t row = at / p.heads, hd = at - row * p.heads;
+        *reinterpret_cast<uint2*>(p.out + row * p.o_st + hd * p.o_sh + 4 * d) =
+            make_uint2(pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f));
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host side: which kernel, how many splits.
 struct Plan {
@@ -1463,7 +1527,7 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     const bool few = pl.kind == Plan::kFew;
     const int64_t unit = few ? kUnit : 64, least = few ? kUnit * kWaves : 256;
     const int64_t most = (keys + least - 1) / least;
-    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? MANYT : 512;
+    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? MANYT : PROMPTT;
     int64_t s = base > 0 ? target / base : 1;
     s = s > most ? most : s;
     s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
@@ -1493,7 +1557,11 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, int parts, const A
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     if (p.rows_all > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)p.rows_all), dim3(kThreads), 0, stream, p);
+    if (p.splits <= kFewSplits)
+        hipLaunchKernelGGL((join_few_kernel<D>), dim3((unsigned)((p.rows_all + kWaves - 1) / kWaves)),
+                           dim3(kThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)p.rows_all), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 
