@@ -25,6 +25,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libif4.so")
 SAN_LIB = os.path.join(HERE, "libif4_san.so")
+CALLS = os.path.join(HERE, "_kv_call.so")
 CLANGXX = "/opt/rocm/llvm/bin/clang++"
 
 SOURCES = ["api.cpp", "quantize.hip", "dequantize.hip", "gemm.hip", "ifn.hip",
@@ -45,6 +46,7 @@ COMMON = [
 def build(verbose: bool = False, jobs: int = 4) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
+    calls = _start_calls(verbose)
     objs, procs = [], []
     for src in SOURCES:
         obj = os.path.join(objdir, src + ".o")
@@ -64,7 +66,31 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _wait(calls)
+    os.replace(CALLS + ".tmp", CALLS)
     return LIB
+
+
+def _start_calls(verbose: bool):
+    """csrc/kv_call.cpp (host code only), the C++ side of kv_cache.py: a CPython
+    module against PyTorch's headers.  It takes the library's entry points as
+    addresses when it is imported, and links PyTorch only."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    cmd = [CLANGXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in inc:
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "kv_call.cpp"), "-o", CALLS + ".tmp", "-L", lib, "-Wl,-rpath," + lib,
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return "kv_call.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 
 def _wait(item):

@@ -8,7 +8,10 @@ offset), `read` gives slots back as bf16 or fp32, `attention` attends from the
 newest tokens of a batch of sequences, each with its row of a page table.
 
 As in the rest of the binding, arguments are checked and marshalled here and
-all work runs in the HIP kernels of libif4.so, on torch's current stream.
+all work runs in the HIP kernels of libif4.so, on torch's current stream.  A
+call whose arguments are in order is marshalled in C++ (csrc/kv_call.cpp: 3 to
+5 us less than here, of calls that take 5 to 10); what that turns down comes to
+the checks below, which say what is wrong.
 """
 import ctypes
 import math
@@ -16,7 +19,14 @@ from typing import NamedTuple
 
 import torch
 
+from . import if4
 from .if4 import GROUP, MODE_ADAPTIVE, _check, _dtype_code, _need, lib
+
+try:
+    from . import _kv_call
+except ImportError as e:
+    raise ImportError(f"the KV cache's C++ calls ({if4.HERE}/_kv_call.so) do not load ({e}); build them "
+                      "with `python -m adaptive_block_scaled_amd.build`") from e
 
 EXPORTS = ("if4_kv_append", "if4_kv_read", "if4_kv_attention", "if4_kv_attention_workspace")
 HEAD_DIMS = (64, 128, 256)
@@ -60,6 +70,7 @@ def _declare():
 
 
 _declare()
+_kv_call.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS))
 
 
 class KVCache(NamedTuple):
@@ -139,6 +150,11 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     D, other strides multiples of 16 bytes: slices of a fused projection are
     fine) into the cache's slots (int64 [tokens], all different; a slot outside
     the cache is skipped).  Returns the cache, which is written in place."""
+    st = _kv_call.append(cache, k, v, slots, k_exp, v_exp, mode)
+    if st == 0:
+        return cache
+    if st:
+        _check("if4_kv_append", st)
     c, index = _cache(cache, k_exp, v_exp)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a 3-D tensor [tokens, kv_heads, D]")
@@ -159,6 +175,12 @@ def read(cache: KVCache, slots: torch.Tensor, k_exp: int = 0, v_exp: int = 0,
     """Values of the cache's slots (int64 [tokens]): (k, v), each [tokens,
     kv_heads, D] of `dtype` (bf16 or fp32).  A slot outside the cache reads as
     zeros.  `out` may pass preallocated (k, v)."""
+    if out is None and (dtype is torch.bfloat16 or dtype is torch.float32):
+        kv = _kv_call.read(cache, slots, k_exp, v_exp, dtype is torch.bfloat16)
+        if type(kv) is tuple:
+            return kv
+        if kv:
+            _check("if4_kv_read", kv)
     c, index = _cache(cache, k_exp, v_exp)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D tensor")
@@ -198,6 +220,13 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_len
     p - window or j < sinks.  Rows that see no key give zeros.  scale defaults
     to 1/sqrt(D).  Returns [total_q, heads, D] bf16; `out` may pass it
     preallocated, `workspace` a uint8 tensor of workspace_bytes()."""
+    if out is None and workspace is None:
+        r = _kv_call.attention(q, cache, page_table, seq_lens, q_starts, max_q, max_len, scale, k_exp,
+                               v_exp, causal, window, sinks)
+        if type(r) is int:
+            _check("if4_kv_attention", r)
+        elif r is not None:
+            return r
     c, index = _cache(cache, k_exp, v_exp)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D tensor [total_q, heads, D]")
