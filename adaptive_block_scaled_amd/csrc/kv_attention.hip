@@ -23,12 +23,6 @@
 #include "kv_internal.h"
 #include "kv_operand.h"
 
-#ifndef PROMPTT
-#define PROMPTT 512
-#endif
-#ifndef MANYT
-#define MANYT 768
-#endif
 namespace if4 {
 namespace {
 
@@ -139,7 +133,8 @@ __device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int
 // at most `hi`, and at least `lo` or at most `sink`.
 struct WholeSteps {
     int lo, hi, sink;
-    __device__ __forceinline__ WholeSteps(const Args& p, int len, int pos_lo, int pos_hi, int step) {
+    __device__ __forceinline__ WholeSteps(const Args& p, int len, int pos_lo, int pos_hi,
+                                          int step) {
         const int n = p.causal && pos_lo + 1 < len ? pos_lo + 1 : len;
         hi = n - step;
         lo = p.window ? pos_hi - p.window + 1 : -1;
@@ -235,6 +230,25 @@ struct RowPlace {
     }
 };
 
+// Scores of keys that a row does not see become -inf.  x[i] is the score of key
+// first + 8 (i / 4) + i % 4 for the row at position pos.
+__device__ __forceinline__ void hide(const Args& p, int len, int pos, int first,
+                                     f32x16& x) {
+    const int last = p.causal && pos < len - 1 ? pos : len - 1;
+    const int hi = last - first;
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        x[i] = 8 * (i >> 2) + (i & 3) <= hi ? x[i] : -__builtin_inff();
+    if (p.window) {
+        const int lo = pos - p.window - first, sink = p.sinks - first;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const int c = 8 * (i >> 2) + (i & 3);
+            x[i] = ((c > lo) | (c < sink)) ? x[i] : -__builtin_inff();
+        }
+    }
+}
+
 // Largest magnitude of 8 bf16 values, and their operand.
 __device__ __forceinline__ float largest(const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -326,7 +340,8 @@ struct FewRows {
 };
 
 template <int D, int kBlocks>
-__global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) few_rows_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy))
+few_rows_kernel(const Args p) {
     constexpr int kRows = 16 * kBlocks, kPad = D + 4, M = D / 16;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint2* const tables = reinterpret_cast<uint2*>(smem);
@@ -584,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) f
             const int64_t row = s.first_row + t, hd = head * p.group + g;
             if (p.splits == 1) {
                 const float f = sum == 0.0f ? 0.0f : p.v_mul / sum;
-                uint32_t* dst =
-                    reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh + (tid & 15) * M);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh +
+                                                            (tid & 15) * M);
 #pragma unroll
                 for (int d = 0; d < M; d += 2) dst[d / 2] = pack_bf16(acc[d] * f, acc[d + 1] * f);
             } else {
@@ -603,8 +618,100 @@ __global__ void __launch_bounds__(kThreads, (FewRows<D, kBlocks>::kOccupancy)) f
 }
 
 // ---------------------------------------------------------------------------
-// Many rows (chunks of prompt): tiles of 128 * kBlocks rows, 4 waves of
-// 32 * kBlocks rows each.
+// What the two kernels with 32 rows per wave share: a lane holds one row (row =
+// lane % 32 of its wave), half = lane / 32.
+
+// q of a row as the operands of D / 16 products: words 2t + half of 8 dims.
+template <int D>
+__device__ __forceinline__ void take_q(const Args& p, const Sequence& s, int head, int r, int rows,
+                                       int half, half8 (&q)[D / 16], float& factor, int& pos) {
+    const RowPlace at(p, s, head, r, rows);
+    const uint16_t* src = p.q + at.row * p.q_st + at.head * p.q_sh + half * 8;
+    uint4 raw[D / 16];
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) {
+        raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
+        a = __builtin_fmaxf(a, largest(raw[i]));
+    }
+    a = __builtin_fmaxf(a, __shfl_xor(a, 32));
+    const int e = row_exponent(a);
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) q[i] = q_operand(raw[i], e);
+    factor = score_factor(p, e);
+    pos = s.pos0 + at.token;
+}
+
+__device__ __forceinline__ bool sees(const Args& p, int len, int pos, int key) {
+    return (key <= pos || !p.causal) & (key < len) &
+           (!p.window || key > pos - p.window || key < p.sinks);
+}
+
+// Probabilities of 32 keys, 16 of them in this lane, as the operands of O's
+// products.  l sums what those see, the fp16 values (v_dot2 adds two exactly).
+__device__ __forceinline__ void probabilities(const f32x16& x, float factor, float m, float& l,
+                                              uint4 (&prob)[2]) {
+    float e[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], factor, -m));
+    uint32_t h[8];
+    float sum[2] = {l, 0.0f};  // two short chains
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        h[i] = pack_half(e[2 * i], e[2 * i + 1]);
+        sum[i & 1] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, h[i]),
+                                            __builtin_bit_cast(half2v, 0x3C003C00u), sum[i & 1],
+                                            false);
+    }
+    l = sum[0] + sum[1];
+    prob[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    prob[1] = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// A row's result: B blocks of 32 dims, accumulator i of block d in V-piece row
+// 8 (i / 4) + 4 half + i % 4 (mod 16), so that a lane holds 2 B dims of 8 pieces.
+template <int D, int B>
+__device__ __forceinline__ void store_row(const Args& p, const Sequence& s, int head, int r,
+                                          int rows, int half, int split, int part_of_o,
+                                          f32x16 (&o)[B], float m, float l, uint32_t poisoned) {
+    l += __shfl_xor(l, 32);
+    if (r >= rows) return;
+    const RowPlace at(p, s, head, r, rows);
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
+        const bool hit = poisoned >> (piece * D / 256) & 1;
+#pragma unroll
+        for (int d = 0; d < B; d++) o[d][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][i];
+    }
+    const int first = part_of_o * 2 * B;
+    if (p.splits == 1) {
+        const float f = l == 0.0f ? 0.0f : p.v_mul / l;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at.row * p.o_st + at.head * p.o_sh +
+                                                        piece * (D / 16) + first);
+#pragma unroll
+            for (int d = 0; d < B; d++) dst[d] = pack_bf16(o[d][i] * f, o[d][i + 8] * f);
+        }
+    } else {
+        const int64_t to = split * p.rows_all + at.row * p.heads + at.head;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
+            f32x2* dst = reinterpret_cast<f32x2*>(p.part_o + to * D + piece * (D / 16) + first);
+#pragma unroll
+            for (int d = 0; d < B; d++) dst[d] = f32x2{o[d][i], o[d][i + 8]};
+        }
+        if (half == 0 && part_of_o == 0)
+            *reinterpret_cast<f32x2*>(p.part_ml + 2 * to) = f32x2{m, l};
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows (33 to 128, D <= 128): tiles of 128 rows, 4 waves of 32 rows each.
 //
 // The four waves share K and V: each decodes one 16-token cache tile of every
 // 64 keys into double-buffered LDS tiles in the order of the operands of
@@ -635,9 +742,9 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-template <int D, int kBlocks>
-__global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) many_rows_kernel(const Args p) {
-    constexpr int kRows = 128 * kBlocks, T = D / 16, B = D / 32, M = D / 16;
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(const Args p) {
+    constexpr int kRows = 128, T = D / 16, B = D / 32, M = D / 16;
     constexpr int kTile = ManyRows<D>::kTile;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint2* const tables = reinterpret_cast<uint2*>(smem);
@@ -669,41 +776,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
     }
     fill_scale_tables(tables, tid, kThreads);
 
-    half8 q[kBlocks][T];
-    float factor[kBlocks], m[kBlocks], l[kBlocks];
-    int see_hi[kBlocks], see_lo[kBlocks];
-    uint32_t poisoned[kBlocks];  // groups of O that are NaN
-    f32x16 o[B][kBlocks], x[2][kBlocks];
+    half8 q[T];
+    float factor, m = kLowest, l = 0.0f;
+    int pos;
+    take_q<D>(p, s, head, row0 + 32 * wave + (lane & 31), rows, half, q, factor, pos);
+    uint32_t poisoned = 0;  // groups of O that are NaN
+    f32x16 o[B], x[2];
 #pragma unroll
-    for (int nr = 0; nr < kBlocks; nr++) {
-        const int r = row0 + 32 * (kBlocks * wave + nr) + (lane & 31);
-        const int rc = r < rows ? r : rows - 1;
-        const int t = rc / p.group, g = rc - t * p.group;
-        const uint16_t* src = p.q + (s.first_row + t) * p.q_st +
-                              (int64_t)(head * p.group + g) * p.q_sh + half * 8;
-        uint4 raw[T];
-        float a = 0.0f;
+    for (int d = 0; d < B; d++)
 #pragma unroll
-        for (int i = 0; i < T; i++) {
-            raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
-            a = __builtin_fmaxf(a, largest(raw[i]));
-        }
-        a = __builtin_fmaxf(a, __shfl_xor(a, 32));
-        const int e = row_exponent(a);
-#pragma unroll
-        for (int i = 0; i < T; i++) q[nr][i] = q_operand(raw[i], e);
-        factor[nr] = score_factor(p, e);
-        const int pos = s.pos0 + t;
-        see_hi[nr] = p.causal && pos < s.len - 1 ? pos : s.len - 1;
-        see_lo[nr] = p.window ? pos - p.window : -1;
-        m[nr] = kLowest;
-        l[nr] = 0.0f;
-        poisoned[nr] = 0;
-#pragma unroll
-        for (int d = 0; d < B; d++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) o[d][nr][i] = 0.0f;
-    }
+        for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
 
     // this lane's codes of its wave's cache tile: K (key lane % 16, quarter
     // lane / 16 of D), V (piece lane % 16, tokens 4 quarter ..); V's quarters
@@ -725,10 +807,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
         const uint8_t* src = p.k_scales + at * D + ks_at;
         if constexpr (D == 64)
             ks = *src;
-        else if constexpr (D == 128)
-            ks = *reinterpret_cast<const uint16_t*>(src);
         else
-            ks = *reinterpret_cast<const uint32_t*>(src);
+            ks = *reinterpret_cast<const uint16_t*>(src);
     };
     auto load_v = [&](uint64_t at) {
         UnitCodes<D>::words(p.v_codes + at * (8 * D) + v_at, vw);
@@ -759,75 +839,35 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
         if (lane == 0) flags[buf * kWaves + wave] = bad != 0;
     };
     // scores of 32 keys
-    auto scores = [&](f32x16 (&to)[kBlocks], int buf, int kb) {
+    auto scores = [&](f32x16& to, int buf, int kb) {
         const uint8_t* src = k_lds + buf * kTile + kb * T * 1024 + lane * 16;
 #pragma unroll
-        for (int nr = 0; nr < kBlocks; nr++)
+        for (int i = 0; i < 16; i++) to[i] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; i++) to[nr][i] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < T; t++) {
-            const half8 a = *reinterpret_cast<const half8*>(src + t * 1024);
-#pragma unroll
-            for (int nr = 0; nr < kBlocks; nr++)
-                to[nr] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[nr][t], to[nr], 0, 0, 0);
-        }
+        for (int t = 0; t < T; t++)
+            to = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                *reinterpret_cast<const half8*>(src + t * 1024), q[t], to, 0, 0, 0);
     };
     // hides what a row does not see, and raises m where it has to
     const WholeSteps whole(p, s.len, pos_lo, pos_hi, 32);
-    auto settle = [&](f32x16 (&sc)[kBlocks], int key0) {
-        if (!whole(key0)) {
+    auto settle = [&](f32x16& sc, int key0) {
+        if (!whole(key0)) hide(p, s.len, pos, key0 + 4 * half, sc);
+        float top = sc[0];
 #pragma unroll
-            for (int nr = 0; nr < kBlocks; nr++)
+        for (int i = 1; i < 16; i++) top = __builtin_fmaxf(top, sc[i]);
+        top *= factor;
+        if (__builtin_amdgcn_ballot_w64(top > m + kSlack) == 0) return;
+        top = __builtin_fmaxf(top, m);
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+        const float alpha = __builtin_amdgcn_exp2f(m - top);
+        m = top;
+        l *= alpha;
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int key = key0 + 8 * (i >> 2) + 4 * half + (i & 3);
-                    const bool seen = key <= see_hi[nr] && (key > see_lo[nr] || key < p.sinks);
-                    sc[nr][i] = seen ? sc[nr][i] : -__builtin_inff();
-                }
-        }
-        float top[kBlocks];
-        bool raise = false;
+        for (int d = 0; d < B; d++)
 #pragma unroll
-        for (int nr = 0; nr < kBlocks; nr++) {
-            top[nr] = sc[nr][0];
-#pragma unroll
-            for (int i = 1; i < 16; i++) top[nr] = __builtin_fmaxf(top[nr], sc[nr][i]);
-            top[nr] *= factor[nr];
-            raise |= top[nr] > m[nr] + kSlack;
-        }
-        if (__builtin_amdgcn_ballot_w64(raise) == 0) return;
-#pragma unroll
-        for (int nr = 0; nr < kBlocks; nr++) {
-            float t = __builtin_fmaxf(top[nr], m[nr]);
-            t = __builtin_fmaxf(t, __shfl_xor(t, 32));
-            const float alpha = __builtin_amdgcn_exp2f(m[nr] - t);
-            m[nr] = t;
-            l[nr] *= alpha;
-#pragma unroll
-            for (int d = 0; d < B; d++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) o[d][nr][i] *= alpha;
-        }
+            for (int i = 0; i < 16; i++) o[d][i] *= alpha;
     };
-    uint4 prob[kBlocks][2];
-    auto probabilities = [&](f32x16 (&sc)[kBlocks]) {
-#pragma unroll
-        for (int nr = 0; nr < kBlocks; nr++) {
-            float e[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nr][i], factor[nr], -m[nr]));
-                l[nr] += e[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-                prob[nr][i] =
-                    make_uint4(pack_half(e[8 * i], e[8 * i + 1]), pack_half(e[8 * i + 2], e[8 * i + 3]),
-                               pack_half(e[8 * i + 4], e[8 * i + 5]),
-                               pack_half(e[8 * i + 6], e[8 * i + 7]));
-        }
-    };
+    uint4 prob[2];
     auto accumulate = [&](int buf, int kb) {
 #pragma unroll
         for (int i = 0; i < 2; i++)
@@ -835,10 +875,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
             for (int d = 0; d < B; d++) {
                 const half8 a = *reinterpret_cast<const half8*>(
                     v_lds + buf * kTile + ((2 * kb + i) * B + d) * 1024 + lane * 16);
-#pragma unroll
-                for (int nr = 0; nr < kBlocks; nr++)
-                    o[d][nr] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        a, __builtin_bit_cast(half8, prob[nr][i]), o[d][nr], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                    a, __builtin_bit_cast(half8, prob[i]), o[d], 0, 0, 0);
             }
     };
     // NaN values of V (decoded as zeros) of a 64-key tile: the groups that turn
@@ -851,12 +889,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
 #pragma unroll 1
             for (int t = 0; t < 16; t++) {
                 const int key = 64 * u + 16 * (j / T) + t;
-                const bool bad = (src[t] & 0x7F) == 0x7F;
-#pragma unroll
-                for (int nr = 0; nr < kBlocks; nr++) {
-                    const bool seen = key <= see_hi[nr] && (key > see_lo[nr] || key < p.sinks);
-                    poisoned[nr] |= (uint32_t)(bad && seen) << (j % T);
-                }
+                const bool hit = (src[t] & 0x7F) == 0x7F && sees(p, s.len, pos, key);
+                poisoned |= (uint32_t)hit << (j % T);
             }
         }
     };
@@ -882,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
             next = ref(i + 3);
             // keys 0 .. 31 of the tile
             scores(x[1], buf, 1);
-            probabilities(x[0]);
+            probabilities(x[0], factor, m, l, prob);
             accumulate(buf, 0);
             decode_k(buf ^ 1);
             load_k(at);
@@ -891,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
             // keys 32 .. 63
             const uint4 f = *reinterpret_cast<const uint4*>(flags + buf * kWaves);
             scores(x[0], buf ^ 1, 0);
-            probabilities(x[1]);
+            probabilities(x[1], factor, m, l, prob);
             accumulate(buf, 1);
             decode_v(buf ^ 1);
             load_v(at);
@@ -901,47 +935,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks == 1 && D <= 128 ? 2 : 1) ma
         }
     }
 
-#pragma unroll
-    for (int nr = 0; nr < kBlocks; nr++) {
-        l[nr] += __shfl_xor(l[nr], 32);
-        const int r = row0 + 32 * (kBlocks * wave + nr) + (lane & 31);
-        if (r >= rows) continue;
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
-            const bool hit = poisoned[nr] >> (piece * M / 16) & 1;
-#pragma unroll
-            for (int d = 0; d < B; d++)
-                o[d][nr][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][nr][i];
-        }
-        const int t = r / p.group, g = r - t * p.group;
-        const int64_t row = s.first_row + t, hd = head * p.group + g;
-        if (p.splits == 1) {
-            const float f = l[nr] == 0.0f ? 0.0f : p.v_mul / l[nr];
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
-                uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh +
-                                                            piece * M);
-#pragma unroll
-                for (int d = 0; d < B; d++)
-                    dst[d] = pack_bf16(o[d][nr][i] * f, o[d][nr][i + 8] * f);
-            }
-        } else {
-            const int64_t at = split * p.rows_all + row * p.heads + hd;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
-                f32x2* dst = reinterpret_cast<f32x2*>(p.part_o + at * D + piece * M);
-#pragma unroll
-                for (int d = 0; d < B; d++) dst[d] = f32x2{o[d][nr][i], o[d][nr][i + 8]};
-            }
-            if (half == 0) {
-                p.part_ml[2 * at] = m[nr];
-                p.part_ml[2 * at + 1] = l[nr];
-            }
-        }
-    }
+    store_row<D, B>(p, s, head, row0 + 32 * wave + (lane & 31), rows, half, split, 0, o, m, l,
+                    poisoned);
 }
 
 // ---------------------------------------------------------------------------
@@ -982,8 +977,8 @@ struct PromptTile {
 template <int D, bool kLate>
 __device__ __forceinline__ void prompt_rows(const Args& p) {
     typedef PromptTile<D> Tile;
-    // products of a step: T for the scores, P = 2 B for O; M dims of a V piece
-    constexpr int kRows = 256, T = D / 16, DV = Tile::kV, B = DV / 32, P = 2 * B, M = DV / 16;
+    // products of a step: T for the scores, P = 2 B for O
+    constexpr int kRows = 256, T = D / 16, DV = Tile::kV, B = DV / 32, P = 2 * B;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint2* const tables = reinterpret_cast<uint2*>(smem);
     uint8_t* const k_lds = smem + kScaleTableBytes;
@@ -1014,32 +1009,6 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
         mark_empty(p, s, head, row0, last_row, split);
         return;
     }
-    fill_scale_tables(tables, tid, kPairThreads);
-
-    half8 q[T];
-    float factor, m = kLowest, l = 0.0f;
-    int pos;
-    {
-        const RowPlace at(p, s, head, row0 + 32 * wave + (lane & 31), rows);
-        pos = s.pos0 + at.token;
-        const uint16_t* src = p.q + at.row * p.q_st + at.head * p.q_sh + half * 8;
-        uint4 raw[T];
-        float a = 0.0f;
-#pragma unroll
-        for (int i = 0; i < T; i++) {
-            raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
-            a = __builtin_fmaxf(a, largest(raw[i]));
-        }
-        a = __builtin_fmaxf(a, __shfl_xor(a, 32));
-        const int e = row_exponent(a);
-#pragma unroll
-        for (int i = 0; i < T; i++) q[i] = q_operand(raw[i], e);
-        factor = score_factor(p, e);
-    }
-    auto sees = [&](int key) KV_INLINE {
-        return (key <= pos || !p.causal) & (key < s.len) &
-               (!p.window || key > pos - p.window || key < p.sinks);
-    };
     uint32_t poisoned = 0;  // groups of O that are NaN
     f32x16 o[B], x;
 #pragma unroll
@@ -1059,38 +1028,59 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     uint8_t* const v_to =
         v_lds + unit16 * B * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8;
 
-    uint32_t w[kLate ? D / 32 : DV / 32], sc;
-    bool bad = false;  // a NaN among the scales of w (V)
-    auto load = [&](uint64_t at) KV_INLINE {
+    struct Codes {
+        uint32_t w[kLate ? D / 32 : DV / 32], sc;
+    };
+    auto load = [&](Codes& c, uint64_t at) KV_INLINE {
         const uint8_t* src = codes + at * (8 * D) + code_at;
         if constexpr (kLate || D == DV) {
-            UnitCodes<D>::words(src, w);
+            UnitCodes<D>::words(src, c.w);
         } else {
 #pragma unroll
             for (int t = 0; t < 4; t++)  // one of the two words of each token
-                w[t] = *reinterpret_cast<const uint32_t*>(src + 4 * part_of_o + 8 * t);
+                c.w[t] = *reinterpret_cast<const uint32_t*>(src + 4 * part_of_o + 8 * t);
         }
         src = scales + at * D + scale_at;
         if constexpr (!kLate || D == 256)
-            sc = *reinterpret_cast<const uint32_t*>(src);
+            c.sc = *reinterpret_cast<const uint32_t*>(src);
         else if constexpr (D == 64)
-            sc = *src;
+            c.sc = *src;
         else
-            sc = *reinterpret_cast<const uint16_t*>(src);
+            c.sc = *reinterpret_cast<const uint16_t*>(src);
     };
-    auto ref = [&](int i) KV_INLINE { return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + unit16); };
-    // The scales of the codes in w, looked up one phase before their decode.
+    Codes now;
+    bool bad = false;  // a NaN among the scales of `now` (V)
+    auto ref = [&](int i) KV_INLINE {
+        return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + unit16);
+    };
+    // the first tiles' codes and q are asked for together
+    Codes first[3];
+    if (begin < end) {
+        TileRef r[3];
+#pragma unroll
+        for (int i = 0; i < 3; i++) r[i] = ref(begin + i);
+#pragma unroll
+        for (int i = 0; i < (kLate ? 3 : 2); i++) load(first[i], cache_tile(p, head, r[i]));
+    }
+    fill_scale_tables(tables, tid, kPairThreads);
+    half8 q[T];
+    float factor, m = kLowest, l = 0.0f;
+    int pos;
+    take_q<D>(p, s, head, row0 + 32 * wave + (lane & 31), rows, half, q, factor, pos);
+    now = first[0];
+
+    // The scales of the codes in `now`, looked up one phase before their decode.
     GroupScale look[4];
     auto look_up = [&]() KV_INLINE {
         if constexpr (kLate) {
 #pragma unroll
-            for (int i = 0; i < D / 64; i++) look[i] = k_scale(tables, (sc >> (8 * i)) & 0xFFu);
+            for (int i = 0; i < D / 64; i++) look[i] = k_scale(tables, (now.sc >> (8 * i)) & 0xFFu);
         } else {
-            VPiece<DV>::look_up(tables, sc, look);
-            bad = __builtin_amdgcn_ballot_w64(nan_bytes(sc) != 0) != 0;
+            VPiece<DV>::look_up(tables, now.sc, look);
+            bad = __builtin_amdgcn_ballot_w64(nan_bytes(now.sc) != 0) != 0;
         }
     };
-    // Decode of w (one 16-token tile), in T + P slices that go between the
+    // Decode of `now` (one 16-token tile), in T + P slices that go between the
     // products of an A phase: the bits first, then operand by operand.
     KGroup kg[D / 64];
     VPiece<DV> vp;
@@ -1098,19 +1088,20 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
         constexpr int n = decltype(slice_c)::value;
         if constexpr (n < T) {
             if constexpr (kLate && n % 2 == 1 && n / 2 < D / 64)
-                kg[n / 2].unpack(w[n - 1], w[n], look[n / 2], four);
+                kg[n / 2].unpack(now.w[n - 1], now.w[n], look[n / 2], four);
             if constexpr (!kLate && n % 2 == 1 && n / 2 < DV / 64)
-                vp.template unpack_words<n / 2>(w, look, four);
+                vp.template unpack_words<n / 2>(now.w, look, four);
             if constexpr (!kLate && n == 0)
                 flags[buf * kWaves + unit16] = bad;  // (every lane the same)
         } else if constexpr (!kLate) {
             constexpr int d = n - T;
-            *reinterpret_cast<uint2*>(v_to + buf * Tile::kVBytes + (d >> 1) * 1024 + (d & 1) * 256) =
+            uint8_t* const to = v_to + buf * Tile::kVBytes + (d >> 1) * 1024 + (d & 1) * 256;
+            *reinterpret_cast<uint2*>(to) =
                 make_uint2(vp.template pair<d, 0>(), vp.template pair<d, 1>());
         } else if constexpr ((n - T) % (P / (D / 32)) == 0) {
             constexpr int i = (n - T) / (P / (D / 32));  // operand of 8 elements
-            *reinterpret_cast<half8*>(k_to + buf * Tile::kKBytes + (i / 2) * 1024 + (i % 2) * 512) =
-                kg[i / 2].template operand<i % 2>();
+            uint8_t* const to = k_to + buf * Tile::kKBytes + (i / 2) * 1024 + (i % 2) * 512;
+            *reinterpret_cast<half8*>(to) = kg[i / 2].template operand<i % 2>();
         }
     };
     half8 ka[P];  // K's operands, P ahead
@@ -1187,7 +1178,8 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 #pragma unroll 1
             for (int t = 0; t < 16; t++) {
                 const int key = 64 * u + 16 * (j / T) + t;
-                poisoned |= (uint32_t)((src[t] & 0x7F) == 0x7F && sees(key)) << (j % T);
+                const bool hit = (src[t] & 0x7F) == 0x7F && sees(p, s.len, pos, key);
+                poisoned |= (uint32_t)hit << (j % T);
             }
         }
     };
@@ -1200,11 +1192,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
         if (all & (__builtin_amdgcn_ballot_w64((top > m + kSlack) | (nan_tile != 0)) == 0)) return;
         if (nan_tile != 0) poison(u);
         if (!all) {
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const int key = key0 + 8 * (i >> 2) + 4 * half + (i & 3);
-                x[i] = sees(key) ? x[i] : -__builtin_inff();
-            }
+            hide(p, s.len, pos, key0 + 4 * half, x);
             each<5>(largest_part);
         }
         if (__builtin_amdgcn_ballot_w64(top > m + kSlack) == 0) return;
@@ -1218,26 +1206,6 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 #pragma unroll
             for (int i = 0; i < 16; i++) o[d][i] *= alpha;
     };
-    auto probabilities = [&]() KV_INLINE {
-        float e[16];
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], factor, -m));
-        uint32_t h[8];
-        float sum[2] = {l, 0.0f};  // two short chains
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            h[i] = pack_half(e[2 * i], e[2 * i + 1]);
-            // l sums what the second product sees, the fp16 probabilities
-            sum[i & 1] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, h[i]),
-                                                __builtin_bit_cast(half2v, 0x3C003C00u),
-                                                sum[i & 1], false);
-        }
-        l = sum[0] + sum[1];
-        prob[0] = make_uint4(h[0], h[1], h[2], h[3]);
-        prob[1] = make_uint4(h[4], h[5], h[6], h[7]);
-    };
-
     __syncthreads();
     if (begin < end) {
         // K of tiles 0 and 1, V of tile 0, probabilities of step 0
@@ -1245,12 +1213,11 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
             look_up();
             each<T + P>([&](auto n) KV_INLINE { decode(buf, n); });
         };
-        load(cache_tile(p, head, ref(begin)));
         decode_tile(0);
-        load(cache_tile(p, head, ref(begin + 1)));
+        now = first[1];
         if constexpr (kLate) {
             decode_tile(1);
-            load(cache_tile(p, head, ref(begin + 2)));
+            now = first[2];
         }
         constexpr int ahead = kLate ? 3 : 2;  // the tile whose codes are loaded next
         TileRef next = ref(begin + ahead);
@@ -1262,7 +1229,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
             x = __builtin_amdgcn_mfma_f32_32x32x16_f16(read_k(0, 0, t), q[t], x, 0, 0, 0);
         each<5>(largest_part);
         settle(64 * units(begin), 0, 0);
-        probabilities();
+        probabilities(x, factor, m, l, prob);
 #pragma unroll
         for (int n = 0; n < P; n++) ka[n] = read_k(0, 1, n);
         if constexpr (!kLate) look_up();
@@ -1281,70 +1248,36 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
                     f = *reinterpret_cast<const uint4*>(flags + buf * kWaves);
                 if constexpr (decltype(n)::value == 2) nan_tile = (f.x | f.y) | (f.z | f.w);
                 if constexpr (!kLate) decode(buf ^ 1, n);
-                if constexpr (!kLate && decltype(n)::value == T) load(at);
+                if constexpr (!kLate && decltype(n)::value == T) load(now, at);
             });
             __builtin_amdgcn_s_setprio(0);
             lds_barrier();
             settle(64 * u + 32, nan_tile, u);
-            probabilities();
+            probabilities(x, factor, m, l, prob);
             if constexpr (kLate) look_up();
             lds_barrier();
             // A(2c + 1), B(2c + 1)
             __builtin_amdgcn_s_setprio(1);
             products(buf, 1, buf ^ 1, 1, [&](auto n) KV_INLINE {
                 if constexpr (kLate) decode(buf, n);
-                if constexpr (kLate && decltype(n)::value == T) load(at);
+                if constexpr (kLate && decltype(n)::value == T) load(now, at);
             });
             __builtin_amdgcn_s_setprio(0);
             lds_barrier();
             settle(i + 1 < end ? 64 * units(i + 1) : kHidden, 0, 0);
-            probabilities();
+            probabilities(x, factor, m, l, prob);
             if constexpr (!kLate) look_up();
             lds_barrier();
         }
         if constexpr (!kLate) lds_barrier();
     }
 
-    l += __shfl_xor(l, 32);
-    // the row's place again, from a lane number that the compiler takes for
-    // another one: kept across the loop it would cost registers
+    // (the row's place from a lane number that the compiler takes for another one:
+    // kept across the loop it would cost registers)
     int lane_again = lane;
     asm volatile("" : "+v"(lane_again));
-    const int r = row0 + 32 * wave + (lane_again & 31);
-    if (r >= rows) return;
-    const RowPlace place(p, s, head, r, rows);
-    const int64_t row = place.row, hd = place.head;
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int piece = (8 * (i >> 2) + 4 * half + (i & 3)) & 15;
-        const bool hit = poisoned >> (piece * D / 256) & 1;
-#pragma unroll
-        for (int d = 0; d < B; d++) o[d][i] = hit ? __uint_as_float(0x7FC00000u) : o[d][i];
-    }
-    if (p.splits == 1) {
-        const float f = l == 0.0f ? 0.0f : p.v_mul / l;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
-            uint32_t* dst =
-                reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh + piece * (D / 16) + part_of_o * M);
-#pragma unroll
-            for (int d = 0; d < B; d++) dst[d] = pack_bf16(o[d][i] * f, o[d][i + 8] * f);
-        }
-    } else {
-        const int64_t at = split * p.rows_all + row * p.heads + hd;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int piece = 8 * (i >> 2) + 4 * half + (i & 3);
-            f32x2* dst = reinterpret_cast<f32x2*>(p.part_o + at * D + piece * (D / 16) + part_of_o * M);
-#pragma unroll
-            for (int d = 0; d < B; d++) dst[d] = f32x2{o[d][i], o[d][i + 8]};
-        }
-        if (half == 0 && part_of_o == 0) {
-            p.part_ml[2 * at] = m;
-            p.part_ml[2 * at + 1] = l;
-        }
-    }
+    store_row<D, B>(p, s, head, row0 + 32 * wave + (lane_again & 31), rows, lane_again >> 5, split,
+                    part_of_o, o, m, l, poisoned);
 }
 
 template <int D>
@@ -1505,6 +1438,10 @@ struct Plan {
 
 Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     Plan pl;
+    // The kernels by rows of the longest chunk.  Up to 32 rows a wave decodes for
+    // its own rows only; beyond, sharing the decode in LDS wins (60 rows of each of
+    // 64 heads: 21 us against 28; 64 rows of 16 heads over 16k keys: 40 against
+    // 54; 128 rows: 38 against 52).
     const int64_t group = a.heads / c.kv_heads, rows = a.max_q * group;
     pl.kind = rows <= 32 ? Plan::kFew
               : rows > 128 || c.head_dim == 256 ? Plan::kPrompt
@@ -1514,20 +1451,26 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
                      : pl.kind == Plan::kMany ? 128
                                               : 256;
     pl.row_tiles = (int)((rows + tile - 1) / tile);
-    // Splits of the keys: enough workgroups to fill 256 CUs a few times over
-    // (twice where a workgroup fills a CU's registers), each with at least one
-    // unit of keys for each of its waves.
+    // Splits of the keys.  Few rows: 256 CUs hold 1024 workgroups (D = 128), and
+    // 3072 leave a short last round where lengths differ (64 sequences of 3-12k
+    // keys: 140 us at 2048, 137 at 3072, 143 at 4096).  Many rows: 2 per CU.
+    // Prompts: one per CU, and no second round for which every workgroup would
+    // start again (a 512-token chunk over 8192 keys, 32 heads: 101 us against 121
+    // with twice as many; 1774 of 1778, 16 heads: 54 against 66).
     int64_t keys = a.max_len;
-    if (a.window && a.window + a.sinks + a.max_q < keys) keys = a.window + a.sinks + a.max_q;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
+    const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
+    const int64_t sinks = a.sinks < kMaxKeys ? a.sinks : kMaxKeys;
+    if (window && window + sinks + a.max_q < keys) keys = window + sinks + a.max_q;
     // row tiles that hold rows: at most one per sequence is not full
     int64_t tiles = a.total_q * group / tile + a.batch;
     tiles = tiles < a.batch * pl.row_tiles ? tiles : a.batch * pl.row_tiles;
-    const int64_t base = c.kv_heads * tiles * (pl.kind == Plan::kPrompt && c.head_dim == 256 ? 2 : 1);
+    const int parts = pl.kind == Plan::kPrompt && c.head_dim == 256 ? 2 : 1;
+    const int64_t base = c.kv_heads * tiles * parts;
     const bool few = pl.kind == Plan::kFew;
     const int64_t unit = few ? kUnit : 64, least = few ? kUnit * kWaves : 256;
     const int64_t most = (keys + least - 1) / least;
-    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? MANYT : PROMPTT;
+    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? 512 : 256;
     int64_t s = base > 0 ? target / base : 1;
     s = s > most ? most : s;
     s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
@@ -1558,10 +1501,12 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, int parts, const A
     if (e != hipSuccess || p.splits == 1) return e;
     if (p.rows_all > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (p.splits <= kFewSplits)
-        hipLaunchKernelGGL((join_few_kernel<D>), dim3((unsigned)((p.rows_all + kWaves - 1) / kWaves)),
-                           dim3(kThreads), 0, stream, p);
+        hipLaunchKernelGGL((join_few_kernel<D>),
+                           dim3((unsigned)((p.rows_all + kWaves - 1) / kWaves)), dim3(kThreads), 0,
+                           stream, p);
     else
-        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)p.rows_all), dim3(kThreads), 0, stream, p);
+        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)p.rows_all), dim3(kThreads), 0, stream,
+                           p);
     return hipGetLastError();
 }
 
@@ -1572,7 +1517,7 @@ hipError_t dispatch(const Args& p, const Plan& pl, hipStream_t stream) {
                          p, stream);
     if constexpr (D <= 128) {
         if (pl.kind == Plan::kMany)
-            return launch<D>(many_rows_kernel<D, 1>, kThreads, ManyRows<D>::kLds, 1, p, stream);
+            return launch<D>(many_rows_kernel<D>, kThreads, ManyRows<D>::kLds, 1, p, stream);
         if (pl.blocks == 2)
             return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, 1, p, stream);
     }
