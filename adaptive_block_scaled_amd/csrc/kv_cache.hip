@@ -18,7 +18,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Where a group (slot, head, group g) lives.  K: a row of D/2 code bytes and
 // D/16 scale bytes per (page, head, offset).  V: the group's 16/(D/16)
@@ -130,9 +131,11 @@ struct ReadArgs {
 };
 
 // blockIdx.z: K or V; x: run of 64 / (D/16) tokens, head fastest.  One wave per
-// workgroup and neighbouring workgroups on neighbouring heads of the same tokens:
-// a context of 32768 tokens (172 MB moved) takes 28.2 us = 6.1 TB/s; four waves
-// and runs of tokens first, as in append, 31.3 us.
+// workgroup and neighbouring workgroups on neighbouring heads of the same tokens,
+// and stores that leave nothing of the output in the caches, which would have to be
+// written back from them before the next call's.  A context of 32768 tokens of 8
+// heads of 128 (172 MB moved), another output every call: 32 us = 5.4 TB/s;
+// ordinary stores 48 us; two or four waves a workgroup 34 to 35 us.
 constexpr int kReadThreads = 64;
 
 template <int D, bool kBf16>
@@ -163,22 +166,19 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadArgs p) {
     decode_word(w.y, e, out + 8);
     const int64_t off = (t * p.kv_heads + head) * D + g * 16;
     if constexpr (kBf16) {
-        uint32_t u[8];
+        bf16x8 b[2];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            bf16x2 b;
-            b[0] = (__bf16)out[2 * i];
-            b[1] = (__bf16)out[2 * i + 1];
-            u[i] = __builtin_bit_cast(uint32_t, b);
-        }
-        uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.y[part]) + off);
-        q[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        q[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        for (int i = 0; i < 16; i++) b[i >> 3][i & 7] = (__bf16)out[i];
+        bf16x8* q = reinterpret_cast<bf16x8*>(reinterpret_cast<uint16_t*>(p.y[part]) + off);
+        __builtin_nontemporal_store(b[0], q);
+        __builtin_nontemporal_store(b[1], q + 1);
     } else {
-        float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.y[part]) + off);
+        f32x4* q = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y[part]) + off);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            q[i] = make_float4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+        for (int i = 0; i < 4; i++) {
+            const f32x4 f = {out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]};
+            __builtin_nontemporal_store(f, q + i);
+        }
     }
 }
 
