@@ -956,18 +956,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
 //     in the same buffer, was last read (as step 2c + 1) in A(2c) of waves 4-7,
 //     phase 4c + 1; K of tile c + 2 is first read in A(2c + 2), phase 4c + 4.
 // Operands and their order are those of many_rows_kernel.
-//
-// At D = 256 one wave's registers do not hold Q, O and the operands in flight:
-// two workgroups take half of O's dims each (kHalves), the words of 8 dims of
-// every V piece that have their number, and both compute the scores.
 constexpr int kPairWaves = 8, kPairThreads = 64 * kPairWaves;
 
 template <int D>
 struct PromptTile {
-    static constexpr int kV = D == 256 ? 128 : D;  // dims of O in one workgroup
-    static constexpr int kHalves = D / kV;
-    static constexpr int kKBytes = 64 * D * 2, kVBytes = 64 * kV * 2;
-    static constexpr int kFlags = kScaleTableBytes + 2 * (kKBytes + kVBytes);
+    static constexpr int kTile = 64 * D * 2;  // bytes of K or V of 64 keys
+    static constexpr int kFlags = kScaleTableBytes + 4 * kTile;
     static constexpr int kLds = kFlags + 2 * kWaves * 4;
 };
 
@@ -978,19 +972,18 @@ template <int D, bool kLate>
 __device__ __forceinline__ void prompt_rows(const Args& p) {
     typedef PromptTile<D> Tile;
     // products of a step: T for the scores, P = 2 B for O
-    constexpr int kRows = 256, T = D / 16, DV = Tile::kV, B = DV / 32, P = 2 * B;
+    constexpr int kRows = 256, T = D / 16, B = D / 32, P = 2 * B;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint2* const tables = reinterpret_cast<uint2*>(smem);
     uint8_t* const k_lds = smem + kScaleTableBytes;
-    uint8_t* const v_lds = k_lds + 2 * Tile::kKBytes;
+    uint8_t* const v_lds = k_lds + 2 * Tile::kTile;
     uint32_t* const flags = reinterpret_cast<uint32_t*>(smem + Tile::kFlags);
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int unit16 = wave & 3;  // which 16 keys of a tile it decodes
     const int bh = blockIdx.x % p.batch_heads;
-    const int part_of_o = blockIdx.x / p.batch_heads % Tile::kHalves;
-    const int rest = blockIdx.x / (p.batch_heads * Tile::kHalves);
+    const int rest = blockIdx.x / p.batch_heads;
     const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
@@ -1029,19 +1022,12 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
         v_lds + unit16 * B * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8;
 
     struct Codes {
-        uint32_t w[kLate ? D / 32 : DV / 32], sc;
+        uint32_t w[D / 32], sc;
     };
     auto load = [&](Codes& c, uint64_t at) KV_INLINE {
-        const uint8_t* src = codes + at * (8 * D) + code_at;
-        if constexpr (kLate || D == DV) {
-            UnitCodes<D>::words(src, c.w);
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; t++)  // one of the two words of each token
-                c.w[t] = *reinterpret_cast<const uint32_t*>(src + 4 * part_of_o + 8 * t);
-        }
-        src = scales + at * D + scale_at;
-        if constexpr (!kLate || D == 256)
+        UnitCodes<D>::words(codes + at * (8 * D) + code_at, c.w);
+        const uint8_t* src = scales + at * D + scale_at;
+        if constexpr (!kLate)
             c.sc = *reinterpret_cast<const uint32_t*>(src);
         else if constexpr (D == 64)
             c.sc = *src;
@@ -1076,37 +1062,37 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 #pragma unroll
             for (int i = 0; i < D / 64; i++) look[i] = k_scale(tables, (now.sc >> (8 * i)) & 0xFFu);
         } else {
-            VPiece<DV>::look_up(tables, now.sc, look);
+            VPiece<D>::look_up(tables, now.sc, look);
             bad = __builtin_amdgcn_ballot_w64(nan_bytes(now.sc) != 0) != 0;
         }
     };
     // Decode of `now` (one 16-token tile), in T + P slices that go between the
     // products of an A phase: the bits first, then operand by operand.
     KGroup kg[D / 64];
-    VPiece<DV> vp;
+    VPiece<D> vp;
     auto decode = [&](int buf, auto slice_c) KV_INLINE {
         constexpr int n = decltype(slice_c)::value;
         if constexpr (n < T) {
             if constexpr (kLate && n % 2 == 1 && n / 2 < D / 64)
                 kg[n / 2].unpack(now.w[n - 1], now.w[n], look[n / 2], four);
-            if constexpr (!kLate && n % 2 == 1 && n / 2 < DV / 64)
+            if constexpr (!kLate && n % 2 == 1 && n / 2 < D / 64)
                 vp.template unpack_words<n / 2>(now.w, look, four);
             if constexpr (!kLate && n == 0)
                 flags[buf * kWaves + unit16] = bad;  // (every lane the same)
         } else if constexpr (!kLate) {
             constexpr int d = n - T;
-            uint8_t* const to = v_to + buf * Tile::kVBytes + (d >> 1) * 1024 + (d & 1) * 256;
+            uint8_t* const to = v_to + buf * Tile::kTile + (d >> 1) * 1024 + (d & 1) * 256;
             *reinterpret_cast<uint2*>(to) =
                 make_uint2(vp.template pair<d, 0>(), vp.template pair<d, 1>());
         } else if constexpr ((n - T) % (P / (D / 32)) == 0) {
             constexpr int i = (n - T) / (P / (D / 32));  // operand of 8 elements
-            uint8_t* const to = k_to + buf * Tile::kKBytes + (i / 2) * 1024 + (i % 2) * 512;
+            uint8_t* const to = k_to + buf * Tile::kTile + (i / 2) * 1024 + (i % 2) * 512;
             *reinterpret_cast<half8*>(to) = kg[i / 2].template operand<i % 2>();
         }
     };
     half8 ka[P];  // K's operands, P ahead
     auto read_k = [&](int buf, int kb, int t) KV_INLINE {
-        return *reinterpret_cast<const half8*>(k_lds + buf * Tile::kKBytes + (kb * T + t) * 1024 +
+        return *reinterpret_cast<const half8*>(k_lds + buf * Tile::kTile + (kb * T + t) * 1024 +
                                                lane * 16);
     };
     uint4 prob[2];
@@ -1126,13 +1112,13 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
         }
     };
     // The products of an A phase: scores of the step whose first P operands of K
-    // are in ka (the others lie at `more`), then V's operands of keys 32 kb .. of a
-    // tile times the probabilities.  Beside each product one operand is asked for,
+    // are in ka, then V's operands of keys 32 kb .. of a tile times the
+    // probabilities.  Beside each product one operand is asked for,
     // P products ahead of its use: the rest of K, V, the first of the next
     // step's K (tile buffer k_buf, half k_half).  The largest score is taken once
     // the scores are there; f(slice) is the work that goes behind each product.
     auto products = [&](int buf, int kb, int k_buf, int k_half, auto&& f) KV_INLINE {
-        const uint8_t* src = v_lds + buf * Tile::kVBytes + 2 * kb * B * 1024 + lane * 16;
+        const uint8_t* src = v_lds + buf * Tile::kTile + 2 * kb * B * 1024 + lane * 16;
         half8 va[P];
         each<T>([&](auto t_c) KV_INLINE {
             constexpr int t = decltype(t_c)::value;
@@ -1277,7 +1263,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     int lane_again = lane;
     asm volatile("" : "+v"(lane_again));
     store_row<D, B>(p, s, head, row0 + 32 * wave + (lane_again & 31), rows, lane_again >> 5, split,
-                    part_of_o, o, m, l, poisoned);
+                    0, o, m, l, poisoned);
 }
 
 template <int D>
@@ -1288,6 +1274,379 @@ __global__ void __launch_bounds__(kPairThreads, D == 64 ? 4 : 2) prompt_kernel(c
         prompt_rows<D, false>(p);
 }
 
+// ---------------------------------------------------------------------------
+// Wide heads (D = 256, more than 16 rows): tiles of 128 rows, 8 waves.
+//
+// Here the registers of one wave do not hold Q, O and the operands in flight, so
+// two waves of a SIMD, w and w + 4, share 32 rows: each has half of O's dims (the
+// words of 8 dims of every V piece that have its number) and computes the
+// scores and probabilities of half of the keys, waves 0-3 those of the even steps
+// of 32, waves 4-7 those of the odd ones.  Probabilities pass through LDS as they
+// are, operands of O's products, and so does the running maximum m, which both
+// use: it is read, raised if need be and written by one wave of the two at a time.
+// Raised are whole powers of two, so that probabilities that are still
+// to be used are scaled exactly.
+//
+// As in prompt_rows one wave issues products (A: 16 of its next scores, 16 of O)
+// while the other does the VALU work of its step (B).  With c = 64-key tile:
+//   phase 2c      waves 0-3: A(c): scores 2c + 2, O += P(2c - 1) V, P(2c) V
+//                 waves 4-7: B(c): P(2c + 1)
+//   phase 2c + 1  waves 0-3: B(c + 1): P(2c + 2)
+//                 waves 4-7: A(c): scores 2c + 3, O += P(2c) V, P(2c + 1) V
+// and waves 0-3 add the last odd step's P V after the loop.
+//   * waves 0-3 decode K of tile c + 2 in A(c), phase 2c.  K of tile c, in the same
+//     buffer, was last read in A(c - 1) of waves 4-7, phase 2c - 1; K of tile c + 2
+//     is first read (its first operands, in a B phase) in phase 2c + 1.
+//   * waves 4-7 decode V of tile c + 1 in A(c), phase 2c + 1.  V of tile c - 1 was
+//     last read in A(c) of waves 0-3, phase 2c; V of tile c + 1 is first read in
+//     phase 2c + 2.  So are the NaN flags of a tile, last read in phase 2c + 1.
+//   * a pair's probabilities and m are written in the B phases, which take turns,
+//     and read by the other wave in its next one, before it writes.
+// (Two workgroups per 256 rows that take half of O's dims each and both compute
+// all scores took 1.5 times the products and twice the softmax.)
+struct WideTile {
+    static constexpr int D = 256, kRows = 128, kTile = 64 * D * 2;
+    static constexpr int kProb = kScaleTableBytes + 4 * kTile;  // [4 pairs][2][64 lanes][16]
+    static constexpr int kMax = kProb + 4 * 2048;               // [4 pairs][32 rows]
+    static constexpr int kFlags = kMax + 4 * 128;
+    static constexpr int kLds = kFlags + 2 * kWaves * 4;
+};
+
+template <bool kLate>
+__device__ __forceinline__ void wide_rows(const Args& p) {
+    typedef WideTile Tile;
+    constexpr int D = Tile::D, kRows = Tile::kRows, T = D / 16, B = 4, P = 8;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    uint2* const tables = reinterpret_cast<uint2*>(smem);
+    uint8_t* const k_lds = smem + kScaleTableBytes;
+    uint8_t* const v_lds = k_lds + 2 * Tile::kTile;
+    uint32_t* const flags = reinterpret_cast<uint32_t*>(smem + Tile::kFlags);
+
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+    // which 32 rows, and which 16 keys of a tile it decodes
+    const int pair = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
+    const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
+    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+
+    const Sequence s = sequence_of(p, b);
+    const int row0 = row_tile * kRows, rows = s.rows * p.group;
+    if (row0 >= rows) return;
+    const uint32_t four = opaque_four(p);
+    const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
+    const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
+    const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, 64);
+    const WholeSteps whole(p, s.len, pos_lo, pos_hi, 32);
+    const int per = units_per_split(p, units.n);
+    const int begin = split * per;
+    const int end = begin + per < units.n ? begin + per : units.n;
+    if (p.splits > 1 && begin >= end) {
+        mark_empty(p, s, head, row0, last_row, split);
+        return;
+    }
+    uint32_t poisoned = 0;  // groups of O that are NaN
+    f32x16 o[B], x;
+#pragma unroll
+    for (int d = 0; d < B; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
+
+    // this lane's codes of the 16 keys that its wave decodes
+    const int kq = lane >> 4, vq = (kq & 1) * 2 + (kq >> 1);
+    const uint32_t code_at = (lane & 15) * (D / 2) + (kLate ? vq : kq) * (D / 8);
+    const uint32_t scale_at = (lane & 15) * (D / 16) + (kLate ? vq : kq) * 4;
+    const uint8_t* const codes = kLate ? p.v_codes : p.k_codes;
+    const uint8_t* const scales = kLate ? p.v_scales : p.k_scales;
+    uint8_t* const to = kLate
+        ? v_lds + pair * 8 * 1024 + ((vq & 1) * 32 + (lane & 15)) * 16 + (vq >> 1) * 8
+        : k_lds + ((pair >> 1) * T + kq * (D / 64)) * 1024 + (16 * (pair & 1) + (lane & 15)) * 16;
+
+    struct Codes {
+        uint32_t w[D / 32], sc;
+    };
+    auto load = [&](Codes& c, uint64_t at) KV_INLINE {
+        UnitCodes<D>::words(codes + at * (8 * D) + code_at, c.w);
+        c.sc = *reinterpret_cast<const uint32_t*>(scales + at * D + scale_at);
+    };
+    auto ref = [&](int i) KV_INLINE {
+        return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + pair);
+    };
+    // the first tiles' codes and q are asked for together
+    Codes now, first[3];
+    if (begin < end) {
+        TileRef r[3];
+#pragma unroll
+        for (int i = 0; i < 3; i++) r[i] = ref(begin + i);
+#pragma unroll
+        for (int i = 0; i < (kLate ? 2 : 3); i++) load(first[i], cache_tile(p, head, r[i]));
+    }
+    fill_scale_tables(tables, tid, kPairThreads);
+    half8 q[T];
+    float factor, m = kLowest, l = 0.0f;
+    int pos;
+    take_q<D>(p, s, head, row0 + 32 * pair + (lane & 31), rows, half, q, factor, pos);
+    now = first[0];
+
+    // The scales of the codes in `now`, looked up one phase before their decode.
+    GroupScale look[4];
+    bool bad = false;  // a NaN among them (V)
+    auto look_up = [&]() KV_INLINE {
+        if constexpr (kLate) {
+            VPiece<D>::look_up(tables, now.sc, look);
+            bad = __builtin_amdgcn_ballot_w64(nan_bytes(now.sc) != 0) != 0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) look[i] = k_scale(tables, (now.sc >> (8 * i)) & 0xFFu);
+        }
+    };
+    // Decode of `now` (one 16-token tile), in 32 slices that go between the
+    // products of an A phase: K group by group; V's bits first, then its operands.
+    // Behind slice kFree its codes are free.
+    constexpr int kFree = kLate ? 8 : 26;
+    KGroup kg;
+    VPiece<D> vp;
+    auto decode = [&](int buf, auto slice_c) KV_INLINE {
+        constexpr int n = decltype(slice_c)::value;
+        if constexpr (!kLate) {
+            constexpr int g = n / 8;
+            uint8_t* const dst = to + buf * Tile::kTile + g * 1024;
+            if constexpr (n % 8 == 1) kg.unpack(now.w[2 * g], now.w[2 * g + 1], look[g], four);
+            if constexpr (n % 8 == 3) *reinterpret_cast<half8*>(dst) = kg.template operand<0>();
+            if constexpr (n % 8 == 6)
+                *reinterpret_cast<half8*>(dst + 512) = kg.template operand<1>();
+        } else if constexpr (n < 8) {
+            if constexpr (n == 0) flags[buf * kWaves + pair] = bad;  // (every lane the same)
+            if constexpr (n % 2 == 1) vp.template unpack_words<n / 2>(now.w, look, four);
+        } else if constexpr (n < 24) {
+            constexpr int d = n - 8;
+            *reinterpret_cast<uint2*>(to + buf * Tile::kTile + (d >> 1) * 1024 + (d & 1) * 256) =
+                make_uint2(vp.template pair<d, 0>(), vp.template pair<d, 1>());
+        }
+    };
+    half8 ring[P];  // operands, P products ahead of their use
+    auto read_k = [&](int buf, int t) KV_INLINE {  // of this wave's step of a tile
+        return *reinterpret_cast<const half8*>(k_lds + buf * Tile::kTile + (kLate * T + t) * 1024 +
+                                               lane * 16);
+    };
+    // of product n of a step's 8, keys 32 kb .. of a tile
+    auto read_v = [&](int buf, int kb, int n) KV_INLINE {
+        return *reinterpret_cast<const half8*>(v_lds + buf * Tile::kTile +
+                                               ((2 * kb + n / B) * 8 + kLate * B + n % B) * 1024 +
+                                               lane * 16);
+    };
+    uint4 prob[2], theirs[2];  // this wave's step and the other one's before it
+#pragma unroll
+    for (int i = 0; i < 2; i++) theirs[i] = make_uint4(0u, 0u, 0u, 0u);
+    uint4* const prob_lds = reinterpret_cast<uint4*>(smem + Tile::kProb) + pair * 128 + lane;
+    float* const max_lds = reinterpret_cast<float*>(smem + Tile::kMax) + pair * 32 + (lane & 31);
+    // Largest score of this lane, in parts that go between products.
+    float part[6], top;
+    auto largest_part = [&](auto part_c) KV_INLINE {
+        constexpr int j = decltype(part_c)::value;
+        if constexpr (j < 3) {
+#pragma unroll
+            for (int i = 2 * j; i < 2 * j + 2 && i < 5; i++)
+                part[i] = __builtin_fmaxf(__builtin_fmaxf(x[3 * i], x[3 * i + 1]), x[3 * i + 2]);
+        } else if constexpr (j == 3) {
+            part[5] = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), x[15]);
+            part[2] = __builtin_fmaxf(__builtin_fmaxf(part[2], part[3]), part[4]);
+        } else {
+            top = __builtin_fmaxf(part[2], part[5]) * factor;
+        }
+    };
+    // Product n of the 8 of one step's O, with the operand in the ring.
+    auto add = [&](const uint4 (&w)[2], auto n_c) KV_INLINE {
+        constexpr int n = decltype(n_c)::value;
+        o[n % B] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            ring[n], __builtin_bit_cast(half8, w[n / B]), o[n % B], 0, 0, 0);
+    };
+    // A: the first P operands of K are in the ring; V's of the other wave's step
+    // lie in tile buffer `before`, this wave's in `buf`.
+    auto products = [&](int buf, int before, auto&& f) KV_INLINE {
+        each<T>([&](auto t_c) KV_INLINE {
+            constexpr int t = decltype(t_c)::value;
+            if constexpr (t == 0) {
+                f32x16 zero;
+#pragma unroll
+                for (int i = 0; i < 16; i++) zero[i] = 0.0f;
+                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[0], q[0], zero, 0, 0, 0);
+            } else {
+                x = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[t % P], q[t], x, 0, 0, 0);
+            }
+            if constexpr (t < T - P)
+                ring[t] = read_k(buf ^ 1, t + P);
+            else
+                ring[t - (T - P)] = read_v(before, 1 - kLate, t - (T - P));
+            f(t_c);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        each<P>([&](auto n_c) KV_INLINE {
+            constexpr int n = decltype(n_c)::value;
+            add(theirs, n_c);
+            ring[n] = read_v(buf, kLate, n);
+            f(std::integral_constant<int, T + n>{});
+            if constexpr (n >= 3) largest_part(std::integral_constant<int, n - 3>{});
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        each<P>([&](auto n_c) KV_INLINE {
+            constexpr int n = decltype(n_c)::value;
+            add(prob, n_c);
+            f(std::integral_constant<int, T + P + n>{});
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // NaN values of V (decoded as zeros) of a 64-key tile: the groups that turn
+    // NaN in the rows that see them
+    auto poison = [&](int u) KV_INLINE {
+#pragma unroll 1
+        for (int j = 0; j < 4 * T; j++) {  // 16-token tile j / T, group j % T (T = D / 16)
+            const uint64_t at = cache_tile(p, head, tile_ref(p, s, 4 * u + j / T));
+            const uint8_t* src = p.v_scales + at * D + (j % T) * 16;
+#pragma unroll 1
+            for (int t = 0; t < 16; t++) {
+                const int key = 64 * u + 16 * (j / T) + t;
+                const bool hit = (src[t] & 0x7F) == 0x7F && sees(p, s.len, pos, key);
+                poisoned |= (uint32_t)hit << (j % T);
+            }
+        }
+    };
+    // B: the probabilities of the step of 32 keys from key0 on, whose scores are
+    // in x.  k_buf: tile buffer of the next scores' K; u: a tile whose V's NaN flags
+    // are in v_buf, and not looked at before (tile 0 comes first: `any`).
+    auto softmax = [&](int key0, int k_buf, bool any, int v_buf, int u) KV_INLINE {
+        float shared = m;
+        uint32_t nan_tile = 0;
+        if (any) {
+            shared = *max_lds;
+            theirs[0] = prob_lds[0];
+            theirs[1] = prob_lds[64];
+            const uint4 f = *reinterpret_cast<const uint4*>(flags + v_buf * kWaves);
+            nan_tile = (f.x | f.y) | (f.z | f.w);
+        }
+#pragma unroll
+        for (int n = 0; n < P; n++) ring[n] = read_k(k_buf, n);
+        // What few steps need, behind one branch: keys that some row does not see
+        // are hidden, m is raised where a score exceeds it by more than the slack,
+        // or follows the other wave's, and NaN values of V are noted.
+        const bool all = whole(key0);
+        if (!all | (__builtin_amdgcn_ballot_w64((top > shared + kSlack) | (shared != m) |
+                                                (nan_tile != 0)) != 0)) {
+            if (__builtin_amdgcn_readfirstlane(nan_tile) != 0) poison(u);
+            if (!all) {
+                hide(p, s.len, pos, key0 + 4 * half, x);
+                each<5>(largest_part);
+            }
+            float next = shared;
+            if (__builtin_amdgcn_ballot_w64(top > shared + kSlack) != 0) {
+                const float raised = __builtin_fmaxf(top, shared);
+                const float both = __builtin_fmaxf(raised, __shfl_xor(raised, 32));
+                // (from the lowest m or to an infinite one there is nothing to keep)
+                const float by = __builtin_ceilf(both - shared);
+                next = by < 65536.0f ? shared + by : both;
+                const float alpha = __builtin_amdgcn_exp2f(-by);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    uint32_t w[4] = {theirs[i].x, theirs[i].y, theirs[i].z, theirs[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const half2v h = __builtin_bit_cast(half2v, w[j]);
+                        w[j] = pack_half((float)h[0] * alpha, (float)h[1] * alpha);
+                    }
+                    theirs[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            const float alpha = __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < B; d++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) o[d][i] *= alpha;
+        }
+        probabilities(x, factor, m, l, prob);
+        prob_lds[0] = prob[0];
+        prob_lds[64] = prob[1];
+        *max_lds = m;
+    };
+    __syncthreads();
+    if (begin < end) {
+        const auto decode_tile = [&](int buf) KV_INLINE {
+            look_up();
+            each<32>([&](auto n) KV_INLINE { decode(buf, n); });
+        };
+        decode_tile(0);
+        now = first[1];
+        if constexpr (!kLate) {
+            decode_tile(1);
+            now = first[2];
+        }
+        constexpr int ahead = kLate ? 2 : 3;  // the tile whose codes are loaded next
+        TileRef next = ref(begin + ahead);
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < 16; i++) x[i] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; t++)
+            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(read_k(0, t), q[t], x, 0, 0, 0);
+        each<5>(largest_part);
+        if constexpr (!kLate) {  // B(0)
+            softmax(64 * units(begin), 1, false, 0, 0);
+            look_up();
+        }
+        lds_barrier();
+#pragma unroll 1
+        for (int i = begin; i < end; i++) {
+            const int buf = (i - begin) & 1, u = units(i);
+            if constexpr (kLate) {  // B(c)
+                softmax(64 * u + 32, buf ^ 1, true, buf, u);
+                look_up();
+                lds_barrier();
+            }
+            // A(c); the first one has no step before it, and adds zeros
+            const uint32_t at = cache_tile(p, head, next);
+            next = ref(i + 1 + ahead);
+            __builtin_amdgcn_s_setprio(1);
+            products(buf, kLate || i == begin ? buf : buf ^ 1, [&](auto n) KV_INLINE {
+                decode(kLate ? buf ^ 1 : buf, n);
+                if constexpr (decltype(n)::value == kFree) load(now, at);
+            });
+            __builtin_amdgcn_s_setprio(0);
+            lds_barrier();
+            if constexpr (!kLate) {  // B(c + 1)
+                softmax(i + 1 < end ? 64 * units(i + 1) : kHidden, buf, true, buf, u);
+                look_up();
+                lds_barrier();
+            }
+        }
+        if constexpr (!kLate) {
+            const int buf = (end - 1 - begin) & 1;
+#pragma unroll
+            for (int n = 0; n < P; n++) ring[n] = read_v(buf, 1, n);
+            each<P>([&](auto n) KV_INLINE { add(theirs, n); });
+        }
+        // both waves' sums
+        float* const sums = reinterpret_cast<float*>(smem + Tile::kProb) + pair * 512 + lane;
+        sums[64 * kLate] = l;
+        lds_barrier();
+        l += sums[64 * !kLate];
+    }
+
+    // (the row's place from a lane number that the compiler takes for another one:
+    // kept across the loop it would cost registers)
+    int lane_again = lane;
+    asm volatile("" : "+v"(lane_again));
+    store_row<D, B>(p, s, head, row0 + 32 * pair + (lane_again & 31), rows, lane_again >> 5, split,
+                    kLate, o, m, l, poisoned);
+}
+
+__global__ void __launch_bounds__(kPairThreads, 2) wide_kernel(const Args p) {
+    if (threadIdx.x >= kPairThreads / 2)
+        wide_rows<true>(p);
+    else
+        wide_rows<false>(p);
+}
+
+// ---------------------------------------------------------------------------
 // Joins the splits of one row per workgroup.  All waves read every split's m
 // and l at once, lane = split mod 64; then D/4 lanes read one split's
 // O as 16 bytes each, the workgroup 1024 / D splits side by side, so that the
@@ -1429,7 +1788,7 @@ __global__ void __launch_bounds__(kThreads) join_few_kernel(const Args p) {
 // ---------------------------------------------------------------------------
 // Host side: which kernel, how many splits.
 struct Plan {
-    enum Kind { kFew, kMany, kPrompt } kind;
+    enum Kind { kFew, kMany, kPrompt, kWide } kind;
     int blocks;  // row blocks of 16 of a tile (few rows)
     int row_tiles;
     int splits, split_units;
@@ -1443,13 +1802,14 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     // 64 heads: 21 us against 28; 64 rows of 16 heads over 16k keys: 40 against
     // 54; 128 rows: 38 against 52).
     const int64_t group = a.heads / c.kv_heads, rows = a.max_q * group;
-    pl.kind = rows <= 32 ? Plan::kFew
-              : rows > 128 || c.head_dim == 256 ? Plan::kPrompt
-                                                : Plan::kMany;
+    pl.kind = rows <= 32             ? Plan::kFew
+              : c.head_dim == 256 ? Plan::kWide
+              : rows > 128        ? Plan::kPrompt
+                                  : Plan::kMany;
     pl.blocks = rows <= 16 || c.head_dim == 256 ? 1 : 2;
     const int tile = pl.kind == Plan::kFew    ? 16 * pl.blocks
-                     : pl.kind == Plan::kMany ? 128
-                                              : 256;
+                     : pl.kind == Plan::kPrompt ? 256
+                                                : 128;
     pl.row_tiles = (int)((rows + tile - 1) / tile);
     // Splits of the keys.  Few rows: 256 CUs hold 1024 workgroups (D = 128), and
     // 3072 leave a short last round where lengths differ (64 sequences of 3-12k
@@ -1465,8 +1825,7 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     // row tiles that hold rows: at most one per sequence is not full
     int64_t tiles = a.total_q * group / tile + a.batch;
     tiles = tiles < a.batch * pl.row_tiles ? tiles : a.batch * pl.row_tiles;
-    const int parts = pl.kind == Plan::kPrompt && c.head_dim == 256 ? 2 : 1;
-    const int64_t base = c.kv_heads * tiles * parts;
+    const int64_t base = c.kv_heads * tiles;
     const bool few = pl.kind == Plan::kFew;
     const int64_t unit = few ? kUnit : 64, least = few ? kUnit * kWaves : 256;
     const int64_t most = (keys + least - 1) / least;
@@ -1487,14 +1846,13 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
 }
 
 template <int D>
-hipError_t launch(void (*kernel)(Args), int threads, int lds, int parts, const Args& p,
-                  hipStream_t stream) {
+hipError_t launch(void (*kernel)(Args), int threads, int lds, const Args& p, hipStream_t stream) {
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kernel,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    const int64_t grid = (int64_t)p.batch_heads * p.row_tiles * p.splits * parts;
+    const int64_t grid = (int64_t)p.batch_heads * p.row_tiles * p.splits;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, stream, p);
     hipError_t e = hipGetLastError();
@@ -1512,16 +1870,17 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, int parts, const A
 
 template <int D>
 hipError_t dispatch(const Args& p, const Plan& pl, hipStream_t stream) {
-    if (pl.kind == Plan::kPrompt)
-        return launch<D>(prompt_kernel<D>, kPairThreads, PromptTile<D>::kLds, PromptTile<D>::kHalves,
-                         p, stream);
     if constexpr (D <= 128) {
+        if (pl.kind == Plan::kPrompt)
+            return launch<D>(prompt_kernel<D>, kPairThreads, PromptTile<D>::kLds, p, stream);
         if (pl.kind == Plan::kMany)
-            return launch<D>(many_rows_kernel<D>, kThreads, ManyRows<D>::kLds, 1, p, stream);
+            return launch<D>(many_rows_kernel<D>, kThreads, ManyRows<D>::kLds, p, stream);
         if (pl.blocks == 2)
-            return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, 1, p, stream);
+            return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, p, stream);
+    } else if (pl.kind == Plan::kWide) {
+        return launch<D>(wide_kernel, kPairThreads, WideTile::kLds, p, stream);
     }
-    return launch<D>(few_rows_kernel<D, 1>, kThreads, FewRows<D, 1>::kLds, 1, p, stream);
+    return launch<D>(few_rows_kernel<D, 1>, kThreads, FewRows<D, 1>::kLds, p, stream);
 }
 
 int clamp_int(int64_t v) { return (int)(v > 0x3FFFFFFF ? 0x3FFFFFFF : v); }
