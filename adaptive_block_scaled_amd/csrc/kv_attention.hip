@@ -1069,14 +1069,15 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     // Decode of `now` (one 16-token tile), in T + P slices that go between the
     // products of an A phase: the bits first, then operand by operand.
     KGroup kg[D / 64];
+    uint4 operand;
     VPiece<D> vp;
     auto decode = [&](int buf, auto slice_c) KV_INLINE {
         constexpr int n = decltype(slice_c)::value;
         if constexpr (n < T) {
-            if constexpr (kLate && n % 2 == 1 && n / 2 < D / 64)
-                kg[n / 2].unpack(now.w[n - 1], now.w[n], look[n / 2], four);
-            if constexpr (!kLate && n % 2 == 1 && n / 2 < D / 64)
-                vp.template unpack_words<n / 2>(now.w, look, four);
+            constexpr int g = n / 4, k = n % 4;
+            if constexpr (kLate && k < 3)
+                kg[g].template unpack_stage<k>(now.w[2 * g], now.w[2 * g + 1], look[g], four);
+            if constexpr (!kLate && k < 3) vp.template unpack_stage<g, k>(now.w, look, four);
             if constexpr (!kLate && n == 0)
                 flags[buf * kWaves + unit16] = bad;  // (every lane the same)
         } else if constexpr (!kLate) {
@@ -1084,10 +1085,17 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
             uint8_t* const to = v_to + buf * Tile::kTile + (d >> 1) * 1024 + (d & 1) * 256;
             *reinterpret_cast<uint2*>(to) =
                 make_uint2(vp.template pair<d, 0>(), vp.template pair<d, 1>());
-        } else if constexpr ((n - T) % (P / (D / 32)) == 0) {
-            constexpr int i = (n - T) / (P / (D / 32));  // operand of 8 elements
-            uint8_t* const to = k_to + buf * Tile::kTile + (i / 2) * 1024 + (i % 2) * 512;
-            *reinterpret_cast<half8*>(to) = kg[i / 2].template operand<i % 2>();
+        } else {
+            constexpr int i = (n - T) / 2;  // operand of 8 elements, in two halves
+            if constexpr ((n - T) % 2 == 0) {
+                operand.x = kg[i / 2].template pair<i % 2, 0>();
+                operand.y = kg[i / 2].template pair<i % 2, 1>();
+            } else {
+                operand.z = kg[i / 2].template pair<i % 2, 2>();
+                operand.w = kg[i / 2].template pair<i % 2, 3>();
+                *reinterpret_cast<uint4*>(k_to + buf * Tile::kTile + (i / 2) * 1024 +
+                                          (i % 2) * 512) = operand;
+            }
         }
     };
     half8 ka[P];  // K's operands, P ahead
@@ -1205,7 +1213,9 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
             decode_tile(1);
             now = first[2];
         }
-        constexpr int ahead = kLate ? 3 : 2;  // the tile whose codes are loaded next
+        // the tile whose codes are loaded next.  (Its page is asked for in a B phase:
+        // a scalar load in flight turns every wait for LDS into one for all of it.)
+        constexpr int ahead = kLate ? 3 : 2;
         TileRef next = ref(begin + ahead);
         lds_barrier();
 #pragma unroll
@@ -1224,7 +1234,6 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
         for (int i = begin; i < end; i++) {
             const int buf = (i - begin) & 1, u = units(i);
             const uint32_t at = cache_tile(p, head, next);
-            next = ref(i + 1 + ahead);
             // A(2c), B(2c)
             uint4 f;
             uint32_t nan_tile;
@@ -1239,6 +1248,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
             __builtin_amdgcn_s_setprio(0);
             lds_barrier();
             settle(64 * u + 32, nan_tile, u);
+            next = ref(i + 1 + ahead);
             probabilities(x, factor, m, l, prob);
             if constexpr (kLate) look_up();
             lds_barrier();
@@ -1402,23 +1412,31 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     // Decode of `now` (one 16-token tile), in 32 slices that go between the
     // products of an A phase: K group by group; V's bits first, then its operands.
     // Behind slice kFree its codes are free.
-    constexpr int kFree = kLate ? 8 : 26;
+    constexpr int kFree = kLate ? 12 : 26;
     KGroup kg;
+    uint4 operand;
     VPiece<D> vp;
     auto decode = [&](int buf, auto slice_c) KV_INLINE {
         constexpr int n = decltype(slice_c)::value;
         if constexpr (!kLate) {
-            constexpr int g = n / 8;
+            constexpr int g = n / 8, k = n % 8;
             uint8_t* const dst = to + buf * Tile::kTile + g * 1024;
-            if constexpr (n % 8 == 1) kg.unpack(now.w[2 * g], now.w[2 * g + 1], look[g], four);
-            if constexpr (n % 8 == 3) *reinterpret_cast<half8*>(dst) = kg.template operand<0>();
-            if constexpr (n % 8 == 6)
-                *reinterpret_cast<half8*>(dst + 512) = kg.template operand<1>();
-        } else if constexpr (n < 8) {
+            if constexpr (k < 3)
+                kg.template unpack_stage<k>(now.w[2 * g], now.w[2 * g + 1], look[g], four);
+            if constexpr (k == 3 || k == 5) {
+                operand.x = kg.template pair<(k - 3) / 2, 0>();
+                operand.y = kg.template pair<(k - 3) / 2, 1>();
+            }
+            if constexpr (k == 4 || k == 6) {
+                operand.z = kg.template pair<(k - 4) / 2, 2>();
+                operand.w = kg.template pair<(k - 4) / 2, 3>();
+                *reinterpret_cast<uint4*>(dst + (k - 4) / 2 * 512) = operand;
+            }
+        } else if constexpr (n < 12) {
             if constexpr (n == 0) flags[buf * kWaves + pair] = bad;  // (every lane the same)
-            if constexpr (n % 2 == 1) vp.template unpack_words<n / 2>(now.w, look, four);
-        } else if constexpr (n < 24) {
-            constexpr int d = n - 8;
+            vp.template unpack_stage<n / 3, n % 3>(now.w, look, four);
+        } else if constexpr (n < 28) {
+            constexpr int d = n - 12;
             *reinterpret_cast<uint2*>(to + buf * Tile::kTile + (d >> 1) * 1024 + (d & 1) * 256) =
                 make_uint2(vp.template pair<d, 0>(), vp.template pair<d, 1>());
         }
@@ -1512,16 +1530,17 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     };
     // B: the probabilities of the step of 32 keys from key0 on, whose scores are
     // in x.  k_buf: tile buffer of the next scores' K; u: a tile whose V's NaN flags
-    // are in v_buf, and not looked at before (tile 0 comes first: `any`).
-    auto softmax = [&](int key0, int k_buf, bool any, int v_buf, int u) KV_INLINE {
+    // are in v_buf, and not looked at before (tile 0 comes first: `any`); f is called
+    // where LDS has answered.
+    auto softmax = [&](int key0, int k_buf, bool any, int v_buf, int u, auto&& f) KV_INLINE {
         float shared = m;
         uint32_t nan_tile = 0;
         if (any) {
             shared = *max_lds;
             theirs[0] = prob_lds[0];
             theirs[1] = prob_lds[64];
-            const uint4 f = *reinterpret_cast<const uint4*>(flags + v_buf * kWaves);
-            nan_tile = (f.x | f.y) | (f.z | f.w);
+            const uint4 nan = *reinterpret_cast<const uint4*>(flags + v_buf * kWaves);
+            nan_tile = (nan.x | nan.y) | (nan.z | nan.w);
         }
 #pragma unroll
         for (int n = 0; n < P; n++) ring[n] = read_k(k_buf, n);
@@ -1563,6 +1582,7 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
 #pragma unroll
                 for (int i = 0; i < 16; i++) o[d][i] *= alpha;
         }
+        f();
         probabilities(x, factor, m, l, prob);
         prob_lds[0] = prob[0];
         prob_lds[64] = prob[1];
@@ -1580,8 +1600,10 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
             decode_tile(1);
             now = first[2];
         }
-        constexpr int ahead = kLate ? 2 : 3;  // the tile whose codes are loaded next
-        TileRef next = ref(begin + ahead);
+        // the tile whose codes are loaded next.  (Its page is asked for in a B phase
+        // behind LDS's last answer: a scalar load in flight turns every wait for LDS
+        // into one for all of it.)
+        TileRef next = ref(begin + 3);
         lds_barrier();
 #pragma unroll
         for (int i = 0; i < 16; i++) x[i] = 0.0f;
@@ -1590,7 +1612,7 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
             x = __builtin_amdgcn_mfma_f32_32x32x16_f16(read_k(0, t), q[t], x, 0, 0, 0);
         each<5>(largest_part);
         if constexpr (!kLate) {  // B(0)
-            softmax(64 * units(begin), 1, false, 0, 0);
+            softmax(64 * units(begin), 1, false, 0, 0, [] {});
             look_up();
         }
         lds_barrier();
@@ -1598,13 +1620,12 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
         for (int i = begin; i < end; i++) {
             const int buf = (i - begin) & 1, u = units(i);
             if constexpr (kLate) {  // B(c)
-                softmax(64 * u + 32, buf ^ 1, true, buf, u);
+                softmax(64 * u + 32, buf ^ 1, true, buf, u, [&]() KV_INLINE { next = ref(i + 2); });
                 look_up();
                 lds_barrier();
             }
             // A(c); the first one has no step before it, and adds zeros
             const uint32_t at = cache_tile(p, head, next);
-            next = ref(i + 1 + ahead);
             __builtin_amdgcn_s_setprio(1);
             products(buf, kLate || i == begin ? buf : buf ^ 1, [&](auto n) KV_INLINE {
                 decode(kLate ? buf ^ 1 : buf, n);
@@ -1613,7 +1634,8 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
             __builtin_amdgcn_s_setprio(0);
             lds_barrier();
             if constexpr (!kLate) {  // B(c + 1)
-                softmax(i + 1 < end ? 64 * units(i + 1) : kHidden, buf, true, buf, u);
+                softmax(i + 1 < end ? 64 * units(i + 1) : kHidden, buf, true, buf, u,
+                        [&]() KV_INLINE { next = ref(i + 4); });
                 look_up();
                 lds_barrier();
             }

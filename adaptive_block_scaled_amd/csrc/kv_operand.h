@@ -39,7 +39,7 @@ struct GroupScale {
 // in place of about eight VALU instructions.  A NaN scale byte gives a NaN
 // multiplier in K's table -- the key's scores are NaN and reach the rows that
 // see it -- and zero in V's, where a product with a hidden key's zero
-// probability would turn NaN; V's NaN are put in afterwards (poison_rows).
+// probability would turn NaN; V's NaN are put in afterwards (the kernels' `poison`).
 constexpr int kScaleTableBytes = 2 * 256 * 8;
 
 __device__ __forceinline__ void fill_scale_tables(uint2* tables, int tid, int threads) {
@@ -63,24 +63,31 @@ __device__ __forceinline__ GroupScale v_scale(const uint2* tables, uint32_t byte
     return {v.x, v.y};
 }
 
-constexpr uint32_t kLoNibbles = 0x0F0F0F0Fu;
+constexpr uint32_t kLoNibbles = 0x0F0F0F0Fu, kMagnitudes = 0x77777777u;
 
 // fp16 high bytes of the even (he) and odd (ho) elements of two words of 8
-// nibbles, whose magnitudes `shifted` already holds at their places.  The
-// shifts by 4 are 64-bit ones, single instructions on gfx950: what they carry
-// from word to word lands in masked-off bits.  `four` is 4, kept opaque
-// (a constant amount is split into 32-bit shifts).
-__device__ __forceinline__ void high_bytes(const uint32_t (&w)[2], const uint32_t (&masked)[2],
-                                           uint64_t shifted, uint32_t four, uint32_t (&he)[2],
-                                           uint32_t (&ho)[2]) {
-    const uint32_t g0 = w[0] ^ masked[0], g1 = w[1] ^ masked[1];  // bits 3 and 7 of each byte
-    const uint64_t low = shifted >> four;
-    const uint64_t up = ((uint64_t)g1 << 32 | g0) << four;
-    he[0] = bit_select((uint32_t)shifted, (uint32_t)up, kLoNibbles);
-    he[1] = bit_select((uint32_t)(shifted >> 32), (uint32_t)(up >> 32), kLoNibbles);
-    ho[0] = bit_select((uint32_t)low, g0, kLoNibbles);
-    ho[1] = bit_select((uint32_t)(low >> 32), g1, kLoNibbles);
-}
+// nibbles, in three stages of four or five instructions each, so that a caller
+// can put other work between them.  The shifts by 4 are 64-bit ones, single
+// instructions on gfx950: what they carry from word to word lands in masked-off
+// bits.  `four` is 4, kept opaque (a constant amount is split into 32-bit shifts).
+struct HighBytes {
+    uint64_t shifted, low, up;  // magnitudes at their places, down by 4; signs up by 4
+    uint32_t g[2];              // bits 3 and 7 of each byte
+    // (stage 0 makes `shifted` out of w & kMagnitudes, by scale)
+    __device__ __forceinline__ void spread(const uint32_t (&w)[2], uint32_t four) {
+        g[0] = w[0] & ~kMagnitudes;
+        g[1] = w[1] & ~kMagnitudes;
+        low = shifted >> four;
+        up = ((uint64_t)g[1] << 32 | g[0]) << four;
+    }
+    __device__ __forceinline__ void merge(uint32_t& he0, uint32_t& he1, uint32_t& ho0,
+                                          uint32_t& ho1) const {
+        he0 = bit_select((uint32_t)shifted, (uint32_t)up, kLoNibbles);
+        he1 = bit_select((uint32_t)(shifted >> 32), (uint32_t)(up >> 32), kLoNibbles);
+        ho0 = bit_select((uint32_t)low, g[0], kLoNibbles);
+        ho1 = bit_select((uint32_t)(low >> 32), g[1], kLoNibbles);
+    }
+};
 
 // byte i of lo and byte j of hi as the high bytes of a pair of fp16 numbers
 template <int i, int j>
@@ -92,17 +99,35 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t hi, uint32_t lo) {
 // as an operand of 8 consecutive elements.
 struct KGroup {
     uint32_t he[2], ho[2], sig;
+    HighBytes bytes;
+    template <int stage>
+    __device__ __forceinline__ void unpack_stage(uint32_t w0, uint32_t w1, GroupScale s,
+                                                 uint32_t four) {
+        if constexpr (stage == 0) {
+            const uint64_t m = (uint64_t)(w1 & kMagnitudes) << 32 | (w0 & kMagnitudes);
+            bytes.shifted = m << (s.sh2 & 63u);
+        } else if constexpr (stage == 1) {
+            const uint32_t w[2] = {w0, w1};
+            bytes.spread(w, four);
+        } else {
+            bytes.merge(he[0], he[1], ho[0], ho[1]);
+            sig = s.sig2;
+        }
+    }
     __device__ __forceinline__ void unpack(uint32_t w0, uint32_t w1, GroupScale s, uint32_t four) {
-        const uint32_t w[2] = {w0, w1}, m[2] = {w0 & 0x77777777u, w1 & 0x77777777u};
-        high_bytes(w, m, ((uint64_t)m[1] << 32 | m[0]) << (s.sh2 & 63u), four, he, ho);
-        sig = s.sig2;
+        unpack_stage<0>(w0, w1, s, four);
+        unpack_stage<1>(w0, w1, s, four);
+        unpack_stage<2>(w0, w1, s, four);
+    }
+    // elements 8 i + 2 j and 8 i + 2 j + 1
+    template <int i, int j>
+    __device__ __forceinline__ uint32_t pair() const {
+        return pk_mul(pair_of<j, j>(ho[i], he[i]), sig);
     }
     template <int i>
     __device__ __forceinline__ half8 operand() const {
-        return __builtin_bit_cast(half8, make_uint4(pk_mul(pair_of<0, 0>(ho[i], he[i]), sig),
-                                                    pk_mul(pair_of<1, 1>(ho[i], he[i]), sig),
-                                                    pk_mul(pair_of<2, 2>(ho[i], he[i]), sig),
-                                                    pk_mul(pair_of<3, 3>(ho[i], he[i]), sig)));
+        return __builtin_bit_cast(half8,
+                                  make_uint4(pair<i, 0>(), pair<i, 1>(), pair<i, 2>(), pair<i, 3>()));
     }
 };
 
@@ -116,6 +141,7 @@ struct VPiece {
     static constexpr int kWords = D / 32;   // even and odd bytes, one word each
     uint32_t he[kWords], ho[kWords];
     uint32_t sig[2];                        // tokens 0 and 1, tokens 2 and 3
+    HighBytes bytes;
 
     // The four tokens' scales, from their four scale bytes.
     __device__ static __forceinline__ void look_up(const uint2* tables, uint32_t scales,
@@ -140,14 +166,21 @@ struct VPiece {
     template <int i>
     __device__ __forceinline__ void unpack_words(const uint32_t (&w)[D / 32],
                                                  const GroupScale (&s)[4], uint32_t four) {
-        if constexpr (i == 0) {
+        unpack_stage<i, 0>(w, s, four);
+        unpack_stage<i, 1>(w, s, four);
+        unpack_stage<i, 2>(w, s, four);
+    }
+    template <int i, int stage>
+    __device__ __forceinline__ void unpack_stage(const uint32_t (&w)[D / 32],
+                                                 const GroupScale (&s)[4], uint32_t four) {
+        const uint32_t x[2] = {w[2 * i], w[2 * i + 1]};
+        if constexpr (stage == 0) {
+            if constexpr (i == 0) {
 #pragma unroll
-            for (int p = 0; p < 2; p++)
-                sig[p] = bit_select(s[2 * p].sig2, s[2 * p + 1].sig2, 0xFFFFu);
-        }
-        {
-            const uint32_t x[2] = {w[2 * i], w[2 * i + 1]};
-            const uint32_t m[2] = {x[0] & 0x77777777u, x[1] & 0x77777777u};
+                for (int p = 0; p < 2; p++)
+                    sig[p] = bit_select(s[2 * p].sig2, s[2 * p + 1].sig2, 0xFFFFu);
+            }
+            const uint32_t m[2] = {x[0] & kMagnitudes, x[1] & kMagnitudes};
             uint32_t sh[2];
             if constexpr (D == 64) {
                 // a word holds two tokens' 4 nibbles: 16-bit shifts
@@ -163,12 +196,11 @@ struct VPiece {
                 sh[0] = m[0] << (s[2 * i / per].sh2 & 31u);
                 sh[1] = m[1] << (s[(2 * i + 1) / per].sh2 & 31u);
             }
-            uint32_t e[2], o[2];
-            high_bytes(x, m, (uint64_t)sh[1] << 32 | sh[0], four, e, o);
-            he[2 * i] = e[0];
-            he[2 * i + 1] = e[1];
-            ho[2 * i] = o[0];
-            ho[2 * i + 1] = o[1];
+            bytes.shifted = (uint64_t)sh[1] << 32 | sh[0];
+        } else if constexpr (stage == 1) {
+            bytes.spread(x, four);
+        } else {
+            bytes.merge(he[2 * i], he[2 * i + 1], ho[2 * i], ho[2 * i + 1]);
         }
     }
     // dim d of tokens 2p and 2p + 1
