@@ -204,19 +204,6 @@ __device__ __forceinline__ float score_factor(const Args& p, int e) {
     return __builtin_fminf(__builtin_fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
 }
 
-// Exponent that brings a row whose largest magnitude is a into [1, 2).
-__device__ __forceinline__ int row_exponent(float a) {
-    const int e = (int)(__float_as_uint(a) >> 23) - 127;
-    return a == 0.0f ? 0 : e;
-}
-
-// q in fp16, divided by 2^e (exact down to 2^-24 of the row's largest); a row
-// with an infinity or NaN has NaN scores, whatever the keys.
-__device__ __forceinline__ float q_value(float x, int e) {
-    return __builtin_fabsf(x) <= 3.40282347e38f ? __builtin_ldexpf(x, -e)
-                                                : __uint_as_float(0x7FC00000u);
-}
-
 // Token, row of q and query head of tile row r (the last row's past the end).
 struct RowPlace {
     int token;
@@ -249,26 +236,41 @@ __device__ __forceinline__ void hide(const Args& p, int len, int pos, int first,
     }
 }
 
-// Largest magnitude of 8 bf16 values, and their operand.
-__device__ __forceinline__ float largest(const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float a = 0.0f;
+// q in fp16, divided by the power of two that brings a row's largest magnitude
+// into [1, 2): exact down to 2^-24 of it.  A row with an infinity or NaN becomes
+// NaN as a whole, and so do its scores, whatever the keys.  The largest
+// magnitude is found on the bits of the bf16 values, two at a time.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+struct RowMagnitude {
+    u16x2 top = {0, 0};
+    __device__ __forceinline__ void take(const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        a = __builtin_fmaxf(a, __uint_as_float((w[j] << 16) & 0x7FFFFFFFu));
-        a = __builtin_fmaxf(a, __uint_as_float(w[j] & 0x7FFF0000u));
+        for (int j = 0; j < 4; j++)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7FFF7FFFu));
     }
-    return a;
-}
-__device__ __forceinline__ half8 q_operand(const uint4& v, int e) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t h[4];
+    // largest bits of this lane
+    __device__ __forceinline__ int bits() const { return top[0] > top[1] ? top[0] : top[1]; }
+};
+// of a row whose largest magnitude has these bits
+struct RowScale {
+    int e;
+    float by;
+    __device__ __forceinline__ RowScale(int bits) {
+        e = bits == 0 ? 0 : (bits >> 7) - 127;
+        by = bits < 0x7F80 ? __builtin_ldexpf(1.0f, -e) : __uint_as_float(0x7FC00000u);
+    }
+    __device__ __forceinline__ half8 operand(const uint4& v) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t h[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-        h[j] = pack_half(q_value(__uint_as_float(w[j] << 16), e),
-                         q_value(__uint_as_float(w[j] & 0xFFFF0000u), e));
-    return __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
-}
+        for (int j = 0; j < 4; j++)
+            h[j] = pack_half(__uint_as_float(w[j] << 16) * by,
+                             __uint_as_float(w[j] & 0xFFFF0000u) * by);
+        return __builtin_bit_cast(half8, make_uint4(h[0], h[1], h[2], h[3]));
+    }
+};
+__device__ __forceinline__ int larger(int a, int b) { return a > b ? a : b; }
 
 // ---------------------------------------------------------------------------
 // Few rows (a decode step, short chunks): tiles of 16 * kBlocks rows.
@@ -387,18 +389,18 @@ few_rows_kernel(const Args p) {
         const uint16_t* src = p.q + (s.first_row + t) * p.q_st +
                               (int64_t)(head * p.group + g) * p.q_sh + (lane >> 4) * (D / 4);
         uint4 raw[D / 32];
-        float a = 0.0f;
+        RowMagnitude a;
 #pragma unroll
         for (int i = 0; i < D / 32; i++) {
             raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-            a = __builtin_fmaxf(a, largest(raw[i]));
+            a.take(raw[i]);
         }
-        a = __builtin_fmaxf(a, __shfl_xor(a, 16));
-        a = __builtin_fmaxf(a, __shfl_xor(a, 32));
-        const int e = row_exponent(a);
+        int bits = a.bits();
+        bits = larger(bits, __shfl_xor(bits, 16));
+        const RowScale scale(larger(bits, __shfl_xor(bits, 32)));
 #pragma unroll
-        for (int i = 0; i < D / 32; i++) q[nr][i] = q_operand(raw[i], e);
-        factor[nr] = score_factor(p, e);
+        for (int i = 0; i < D / 32; i++) q[nr][i] = scale.operand(raw[i]);
+        factor[nr] = score_factor(p, scale.e);
         const int pos = s.pos0 + t;
         see_hi[nr] = p.causal && pos < s.len - 1 ? pos : s.len - 1;
         see_lo[nr] = p.window ? pos - p.window : -1;
@@ -628,17 +630,16 @@ __device__ __forceinline__ void take_q(const Args& p, const Sequence& s, int hea
     const RowPlace at(p, s, head, r, rows);
     const uint16_t* src = p.q + at.row * p.q_st + at.head * p.q_sh + half * 8;
     uint4 raw[D / 16];
-    float a = 0.0f;
+    RowMagnitude a;
 #pragma unroll
     for (int i = 0; i < D / 16; i++) {
         raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
-        a = __builtin_fmaxf(a, largest(raw[i]));
+        a.take(raw[i]);
     }
-    a = __builtin_fmaxf(a, __shfl_xor(a, 32));
-    const int e = row_exponent(a);
+    const RowScale scale(larger(a.bits(), __shfl_xor(a.bits(), 32)));
 #pragma unroll
-    for (int i = 0; i < D / 16; i++) q[i] = q_operand(raw[i], e);
-    factor = score_factor(p, e);
+    for (int i = 0; i < D / 16; i++) q[i] = scale.operand(raw[i]);
+    factor = score_factor(p, scale.e);
     pos = s.pos0 + at.token;
 }
 
@@ -1335,7 +1336,9 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     // which 32 rows, and which 16 keys of a tile it decodes
     const int pair = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
-    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
+    // (workgroups 8 apart share an XCD: turned by 3 per row tile and split, those of
+    // one long sequence are spread over all of them)
+    const int rest = blockIdx.x / p.batch_heads, bh = (blockIdx.x + 3 * rest) % p.batch_heads;
     const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
@@ -1838,7 +1841,10 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     // keys: 140 us at 2048, 137 at 3072, 143 at 4096).  Many rows: 2 per CU.
     // Prompts: one per CU, and no second round for which every workgroup would
     // start again (a 512-token chunk over 8192 keys, 32 heads: 101 us against 121
-    // with twice as many; 1774 of 1778, 16 heads: 54 against 66).
+    // with twice as many; 1774 of 1778, 16 heads: 54 against 66).  Where chunks
+    // differ in length, contexts will, and about two thirds of the workgroups have
+    // keys (24 chunks of 1 to 61 tokens, 61 to 5003 keys, 21 heads: D = 256 141 us
+    // at 256, 117 at 400; D = 128 138 and 91; 8 of 16 to 64 tokens 78 and 66).
     int64_t keys = a.max_len;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
@@ -1851,7 +1857,8 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     const bool few = pl.kind == Plan::kFew;
     const int64_t unit = few ? kUnit : 64, least = few ? kUnit * kWaves : 256;
     const int64_t most = (keys + least - 1) / least;
-    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? 512 : 256;
+    const bool ragged = a.total_q < a.batch * a.max_q;
+    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? 512 : ragged ? 400 : 256;
     int64_t s = base > 0 ? target / base : 1;
     s = s > most ? most : s;
     s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
