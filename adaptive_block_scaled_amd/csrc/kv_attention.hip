@@ -53,9 +53,7 @@ struct Args {
     int64_t rows_all;         // total_q * heads
     int total_q, pages, kv_heads, heads, group, batch_heads, row_tiles, splits, split_units;
     int causal, window, sinks;
-    // 16-token tiles per page, and its reciprocal: n / d = n * magic >> shift
-    uint32_t page_tiles, page_magic;
-    int page_shift;
+    PageTiles tiles;
     float q_scale;  // scale * log2(e)
     int k_exp;      // E of K plus the 9 of its operands
     float v_mul;    // 2^(E of V + 9)
@@ -75,7 +73,7 @@ __device__ __forceinline__ Sequence sequence_of(const Args& p, int b) {
     q1 = q1 < q0 ? q0 : q1 > p.total_q ? p.total_q : q1;
     s.first_row = q0;
     s.rows = q1 - q0;
-    int64_t room = p.table_stride * p.page_tiles * 16;
+    int64_t room = p.table_stride * p.tiles.n * 16;
     room = room < kMaxLen ? room : kMaxLen;
     const int64_t len = p.seq_lens[b];
     s.len = (int)(len < 0 ? 0 : len > room ? room : len);
@@ -156,8 +154,8 @@ struct TileRef {
 __device__ __forceinline__ TileRef tile_ref_of(const Args& p, const Sequence& s, int n) {
     const int last = s.len > 0 ? (s.len - 1) >> 4 : 0;
     const uint32_t m = (uint32_t)(n < last ? n : last);
-    const uint32_t i = (uint32_t)((uint64_t)m * p.page_magic >> p.page_shift);
-    return {(int)i, m - i * p.page_tiles};
+    const uint32_t i = p.tiles.page_of(m);
+    return {(int)i, m - i * p.tiles.n};
 }
 __device__ __forceinline__ TileRef tile_ref(const Args& p, const Sequence& s, int n) {
     const TileRef r = tile_ref_of(p, s, n);
@@ -170,7 +168,7 @@ __device__ __forceinline__ uint32_t cache_tile(const Args& p, int head, TileRef 
     const int last = p.pages - 1;
     int page = r.page < last ? r.page : last;
     page = page > 0 ? page : 0;
-    return (uint32_t)(page * p.kv_heads + head) * p.page_tiles + r.rest;
+    return (uint32_t)(page * p.kv_heads + head) * p.tiles.n + r.rest;
 }
 
 // 4, as a value that the compiler cannot fold (see high_bytes).
@@ -281,6 +279,13 @@ __device__ __forceinline__ int larger(int a, int b) { return a > b ? a : b; }
 // cache per load at D = 128, and so is V's, lane l = (piece l % 16, tokens
 // 4 (l / 16) ..).  Nothing is shared but the scale tables, until the four
 // waves' results are joined in LDS.
+//
+// Bound by memory while the rows are few: 64 sequences of 3001 to 12289 keys, 64
+// heads, D = 128 (566 MB): 119 us = 4.8 TB/s of a copy's 5.2; 4 of 100003 to 131071
+// (533 MB): 115 us.  One sequence of 4097 keys is latency: 7.2 us for a launch, the
+// lengths, the page table, the codes, one after another.  With 32 rows per tile the
+// decode has twice the products to hide behind: 16 chunks of 4 tokens over 8192
+// keys, 64 heads: 84 us, 1.8 TB/s.
 template <int D>
 struct UnitCodes {
     uint32_t k[2][D / 32], v[2][D / 32];
@@ -727,7 +732,9 @@ __device__ __forceinline__ void store_row(const Args& p, const Sequence& s, int 
 //
 // Steps of 32 keys are pipelined: while the matrix cores compute the scores of
 // step k + 1, the VALU turns those of step k into probabilities, and while
-// they add step k to O, it decodes the next tile.
+// they add step k to O, it decodes the next tile.  Bound by instruction issue, the
+// decode's and the softmax's beside the products': 4 chunks of 16 tokens over 16384
+// keys, 64 heads, D = 128 (128 rows each): 71 us, 483 TFLOP/s, 1.1 TB/s.
 template <int D>
 struct ManyRows {
     static constexpr int kTile = 64 * D * 2;  // bytes of K or V of 64 keys
@@ -956,7 +963,16 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
 //   * waves 4-7 decode K of tile c + 2 in A(2c + 1), phase 4c + 3.  K of tile c,
 //     in the same buffer, was last read (as step 2c + 1) in A(2c) of waves 4-7,
 //     phase 4c + 1; K of tile c + 2 is first read in A(2c + 2), phase 4c + 4.
-// Operands and their order are those of many_rows_kernel.
+// Operands and their order are those of many_rows_kernel.  The decode's work is cut
+// into even slices of about four instructions behind each product: with a group's
+// unpacking in one piece, D = 128 was 1% slower, D = 256 3%.
+//
+// 2048 new of 16384 tokens, 64 heads, D = 128: 974 us, 1058 TFLOP/s (with all waves
+// in step, as in many_rows_kernel, 1161 us); D = 64: 587 us, 878 TFLOP/s.  Bound by
+// instruction issue at a power-limited clock of about 2 GHz: the matrix cores are
+// busy half of the time, 6.5 other VALU instructions per product (decode 2, softmax
+// 3) share the issue of two waves, and a workgroup's start (lengths, pages, codes
+// and q one after another, then code that no cache holds yet) takes 5 to 7 us.
 constexpr int kPairWaves = 8, kPairThreads = 64 * kPairWaves;
 
 template <int D>
@@ -1315,6 +1331,10 @@ __global__ void __launch_bounds__(kPairThreads, D == 64 ? 4 : 2) prompt_kernel(c
 //     and read by the other wave in its next one, before it writes.
 // (Two workgroups per 256 rows that take half of O's dims each and both compute
 // all scores took 1.5 times the products and twice the softmax.)
+//
+// 2048 new of 16384 tokens, 32 heads: 990 us, 1041 TFLOP/s (the two workgroups:
+// 727).  Bound as prompt_rows is, with more decode per product, 128 rows sharing it
+// instead of 256.
 struct WideTile {
     static constexpr int D = 256, kRows = 128, kTile = 64 * D * 2;
     static constexpr int kProb = kScaleTableBytes + 4 * kTile;  // [4 pairs][2][64 lanes][16]
@@ -1672,7 +1692,8 @@ __global__ void __launch_bounds__(kPairThreads, 2) wide_kernel(const Args p) {
 }
 
 // ---------------------------------------------------------------------------
-// Joins the splits of one row per workgroup.  All waves read every split's m
+// Joins the splits of one row per workgroup: latency, 3.5 us for 64 rows of 33
+// splits, 5.6 for 256 rows of 94.  All waves read every split's m
 // and l at once, lane = split mod 64; then D/4 lanes read one split's
 // O as 16 bytes each, the workgroup 1024 / D splits side by side, so that the
 // whole row is a handful of independent loads.  (One wave per row with a loop
@@ -1749,7 +1770,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
     }
 }
 
-// The same for at most kFewSplits splits: one wave per row, no LDS.
+// The same for at most kFewSplits splits: one wave per row, no LDS (4096 rows of 6
+// splits at D = 128: 5.7 us against 9 a workgroup per row).
 constexpr int kFewSplits = 8;
 
 template <int D>
@@ -1954,14 +1976,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.causal = a.causal != 0;
     p.window = clamp_int(a.window);
     p.sinks = clamp_int(a.sinks);
-    // n / d = n * ceil(2^(31 + s) / d) >> (31 + s) for n < 2^31 and
-    // s = ceil(log2 d): the multiplier exceeds 2^(31 + s) / d by less than
-    // 1 <= 2^s / d, which adds less than 1 / d to the quotient
-    p.page_tiles = (uint32_t)(c.page_size / 16);
-    int sh = 0;
-    while (((uint64_t)1 << sh) < p.page_tiles) sh++;
-    p.page_shift = 31 + sh;
-    p.page_magic = (uint32_t)((((uint64_t)1 << p.page_shift) + p.page_tiles - 1) / p.page_tiles);
+    p.tiles = PageTiles(c.page_size);
     p.q_scale = a.scale * 1.44269504f;
     p.k_exp = c.k_exp + 9;
     p.v_mul = pow2f(c.v_exp + 9);

@@ -29,12 +29,12 @@ struct Place {
     int64_t row;  // (page * kv_heads + head) * page_size + offset
     int64_t tile;
     int tok;
-    __device__ __forceinline__ Place(int64_t slot, int head, int kv_heads, int64_t page_size) {
-        const int64_t page = slot / page_size, off = slot - page * page_size;
-        const int64_t first = (page * kv_heads + head) * page_size;
-        row = first + off;
-        tile = (first + off) >> 4;
-        tok = (int)(off & 15);
+    // (all tiles of a cache, pages x kv heads x tiles of a page, fit 31 bits)
+    __device__ __forceinline__ Place(int64_t slot, int head, int kv_heads, const PageTiles& tiles) {
+        const uint32_t t = (uint32_t)(slot >> 4), page = tiles.page_of(t);
+        tile = (page * kv_heads + head) * tiles.n + (t - page * tiles.n);
+        tok = (int)(slot & 15);
+        row = tile * 16 + tok;
     }
     __device__ __forceinline__ int64_t k_code(int g) const { return row * (D / 2) + g * 8; }
     __device__ __forceinline__ int64_t k_scale(int g) const { return row * (D / 16) + g; }
@@ -86,13 +86,16 @@ struct AppendArgs {
     uint8_t* codes[2];
     uint8_t* scales[2];
     float p_exp[2], p_negexp[2];
-    int64_t tokens, page_size, nslots;
+    int64_t tokens, nslots;
+    PageTiles tiles;
     int kv_heads;
 };
 
-// blockIdx.z: K or V; y: head; x: run of kThreads / (D/16) tokens.  8192 tokens of
-// 8 heads (43 MB moved): 12.5 us = 3.4 TB/s; one wave per workgroup 13.0, heads
-// before tokens 13.2.
+// Quantize as written.  blockIdx.z: K or V; y: head; x: run of kThreads / (D/16)
+// tokens.  Small calls are launch and latency (64 tokens of 8 heads of 128: 3.6 us,
+// slot and values asked for together), large ones memory: 8192 tokens (43 MB moved)
+// 12.5 us = 3.4 TB/s, the start and tail of a short kernel among them; one wave per
+// workgroup 13.0, heads before tokens 13.2, loads past the caches 13.5.
 template <int D, bool kBf16, int kMode>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs p) {
     constexpr int G = D / 16;
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs p) {
         fast_group<kMode>(v, p.p_exp[part], p.p_negexp[part], lo, hi, byte);
     else
         exact_group<kMode>(v, p.p_exp[part], p.p_negexp[part], lo, hi, byte);
-    const Place<D> at(slot, head, p.kv_heads, p.page_size);
+    const Place<D> at(slot, head, p.kv_heads, p.tiles);
     if (part == 0) {
         *reinterpret_cast<uint2*>(p.codes[0] + at.k_code(g)) = make_uint2(lo, hi);
         p.scales[0][at.k_scale(g)] = (uint8_t)byte;
@@ -126,17 +129,38 @@ struct ReadArgs {
     void* y[2];
     const int64_t* slots;
     float p_exp[2];
-    int64_t tokens, page_size, nslots;
+    int64_t tokens, nslots;
+    PageTiles tiles;
     int kv_heads;
 };
+
+// Stores past the caches that follow one another at once: the compiler is told
+// that all values are needed before the first.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void store_all(void* to, u32x4 a, u32x4 b) {
+    asm volatile("" : "+v"(a), "+v"(b));
+    u32x4* const q = reinterpret_cast<u32x4*>(to);
+    __builtin_nontemporal_store(a, q);
+    __builtin_nontemporal_store(b, q + 1);
+}
+__device__ __forceinline__ void store_all(void* to, u32x4 a, u32x4 b, u32x4 c, u32x4 d) {
+    asm volatile("" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+    u32x4* const q = reinterpret_cast<u32x4*>(to);
+    __builtin_nontemporal_store(a, q);
+    __builtin_nontemporal_store(b, q + 1);
+    __builtin_nontemporal_store(c, q + 2);
+    __builtin_nontemporal_store(d, q + 3);
+}
 
 // blockIdx.z: K or V; x: run of kThreads / (D/16) tokens, head fastest, so that
 // neighbouring workgroups write neighbouring heads of the same tokens.  The stores
 // leave nothing of the output in the caches, which would have to be written back
-// from them before the next call's.  A context of 32768 tokens of 8 heads of 128
-// (172 MB moved), 3000 calls in a row: 31.8 us = 5.4 TB/s; ordinary stores 47.9 us;
-// one wave per workgroup 47.2, two 33.3, eight 34.6; 8 values per lane, so that a
-// wave stores 1 KB in one piece, 39 us (half as much in flight).
+// from them before the next call's; a lane's follow one another at once, or half
+// lines reach the memory.  A context of 32768 tokens of 8 heads of 128 (172 MB
+// moved), 3000 calls in a row: 33.8 us = 5.1 TB/s, the rate of a large copy;
+// ordinary stores 47.9 us, stores apart 49.0; two waves per workgroup 33.3, one 47
+// (stores apart), eight 34.6; 8 values per lane, so that a wave stores 1 KB in one
+// piece, 39 us (half as much in flight).
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs p) {
     constexpr int G = D / 16;
@@ -150,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs p) {
     uint2 w = make_uint2(0u, 0u);
     uint32_t byte = 0;
     if (slot >= 0 && slot < p.nslots) {
-        const Place<D> at(slot, head, p.kv_heads, p.page_size);
+        const Place<D> at(slot, head, p.kv_heads, p.tiles);
         if (part == 0) {
             w = *reinterpret_cast<const uint2*>(p.codes[0] + at.k_code(g));
             byte = p.scales[0][at.k_scale(g)];
@@ -168,16 +192,15 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs p) {
         bf16x8 b[2];
 #pragma unroll
         for (int i = 0; i < 16; i++) b[i >> 3][i & 7] = (__bf16)out[i];
-        bf16x8* q = reinterpret_cast<bf16x8*>(reinterpret_cast<uint16_t*>(p.y[part]) + off);
-        __builtin_nontemporal_store(b[0], q);
-        __builtin_nontemporal_store(b[1], q + 1);
+        store_all(reinterpret_cast<uint16_t*>(p.y[part]) + off,
+                  __builtin_bit_cast(u32x4, b[0]), __builtin_bit_cast(u32x4, b[1]));
     } else {
-        f32x4* q = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y[part]) + off);
+        f32x4 f[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const f32x4 f = {out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]};
-            __builtin_nontemporal_store(f, q + i);
-        }
+        for (int i = 0; i < 16; i++) f[i >> 2][i & 3] = out[i];
+        store_all(reinterpret_cast<float*>(p.y[part]) + off, __builtin_bit_cast(u32x4, f[0]),
+                  __builtin_bit_cast(u32x4, f[1]), __builtin_bit_cast(u32x4, f[2]),
+                  __builtin_bit_cast(u32x4, f[3]));
     }
 }
 
@@ -239,7 +262,7 @@ hipError_t launch_kv_append(const if4_kv_cache& c, const void* k, const void* v,
     p.scales[0] = c.k_scales;
     p.scales[1] = c.v_scales;
     p.tokens = tokens;
-    p.page_size = c.page_size;
+    p.tiles = PageTiles(c.page_size);
     p.nslots = c.pages * c.page_size;
     p.kv_heads = (int)c.kv_heads;
     if (c.head_dim == 64) return append<64>(c, p, bf16, mode, stream);
@@ -260,7 +283,7 @@ hipError_t launch_kv_read(const if4_kv_cache& c, const int64_t* slots, int64_t t
     p.p_exp[0] = pow2f(c.k_exp);
     p.p_exp[1] = pow2f(c.v_exp);
     p.tokens = tokens;
-    p.page_size = c.page_size;
+    p.tiles = PageTiles(c.page_size);
     p.nslots = c.pages * c.page_size;
     p.kv_heads = (int)c.kv_heads;
     if (c.head_dim == 64) return read<64>(c, p, bf16, stream);

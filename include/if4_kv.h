@@ -23,6 +23,8 @@
  * D is 64, 128 or 256 and page_size a multiple of 16 (else IF4_ERR_SHAPE).
  * Conventions, status codes and streams are those of if4.h: device pointers,
  * nothing allocated, arguments checked on the host, work only enqueued.
+ * A cache's tiles of 16 tokens, pages * kv_heads * page_size / 16, fit 31 bits
+ * (else IF4_ERR_SHAPE): 2^35 tokens of one head.
  * Indices that live in device memory (slots, page table, lengths) cannot be
  * checked on the host; the kernels check them as stated at each call, so that
  * no value of theirs makes an access outside the buffers.
@@ -89,6 +91,8 @@ int if4_kv_read(const if4_kv_cache* cache, const int64_t* slots, int64_t tokens,
  *            [0, pages) are read as the nearest valid page;
  *            seq_lens above table_stride * page_size count as that
  *   q_starts device int32 [batch + 1], ascending, 0 .. total_q
+ *   seq_lens device int32 [batch]; a length below zero counts as zero, one above
+ *            2^30 - 256 as that
  *   max_q    no sequence has more rows of q than this (further rows are not
  *            computed); max_len: about how long the longest sequence is (only
  *            the speed depends on it)
@@ -97,8 +101,8 @@ int if4_kv_read(const if4_kv_cache* cache, const int64_t* slots, int64_t tokens,
  * Arithmetic: K and V are decoded to fp16 with 2^-9 as if4_gemm decodes its
  * operands, q is taken as fp16 after an exact power of two per row and head,
  * products are summed in fp32, probabilities are rounded to fp16 for the
- * second product, the maximum, the sum and the output are fp32 up to
- * the one rounding of out to bf16.  Results do not depend on timing.
+ * second product (their sum is that of the rounded ones), the maximum, the sum and
+ * the output are fp32 up to the one rounding of out to bf16.  Results do not depend on timing.
  */
 typedef struct if4_kv_attention_args {
     const void* q;
