@@ -29,6 +29,7 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // (lambdas that hold a kernel's state have to be inlined, whatever their size)
@@ -51,9 +52,10 @@ struct Args {
     int64_t table_stride;
     float *part_o, *part_ml;  // splits > 1: [splits][total_q * heads][D], [..][2]
     int64_t rows_all;         // total_q * heads
-    int total_q, pages, kv_heads, heads, group, batch_heads, row_tiles, splits, split_units;
+    int total_q, pages, kv_heads, heads, batch_heads, row_tiles, splits, split_units;
     int causal, window, sinks;
-    PageTiles tiles;
+    Divisor tiles;  // of 16 tokens in a page
+    Divisor group;  // query heads of a kv head
     float q_scale;  // scale * log2(e)
     int k_exp;      // E of K plus the 9 of its operands
     float v_mul;    // 2^(E of V + 9)
@@ -120,9 +122,9 @@ __device__ __forceinline__ int units_per_split(const Args& p, int n) {
 __device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int head, int row0,
                                            int last_row, int split) {
     for (int r = row0 + threadIdx.x; r <= last_row; r += blockDim.x) {
-        const int t = r / p.group, g = r - t * p.group;
+        const int t = (int)p.group.into(r), g = r - t * (int)p.group.n;
         const int64_t at = split * p.rows_all + (int64_t)(s.first_row + t) * p.heads +
-                           head * p.group + g;
+                           head * (int)p.group.n + g;
         *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, 0.0f};
     }
 }
@@ -154,7 +156,7 @@ struct TileRef {
 __device__ __forceinline__ TileRef tile_ref_of(const Args& p, const Sequence& s, int n) {
     const int last = s.len > 0 ? (s.len - 1) >> 4 : 0;
     const uint32_t m = (uint32_t)(n < last ? n : last);
-    const uint32_t i = p.tiles.page_of(m);
+    const uint32_t i = p.tiles.into(m);
     return {(int)i, m - i * p.tiles.n};
 }
 __device__ __forceinline__ TileRef tile_ref(const Args& p, const Sequence& s, int n) {
@@ -209,9 +211,9 @@ struct RowPlace {
     __device__ __forceinline__ RowPlace(const Args& p, const Sequence& s, int kv_head, int r,
                                         int rows) {
         const int rc = r < rows ? r : rows - 1;
-        token = rc / p.group;
+        token = (int)p.group.into(rc);
         row = s.first_row + token;
-        head = kv_head * p.group + (rc - token * p.group);
+        head = kv_head * (int)p.group.n + (rc - token * (int)p.group.n);
     }
 };
 
@@ -366,11 +368,11 @@ few_rows_kernel(const Args p) {
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * p.group;
+    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
     if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
-    const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
+    const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
     const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, kUnit);
     const int per = units_per_split(p, units.n);
     const int begin = split * per;
@@ -390,9 +392,9 @@ few_rows_kernel(const Args p) {
     for (int nr = 0; nr < kBlocks; nr++) {
         const int r = row0 + 16 * nr + (lane & 15);
         const int rc = r < rows ? r : rows - 1;
-        const int t = rc / p.group, g = rc - t * p.group;
+        const int t = (int)p.group.into(rc), g = rc - t * (int)p.group.n;
         const uint16_t* src = p.q + (s.first_row + t) * p.q_st +
-                              (int64_t)(head * p.group + g) * p.q_sh + (lane >> 4) * (D / 4);
+                              (int64_t)(head * (int)p.group.n + g) * p.q_sh + (lane >> 4) * (D / 4);
         uint4 raw[D / 32];
         RowMagnitude a;
 #pragma unroll
@@ -602,8 +604,8 @@ few_rows_kernel(const Args p) {
 #pragma unroll
                 for (int d = 0; d < M; d++) acc[d] = __builtin_fmaf(f, src[d], acc[d]);
             }
-            const int t = r / p.group, g = r - t * p.group;
-            const int64_t row = s.first_row + t, hd = head * p.group + g;
+            const int t = (int)p.group.into(r), g = r - t * (int)p.group.n;
+            const int64_t row = s.first_row + t, hd = head * (int)p.group.n + g;
             if (p.splits == 1) {
                 const float f = sum == 0.0f ? 0.0f : p.v_mul / sum;
                 uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * p.o_st + hd * p.o_sh +
@@ -629,23 +631,72 @@ few_rows_kernel(const Args p) {
 // lane % 32 of its wave), half = lane / 32.
 
 // q of a row as the operands of D / 16 products: words 2t + half of 8 dims.
+template <int D, typename Word>
+__device__ __forceinline__ void make_q(const Args& p, Word&& word, half8 (&q)[D / 16],
+                                       float& factor) {
+    uint4 w[D / 16];
+    RowMagnitude a;
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) {
+        w[i] = word(i);
+        a.take(w[i]);
+    }
+    const RowScale scale(larger(a.bits(), __shfl_xor(a.bits(), 32)));
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) q[i] = scale.operand(w[i]);
+    factor = score_factor(p, scale.e);
+}
 template <int D>
 __device__ __forceinline__ void take_q(const Args& p, const Sequence& s, int head, int r, int rows,
                                        int half, half8 (&q)[D / 16], float& factor, int& pos) {
     const RowPlace at(p, s, head, r, rows);
     const uint16_t* src = p.q + at.row * p.q_st + at.head * p.q_sh + half * 8;
-    uint4 raw[D / 16];
-    RowMagnitude a;
-#pragma unroll
-    for (int i = 0; i < D / 16; i++) {
-        raw[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
-        a.take(raw[i]);
-    }
-    const RowScale scale(larger(a.bits(), __shfl_xor(a.bits(), 32)));
-#pragma unroll
-    for (int i = 0; i < D / 16; i++) q[i] = scale.operand(raw[i]);
-    factor = score_factor(p, scale.e);
+    make_q<D>(p, [&](int i) { return *reinterpret_cast<const uint4*>(src + 16 * i); }, q, factor);
     pos = s.pos0 + at.token;
+}
+
+// q of a tile of kRows rows, on its way through LDS.  Each row is asked for by
+// neighbouring lanes, 16 bytes each, and taken from LDS by the lanes that need it as
+// operands: straight from memory the 32 rows of a wave's operand would be 32 lines
+// of 32 bytes (D = 256: 13200 cycles until q and the first codes are there, so 7800;
+// 2 prompts of 4096 tokens at D = 128 583 -> 580 us.  Many rows, whose workgroups ask
+// for half as much and have no cycles to spare for LDS, are 3% faster without).
+// In LDS (kRows * 2 D bytes of a tile buffer) a row's 16-byte words are permuted so that
+// a column of words lies in different banks.
+template <int D, int kRows, int kThreadsOf>
+struct TileQ {
+    static constexpr int kWords = D / 8, kPasses = kRows * kWords / kThreadsOf;
+    typedef u32x4 Words[kPasses];
+    __device__ static __forceinline__ uint32_t place(int r, int word) {
+        const int turn = (D == 64 ? r >> 1 : r) & (kWords < 16 ? kWords - 1 : 15);
+        return (uint32_t)(r * kWords + (word ^ turn)) * 16;
+    }
+    __device__ static __forceinline__ void ask(const Args& p, const Sequence& s, int head,
+                                               int row0, int rows, int tid, Words& raw) {
+#pragma unroll
+        for (int i = 0; i < kPasses; i++) {
+            const RowPlace at(p, s, head, row0 + (i * kThreadsOf + tid) / kWords, rows);
+            raw[i] = *reinterpret_cast<const u32x4*>(p.q + at.row * p.q_st + at.head * p.q_sh +
+                                                     tid % kWords * 8);
+        }
+    }
+    __device__ static __forceinline__ void put(uint8_t* lds, int tid, const Words& raw) {
+#pragma unroll
+        for (int i = 0; i < kPasses; i++)
+            *reinterpret_cast<u32x4*>(
+                lds + place((i * kThreadsOf + tid) / kWords, tid % kWords)) = raw[i];
+    }
+    // row r of the tile
+    __device__ static __forceinline__ void take(const Args& p, const uint8_t* lds, int r, int half,
+                                                half8 (&q)[D / 16], float& factor) {
+        make_q<D>(
+            p, [&](int i) { return *reinterpret_cast<const uint4*>(lds + place(r, 2 * i + half)); },
+            q, factor);
+    }
+};
+// Position of tile row r (the last row's past the end).
+__device__ __forceinline__ int position_of(const Args& p, const Sequence& s, int r, int rows) {
+    return s.pos0 + (int)p.group.into(r < rows ? r : rows - 1);
 }
 
 __device__ __forceinline__ bool sees(const Args& p, int len, int pos, int key) {
@@ -769,11 +820,11 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * p.group;
+    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
     if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
-    const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
+    const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
     const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, 64);
     const int per = units_per_split(p, units.n);
     const int begin = split * per;
@@ -1005,11 +1056,11 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * p.group;
+    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
     if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
-    const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
+    const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
     const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, 64);
     const WholeSteps whole(p, s.len, pos_lo, pos_hi, 32);
     const int per = units_per_split(p, units.n);
@@ -1056,7 +1107,11 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     auto ref = [&](int i) KV_INLINE {
         return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + unit16);
     };
-    // the first tiles' codes and q are asked for together
+    // q and the first tiles' codes are asked for together
+    typedef TileQ<D, kRows, kPairThreads> QTile;
+    typename QTile::Words q_words;
+    QTile::ask(p, s, head, row0, rows, tid, q_words);
+    __builtin_amdgcn_sched_barrier(0);
     Codes first[3];
     if (begin < end) {
         TileRef r[3];
@@ -1069,7 +1124,10 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     half8 q[T];
     float factor, m = kLowest, l = 0.0f;
     int pos;
-    take_q<D>(p, s, head, row0 + 32 * wave + (lane & 31), rows, half, q, factor, pos);
+    QTile::put(k_lds, tid, q_words);
+    __syncthreads();
+    QTile::take(p, k_lds, 32 * wave + (lane & 31), half, q, factor);
+    pos = position_of(p, s, row0 + 32 * wave + (lane & 31), rows);
     now = first[0];
 
     // The scales of the codes in `now`, looked up one phase before their decode.
@@ -1217,18 +1275,19 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 #pragma unroll
             for (int i = 0; i < 16; i++) o[d][i] *= alpha;
     };
-    __syncthreads();
+    lds_barrier();
     if (begin < end) {
         // K of tiles 0 and 1, V of tile 0, probabilities of step 0
         const auto decode_tile = [&](int buf) KV_INLINE {
             look_up();
             each<T + P>([&](auto n) KV_INLINE { decode(buf, n); });
         };
-        decode_tile(0);
-        now = first[1];
-        if constexpr (kLate) {
-            decode_tile(1);
-            now = first[2];
+        // (a loop: its code is not in the caches yet)
+#pragma unroll 1
+        for (int t = 0; t < (kLate ? 2 : 1); t++) {
+            decode_tile(t);
+            now = first[1];
+            first[1] = first[2];
         }
         // the tile whose codes are loaded next.  (Its page is asked for in a B phase:
         // a scalar load in flight turns every wait for LDS into one for all of it.)
@@ -1363,11 +1422,11 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * p.group;
+    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
     if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
-    const int pos_lo = s.pos0 + row0 / p.group, pos_hi = s.pos0 + last_row / p.group;
+    const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
     const KeyUnits units = key_units(p, s.len, pos_lo, pos_hi, 64);
     const WholeSteps whole(p, s.len, pos_lo, pos_hi, 32);
     const int per = units_per_split(p, units.n);
@@ -1404,7 +1463,11 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     auto ref = [&](int i) KV_INLINE {
         return tile_ref(p, s, 4 * units(i < end ? i : end - 1) + pair);
     };
-    // the first tiles' codes and q are asked for together
+    // q and the first tiles' codes are asked for together
+    typedef TileQ<D, kRows, kPairThreads> QTile;
+    typename QTile::Words q_words;
+    QTile::ask(p, s, head, row0, rows, tid, q_words);
+    __builtin_amdgcn_sched_barrier(0);
     Codes now, first[3];
     if (begin < end) {
         TileRef r[3];
@@ -1417,7 +1480,10 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     half8 q[T];
     float factor, m = kLowest, l = 0.0f;
     int pos;
-    take_q<D>(p, s, head, row0 + 32 * pair + (lane & 31), rows, half, q, factor, pos);
+    QTile::put(k_lds, tid, q_words);
+    __syncthreads();
+    QTile::take(p, k_lds, 32 * pair + (lane & 31), half, q, factor);
+    pos = position_of(p, s, row0 + 32 * pair + (lane & 31), rows);
     now = first[0];
 
     // The scales of the codes in `now`, looked up one phase before their decode.
@@ -1611,17 +1677,18 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
         prob_lds[64] = prob[1];
         *max_lds = m;
     };
-    __syncthreads();
+    lds_barrier();
     if (begin < end) {
         const auto decode_tile = [&](int buf) KV_INLINE {
             look_up();
             each<32>([&](auto n) KV_INLINE { decode(buf, n); });
         };
-        decode_tile(0);
-        now = first[1];
-        if constexpr (!kLate) {
-            decode_tile(1);
-            now = first[2];
+        // (a loop: its code is not in the caches yet)
+#pragma unroll 1
+        for (int t = 0; t < (kLate ? 1 : 2); t++) {
+            decode_tile(t);
+            now = first[1];
+            first[1] = first[2];
         }
         // the tile whose codes are loaded next.  (Its page is asked for in a B phase
         // behind LDS's last answer: a scalar load in flight turns every wait for LDS
@@ -1968,7 +2035,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.pages = (int)c.pages;
     p.kv_heads = (int)c.kv_heads;
     p.heads = (int)a.heads;
-    p.group = (int)(a.heads / c.kv_heads);
+    p.group = Divisor(a.heads / c.kv_heads);
     p.batch_heads = (int)(a.batch * c.kv_heads);
     p.row_tiles = pl.row_tiles;
     p.splits = pl.splits;
@@ -1976,7 +2043,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.causal = a.causal != 0;
     p.window = clamp_int(a.window);
     p.sinks = clamp_int(a.sinks);
-    p.tiles = PageTiles(c.page_size);
+    p.tiles = Divisor(c.page_size / 16);
     p.q_scale = a.scale * 1.44269504f;
     p.k_exp = c.k_exp + 9;
     p.v_mul = pow2f(c.v_exp + 9);

@@ -30,8 +30,8 @@ struct Place {
     int64_t tile;
     int tok;
     // (all tiles of a cache, pages x kv heads x tiles of a page, fit 31 bits)
-    __device__ __forceinline__ Place(int64_t slot, int head, int kv_heads, const PageTiles& tiles) {
-        const uint32_t t = (uint32_t)(slot >> 4), page = tiles.page_of(t);
+    __device__ __forceinline__ Place(int64_t slot, int head, int kv_heads, const Divisor& tiles) {
+        const uint32_t t = (uint32_t)(slot >> 4), page = tiles.into(t);
         tile = (page * kv_heads + head) * tiles.n + (t - page * tiles.n);
         tok = (int)(slot & 15);
         row = tile * 16 + tok;
@@ -87,7 +87,7 @@ struct AppendArgs {
     uint8_t* scales[2];
     float p_exp[2], p_negexp[2];
     int64_t tokens, nslots;
-    PageTiles tiles;
+    Divisor tiles;  // of 16 tokens in a page
     int kv_heads;
 };
 
@@ -130,7 +130,7 @@ struct ReadArgs {
     const int64_t* slots;
     float p_exp[2];
     int64_t tokens, nslots;
-    PageTiles tiles;
+    Divisor tiles;  // of 16 tokens in a page
     int kv_heads;
 };
 
@@ -262,7 +262,7 @@ hipError_t launch_kv_append(const if4_kv_cache& c, const void* k, const void* v,
     p.scales[0] = c.k_scales;
     p.scales[1] = c.v_scales;
     p.tokens = tokens;
-    p.tiles = PageTiles(c.page_size);
+    p.tiles = Divisor(c.page_size / 16);
     p.nslots = c.pages * c.page_size;
     p.kv_heads = (int)c.kv_heads;
     if (c.head_dim == 64) return append<64>(c, p, bf16, mode, stream);
@@ -283,7 +283,7 @@ hipError_t launch_kv_read(const if4_kv_cache& c, const int64_t* slots, int64_t t
     p.p_exp[0] = pow2f(c.k_exp);
     p.p_exp[1] = pow2f(c.v_exp);
     p.tokens = tokens;
-    p.tiles = PageTiles(c.page_size);
+    p.tiles = Divisor(c.page_size / 16);
     p.nslots = c.pages * c.page_size;
     p.kv_heads = (int)c.kv_heads;
     if (c.head_dim == 64) return read<64>(c, p, bf16, stream);

@@ -21,24 +21,23 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
 
 int64_t kv_attention_workspace(const if4_kv_cache& c, const if4_kv_attention_args& a);
 
-// 16-token tiles per page, and its reciprocal: n / d = n * magic >> shift for
-// n < 2^31.  magic = ceil(2^shift / d) with shift = 31 + ceil(log2 d) exceeds
-// 2^shift / d by less than 1 <= 2^(shift - 31) / d, which adds less than 1 / d to
-// the quotient.
-struct PageTiles {
+// A divisor fixed for a call: m / n = m * magic >> shift for m < 2^31.  magic =
+// ceil(2^shift / n) with shift = 31 + ceil(log2 n) exceeds 2^shift / n by less than
+// 1 <= 2^(shift - 31) / n, which adds less than 1 / n to the quotient.
+struct Divisor {
     uint32_t n, magic;
     int shift;
-    explicit PageTiles(int64_t page_size) {
-        n = (uint32_t)(page_size / 16);
+    Divisor() = default;
+    explicit Divisor(int64_t by) {
+        n = (uint32_t)by;
         int s = 0;
         while (((uint64_t)1 << s) < n) s++;
         shift = 31 + s;
         magic = (uint32_t)((((uint64_t)1 << shift) + n - 1) / n);
     }
-    PageTiles() = default;
 #ifdef __HIP__
-    __device__ __forceinline__ uint32_t page_of(uint32_t tile) const {
-        return (uint32_t)((uint64_t)tile * magic >> shift);
+    __device__ __forceinline__ uint32_t into(uint32_t m) const {
+        return (uint32_t)((uint64_t)m * magic >> shift);
     }
 #endif
 };
