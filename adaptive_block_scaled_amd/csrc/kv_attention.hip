@@ -1925,15 +1925,6 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
                      : pl.kind == Plan::kPrompt ? 256
                                                 : 128;
     pl.row_tiles = (int)((rows + tile - 1) / tile);
-    // Splits of the keys.  Few rows: 256 CUs hold 1024 workgroups (D = 128), and
-    // 3072 leave a short last round where lengths differ (64 sequences of 3-12k
-    // keys: 140 us at 2048, 137 at 3072, 143 at 4096).  Many rows: 2 per CU.
-    // Prompts: one per CU, and no second round for which every workgroup would
-    // start again (a 512-token chunk over 8192 keys, 32 heads: 101 us against 121
-    // with twice as many; 1774 of 1778, 16 heads: 54 against 66).  Where chunks
-    // differ in length, contexts will, and about two thirds of the workgroups have
-    // keys (24 chunks of 1 to 61 tokens, 61 to 5003 keys, 21 heads: D = 256 141 us
-    // at 256, 117 at 400; D = 128 138 and 91; 8 of 16 to 64 tokens 78 and 66).
     int64_t keys = a.max_len;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
@@ -1943,14 +1934,42 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     int64_t tiles = a.total_q * group / tile + a.batch;
     tiles = tiles < a.batch * pl.row_tiles ? tiles : a.batch * pl.row_tiles;
     const int64_t base = c.kv_heads * tiles;
-    const bool few = pl.kind == Plan::kFew;
-    const int64_t unit = few ? kUnit : 64, least = few ? kUnit * kWaves : 256;
-    const int64_t most = (keys + least - 1) / least;
-    const bool ragged = a.total_q < a.batch * a.max_q;
-    const int64_t target = few ? 3072 : pl.kind == Plan::kMany ? 512 : ragged ? 400 : 256;
-    int64_t s = base > 0 ? target / base : 1;
-    s = s > most ? most : s;
-    s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+    // Splits of the keys: as many as fill a number of workgroups, with at least so
+    // many keys each.
+    const bool few = pl.kind == Plan::kFew, ragged = a.total_q < a.batch * a.max_q;
+    const int64_t unit = few ? kUnit : 64;
+    int64_t s = 1;
+    const auto fill = [&](int64_t workgroups, int64_t least) {
+        const int64_t n = base > 0 ? workgroups / base : 1, most = (keys + least - 1) / least;
+        const int64_t t = n < most ? n : most;
+        s = s > t ? s : t;
+    };
+    if (few) {
+        // One workgroup per CU down to one unit of each wave (one sequence of 4097 keys:
+        // 10 us, whole 39).  Beyond that the join and the partial sums cost more
+        // than fuller CUs bring, unless the splits are long: as many workgroups as
+        // the chip holds where each has 1024 keys (64 heads, 8 kv heads, D = 128; 128
+        // keys each up to 3072 workgroups before: 32 sequences of 512 keys 16.0 us,
+        // so 10.6; 64 of 512 to 1024 26.9, 18.5; 8 of 1000 to 4000 20.3, 17.1; 4 of
+        // 100003 to 131071 120, 114).  Where that leaves few splits of each sequence
+        // a long one ends late: three rounds of long splits (64 of 3001 to 12289 keys
+        // 127 us, so 123).
+        const int64_t held = c.head_dim * pl.blocks <= 128 ? 1024 : 512;
+        fill(256, kUnit * kWaves);
+        fill(512, 512);
+        fill(held, 1024);
+        if (base >= held / 4) fill(3 * held, 2048);
+    } else {
+        // Many rows: 2 per CU.  Prompts: one per CU, and no second round for which every
+        // workgroup would start again (a 512-token chunk over 8192 keys, 32 heads: 101 us
+        // against 121 with twice as many; 1774 of 1778, 16 heads: 54 against 66).
+        // Where chunks differ in length, contexts will, and about two thirds of the
+        // workgroups have keys (24 chunks of 1 to 61 tokens, 61 to 5003 keys, 21 heads:
+        // D = 256 141 us at 256, 117 at 400; D = 128 138 and 91; 8 of 16 to 64 tokens
+        // 78 and 66).
+        fill(pl.kind == Plan::kMany ? 512 : ragged ? 400 : 256, 256);
+    }
+    s = s > kMaxSplits ? kMaxSplits : s;
     const int64_t units = (keys + unit - 1) / unit;
     pl.split_units = (int)((units + s - 1) / s);
     // whole rounds of the waves, and no split that the hint leaves empty
