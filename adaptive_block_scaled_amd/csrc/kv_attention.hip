@@ -1929,7 +1929,9 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
     const int64_t sinks = a.sinks < kMaxKeys ? a.sinks : kMaxKeys;
-    if (window && window + sinks + a.max_q < keys) keys = window + sinks + a.max_q;
+    // with a window, what the tokens of one tile see
+    const int64_t span = a.max_q < tile / group + 2 ? a.max_q : tile / group + 2;
+    if (window && window + sinks + span < keys) keys = window + sinks + span;
     // row tiles that hold rows: at most one per sequence is not full
     int64_t tiles = a.total_q * group / tile + a.batch;
     tiles = tiles < a.batch * pl.row_tiles ? tiles : a.batch * pl.row_tiles;
@@ -1959,15 +1961,35 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
         fill(512, 512);
         fill(held, 1024);
         if (base >= held / 4) fill(3 * held, 2048);
+    } else if (pl.kind == Plan::kMany) {
+        // The same with more work per workgroup (32 chunks of 16 tokens over 512 keys, 64
+        // heads: 42 us with 512 workgroups of 256 keys, so 23.5; 32 of 10 over 1000 to
+        // 4000 106 with 256 workgroups, so 91).
+        fill(256, 256);
+        fill(512, 512);
     } else {
-        // Many rows: 2 per CU.  Prompts: one per CU, and no second round for which every
-        // workgroup would start again (a 512-token chunk over 8192 keys, 32 heads: 101 us
-        // against 121 with twice as many; 1774 of 1778, 16 heads: 54 against 66).
-        // Where chunks differ in length, contexts will, and about two thirds of the
-        // workgroups have keys (24 chunks of 1 to 61 tokens, 61 to 5003 keys, 21 heads:
-        // D = 256 141 us at 256, 117 at 400; D = 128 138 and 91; 8 of 16 to 64 tokens
-        // 78 and 66).
-        fill(pl.kind == Plan::kMany ? 512 : ragged ? 400 : 256, 256);
+        // Prompts, whose partial sums are large: the least of rounds * (start of a
+        // workgroup + its tiles of 64 keys) + join, in ns as measured (500 tokens, 32
+        // heads, D = 256: 40 us in two splits, 30 whole; 512 of 8192 tokens 164 in two,
+        // 250 whole).  Where chunks differ in length contexts will: about two thirds of
+        // the workgroups have keys, and a tenth more than the chip holds costs little
+        // (24 chunks of 1 to 61 tokens, 61 to 5003 keys, 21 heads: D = 256 141 us
+        // whole, 116 in two; D = 128 138 and 90 in three; 16 of 16 to 64, 500 to 4000
+        // keys, 32 heads, D = 256: 118 whole, 131 in two).
+        const int64_t held = c.head_dim == 64 ? 512 : 256, start = 7000, step = 1800;
+        const int64_t n = (keys + 63) / 64, partial = a.total_q * a.heads * c.head_dim * 8 / 4000;
+        int64_t best = INT64_MAX;
+        for (int64_t t = 1; t <= kMaxSplits && (t == 1 || (t * 4 <= n && t * base <= 4 * held));
+             t++) {
+            const int64_t all = ragged ? base * t * 2 / 3 * 10 / 11 : base * t;
+            const int64_t rounds = all > held ? (all + held - 1) / held : 1;
+            const int64_t cost = rounds * (start + (n + t - 1) / t * step) +
+                                 (t > 1 ? 4000 + t * partial : 0);
+            if (cost < best) {
+                best = cost;
+                s = t;
+            }
+        }
     }
     s = s > kMaxSplits ? kMaxSplits : s;
     const int64_t units = (keys + unit - 1) / unit;
