@@ -1932,13 +1932,19 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     // with a window, what the tokens of one tile see
     const int64_t span = a.max_q < tile / group + 2 ? a.max_q : tile / group + 2;
     if (window && window + sinks + span < keys) keys = window + sinks + span;
-    // row tiles that hold rows: at most one per sequence is not full
-    int64_t tiles = a.total_q * group / tile + a.batch;
-    tiles = tiles < a.batch * pl.row_tiles ? tiles : a.batch * pl.row_tiles;
+    // row tiles that hold rows: where chunks differ in length, one of each sequence is
+    // half full as a rule
+    const bool ragged = a.total_q < a.batch * a.max_q;
+    int64_t tiles = a.batch * pl.row_tiles;
+    if (ragged) {
+        int64_t about = a.total_q * group / tile + a.batch / 2;
+        about = about > a.batch ? about : a.batch;
+        tiles = tiles < about ? tiles : about;
+    }
     const int64_t base = c.kv_heads * tiles;
     // Splits of the keys: as many as fill a number of workgroups, with at least so
     // many keys each.
-    const bool few = pl.kind == Plan::kFew, ragged = a.total_q < a.batch * a.max_q;
+    const bool few = pl.kind == Plan::kFew;
     const int64_t unit = few ? kUnit : 64;
     int64_t s = 1;
     const auto fill = [&](int64_t workgroups, int64_t least) {
@@ -1971,17 +1977,18 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
         // Prompts, whose partial sums are large: the least of rounds * (start of a
         // workgroup + its tiles of 64 keys) + join, in ns as measured (500 tokens, 32
         // heads, D = 256: 40 us in two splits, 30 whole; 512 of 8192 tokens 164 in two,
-        // 250 whole).  Where chunks differ in length contexts will: about two thirds of
-        // the workgroups have keys, and a tenth more than the chip holds costs little
-        // (24 chunks of 1 to 61 tokens, 61 to 5003 keys, 21 heads: D = 256 141 us
-        // whole, 116 in two; D = 128 138 and 90 in three; 16 of 16 to 64, 500 to 4000
-        // keys, 32 heads, D = 256: 118 whole, 131 in two).
+        // 250 whole).  Where chunks differ in length contexts will, and workgroups that
+        // have no keys leave at once: a quarter more than the chip holds is one round (16
+        // chunks of 1 to 32 tokens, 500 to 8000 keys, 32 heads, D = 128: 77 us with 256
+        // workgroups, 69 with 320, 97 with 384; D = 256, 24 of 1 to 61 tokens, 61 to
+        // 5003 keys, 21 heads: 141 whole, 116 in two; 16 of 16 to 64, 500 to 4000 keys,
+        // 32 heads: 118 whole, 131 in two).
         const int64_t held = c.head_dim == 64 ? 512 : 256, start = 7000, step = 1800;
         const int64_t n = (keys + 63) / 64, partial = a.total_q * a.heads * c.head_dim * 8 / 4000;
         int64_t best = INT64_MAX;
         for (int64_t t = 1; t <= kMaxSplits && (t == 1 || (t * 4 <= n && t * base <= 4 * held));
              t++) {
-            const int64_t all = ragged ? base * t * 2 / 3 * 10 / 11 : base * t;
+            const int64_t all = ragged ? base * t * 4 / 5 : base * t;
             const int64_t rounds = all > held ? (all + held - 1) / held : 1;
             const int64_t cost = rounds * (start + (n + t - 1) / t * step) +
                                  (t > 1 ? 4000 + t * partial : 0);
