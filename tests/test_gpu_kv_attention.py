@@ -154,6 +154,32 @@ def test_splits_of_the_keys(kvc, dim, chunk):
     b.check(kvc, window=100, sinks=5, max_len=100000)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("chunk", [1, 20, 150])
+def test_scores_that_rise_and_fall_along_the_keys(kvc, dim, chunk):
+    # the running maximum moves in nearly every step of the first half of the
+    # heads' rows, by little or by much, and in none of the others'
+    def edit(b, k, v):
+        ramp = torch.linspace(-20, 40, len(k))
+        k[:, 0, :16] = torch.sign(torch.randn(16, generator=torch.Generator().manual_seed(1))) * ramp[:, None]
+        k[:, 1, 16:32] = (ramp.flip(0) ** 3 / 1600)[:, None]
+    b = Batch(kvc, [700, 411], [chunk, chunk], 8, 2, dim, 16, 15, k_exp=-4, edit=edit)
+    b.check(kvc)
+    b.check(kvc, max_len=64)
+    b.check(kvc, window=200, sinks=70)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 64), (7, 1, 128), (6, 1, 256)])
+def test_many_lengths_at_once(kvc, heads, kv_heads, dim):
+    # decodes and chunks of all sizes in one call: tiles with few rows, with many, none
+    lens = [1, 16, 63, 64, 65, 128, 191, 300, 511, 640, 777, 900]
+    chunks = [1, 16, 2, 60, 65, 1, 0, 37, 5, 22, 1, 48]
+    b = Batch(kvc, lens, chunks, heads, kv_heads, dim, 32, 16)
+    for max_len in (None, 900, 6000):
+        b.check(kvc, max_len=max_len)
+    b.check(kvc, window=65, sinks=1)
+
+
 @pytest.mark.parametrize("chunk", [1, 33])
 def test_large_scores_and_scales(kvc, chunk):
     # sharp softmax (one key takes nearly all), tiny and huge q, scale 0
