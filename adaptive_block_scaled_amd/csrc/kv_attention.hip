@@ -283,11 +283,11 @@ __device__ __forceinline__ int larger(int a, int b) { return a > b ? a : b; }
 // waves' results are joined in LDS.
 //
 // Bound by memory while the rows are few: 64 sequences of 3001 to 12289 keys, 64
-// heads, D = 128 (566 MB): 119 us = 4.8 TB/s of a copy's 5.2; 4 of 100003 to 131071
-// (533 MB): 115 us.  One sequence of 4097 keys is latency: 7.2 us for a launch, the
-// lengths, the page table, the codes, one after another.  With 32 rows per tile the
-// decode has twice the products to hide behind: 16 chunks of 4 tokens over 8192
-// keys, 64 heads: 84 us, 1.8 TB/s.
+// heads, D = 128 (566 MB): 117 us = 4.8 TB/s of a copy's 5.2; 4 of 100003 to 131071
+// (533 MB): 108 us = 4.9 TB/s.  One sequence of 4097 keys is latency: 7 us for a
+// launch, the lengths, the page table, the codes, one after another.  With 32 rows per
+// tile two waves of a SIMD hide less of it: 16 chunks of 4 tokens over 8192 keys, 64
+// heads: 56 us, 2.8 TB/s.
 template <int D>
 struct UnitCodes {
     uint32_t k[2][D / 32], v[2][D / 32];
@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
 // instruction issue at a power-limited clock of about 2 GHz: the matrix cores are
 // busy half of the time, 6.5 other VALU instructions per product (decode 2, softmax
 // 3) share the issue of two waves, and a workgroup's start (lengths, pages, codes
-// and q one after another, then code that no cache holds yet) takes 5 to 7 us.
+// and q one after another, then code that no cache holds yet) takes about 5 us.
 constexpr int kPairWaves = 8, kPairThreads = 64 * kPairWaves;
 
 template <int D>
@@ -1760,7 +1760,7 @@ __global__ void __launch_bounds__(kPairThreads, 2) wide_kernel(const Args p) {
 
 // ---------------------------------------------------------------------------
 // Joins the splits of one row per workgroup: latency, 3.5 us for 64 rows of 33
-// splits, 5.6 for 256 rows of 94.  All waves read every split's m
+// splits, 4.9 for 256 rows of 32.  All waves read every split's m
 // and l at once, lane = split mod 64; then D/4 lanes read one split's
 // O as 16 bytes each, the workgroup 1024 / D splits side by side, so that the
 // whole row is a handful of independent loads.  (One wave per row with a loop
