@@ -53,6 +53,7 @@ struct Args {
     float *part_o, *part_ml;  // splits > 1: [splits][total_q * heads][D], [..][2]
     int64_t rows_all;         // total_q * heads
     int total_q, pages, kv_heads, heads, batch_heads, row_tiles, splits, split_units;
+    int above, upto;  // sequences with rows of a head in (above, upto] are this launch's
     int causal, window, sinks;
     Divisor tiles;  // of 16 tokens in a page
     Divisor group;  // query heads of a kv head
@@ -127,6 +128,20 @@ __device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int
                            head * (int)p.group.n + g;
         *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, 0.0f};
     }
+}
+
+// Whether a sequence is another launch's.  The join then leaves its rows alone: the sum
+// of their first split is -1, by one workgroup per head.
+__device__ __forceinline__ bool another_launch(const Args& p, const Sequence& s, int head, int rows,
+                                               int row0, int split) {
+    if (rows > p.above && rows <= p.upto) return false;
+    if (p.splits > 1 && row0 == 0 && split == 0)
+        for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+            const int t = (int)p.group.into(r), g = r - t * (int)p.group.n;
+            const int64_t at = (int64_t)(s.first_row + t) * p.heads + head * (int)p.group.n + g;
+            *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, -1.0f};
+        }
+    return true;
 }
 
 // First keys of the steps of `step` keys that every row of a tile sees whole:
@@ -369,7 +384,7 @@ few_rows_kernel(const Args p) {
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows) return;
+    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -821,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows) return;
+    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -1057,7 +1072,7 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows) return;
+    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -1423,7 +1438,7 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows) return;
+    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -1791,6 +1806,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
             part[i] = *reinterpret_cast<const f32x4*>(
                 p.part_o + ((split < p.splits ? split : 0) * p.rows_all + at) * D + 4 * d);
     }
+    if (__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(ml[0][1]))) < 0.0f)
+        return;  // (of split 0: another launch's row)
     uint64_t used[kPer];
     float top = ml[0][0], sum = 0.0f;
 #pragma unroll
@@ -1860,6 +1877,7 @@ __global__ void __launch_bounds__(kThreads) join_few_kernel(const Args p) {
             part[i] = *reinterpret_cast<const f32x4*>(
                 p.part_o + ((split < p.splits ? split : 0) * p.rows_all + at) * D + 4 * d);
     }
+    if (ml[0][1] < 0.0f) return;  // another launch's row
     float top = ml[0][0], sum = 0.0f;
 #pragma unroll
     for (int i = 1; i < kFewSplits; i++) top = __builtin_fmaxf(top, ml[i][0]);
@@ -1906,16 +1924,19 @@ struct Plan {
     int blocks;  // row blocks of 16 of a tile (few rows)
     int row_tiles;
     int splits, split_units;
+    int above, upto;      // rows of a head of its sequences
     int64_t ws_o, ws_ml;  // bytes
 };
 
-Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+// Of `batch` sequences with `total_q` tokens together, none with more than `max_q`.
+Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batch, int64_t total_q,
+             int64_t max_q) {
     Plan pl;
     // The kernels by rows of the longest chunk.  Up to 32 rows a wave decodes for
     // its own rows only; beyond, sharing the decode in LDS wins (60 rows of each of
     // 64 heads: 21 us against 28; 64 rows of 16 heads over 16k keys: 40 against
     // 54; 128 rows: 38 against 52).
-    const int64_t group = a.heads / c.kv_heads, rows = a.max_q * group;
+    const int64_t group = a.heads / c.kv_heads, rows = max_q * group;
     pl.kind = rows <= 32             ? Plan::kFew
               : c.head_dim == 256 ? Plan::kWide
               : rows > 128        ? Plan::kPrompt
@@ -1925,20 +1946,22 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
                      : pl.kind == Plan::kPrompt ? 256
                                                 : 128;
     pl.row_tiles = (int)((rows + tile - 1) / tile);
+    pl.above = 0;
+    pl.upto = INT32_MAX;
     int64_t keys = a.max_len;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
     const int64_t sinks = a.sinks < kMaxKeys ? a.sinks : kMaxKeys;
     // with a window, what the tokens of one tile see
-    const int64_t span = a.max_q < tile / group + 2 ? a.max_q : tile / group + 2;
+    const int64_t span = max_q < tile / group + 2 ? max_q : tile / group + 2;
     if (window && window + sinks + span < keys) keys = window + sinks + span;
     // row tiles that hold rows: where chunks differ in length, one of each sequence is
     // half full as a rule
-    const bool ragged = a.total_q < a.batch * a.max_q;
-    int64_t tiles = a.batch * pl.row_tiles;
+    const bool ragged = total_q < batch * max_q;
+    int64_t tiles = batch * pl.row_tiles;
     if (ragged) {
-        int64_t about = a.total_q * group / tile + a.batch / 2;
-        about = about > a.batch ? about : a.batch;
+        int64_t about = total_q * group / tile + batch / 2;
+        about = about > batch ? about : batch;
         tiles = tiles < about ? tiles : about;
     }
     const int64_t base = c.kv_heads * tiles;
@@ -1984,7 +2007,7 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
         // 5003 keys, 21 heads: 141 whole, 116 in two; 16 of 16 to 64, 500 to 4000 keys,
         // 32 heads: 118 whole, 131 in two).
         const int64_t held = c.head_dim == 64 ? 512 : 256, start = 7000, step = 1800;
-        const int64_t n = (keys + 63) / 64, partial = a.total_q * a.heads * c.head_dim * 8 / 4000;
+        const int64_t n = (keys + 63) / 64, partial = total_q * a.heads * c.head_dim * 8 / 4000;
         int64_t best = INT64_MAX;
         for (int64_t t = 1; t <= kMaxSplits && (t == 1 || (t * 4 <= n && t * base <= 4 * held));
              t++) {
@@ -2009,6 +2032,41 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     pl.ws_o = pl.splits > 1 ? pl.splits * rows_all * c.head_dim * 4 : 0;
     pl.ws_ml = pl.splits > 1 ? pl.splits * rows_all * 8 : 0;
     return pl;
+}
+
+// The launches of a call: one, or where most sequences bring much less than the longest
+// (single tokens beside a long chunk), one for those that fit a tile of few rows and
+// one for the rest, each with its own splits and join (32 single tokens and a chunk of
+// 512 over 4096 keys, 64 heads: 254 us in tiles of 256 rows all, so XX).
+struct Launches {
+    Plan of[2];
+    int n;
+    int64_t workspace;
+};
+Launches launches_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    Launches l;
+    l.n = 0;
+    const int64_t group = a.heads / c.kv_heads;
+    const int64_t few = group <= 16 || c.head_dim == 256 ? 16 : 32;
+    if (a.max_q * group > 32 && group <= few && a.total_q * 4 < a.batch * a.max_q) {
+        l.of[0] = plan_of(c, a, a.batch, a.batch, few / group);
+        l.of[0].upto = (int)few;
+        // as if all that is not single tokens came in chunks of the longest
+        int64_t rest = (a.total_q - a.batch + a.max_q - 2) / (a.max_q - 1);
+        rest = rest < 1 ? 1 : rest > a.batch ? a.batch : rest;
+        l.of[1] = plan_of(c, a, rest, rest * a.max_q, a.max_q);
+        l.of[1].above = (int)few;
+        l.n = 2;
+    } else {
+        l.of[0] = plan_of(c, a, a.batch, a.total_q, a.max_q);
+        l.n = 1;
+    }
+    l.workspace = 0;
+    for (int i = 0; i < l.n; i++) {
+        const int64_t need = l.of[i].ws_o + l.of[i].ws_ml;
+        l.workspace = l.workspace > need ? l.workspace : need;
+    }
+    return l;
 }
 
 template <int D>
@@ -2054,13 +2112,11 @@ int clamp_int(int64_t v) { return (int)(v > 0x3FFFFFFF ? 0x3FFFFFFF : v); }
 }  // namespace
 
 int64_t kv_attention_workspace(const if4_kv_cache& c, const if4_kv_attention_args& a) {
-    const Plan pl = plan_of(c, a);
-    return pl.ws_o + pl.ws_ml;
+    return launches_of(c, a).workspace;
 }
 
 hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_args& a,
                                void* workspace, hipStream_t stream) {
-    const Plan pl = plan_of(c, a);
     Args p;
     p.k_codes = c.k_codes;
     p.k_scales = c.k_scales;
@@ -2077,7 +2133,6 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.q_starts = a.q_starts;
     p.table_stride = c.pages > 0 ? a.table_stride : 0;  // no pages: no keys
     p.part_o = reinterpret_cast<float*>(workspace);
-    p.part_ml = p.part_o + pl.ws_o / 4;
     p.rows_all = a.total_q * a.heads;
     p.total_q = (int)a.total_q;
     p.pages = (int)c.pages;
@@ -2085,9 +2140,6 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.heads = (int)a.heads;
     p.group = Divisor(a.heads / c.kv_heads);
     p.batch_heads = (int)(a.batch * c.kv_heads);
-    p.row_tiles = pl.row_tiles;
-    p.splits = pl.splits;
-    p.split_units = pl.split_units;
     p.causal = a.causal != 0;
     p.window = clamp_int(a.window);
     p.sinks = clamp_int(a.sinks);
@@ -2095,9 +2147,21 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.q_scale = a.scale * 1.44269504f;
     p.k_exp = c.k_exp + 9;
     p.v_mul = pow2f(c.v_exp + 9);
-    if (c.head_dim == 64) return dispatch<64>(p, pl, stream);
-    if (c.head_dim == 128) return dispatch<128>(p, pl, stream);
-    return dispatch<256>(p, pl, stream);
+    const Launches l = launches_of(c, a);
+    for (int i = 0; i < l.n; i++) {
+        const Plan& pl = l.of[i];
+        p.part_ml = p.part_o + pl.ws_o / 4;
+        p.row_tiles = pl.row_tiles;
+        p.splits = pl.splits;
+        p.split_units = pl.split_units;
+        p.above = pl.above;
+        p.upto = pl.upto;
+        const hipError_t e = c.head_dim == 64    ? dispatch<64>(p, pl, stream)
+                             : c.head_dim == 128 ? dispatch<128>(p, pl, stream)
+                                                 : dispatch<256>(p, pl, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace if4

@@ -180,6 +180,19 @@ def test_many_lengths_at_once(kvc, heads, kv_heads, dim):
     b.check(kvc, window=65, sinks=1)
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 64), (24, 1, 64), (16, 2, 128), (6, 1, 256), (40, 1, 128)])
+def test_single_tokens_beside_a_long_chunk(kvc, heads, kv_heads, dim):
+    # most sequences bring one token or two, some none, one a chunk that is far longer
+    lens = [700, 33, 1, 400, 257, 64, 900, 5, 650, 310, 12, 800]
+    chunks = [1, 1, 1, 150, 1, 2, 1, 0, 1, 17, 1, 3]
+    b = Batch(kvc, lens, chunks, heads, kv_heads, dim, 16, 17)
+    for max_len in (None, 64, 900, 9000):
+        b.check(kvc, max_len=max_len)
+    b.check(kvc, window=100, sinks=3)
+    got = [b.run(kvc) for _ in range(3)]
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
 @pytest.mark.parametrize("chunk", [1, 33])
 def test_large_scores_and_scales(kvc, chunk):
     # sharp softmax (one key takes nearly all), tiny and huge q, scale 0
