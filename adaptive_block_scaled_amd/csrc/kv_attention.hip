@@ -53,6 +53,7 @@ struct Args {
     float *part_o, *part_ml;  // splits > 1: [splits][total_q * heads][D], [..][2]
     int64_t rows_all;         // total_q * heads
     int total_q, pages, kv_heads, heads, batch_heads, row_tiles, splits, split_units;
+    int batch, compact;  // see item_of
     int above, upto;  // sequences with rows of a head in (above, upto] are this launch's
     int causal, window, sinks;
     Divisor tiles;  // of 16 tokens in a page
@@ -141,6 +142,95 @@ __device__ __forceinline__ bool another_launch(const Args& p, const Sequence& s,
             const int64_t at = (int64_t)(s.first_row + t) * p.heads + head * (int)p.group.n + g;
             *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, -1.0f};
         }
+    return true;
+}
+
+// What a workgroup of the tiles of many rows does: a row tile of a (sequence, head)
+// pair, a split of its keys.  Pairs are fastest and the last row tiles, which see
+// the most keys, come first.  Where chunks differ in length (compact) the tiles that
+// hold rows and their splits that hold keys are counted, 64 sequences at a time, and
+// come first and without gaps: a grid of max_q for every sequence would be empty for
+// the most part, and workgroups that leave at once hold up those behind them, of which
+// each place on the chip gets its share in turn (6 chunks of 100 to 700 tokens over
+// 1000 to 6000 keys, 32 heads, D = 128: 279 us, so XX; 8 single tokens and a chunk of
+// 2048: 394, so XX).  Sequences of another launch have none; their rows are marked for
+// the join here.
+struct Item {
+    int b, head, row_tile, split;
+    int splits;  // of this sequence that may hold keys; the others are marked by split 0
+};
+template <int kRows, bool kTurn>
+__device__ __forceinline__ bool item_of(const Args& p, Item& it) {
+    const int index = blockIdx.x;
+    it.splits = p.splits;
+    if (!p.compact) {
+        const int rest = index / p.batch_heads;
+        // (workgroups 8 apart share an XCD: turned by 3 per row tile and split, those
+        // of one long sequence are spread over all of them)
+        const int bh = (index + (kTurn ? 3 * rest : 0)) % p.batch_heads;
+        it.row_tile = p.row_tiles - 1 - rest % p.row_tiles;
+        it.split = rest / p.row_tiles;
+        it.b = bh / p.kv_heads;
+        it.head = bh - it.b * p.kv_heads;
+        return true;
+    }
+    const int lane = threadIdx.x & 63;
+    int splits = 0;  // of this lane's sequence
+    const auto count = [&](int i) KV_INLINE {
+        if (i >= p.batch) return 0;
+        const Sequence s = sequence_of(p, i);
+        const int rows = s.rows * (int)p.group.n, n = (rows + kRows - 1) / kRows;
+        // (not less than any row tile has, see units_per_split)
+        splits = ((s.len + 63) / 64 + p.split_units - 1) / p.split_units;
+        splits = splits < p.splits ? splits > 0 ? splits : 1 : p.splits;
+        return rows > p.above && rows <= p.upto ? (n < p.row_tiles ? n : p.row_tiles) * splits : 0;
+    };
+    const auto up_to = [&](int n) KV_INLINE {  // inclusive sums over the lanes
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int other = __shfl_up(n, d);
+            n += lane >= d ? other : 0;
+        }
+        return n;
+    };
+    it.head = index % p.kv_heads;
+    if (p.above > 0 && p.splits > 1 && index < p.kv_heads)
+        for (int i = threadIdx.x; i < p.batch; i += blockDim.x) {
+            const Sequence s = sequence_of(p, i);
+            if (s.rows * (int)p.group.n > p.above) continue;
+            for (int t = 0; t < s.rows; t++)
+                for (int g = 0; g < (int)p.group.n; g++) {
+                    const int64_t at = (int64_t)(s.first_row + t) * p.heads +
+                                       it.head * (int)p.group.n + g;
+                    *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, -1.0f};
+                }
+        }
+    // the sums of all before sequences from .. from + 63, the last ones first
+    const int last = (p.batch - 1) & ~63;
+    int total = 0;
+    for (int i = 0; i < last; i += 64)
+        total += __builtin_amdgcn_readlane(up_to(count(i + lane)), 63);
+    int from = last, sums = up_to(count(from + lane)) + total;
+    int t = __builtin_amdgcn_readlane(sums, 63) - 1 - index / p.kv_heads;
+    if (t < 0) return false;
+    while (t < total) {
+        from -= 64;
+        if (from < 0) return false;
+        sums = up_to(count(from + lane));
+        total -= __builtin_amdgcn_readlane(sums, 63);
+        sums += total;
+    }
+    const int before = __builtin_popcountll(__builtin_amdgcn_ballot_w64(sums <= t));
+    if (before > 63) return false;
+    t -= before ? __builtin_amdgcn_readlane(sums, before - 1) : total;
+    it.b = from + before;
+    it.splits = __builtin_amdgcn_readlane(splits, before);
+    // row tiles fastest
+    const int all = __builtin_amdgcn_readlane(sums, before) -
+                    (before ? __builtin_amdgcn_readlane(sums, before - 1) : total);
+    const int tiles = all / it.splits;
+    it.split = t / tiles;
+    it.row_tile = t - it.split * tiles;
     return true;
 }
 
@@ -828,15 +918,17 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // (sequence, kv head) fastest, as for few rows; the last row tiles, which
-    // see the most keys, first
-    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
-    const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
-    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+    Item it;
+    if (!item_of<kRows, false>(p, it)) return;
+    const int b = __builtin_amdgcn_readfirstlane(it.b);
+    const int head = __builtin_amdgcn_readfirstlane(it.head);
+    const int row_tile = __builtin_amdgcn_readfirstlane(it.row_tile);
+    const int split = __builtin_amdgcn_readfirstlane(it.split);
+    const int own_splits = __builtin_amdgcn_readfirstlane(it.splits);
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
+    if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -844,6 +936,8 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
     const int per = units_per_split(p, units.n);
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
+    if (split == 0)
+        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s, head, row0, last_row, i);
     if (p.splits > 1 && begin >= end) {
         mark_empty(p, s, head, row0, last_row, split);
         return;
@@ -1065,14 +1159,17 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int unit16 = wave & 3;  // which 16 keys of a tile it decodes
-    const int bh = blockIdx.x % p.batch_heads;
-    const int rest = blockIdx.x / p.batch_heads;
-    const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
-    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+    Item it;
+    if (!item_of<kRows, false>(p, it)) return;
+    const int b = __builtin_amdgcn_readfirstlane(it.b);
+    const int head = __builtin_amdgcn_readfirstlane(it.head);
+    const int row_tile = __builtin_amdgcn_readfirstlane(it.row_tile);
+    const int split = __builtin_amdgcn_readfirstlane(it.split);
+    const int own_splits = __builtin_amdgcn_readfirstlane(it.splits);
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
+    if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -1081,6 +1178,8 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     const int per = units_per_split(p, units.n);
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
+    if (split == 0)
+        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s, head, row0, last_row, i);
     if (p.splits > 1 && begin >= end) {
         mark_empty(p, s, head, row0, last_row, split);
         return;
@@ -1430,15 +1529,17 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
     // which 32 rows, and which 16 keys of a tile it decodes
     const int pair = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
-    // (workgroups 8 apart share an XCD: turned by 3 per row tile and split, those of
-    // one long sequence are spread over all of them)
-    const int rest = blockIdx.x / p.batch_heads, bh = (blockIdx.x + 3 * rest) % p.batch_heads;
-    const int row_tile = p.row_tiles - 1 - rest % p.row_tiles, split = rest / p.row_tiles;
-    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+    Item it;
+    if (!item_of<kRows, true>(p, it)) return;
+    const int b = __builtin_amdgcn_readfirstlane(it.b);
+    const int head = __builtin_amdgcn_readfirstlane(it.head);
+    const int row_tile = __builtin_amdgcn_readfirstlane(it.row_tile);
+    const int split = __builtin_amdgcn_readfirstlane(it.split);
+    const int own_splits = __builtin_amdgcn_readfirstlane(it.splits);
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
+    if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -1447,6 +1548,8 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     const int per = units_per_split(p, units.n);
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
+    if (split == 0)
+        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s, head, row0, last_row, i);
     if (p.splits > 1 && begin >= end) {
         mark_empty(p, s, head, row0, last_row, split);
         return;
@@ -1924,6 +2027,8 @@ struct Plan {
     int blocks;  // row blocks of 16 of a tile (few rows)
     int row_tiles;
     int splits, split_units;
+    int64_t items;        // workgroups of a split
+    bool compact;
     int above, upto;      // rows of a head of its sequences
     int64_t ws_o, ws_ml;  // bytes
 };
@@ -1948,6 +2053,10 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
     pl.row_tiles = (int)((rows + tile - 1) / tile);
     pl.above = 0;
     pl.upto = INT32_MAX;
+    // each sequence has at most one tile that is not full
+    pl.compact = pl.kind != Plan::kFew && a.total_q < a.batch * a.max_q;
+    const int64_t most_tiles = a.total_q * group / tile + a.batch, all_tiles = a.batch * pl.row_tiles;
+    pl.items = c.kv_heads * (pl.compact && most_tiles < all_tiles ? most_tiles : all_tiles);
     int64_t keys = a.max_len;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
@@ -2070,13 +2179,13 @@ Launches launches_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
 }
 
 template <int D>
-hipError_t launch(void (*kernel)(Args), int threads, int lds, const Args& p, hipStream_t stream) {
+hipError_t launch(void (*kernel)(Args), int threads, int lds, int64_t grid, const Args& p,
+                  hipStream_t stream) {
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kernel,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    const int64_t grid = (int64_t)p.batch_heads * p.row_tiles * p.splits;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, stream, p);
     hipError_t e = hipGetLastError();
@@ -2094,17 +2203,19 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, const Args& p, hip
 
 template <int D>
 hipError_t dispatch(const Args& p, const Plan& pl, hipStream_t stream) {
+    if (pl.items > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t grid = pl.items * pl.splits;
     if constexpr (D <= 128) {
         if (pl.kind == Plan::kPrompt)
-            return launch<D>(prompt_kernel<D>, kPairThreads, PromptTile<D>::kLds, p, stream);
+            return launch<D>(prompt_kernel<D>, kPairThreads, PromptTile<D>::kLds, grid, p, stream);
         if (pl.kind == Plan::kMany)
-            return launch<D>(many_rows_kernel<D>, kThreads, ManyRows<D>::kLds, p, stream);
+            return launch<D>(many_rows_kernel<D>, kThreads, ManyRows<D>::kLds, grid, p, stream);
         if (pl.blocks == 2)
-            return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, p, stream);
+            return launch<D>(few_rows_kernel<D, 2>, kThreads, FewRows<D, 2>::kLds, grid, p, stream);
     } else if (pl.kind == Plan::kWide) {
-        return launch<D>(wide_kernel, kPairThreads, WideTile::kLds, p, stream);
+        return launch<D>(wide_kernel, kPairThreads, WideTile::kLds, grid, p, stream);
     }
-    return launch<D>(few_rows_kernel<D, 1>, kThreads, FewRows<D, 1>::kLds, p, stream);
+    return launch<D>(few_rows_kernel<D, 1>, kThreads, FewRows<D, 1>::kLds, grid, p, stream);
 }
 
 int clamp_int(int64_t v) { return (int)(v > 0x3FFFFFFF ? 0x3FFFFFFF : v); }
@@ -2140,6 +2251,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.heads = (int)a.heads;
     p.group = Divisor(a.heads / c.kv_heads);
     p.batch_heads = (int)(a.batch * c.kv_heads);
+    p.batch = (int)a.batch;
     p.causal = a.causal != 0;
     p.window = clamp_int(a.window);
     p.sinks = clamp_int(a.sinks);
@@ -2151,6 +2263,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     for (int i = 0; i < l.n; i++) {
         const Plan& pl = l.of[i];
         p.part_ml = p.part_o + pl.ws_o / 4;
+        p.compact = pl.compact;
         p.row_tiles = pl.row_tiles;
         p.splits = pl.splits;
         p.split_units = pl.split_units;
