@@ -152,8 +152,8 @@ __device__ __forceinline__ bool another_launch(const Args& p, const Sequence& s,
 // come first and without gaps: a grid of max_q for every sequence would be empty for
 // the most part, and workgroups that leave at once hold up those behind them, of which
 // each place on the chip gets its share in turn (6 chunks of 100 to 700 tokens over
-// 1000 to 6000 keys, 32 heads, D = 128: 279 us, so XX; 8 single tokens and a chunk of
-// 2048: 394, so XX).  Sequences of another launch have none; their rows are marked for
+// 1000 to 6000 keys, 32 heads, D = 128: 279 us, so 202; 24 of 1 to 61, 61 to 5003 keys, 21
+// heads, D = 256: 106, so 91).  Sequences of another launch have none; their rows are marked for
 // the join here.
 struct Item {
     int b, head, row_tile, split;
@@ -2033,10 +2033,13 @@ struct Plan {
     int64_t ws_o, ws_ml;  // bytes
 };
 
-// Of `batch` sequences with `total_q` tokens together, none with more than `max_q`.
+// Of `batch` sequences with `total_q` tokens together, none with more than `max_q`;
+// above: of those with more rows only.
 Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batch, int64_t total_q,
-             int64_t max_q) {
+             int64_t max_q, int64_t above) {
     Plan pl;
+    pl.above = (int)above;
+    pl.upto = INT32_MAX;
     // The kernels by rows of the longest chunk.  Up to 32 rows a wave decodes for
     // its own rows only; beyond, sharing the decode in LDS wins (60 rows of each of
     // 64 heads: 21 us against 28; 64 rows of 16 heads over 16k keys: 40 against
@@ -2051,12 +2054,6 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
                      : pl.kind == Plan::kPrompt ? 256
                                                 : 128;
     pl.row_tiles = (int)((rows + tile - 1) / tile);
-    pl.above = 0;
-    pl.upto = INT32_MAX;
-    // each sequence has at most one tile that is not full
-    pl.compact = pl.kind != Plan::kFew && a.total_q < a.batch * a.max_q;
-    const int64_t most_tiles = a.total_q * group / tile + a.batch, all_tiles = a.batch * pl.row_tiles;
-    pl.items = c.kv_heads * (pl.compact && most_tiles < all_tiles ? most_tiles : all_tiles);
     int64_t keys = a.max_len;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
@@ -2137,6 +2134,13 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
     if (few && s > 1) pl.split_units = (pl.split_units + kWaves - 1) / kWaves * kWaves;
     if (s > 1) s = (units + pl.split_units - 1) / pl.split_units;
     pl.splits = (int)s;
+    // Each sequence has at most one tile that is not full.  Counting costs a workgroup's
+    // start 1 to 2 us and pays where keys are split or a quarter of the grid would be
+    // empty (3 chunks of 700 to 1531 tokens, D = 64, window 1024: 62 us, so 60).
+    const int64_t most_tiles = a.total_q * group / tile + a.batch, all_tiles = a.batch * pl.row_tiles;
+    pl.compact = pl.kind != Plan::kFew && a.total_q < a.batch * a.max_q &&
+                 (above > 0 || s > 1 || most_tiles * 4 < all_tiles * 3);
+    pl.items = c.kv_heads * (pl.compact && most_tiles < all_tiles ? most_tiles : all_tiles);
     const int64_t rows_all = a.total_q * a.heads;
     pl.ws_o = pl.splits > 1 ? pl.splits * rows_all * c.head_dim * 4 : 0;
     pl.ws_ml = pl.splits > 1 ? pl.splits * rows_all * 8 : 0;
@@ -2146,7 +2150,7 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
 // The launches of a call: one, or where most sequences bring much less than the longest
 // (single tokens beside a long chunk), one for those that fit a tile of few rows and
 // one for the rest, each with its own splits and join (32 single tokens and a chunk of
-// 512 over 4096 keys, 64 heads: 254 us in tiles of 256 rows all, so XX).
+// 512 over 4096 keys, 64 heads: 254 us in tiles of 256 rows all, so 147).
 struct Launches {
     Plan of[2];
     int n;
@@ -2158,16 +2162,15 @@ Launches launches_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     const int64_t group = a.heads / c.kv_heads;
     const int64_t few = group <= 16 || c.head_dim == 256 ? 16 : 32;
     if (a.max_q * group > 32 && group <= few && a.total_q * 4 < a.batch * a.max_q) {
-        l.of[0] = plan_of(c, a, a.batch, a.batch, few / group);
+        l.of[0] = plan_of(c, a, a.batch, a.batch, few / group, 0);
         l.of[0].upto = (int)few;
         // as if all that is not single tokens came in chunks of the longest
         int64_t rest = (a.total_q - a.batch + a.max_q - 2) / (a.max_q - 1);
         rest = rest < 1 ? 1 : rest > a.batch ? a.batch : rest;
-        l.of[1] = plan_of(c, a, rest, rest * a.max_q, a.max_q);
-        l.of[1].above = (int)few;
+        l.of[1] = plan_of(c, a, rest, rest * a.max_q, a.max_q, few);
         l.n = 2;
     } else {
-        l.of[0] = plan_of(c, a, a.batch, a.total_q, a.max_q);
+        l.of[0] = plan_of(c, a, a.batch, a.total_q, a.max_q, 0);
         l.n = 1;
     }
     l.workspace = 0;
