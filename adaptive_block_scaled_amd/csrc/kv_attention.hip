@@ -54,6 +54,7 @@ struct Args {
     int64_t rows_all;         // total_q * heads
     int total_q, pages, kv_heads, heads, batch_heads, row_tiles, splits, split_units;
     int batch, compact;  // see item_of
+    int join_tokens;     // see joined_row
     int above, upto;  // sequences with rows of a head in (above, upto] are this launch's
     int causal, window, sinks;
     Divisor tiles;  // of 16 tokens in a page
@@ -129,20 +130,6 @@ __device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int
                            head * (int)p.group.n + g;
         *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, 0.0f};
     }
-}
-
-// Whether a sequence is another launch's.  The join then leaves its rows alone: the sum
-// of their first split is -1, by one workgroup per head.
-__device__ __forceinline__ bool another_launch(const Args& p, const Sequence& s, int head, int rows,
-                                               int row0, int split) {
-    if (rows > p.above && rows <= p.upto) return false;
-    if (p.splits > 1 && row0 == 0 && split == 0)
-        for (int r = threadIdx.x; r < rows; r += blockDim.x) {
-            const int t = (int)p.group.into(r), g = r - t * (int)p.group.n;
-            const int64_t at = (int64_t)(s.first_row + t) * p.heads + head * (int)p.group.n + g;
-            *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, -1.0f};
-        }
-    return true;
 }
 
 // What a workgroup of the tiles of many rows does: a row tile of a (sequence, head)
@@ -474,7 +461,7 @@ few_rows_kernel(const Args p) {
 
     const Sequence s = sequence_of(p, b);
     const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows || another_launch(p, s, head, rows, row0, split)) return;
+    if (row0 >= rows || rows > p.upto) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -1886,12 +1873,25 @@ __global__ void __launch_bounds__(kPairThreads, 2) wide_kernel(const Args p) {
 constexpr int kMaxSplits = 128;
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;  // of a length hint
 
+// Row of q and query head, as one number, of the join's n-th row; negative: none.  In a
+// launch of sequences with few rows (upto) n counts join_tokens for each sequence.
+__device__ __forceinline__ int64_t joined_row(const Args& p, int64_t n) {
+    if (p.join_tokens == 0) return n < p.rows_all ? n : -1;
+    const int64_t token = n / p.heads;
+    const int b = (int)(token / p.join_tokens), t = (int)(token - (int64_t)b * p.join_tokens);
+    if (b >= p.batch) return -1;
+    const Sequence s = sequence_of(p, b);
+    if (t >= s.rows || s.rows * (int)p.group.n > p.upto) return -1;
+    return (int64_t)(s.first_row + t) * p.heads + (n - token * p.heads);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
     constexpr int kLanes = D / 4, kSide = kThreads / kLanes, kRounds = kMaxSplits / kSide;
     __shared__ float weights[kMaxSplits];
     __shared__ __attribute__((aligned(16))) float sums[kThreads * 4];
-    const int64_t at = blockIdx.x;
+    const int64_t at = joined_row(p, blockIdx.x);
+    if (at < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, side = tid / kLanes, d = tid % kLanes;
     constexpr int kPer = kMaxSplits / 64;
     f32x2 ml[kPer];
@@ -1964,9 +1964,10 @@ constexpr int kFewSplits = 8;
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_few_kernel(const Args p) {
     constexpr int kLanes = D / 4, kSide = 64 / kLanes, kRounds = kFewSplits / kSide;
-    const int64_t at = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+    const int64_t at = joined_row(p, (int64_t)blockIdx.x * kWaves +
+                                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
     const int lane = threadIdx.x & 63, side = lane / kLanes, d = lane % kLanes;
-    if (at >= p.rows_all) return;
+    if (at < 0) return;
     f32x2 ml[kFewSplits];
 #pragma unroll
     for (int i = 0; i < kFewSplits; i++)
@@ -2150,7 +2151,8 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
 // The launches of a call: one, or where most sequences bring much less than the longest
 // (single tokens beside a long chunk), one for those that fit a tile of few rows and
 // one for the rest, each with its own splits and join (32 single tokens and a chunk of
-// 512 over 4096 keys, 64 heads: 254 us in tiles of 256 rows all, so 147).
+// 512 over 4096 keys, 64 heads: 254 us in tiles of 256 rows all, so 139; 8 and
+// a chunk of 2048: 329, 230, of which the chunk alone takes 209).
 struct Launches {
     Plan of[2];
     int n;
@@ -2193,14 +2195,13 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, int64_t grid, cons
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    if (p.rows_all > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int64_t rows = p.join_tokens ? (int64_t)p.batch * p.join_tokens * p.heads : p.rows_all;
+    if (rows > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (p.splits <= kFewSplits)
-        hipLaunchKernelGGL((join_few_kernel<D>),
-                           dim3((unsigned)((p.rows_all + kWaves - 1) / kWaves)), dim3(kThreads), 0,
-                           stream, p);
+        hipLaunchKernelGGL((join_few_kernel<D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
+                           dim3(kThreads), 0, stream, p);
     else
-        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)p.rows_all), dim3(kThreads), 0, stream,
-                           p);
+        hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)rows), dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -2272,6 +2273,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
         p.split_units = pl.split_units;
         p.above = pl.above;
         p.upto = pl.upto;
+        p.join_tokens = pl.upto < INT32_MAX ? pl.upto / (int)p.group.n : 0;
         const hipError_t e = c.head_dim == 64    ? dispatch<64>(p, pl, stream)
                              : c.head_dim == 128 ? dispatch<128>(p, pl, stream)
                                                  : dispatch<256>(p, pl, stream);
