@@ -2087,8 +2087,8 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
         // 10 us, whole 39).  Beyond that the join and the partial sums cost more
         // than fuller CUs bring, unless the splits are long: as many workgroups as
         // the chip holds where each has 1024 keys (64 heads, 8 kv heads, D = 128; 128
-        // keys each up to 3072 workgroups before: 32 sequences of 512 keys 16.0 us,
-        // so 10.6; 64 of 512 to 1024 26.9, 18.5; 8 of 1000 to 4000 20.3, 17.1; 4 of
+        // keys each up to three rounds of workgroups before: 32 sequences of 512 keys
+        // 16.0 us, so 10.6; 64 of 512 to 1024 26.9, 18.5; 8 of 1000 to 4000 20.3, 17.1; 4 of
         // 100003 to 131071 120, 114).  Where that leaves few splits of each sequence
         // a long one ends late: three rounds of long splits (64 of 3001 to 12289 keys
         // 127 us, so 123).
