@@ -65,7 +65,9 @@ struct Cache {
         c.kv_heads = t[0].size(1);
         c.page_size = t[0].size(2);
         const int64_t d = c.head_dim = 2 * t[0].size(3);
-        if ((d != 64 && d != 128 && d != 256) || c.page_size <= 0 || c.page_size % 16) return false;
+        if ((d != 64 && d != 128 && d != 256) || c.page_size <= 0 || c.page_size % 16 ||
+            c.kv_heads <= 0)
+            return false;
         const int64_t tiles = c.page_size / 16;
         if (t[0].scalar_type() != at::kByte || !t[0].is_contiguous() ||
             !plain(PyTuple_GET_ITEM(o, 1), t[1], at::kByte, device,

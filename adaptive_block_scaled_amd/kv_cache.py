@@ -83,12 +83,18 @@ class KVCache(NamedTuple):
 
 def empty(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> KVCache:
     """A cache of zeros (every slot reads as zeros)."""
+    _sizes(page_size, kv_heads, head_dim)
+    return KVCache(*(torch.zeros(shape, dtype=torch.uint8, device=device)
+                     for shape in _shapes(pages, page_size, kv_heads, head_dim)))
+
+
+def _sizes(page_size, kv_heads, head_dim):
     if head_dim not in HEAD_DIMS:
         raise ValueError(f"head_dim must be one of {HEAD_DIMS}, not {head_dim}")
     if page_size <= 0 or page_size % 16:
         raise ValueError(f"page_size must be a multiple of 16, not {page_size}")
-    return KVCache(*(torch.zeros(shape, dtype=torch.uint8, device=device)
-                     for shape in _shapes(pages, page_size, kv_heads, head_dim)))
+    if kv_heads <= 0:
+        raise ValueError(f"kv_heads must be positive, not {kv_heads}")
 
 
 def _shapes(pages, page_size, kv_heads, head_dim):
@@ -113,10 +119,7 @@ def _cache(cache: KVCache, k_exp: int, v_exp: int):
     if not isinstance(kc, torch.Tensor) or not kc.is_cuda or kc.dim() != 4:
         raise ValueError("k_codes must be a CUDA tensor [pages, kv_heads, page_size, D/2]")
     pages, kv_heads, page_size, half = kc.shape
-    if 2 * half not in HEAD_DIMS:
-        raise ValueError(f"head_dim must be one of {HEAD_DIMS}, not {2 * half}")
-    if page_size <= 0 or page_size % 16:
-        raise ValueError(f"page_size must be a multiple of 16, not {page_size}")
+    _sizes(page_size, kv_heads, 2 * half)
     u8, index = torch.uint8, kc.get_device()
     shapes = _shapes(pages, page_size, kv_heads, 2 * half)
     if not (_is(kc, shapes[0], u8, index) and _is(ks, shapes[1], u8, index) and
