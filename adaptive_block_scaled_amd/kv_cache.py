@@ -105,6 +105,14 @@ def _shapes(pages, page_size, kv_heads, head_dim):
             (pages, kv_heads, tiles, head_dim // GROUP, 16))
 
 
+def _held(v, bits):
+    """The int nearest to v that a C integer of `bits` bits holds.  ctypes takes the
+    low bits of a larger one, which can name a value in order; the nearest one
+    means the same to a size or a bound, and is refused where v has to be."""
+    top = 1 << (bits - 1)
+    return max(-top, min(int(v), top - 1))
+
+
 def _is(t, shape, dtype, index) -> bool:
     """Whether t is a contiguous tensor of this shape and type on CUDA device
     `index`: the check of a call that is in order.  It costs a third of a
@@ -127,7 +135,7 @@ def _cache(cache: KVCache, k_exp: int, v_exp: int):
         for t, name, shape in zip(cache, KVCache._fields, shapes):
             _need(t, name, shape, u8, kc.device)
     return _Cache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, page_size,
-                  kv_heads, 2 * half, int(k_exp), int(v_exp)), index
+                  kv_heads, 2 * half, _held(k_exp, 32), _held(v_exp, 32)), index
 
 
 def _vectors(t, name, shape, dtype, index):
@@ -167,7 +175,7 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     _plain(slots, "slots", shape[:1], torch.int64, index)
     (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
     st = lib.if4_kv_append(c, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), shape[0], kt, kh,
-                           vt, vh, slots.data_ptr(), int(mode), _raw_stream(index))
+                           vt, vh, slots.data_ptr(), _held(mode, 32), _raw_stream(index))
     if st:
         _check("if4_kv_append", st)
     return cache
@@ -254,9 +262,9 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_len
         _vectors(out, "out", shape, torch.bfloat16, index)
     (qt, qh, _), (ot, oh, _) = q.stride(), out.stride()
     a = _Attention(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, page_table.data_ptr(), width,
-                   seq_lens.data_ptr(), q_starts.data_ptr(), batch, total, heads, int(max_q),
-                   width * c.page_size if max_len is None else int(max_len), int(window),
-                   int(sinks), scale, 1 if causal else 0)
+                   seq_lens.data_ptr(), q_starts.data_ptr(), batch, total, heads, _held(max_q, 64),
+                   width * c.page_size if max_len is None else _held(max_len, 64),
+                   _held(window, 64), _held(sinks, 64), scale, 1 if causal else 0)
     need = lib.if4_kv_attention_workspace(c, a)
     if need < 0:
         _check("if4_kv_attention", -need)
@@ -279,8 +287,9 @@ def workspace_bytes(cache: KVCache, *, total_q: int, heads: int, batch: int, max
     """Bytes that attention() needs for these sizes: a program that captures
     calls in a graph, or makes many, allocates them once."""
     c, _ = _cache(cache, 0, 0)
-    a = _Attention(batch=batch, total_q=total_q, heads=heads, max_q=max_q, max_len=max_len,
-                   window=window, sinks=sinks, scale=1.0, causal=1)
+    sizes = dict(batch=batch, total_q=total_q, heads=heads, max_q=max_q, max_len=max_len,
+                 window=window, sinks=sinks)
+    a = _Attention(scale=1.0, causal=1, **{name: _held(n, 64) for name, n in sizes.items()})
     need = lib.if4_kv_attention_workspace(c, a)
     if need < 0:
         _check("if4_kv_attention_workspace", -need)
