@@ -52,7 +52,7 @@ struct Args {
     int64_t table_stride;
     float *part_o, *part_ml;  // splits > 1: [splits][total_q * heads][D], [..][2]
     int64_t rows_all;         // total_q * heads
-    int total_q, pages, kv_heads, heads, batch_heads, row_tiles, splits, split_units;
+    int total_q, max_q, pages, kv_heads, heads, batch_heads, row_tiles, splits, split_units;
     int batch, compact;  // see item_of
     int join_tokens;     // see joined_row
     int above, upto;  // sequences with rows of a head in (above, upto] are this launch's
@@ -69,6 +69,10 @@ struct Sequence {
     int first_row, rows;  // rows of q
     int len, pos0;        // keys, position of its first row
     const int32_t* table;
+    // tile rows of a kv head, those of the first max_q rows of q
+    __device__ __forceinline__ int tile_rows(const Args& p) const {
+        return (rows < p.max_q ? rows : p.max_q) * (int)p.group.n;
+    }
 };
 
 __device__ __forceinline__ Sequence sequence_of(const Args& p, int b) {
@@ -121,15 +125,43 @@ __device__ __forceinline__ int units_per_split(const Args& p, int n) {
     return own > p.split_units ? own : p.split_units;
 }
 
-// A split without keys: its rows' sums are zero, which the join skips.
-__device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int head, int row0,
-                                           int last_row, int split) {
+// A sum that no split has: the join leaves the row of out as it is.
+constexpr float kLeftAlone = -1.0f;
+
+// Tile rows row0 .. last_row of a split that nothing is computed for.  Without keys
+// (sum 0) the join skips the split.
+__device__ __forceinline__ void mark(const Args& p, const Sequence& s, int head, int row0,
+                                     int last_row, int split, float sum) {
     for (int r = row0 + threadIdx.x; r <= last_row; r += blockDim.x) {
         const int t = (int)p.group.into(r), g = r - t * (int)p.group.n;
         const int64_t at = split * p.rows_all + (int64_t)(s.first_row + t) * p.heads +
                            head * (int)p.group.n + g;
-        *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, 0.0f};
+        *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, sum};
     }
+}
+__device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int head, int row0,
+                                           int last_row, int split) {
+    mark(p, s, head, row0, last_row, split, 0.0f);
+}
+
+// Rows of q that no workgroup computes, for a join that goes over all rows: those
+// before the first sequence and behind the last one, and those past max_q of each.
+__device__ __forceinline__ void mark_ends(const Args& p, int head, int first, int end) {
+    const Sequence before = {0, first, 0, 0, nullptr}, behind = {end, p.total_q - end, 0, 0, nullptr};
+    mark(p, before, head, 0, before.rows * (int)p.group.n - 1, 0, kLeftAlone);
+    mark(p, behind, head, 0, behind.rows * (int)p.group.n - 1, 0, kLeftAlone);
+}
+__device__ __forceinline__ int last_token(const Args& p) {
+    const Sequence s = sequence_of(p, p.batch - 1);
+    return s.first_row + s.rows;
+}
+// (by the first workgroup of a sequence and head; item_of has marked the ends of a
+// compact grid, in which a sequence without rows has no workgroup)
+__device__ __forceinline__ void mark_unowned(const Args& p, const Sequence& s, int b, int head) {
+    mark(p, s, head, s.tile_rows(p), s.rows * (int)p.group.n - 1, 0, kLeftAlone);
+    if (p.compact || (b > 0 && b < p.batch - 1)) return;
+    mark_ends(p, head, b == 0 ? s.first_row : 0,
+              b == p.batch - 1 ? s.first_row + s.rows : p.total_q);
 }
 
 // What a workgroup of the tiles of many rows does: a row tile of a (sequence, head)
@@ -166,7 +198,7 @@ __device__ __forceinline__ bool item_of(const Args& p, Item& it) {
     const auto count = [&](int i) KV_INLINE {
         if (i >= p.batch) return 0;
         const Sequence s = sequence_of(p, i);
-        const int rows = s.rows * (int)p.group.n, n = (rows + kRows - 1) / kRows;
+        const int rows = s.rows * (int)p.group.n, n = (s.tile_rows(p) + kRows - 1) / kRows;
         // (not less than any row tile has, see units_per_split)
         splits = ((s.len + 63) / 64 + p.split_units - 1) / p.split_units;
         splits = splits < p.splits ? splits > 0 ? splits : 1 : p.splits;
@@ -181,6 +213,8 @@ __device__ __forceinline__ bool item_of(const Args& p, Item& it) {
         return n;
     };
     it.head = index % p.kv_heads;
+    if (p.splits > 1 && index < p.kv_heads)
+        mark_ends(p, it.head, sequence_of(p, 0).first_row, last_token(p));
     if (p.above > 0 && p.splits > 1 && index < p.kv_heads)
         for (int i = threadIdx.x; i < p.batch; i += blockDim.x) {
             const Sequence s = sequence_of(p, i);
@@ -189,7 +223,7 @@ __device__ __forceinline__ bool item_of(const Args& p, Item& it) {
                 for (int g = 0; g < (int)p.group.n; g++) {
                     const int64_t at = (int64_t)(s.first_row + t) * p.heads +
                                        it.head * (int)p.group.n + g;
-                    *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, -1.0f};
+                    *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, kLeftAlone};
                 }
         }
     // the sums of all before sequences from .. from + 63, the last ones first
@@ -460,8 +494,10 @@ few_rows_kernel(const Args p) {
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
-    if (row0 >= rows || rows > p.upto) return;
+    const int row0 = row_tile * kRows, rows = s.tile_rows(p);
+    if (p.splits > 1 && p.join_tokens == 0 && split == 0 && row_tile == 0)
+        mark_unowned(p, s, b, head);
+    if (row0 >= rows || s.rows * (int)p.group.n > p.upto) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
     const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(last_row);
@@ -914,7 +950,8 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
     const int own_splits = __builtin_amdgcn_readfirstlane(it.splits);
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
+    const int row0 = row_tile * kRows, rows = s.tile_rows(p);
+    if (p.splits > 1 && split == 0 && row_tile == 0) mark_unowned(p, s, b, head);
     if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
@@ -1155,7 +1192,8 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     const int own_splits = __builtin_amdgcn_readfirstlane(it.splits);
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
+    const int row0 = row_tile * kRows, rows = s.tile_rows(p);
+    if (p.splits > 1 && split == 0 && row_tile == 0) mark_unowned(p, s, b, head);
     if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
@@ -1525,7 +1563,8 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     const int own_splits = __builtin_amdgcn_readfirstlane(it.splits);
 
     const Sequence s = sequence_of(p, b);
-    const int row0 = row_tile * kRows, rows = s.rows * (int)p.group.n;
+    const int row0 = row_tile * kRows, rows = s.tile_rows(p);
+    if (p.splits > 1 && split == 0 && row_tile == 0) mark_unowned(p, s, b, head);
     if (row0 >= rows) return;
     const uint32_t four = opaque_four(p);
     const int last_row = (row0 + kRows < rows ? row0 + kRows : rows) - 1;
@@ -1910,7 +1949,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
                 p.part_o + ((split < p.splits ? split : 0) * p.rows_all + at) * D + 4 * d);
     }
     if (__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(ml[0][1]))) < 0.0f)
-        return;  // (of split 0: another launch's row)
+        return;  // (of split 0: another launch's row, or none's)
     uint64_t used[kPer];
     float top = ml[0][0], sum = 0.0f;
 #pragma unroll
@@ -1981,7 +2020,7 @@ __global__ void __launch_bounds__(kThreads) join_few_kernel(const Args p) {
             part[i] = *reinterpret_cast<const f32x4*>(
                 p.part_o + ((split < p.splits ? split : 0) * p.rows_all + at) * D + 4 * d);
     }
-    if (ml[0][1] < 0.0f) return;  // another launch's row
+    if (ml[0][1] < 0.0f) return;  // another launch's row, or none's
     float top = ml[0][0], sum = 0.0f;
 #pragma unroll
     for (int i = 1; i < kFewSplits; i++) top = __builtin_fmaxf(top, ml[i][0]);
@@ -2250,6 +2289,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.part_o = reinterpret_cast<float*>(workspace);
     p.rows_all = a.total_q * a.heads;
     p.total_q = (int)a.total_q;
+    p.max_q = (int)a.max_q;
     p.pages = (int)c.pages;
     p.kv_heads = (int)c.kv_heads;
     p.heads = (int)a.heads;

@@ -227,6 +227,9 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_len
     any sequence.  max_len: about how long the longest is (default: what the
     page table has room for); it only steers how the work is split.
 
+    Rows past a sequence's first max_q and rows of no sequence (a padded batch)
+    are not written: they keep what `out` holds, and are unset without one.
+
     A row at position p sees key j iff j <= p (causal) and, with a window, j >
     p - window or j < sinks.  Rows that see no key give zeros.  scale defaults
     to 1/sqrt(D).  Returns [total_q, heads, D] bf16; `out` may pass it

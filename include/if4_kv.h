@@ -93,9 +93,10 @@ int if4_kv_read(const if4_kv_cache* cache, const int64_t* slots, int64_t tokens,
  *   q_starts device int32 [batch + 1], ascending, 0 .. total_q
  *   seq_lens device int32 [batch]; a length below zero counts as zero, one above
  *            2^30 - 256 as that
- *   max_q    no sequence has more rows of q than this (further rows are not
- *            computed); max_len: about how long the longest sequence is (only
- *            the speed depends on it)
+ *   max_q    no sequence has more rows of q than this.  Rows of out past a sequence's
+ *            first max_q, before q_starts[0] and from q_starts[batch] on keep what
+ *            they hold (a batch may be padded)
+ *   max_len  about how long the longest sequence is (only the speed depends on it)
  *   workspace  device, 16-byte aligned, of if4_kv_attention_workspace() bytes
  *            (NULL where that is 0); holds nothing between calls
  * Arithmetic: K and V are decoded to fp16 with 2^-9 as if4_gemm decodes its
