@@ -245,14 +245,18 @@ __device__ __forceinline__ bool item_of(const Args& p, Item& it) {
     if (before > 63) return false;
     t -= before ? __builtin_amdgcn_readlane(sums, before - 1) : total;
     it.b = from + before;
+    if (it.b >= p.batch) return false;
     it.splits = __builtin_amdgcn_readlane(splits, before);
     // row tiles fastest
     const int all = __builtin_amdgcn_readlane(sums, before) -
                     (before ? __builtin_amdgcn_readlane(sums, before - 1) : total);
     const int tiles = all / it.splits;
+    // (where q_starts do not ascend, chunks can overlap and the sums pass 31 bits: no
+    // item outside the batch or its tiles comes of that)
+    if (t < 0 || t >= all || tiles <= 0) return false;
     it.split = t / tiles;
     it.row_tile = t - it.split * tiles;
-    return true;
+    return it.split < it.splits && it.row_tile < p.row_tiles;
 }
 
 // First keys of the steps of `step` keys that every row of a tile sees whole:
