@@ -2098,7 +2098,8 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
                      : pl.kind == Plan::kPrompt ? 256
                                                 : 128;
     pl.row_tiles = (int)((rows + tile - 1) / tile);
-    int64_t keys = a.max_len;
+    // (at least one, of which a split has at least one unit: kernels divide by its units)
+    int64_t keys = a.max_len > 0 ? a.max_len : 1;
     keys = keys < kMaxKeys ? keys : kMaxKeys;
     const int64_t window = a.window < kMaxKeys ? a.window : kMaxKeys;
     const int64_t sinks = a.sinks < kMaxKeys ? a.sinks : kMaxKeys;

@@ -94,3 +94,16 @@ def test_the_lower_edge_of_a_window(kvc, dim, heads, chunk, window):
             got = b.check(kvc, window=window, max_len=max_len)
             rows = np.isnan(got).any((1, 2))
             assert rows.any() == (shift == 1 or chunk > 4) and (chunk == 1 or not rows[-1])
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(2, 2, 64), (8, 2, 64), (40, 1, 128), (6, 1, 256)])
+def test_a_hint_of_no_keys(kvc, heads, kv_heads, dim):
+    # max_len = 0 is in order (only the speed depends on it), also by default, where the
+    # page table has no room; chunks that differ, so that workgroups count what there is
+    for chunks in ([1, 1, 1], [70, 1, 0, 3, 1, 1], [1, 1, 1, 1, 1, 1, 1, 90, 1]):
+        lens = [300, 40, 0, 7, 64, 1, 33, 200, 5][:len(chunks)]
+        b = Batch(kvc, lens, chunks, heads, kv_heads, dim, 16, 35)
+        b.check(kvc, max_len=0)
+        table, seq_lens, starts = b.device()
+        out = kvc.attention(b.q.cuda(), b.cache, table[:, :0].contiguous(), seq_lens, starts, max_q=max(chunks), **b.exps)
+        assert bool((out == 0).all())
