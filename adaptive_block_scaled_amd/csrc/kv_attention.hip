@@ -322,6 +322,12 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(t, half2v));
 }
 
+// sum + both fp16 values of h (v_dot2 adds two exactly): l sums what O's products see.
+__device__ __forceinline__ float add_half2(uint32_t h, float sum) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, h),
+                                  __builtin_bit_cast(half2v, 0x3C003C00u), sum, false);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const f32x2 t = {a, b};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(t, bf16x2));
@@ -616,12 +622,15 @@ few_rows_kernel(const Args p) {
                     for (int i = 0; i < 4; i++) o[d][nr][i] *= alpha;
             }
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
+            for (int j = 0; j < 8; j++)
                 x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], factor[nr], -m[nr]));
-                l[nr] += x[j];
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                h[j] = pack_half(x[2 * j], x[2 * j + 1]);
+                l[nr] = add_half2(h[j], l[nr]);
             }
-            prob[nr] = make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]),
-                                  pack_half(x[4], x[5]), pack_half(x[6], x[7]));
+            prob[nr] = make_uint4(h[0], h[1], h[2], h[3]);
         }
         VPiece<D> v[2];
 #pragma unroll
@@ -849,9 +858,7 @@ __device__ __forceinline__ void probabilities(const f32x16& x, float factor, flo
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         h[i] = pack_half(e[2 * i], e[2 * i + 1]);
-        sum[i & 1] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, h[i]),
-                                            __builtin_bit_cast(half2v, 0x3C003C00u), sum[i & 1],
-                                            false);
+        sum[i & 1] = add_half2(h[i], sum[i & 1]);
     }
     l = sum[0] + sum[1];
     prob[0] = make_uint4(h[0], h[1], h[2], h[3]);

@@ -1,0 +1,49 @@
+"""Attention over the KV cache where one key takes nearly all of a row: how the
+many small probabilities of a long context count."""
+import math
+
+import pytest
+
+from test_gpu_kv_attention import kvc  # noqa: F401  (the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+PAGE = 1024
+# (heads of the one kv head, dim): one token's rows for the kernels of 16 and 32 rows, of up to
+# 128, of prompts, and of wide heads
+ROWS = [(1, 64), (32, 64), (40, 64), (150, 64), (8, 128), (24, 128), (60, 128), (130, 128), (8, 256), (40, 256)]
+
+
+def one_large_key(kvc, keys, heads, dim, log2_p, first_v):
+    """One token over `keys` keys, the first of which has a score that is log2_p (in powers of
+    two) above all others'.  K is 6 in the first key and -6 in the others, V is 6 and
+    in the first key `first_v`: FP4 codes 7 and 15 at scale 1, all exact."""
+    cache = kvc.empty(keys // PAGE, PAGE, 1, dim)
+    cache.k_codes.fill_(0xFF)
+    cache.k_codes[0, 0, 0] = 0x77
+    cache.k_scales.fill_(0x38)
+    cache.v_codes.fill_(0x77)
+    cache.v_scales.fill_(0x38)
+    if first_v == 0:
+        cache.v_codes[0, 0, 0, :, 0] = 0
+    else:
+        assert first_v == 6
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.ones(1, heads, dim, dtype=torch.bfloat16, device="cuda")
+    scale = log2_p * math.log(2) / (12 * dim)
+    # (a hint of one key: no splits, so that one running maximum meets as many keys as can be)
+    return kvc.attention(q, cache, torch.arange(keys // PAGE, **i32)[None], torch.tensor([keys], **i32),
+                         torch.tensor([0, 1], **i32), max_q=1, max_len=1, scale=scale).double()
+
+
+@pytest.mark.parametrize("heads,dim", ROWS)
+@pytest.mark.parametrize("log2_p", [20.6, 23.4, 24.5, 25.02])
+def test_the_sum_is_that_of_the_rounded_probabilities(kvc, heads, dim, log2_p):
+    # all values are 6, so every row is 6 whatever the probabilities are, if the sum that
+    # it is divided by counts what the product with V counts.  What is left: sums in fp32
+    # (at most 2^20 / 4 / 4 additions in a row, of 2^-25 of the sum on average: 2^-9 at the
+    # worst) and the rounding to bf16 (2^-9)
+    out = one_large_key(kvc, 1 << 20, heads, dim, log2_p, 6)
+    assert float((out - 6).abs().max()) <= 6 * 2.0 ** -8
