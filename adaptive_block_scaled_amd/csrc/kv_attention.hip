@@ -14,6 +14,13 @@
 // where a score exceeds it by more than 8 (in powers of two): p <= 2^8 is far
 // inside fp16, and most units then need neither a cross-lane maximum nor a
 // rescale of the accumulators.
+//
+// Small probabilities.  fp16 holds what is 2^-14 in full and what is 2^-25 at all.  With
+// few rows m lies 7 below the largest score, and small ones keep 7 bits more.  The
+// other kernels leave it out: there one wave adds up to all keys of a row to one
+// accumulator, in which the matrix core rounds what is below 2^-24 of it, and with
+// probabilities finer than that the products and l no longer round alike (2^20 keys
+// of one value, the first with 2^24.5 times the others' weight: 0.5% low).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -39,7 +46,8 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kUnit = 32;             // keys that a wave takes at once
 constexpr float kLowest = -3.0e38f;   // running maximum before any key
-constexpr float kSlack = 8.0f;        // how far scores may exceed it
+constexpr float kSlack = 8.0f;        // how far scores may exceed the largest one it was raised to
+constexpr float kLift = 7.0f;         // how far it lies below that one, few rows
 constexpr int kMaxLen = 0x3FFFFF00;   // keys of a sequence
 constexpr int kHidden = 0x3FFFFF80;   // first key of a step that no row sees
 
@@ -303,7 +311,7 @@ __device__ __forceinline__ uint32_t cache_tile(const Args& p, int head, TileRef 
     return (uint32_t)(page * p.kv_heads + head) * p.tiles.n + r.rest;
 }
 
-// 4, as a value that the compiler cannot fold (see high_bytes).
+// 4, as a value that the compiler cannot fold (see HighBytes).
 __device__ __forceinline__ uint32_t opaque_four(const Args& p) {
     return 4u + ((uint32_t)p.total_q >> 31);
 }
@@ -338,6 +346,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float score_factor(const Args& p, int e) {
     const float c = __builtin_ldexpf(p.q_scale, p.k_exp + e);
     return __builtin_fminf(__builtin_fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
+}
+
+// How far a score x (of a row with this factor) lies above m: the exponent of its
+// probability, so that what does not exceed the slack is inside fp16 at any size of m.
+__device__ __forceinline__ float above(float x, float factor, float m) {
+    return __builtin_fmaf(x, factor, -m);
 }
 
 // Token, row of q and query head of tile row r (the last row's past the end).
@@ -608,9 +622,8 @@ few_rows_kernel(const Args p) {
             float top = x[0];
 #pragma unroll
             for (int j = 1; j < 8; j++) top = __builtin_fmaxf(top, x[j]);
-            top *= factor[nr];
-            if (__builtin_amdgcn_ballot_w64(top > m[nr] + kSlack) != 0) {
-                top = __builtin_fmaxf(top, m[nr]);
+            if (__builtin_amdgcn_ballot_w64(above(top, factor[nr], m[nr]) > kSlack + kLift) != 0) {
+                top = __builtin_fmaxf(above(top, factor[nr], kLift), m[nr]);
                 top = __builtin_fmaxf(top, __shfl_xor(top, 16));
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32));
                 const float alpha = __builtin_amdgcn_exp2f(m[nr] - top);
@@ -623,13 +636,16 @@ few_rows_kernel(const Args p) {
             }
 #pragma unroll
             for (int j = 0; j < 8; j++)
-                x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], factor[nr], -m[nr]));
+                x[j] = __builtin_amdgcn_exp2f(above(x[j], factor[nr], m[nr]));
+            // (a unit's sum first: added pair by pair, small ones to a large l lose more)
             uint32_t h[4];
+            float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 h[j] = pack_half(x[2 * j], x[2 * j + 1]);
-                l[nr] = add_half2(h[j], l[nr]);
+                sum = add_half2(h[j], sum);
             }
+            l[nr] += sum;
             prob[nr] = make_uint4(h[0], h[1], h[2], h[3]);
         }
         VPiece<D> v[2];

@@ -47,3 +47,41 @@ def test_the_sum_is_that_of_the_rounded_probabilities(kvc, heads, dim, log2_p):
     # worst) and the rounding to bf16 (2^-9)
     out = one_large_key(kvc, 1 << 20, heads, dim, log2_p, 6)
     assert float((out - 6).abs().max()) <= 6 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("heads,dim", [r for r in ROWS if r[0] <= 32])
+@pytest.mark.parametrize("log2_p", [16.3, 20.6, 23.4, 24.5, 25.2])
+def test_many_small_probabilities_count(kvc, heads, dim, log2_p):
+    # the first key takes nearly all and has V = 0, so a row is what 131071 small
+    # probabilities p make of V = 6.  In tiles of few rows probabilities carry 2^6 at the least
+    # where the largest one is 1, so fp16 holds p 2^6 within 2^-25 (or 2^-11 of it, where it is not
+    # subnormal); exp2 and its argument are within 2^-16 for scores of these sizes, the
+    # output's rounding 2^-9
+    keys = 1 << 17
+    out = one_large_key(kvc, keys, heads, dim, log2_p, 0)
+    p = (keys - 1) * 2.0 ** -log2_p
+    want = 6 * p / (1 + p)
+    far = max(2.0 ** (log2_p - 31), 2.0 ** -11) + 2.0 ** -9 + 2.0 ** -12
+    assert float((out / want - 1).abs().max()) <= far
+
+
+@pytest.mark.parametrize("heads,dim", ROWS)
+@pytest.mark.parametrize("log2_score", [10, 20, 24, 26])
+def test_scores_of_any_size_stay_finite(kvc, heads, dim, log2_score):
+    # scores of +- 2^log2_score powers of two, whose fp32 spacing reaches 4: the keys that score highest
+    # share a row, the others have nothing of it
+    cache = kvc.empty(2, PAGE, 1, dim)
+    cache.k_codes.fill_(0xFF)
+    cache.k_codes[1, 0, 7::64] = 0x77
+    cache.k_scales.fill_(0x38)
+    cache.v_codes.fill_(0x77)
+    cache.v_codes[1, 0, :, :, 7::8] = 0x55
+    cache.v_scales.fill_(0x38)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.ones(1, heads, dim, dtype=torch.bfloat16, device="cuda")
+    scale = 2.0 ** log2_score * math.log(2) / (6 * dim)
+    for max_len in (1, 2 * PAGE):
+        out = kvc.attention(q, cache, torch.arange(2, **i32)[None], torch.tensor([2 * PAGE], **i32),
+                            torch.tensor([0, 1], **i32), max_q=1, max_len=max_len, scale=scale).double()
+        # V: code 5 (3) in tokens 7, 15, .. of each tile, those of the keys 7, 71, .. among them
+        assert float((out - 3).abs().max()) <= 3 * 2.0 ** -8
