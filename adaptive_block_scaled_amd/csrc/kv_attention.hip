@@ -1536,8 +1536,9 @@ __global__ void __launch_bounds__(kPairThreads, D == 64 ? 4 : 2) prompt_kernel(c
 // of 32, waves 4-7 those of the odd ones.  Probabilities pass through LDS as they
 // are, operands of O's products, and so does the running maximum m, which both
 // use: it is read, raised if need be and written by one wave of the two at a time.
-// Raised are whole powers of two, so that probabilities that are still
-// to be used are scaled exactly.
+// Raised are whole powers of two, so that probabilities that are still to be used are
+// scaled exactly as far as fp16 holds them (down to 2^-14 of the largest one, in steps of
+// 2^-24 below), and rounded down, so that the largest is at least 1.
 //
 // As in prompt_rows one wave issues products (A: 16 of its next scores, 16 of O)
 // while the other does the VALU work of its step (B).  With c = 64-key tile:
@@ -1820,7 +1821,7 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
                 const float raised = __builtin_fmaxf(top, shared);
                 const float both = __builtin_fmaxf(raised, __shfl_xor(raised, 32));
                 // (from the lowest m or to an infinite one there is nothing to keep)
-                const float by = __builtin_ceilf(both - shared);
+                const float by = __builtin_floorf(both - shared);
                 next = by < 65536.0f ? shared + by : both;
                 const float alpha = __builtin_amdgcn_exp2f(-by);
 #pragma unroll

@@ -85,3 +85,33 @@ def test_scores_of_any_size_stay_finite(kvc, heads, dim, log2_score):
                             torch.tensor([0, 1], **i32), max_q=1, max_len=max_len, scale=scale).double()
         # V: code 5 (3) in tokens 7, 15, .. of each tile, those of the keys 7, 71, .. among them
         assert float((out - 3).abs().max()) <= 3 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("heads,dim", ROWS)
+def test_the_largest_probability_is_at_least_one(kvc, heads, dim):
+    # scores rise once, by a little more than a whole number of powers of two, and what is
+    # 2^-24.64 of the largest is left: half of the smallest fp16 number is 2^-25, so it
+    # counts as something if the largest probability is held as 1 or more.
+    # K: 64 keys with 13/16 of the dims at -6 and the rest at 6, one of 6, the others of -6;
+    # V is 6 in the others only.  A probability is 2^-25 off at the most, the output 2^-9,
+    # and the other roundings (exp2, sums of 2^16 / 16 additions, V's normaliser) 2^-10
+    keys, log2_p = 1 << 16, 24.64
+    cache = kvc.empty(keys // PAGE, PAGE, 1, dim)
+    cache.k_codes.fill_(0xFF)
+    cache.k_codes[0, 0, :64, :dim * 3 // 32] = 0x77
+    cache.k_codes[0, 0, 64] = 0x77
+    cache.k_scales.fill_(0x38)
+    cache.v_codes.fill_(0x77)
+    cache.v_codes[0, 0, :4] = 0
+    cache.v_codes[0, 0, 4, :, 0] = 0
+    cache.v_scales.fill_(0x38)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.ones(1, heads, dim, dtype=torch.bfloat16, device="cuda")
+    scale = log2_p * math.log(2) / (12 * dim)
+    out = kvc.attention(q, cache, torch.arange(keys // PAGE, **i32)[None], torch.tensor([keys], **i32),
+                        torch.tensor([0, 1], **i32), max_q=1, max_len=1, scale=scale).double()
+    rest = keys - 65
+    whole = 1 + 64 * 2.0 ** (-log2_p * 13 / 16) + rest * 2.0 ** -log2_p
+    want = 6 * rest * 2.0 ** -log2_p / whole
+    far = 6 * rest * 2.0 ** -25 + want * (2.0 ** -9 + 2.0 ** -10)
+    assert float((out - want).abs().max()) <= far
