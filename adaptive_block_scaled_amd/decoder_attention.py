@@ -33,13 +33,25 @@ class Pages:
 
     def extend(self, seq, tokens: int):
         """Room for `tokens` more of a sequence: their slots, as a list."""
-        pages, n = self.owned.setdefault(seq, []), self.lens.get(seq, 0)
-        while len(pages) * self.size < n + tokens:
-            if not self.free:
-                raise MemoryError("the cache has no free page")
-            pages.append(self.free.pop())
-        self.lens[seq] = n + tokens
-        return [pages[j // self.size] * self.size + j % self.size for j in range(n, n + tokens)]
+        return self.extend_all([seq], [tokens])
+
+    def extend_all(self, seqs, counts):
+        """Room for counts[i] more tokens of seqs[i], all different: their slots, one
+        sequence after another.  Where the free pages are too few for all of
+        them, none gets any."""
+        if len(set(seqs)) != len(seqs):
+            raise ValueError("a sequence comes twice")
+        missing = [-(-(self.lens.get(s, 0) + n) // self.size) - len(self.owned.get(s, ()))
+                   for s, n in zip(seqs, counts)]
+        if sum(missing) > len(self.free):
+            raise MemoryError("the cache has too few free pages")
+        slots = []
+        for seq, tokens, more in zip(seqs, counts, missing):
+            pages, n = self.owned.setdefault(seq, []), self.lens.get(seq, 0)
+            pages += [self.free.pop() for _ in range(more)]
+            self.lens[seq] = n + tokens
+            slots += [pages[j // self.size] * self.size + j % self.size for j in range(n, n + tokens)]
+        return slots
 
     def release(self, seq):
         self.free += self.owned.pop(seq, [])
@@ -83,7 +95,7 @@ class AttentionBlock:
         fp32."""
         h, kv, d = self.heads, self.kv_heads, self.dim
         qkv = self._linear(x, self.w_qkv, x_exp).view(-1, h + 2 * kv, d)
-        slots = [s for seq, n in zip(seqs, counts) for s in self.pages.extend(seq, n)]
+        slots = self.pages.extend_all(seqs, counts)
         kv_cache.append(self.cache, qkv[:, h:h + kv], qkv[:, h + kv:],
                         torch.tensor(slots, device=x.device), **self.exps)
         table, lens = self.pages.table(seqs)
