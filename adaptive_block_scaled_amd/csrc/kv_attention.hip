@@ -58,11 +58,11 @@ struct Args {
     int64_t q_st, q_sh, o_st, o_sh;
     const int32_t *page_table, *seq_lens, *q_starts;
     int64_t table_stride;
-    float *part_o, *part_ml;  // splits > 1: [splits][total_q * heads][D], [..][2]
-    int64_t rows_all;         // total_q * heads
+    float *part_o, *part_ml;  // splits > 1: [splits][rows_all][D], [..][2]
+    int64_t rows_all;         // rows of q times heads, or see part_row
     int total_q, max_q, pages, kv_heads, heads, batch_heads, row_tiles, splits, split_units;
     int batch, compact;  // see item_of
-    int join_tokens;     // see joined_row
+    int join_tokens;     // see part_row
     int above, upto;  // sequences with rows of a head in (above, upto] are this launch's
     int causal, window, sinks;
     Divisor tiles;  // of 16 tokens in a page
@@ -136,28 +136,33 @@ __device__ __forceinline__ int units_per_split(const Args& p, int n) {
 // A sum that no split has: the join leaves the row of out as it is.
 constexpr float kLeftAlone = -1.0f;
 
-// Tile rows row0 .. last_row of a split that nothing is computed for.  Without keys
-// (sum 0) the join skips the split.
-__device__ __forceinline__ void mark(const Args& p, const Sequence& s, int head, int row0,
-                                     int last_row, int split, float sum) {
+// First row of a sequence in the partial sums: that of q, and in the launch of
+// sequences with few rows (see launches_of) one of join_tokens rows for each of the batch.
+__device__ __forceinline__ int part_row(const Args& p, const Sequence& s, int b) {
+    return p.join_tokens == 0 ? s.first_row : b * p.join_tokens;
+}
+
+// Tile rows row0 .. last_row of a split that nothing is computed for, of the sequence whose
+// partial sums start at row `first`.  Without keys (sum 0) the join skips the split.
+__device__ __forceinline__ void mark(const Args& p, int first, int head, int row0, int last_row,
+                                     int split, float sum) {
     for (int r = row0 + threadIdx.x; r <= last_row; r += blockDim.x) {
         const int t = (int)p.group.into(r), g = r - t * (int)p.group.n;
-        const int64_t at = split * p.rows_all + (int64_t)(s.first_row + t) * p.heads +
+        const int64_t at = split * p.rows_all + (int64_t)(first + t) * p.heads +
                            head * (int)p.group.n + g;
         *reinterpret_cast<f32x2*>(p.part_ml + 2 * at) = f32x2{kLowest, sum};
     }
 }
-__device__ __forceinline__ void mark_empty(const Args& p, const Sequence& s, int head, int row0,
+__device__ __forceinline__ void mark_empty(const Args& p, int first, int head, int row0,
                                            int last_row, int split) {
-    mark(p, s, head, row0, last_row, split, 0.0f);
+    mark(p, first, head, row0, last_row, split, 0.0f);
 }
 
 // Rows of q that no workgroup computes, for a join that goes over all rows: those
 // before the first sequence and behind the last one, and those past max_q of each.
 __device__ __forceinline__ void mark_ends(const Args& p, int head, int first, int end) {
-    const Sequence before = {0, first, 0, 0, nullptr}, behind = {end, p.total_q - end, 0, 0, nullptr};
-    mark(p, before, head, 0, before.rows * (int)p.group.n - 1, 0, kLeftAlone);
-    mark(p, behind, head, 0, behind.rows * (int)p.group.n - 1, 0, kLeftAlone);
+    mark(p, 0, head, 0, first * (int)p.group.n - 1, 0, kLeftAlone);
+    mark(p, end, head, 0, (p.total_q - end) * (int)p.group.n - 1, 0, kLeftAlone);
 }
 __device__ __forceinline__ int last_token(const Args& p) {
     const Sequence s = sequence_of(p, p.batch - 1);
@@ -166,7 +171,7 @@ __device__ __forceinline__ int last_token(const Args& p) {
 // (by the first workgroup of a sequence and head; item_of has marked the ends of a
 // compact grid, in which a sequence without rows has no workgroup)
 __device__ __forceinline__ void mark_unowned(const Args& p, const Sequence& s, int b, int head) {
-    mark(p, s, head, s.tile_rows(p), s.rows * (int)p.group.n - 1, 0, kLeftAlone);
+    mark(p, s.first_row, head, s.tile_rows(p), s.rows * (int)p.group.n - 1, 0, kLeftAlone);
     if (p.compact || (b > 0 && b < p.batch - 1)) return;
     mark_ends(p, head, b == 0 ? s.first_row : 0,
               b == p.batch - 1 ? s.first_row + s.rows : p.total_q);
@@ -530,7 +535,7 @@ few_rows_kernel(const Args p) {
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
     if (p.splits > 1 && begin >= end) {
-        mark_empty(p, s, head, row0, last_row, split);
+        mark_empty(p, part_row(p, s, b), head, row0, last_row, split);
         return;
     }
     fill_scale_tables(tables, tid, kThreads);
@@ -770,7 +775,7 @@ few_rows_kernel(const Args p) {
 #pragma unroll
                 for (int d = 0; d < M; d += 2) dst[d / 2] = pack_bf16(acc[d] * f, acc[d + 1] * f);
             } else {
-                const int64_t at = split * p.rows_all + row * p.heads + hd;
+                const int64_t at = split * p.rows_all + (part_row(p, s, b) + t) * (int64_t)p.heads + hd;
                 float* dst = p.part_o + at * D + (tid & 15) * M;
 #pragma unroll
                 for (int d = 0; d < M; d++) dst[d] = acc[d];
@@ -988,9 +993,9 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
     if (split == 0)
-        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s, head, row0, last_row, i);
+        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s.first_row, head, row0, last_row, i);
     if (p.splits > 1 && begin >= end) {
-        mark_empty(p, s, head, row0, last_row, split);
+        mark_empty(p, s.first_row, head, row0, last_row, split);
         return;
     }
     fill_scale_tables(tables, tid, kThreads);
@@ -1231,9 +1236,9 @@ __device__ __forceinline__ void prompt_rows(const Args& p) {
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
     if (split == 0)
-        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s, head, row0, last_row, i);
+        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s.first_row, head, row0, last_row, i);
     if (p.splits > 1 && begin >= end) {
-        mark_empty(p, s, head, row0, last_row, split);
+        mark_empty(p, s.first_row, head, row0, last_row, split);
         return;
     }
     uint32_t poisoned = 0;  // groups of O that are NaN
@@ -1603,9 +1608,9 @@ __device__ __forceinline__ void wide_rows(const Args& p) {
     const int begin = split * per;
     const int end = begin + per < units.n ? begin + per : units.n;
     if (split == 0)
-        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s, head, row0, last_row, i);
+        for (int i = own_splits; i < p.splits; i++) mark_empty(p, s.first_row, head, row0, last_row, i);
     if (p.splits > 1 && begin >= end) {
-        mark_empty(p, s, head, row0, last_row, split);
+        mark_empty(p, s.first_row, head, row0, last_row, split);
         return;
     }
     uint32_t poisoned = 0;  // groups of O that are NaN
@@ -1940,13 +1945,12 @@ __global__ void __launch_bounds__(kPairThreads, 2) wide_kernel(const Args p) {
 constexpr int kMaxSplits = 128;
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;  // of a length hint
 
-// Row of q and query head, as one number, of the join's n-th row; negative: none.  In a
-// launch of sequences with few rows (upto) n counts join_tokens for each sequence.
+// Row of q and query head, as one number, of the n-th row of the partial sums; negative: none.
 __device__ __forceinline__ int64_t joined_row(const Args& p, int64_t n) {
-    if (p.join_tokens == 0) return n < p.rows_all ? n : -1;
+    if (n >= p.rows_all) return -1;
+    if (p.join_tokens == 0) return n;
     const int64_t token = n / p.heads;
     const int b = (int)(token / p.join_tokens), t = (int)(token - (int64_t)b * p.join_tokens);
-    if (b >= p.batch) return -1;
     const Sequence s = sequence_of(p, b);
     if (t >= s.rows || s.rows * (int)p.group.n > p.upto) return -1;
     return (int64_t)(s.first_row + t) * p.heads + (n - token * p.heads);
@@ -1957,8 +1961,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
     constexpr int kLanes = D / 4, kSide = kThreads / kLanes, kRounds = kMaxSplits / kSide;
     __shared__ float weights[kMaxSplits];
     __shared__ __attribute__((aligned(16))) float sums[kThreads * 4];
-    const int64_t at = joined_row(p, blockIdx.x);
-    if (at < 0) return;
+    const int64_t at = blockIdx.x, place = joined_row(p, at);
+    if (place < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, side = tid / kLanes, d = tid % kLanes;
     constexpr int kPer = kMaxSplits / 64;
     f32x2 ml[kPer];
@@ -2018,7 +2022,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args p) {
             for (int j = 0; j < 4; j++) acc[j] += o[j];
         }
         const float f = sum == 0.0f ? 0.0f : p.v_mul / sum;
-        const int64_t row = at / p.heads, hd = at - row * p.heads;
+        const int64_t row = place / p.heads, hd = place - row * p.heads;
         *reinterpret_cast<uint2*>(p.out + row * p.o_st + hd * p.o_sh + 4 * tid) =
             make_uint2(pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f));
     }
@@ -2031,10 +2035,11 @@ constexpr int kFewSplits = 8;
 template <int D>
 __global__ void __launch_bounds__(kThreads) join_few_kernel(const Args p) {
     constexpr int kLanes = D / 4, kSide = 64 / kLanes, kRounds = kFewSplits / kSide;
-    const int64_t at = joined_row(p, (int64_t)blockIdx.x * kWaves +
-                                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    const int64_t at = (int64_t)blockIdx.x * kWaves +
+                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6),
+                  place = joined_row(p, at);
     const int lane = threadIdx.x & 63, side = lane / kLanes, d = lane % kLanes;
-    if (at < 0) return;
+    if (place < 0) return;
     f32x2 ml[kFewSplits];
 #pragma unroll
     for (int i = 0; i < kFewSplits; i++)
@@ -2082,7 +2087,7 @@ __global__ void __launch_bounds__(kThreads) join_few_kernel(const Args p) {
         for (int j = 0; j < 4; j++) acc[j] += __shfl_xor(acc[j], i);
     if (side == 0) {
         const float f = sum == 0.0f ? 0.0f : p.v_mul / sum;
-        const int64_t row = at / p.heads, hd = at - row * p.heads;
+        const int64_t row = place / p.heads, hd = place - row * p.heads;
         *reinterpret_cast<uint2*>(p.out + row * p.o_st + hd * p.o_sh + 4 * d) =
             make_uint2(pack_bf16(acc[0] * f, acc[1] * f), pack_bf16(acc[2] * f, acc[3] * f));
     }
@@ -2098,13 +2103,23 @@ struct Plan {
     int64_t items;        // workgroups of a split
     bool compact;
     int above, upto;      // rows of a head of its sequences
+    int64_t rows_all;     // of the partial sums
     int64_t ws_o, ws_ml;  // bytes
 };
 
+// Rows that the partial sums of a launch have at the most, all splits together: 52 MB of
+// them for few rows, 277 MB for the others.  plan_of's rules stay below it: a launch of more than
+// one split has no more workgroups than 3 * held (few rows) or 4 * held, each with the rows of
+// a tile, and rows that fill less than a whole number of tiles at most twice that.  It
+// binds where rows of q are many beside those that the launch is for.
+int64_t most_partial_rows(const if4_kv_cache& c, bool few) {
+    return (few ? 12582912 : 67108864) / c.head_dim;
+}
+
 // Of `batch` sequences with `total_q` tokens together, none with more than `max_q`;
-// above: of those with more rows only.
+// above: of those with more rows only.  rows_all: of the partial sums.
 Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batch, int64_t total_q,
-             int64_t max_q, int64_t above) {
+             int64_t max_q, int64_t above, int64_t rows_all) {
     Plan pl;
     pl.above = (int)above;
     pl.upto = INT32_MAX;
@@ -2197,6 +2212,8 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
         }
     }
     s = s > kMaxSplits ? kMaxSplits : s;
+    const int64_t most = most_partial_rows(c, few) / rows_all;
+    s = s < most ? s : most > 1 ? most : 1;
     const int64_t units = (keys + unit - 1) / unit;
     pl.split_units = (int)((units + s - 1) / s);
     // whole rounds of the waves, and no split that the hint leaves empty
@@ -2210,7 +2227,7 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
     pl.compact = pl.kind != Plan::kFew && a.total_q < a.batch * a.max_q &&
                  (above > 0 || s > 1 || most_tiles * 4 < all_tiles * 3);
     pl.items = c.kv_heads * (pl.compact && most_tiles < all_tiles ? most_tiles : all_tiles);
-    const int64_t rows_all = a.total_q * a.heads;
+    pl.rows_all = rows_all;
     pl.ws_o = pl.splits > 1 ? pl.splits * rows_all * c.head_dim * 4 : 0;
     pl.ws_ml = pl.splits > 1 ? pl.splits * rows_all * 8 : 0;
     return pl;
@@ -2218,9 +2235,11 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a, int64_t batc
 
 // The launches of a call: one, or where most sequences bring much less than the longest
 // (single tokens beside a long chunk), one for those that fit a tile of few rows and
-// one for the rest, each with its own splits and join (32 single tokens and a chunk of
-// 512 over 4096 keys, 64 heads: 254 us in tiles of 256 rows all, so 139; 8 and
-// a chunk of 2048: 329, 230, of which the chunk alone takes 209).
+// one for the rest, each with its own splits, join and rows of partial sums (32 single
+// tokens and a chunk of 512 over 4096 keys, 64 heads: 254 us in tiles of 256 rows all, so
+// 139; 8 and a chunk of 2048: 329, 230, of which the chunk alone takes 209; with
+// partial sums for all rows of q in both launches the latter took a workspace of 479 MB,
+// so 4).
 struct Launches {
     Plan of[2];
     int n;
@@ -2232,15 +2251,15 @@ Launches launches_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     const int64_t group = a.heads / c.kv_heads;
     const int64_t few = group <= 16 || c.head_dim == 256 ? 16 : 32;
     if (a.max_q * group > 32 && group <= few && a.total_q * 4 < a.batch * a.max_q) {
-        l.of[0] = plan_of(c, a, a.batch, a.batch, few / group, 0);
+        l.of[0] = plan_of(c, a, a.batch, a.batch, few / group, 0, a.batch * (few / group) * a.heads);
         l.of[0].upto = (int)few;
         // as if all that is not single tokens came in chunks of the longest
         int64_t rest = (a.total_q - a.batch + a.max_q - 2) / (a.max_q - 1);
         rest = rest < 1 ? 1 : rest > a.batch ? a.batch : rest;
-        l.of[1] = plan_of(c, a, rest, rest * a.max_q, a.max_q, few);
+        l.of[1] = plan_of(c, a, rest, rest * a.max_q, a.max_q, few, a.total_q * a.heads);
         l.n = 2;
     } else {
-        l.of[0] = plan_of(c, a, a.batch, a.total_q, a.max_q, 0);
+        l.of[0] = plan_of(c, a, a.batch, a.total_q, a.max_q, 0, a.total_q * a.heads);
         l.n = 1;
     }
     l.workspace = 0;
@@ -2263,7 +2282,7 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, int64_t grid, cons
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t rows = p.join_tokens ? (int64_t)p.batch * p.join_tokens * p.heads : p.rows_all;
+    const int64_t rows = p.rows_all;
     if (rows > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (p.splits <= kFewSplits)
         hipLaunchKernelGGL((join_few_kernel<D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
@@ -2316,7 +2335,6 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     p.q_starts = a.q_starts;
     p.table_stride = c.pages > 0 ? a.table_stride : 0;  // no pages: no keys
     p.part_o = reinterpret_cast<float*>(workspace);
-    p.rows_all = a.total_q * a.heads;
     p.total_q = (int)a.total_q;
     p.max_q = (int)a.max_q;
     p.pages = (int)c.pages;
@@ -2335,6 +2353,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
     const Launches l = launches_of(c, a);
     for (int i = 0; i < l.n; i++) {
         const Plan& pl = l.of[i];
+        p.rows_all = pl.rows_all;
         p.part_ml = p.part_o + pl.ws_o / 4;
         p.compact = pl.compact;
         p.row_tiles = pl.row_tiles;
