@@ -255,6 +255,14 @@ int64_t if4_kv_attention_workspace(const if4_kv_cache* cache, const if4_kv_atten
     return if4::kv_attention_workspace(*cache, a);
 }
 
+int64_t if4_kv_attention_workspace_most(const if4_kv_cache* cache, const if4_kv_attention_args* args) {
+    const int st = check_attention(cache, args);
+    if (st != IF4_OK) return -st;
+    const if4_kv_attention_args a = bounded(*args);
+    if (a.batch == 0 || a.max_q == 0) return 0;
+    return if4::kv_attention_workspace_most(*cache, a);
+}
+
 int if4_kv_attention(const if4_kv_cache* cache, const if4_kv_attention_args* args, void* workspace,
                      int64_t workspace_bytes, void* stream) {
     int st = check_attention(cache, args);

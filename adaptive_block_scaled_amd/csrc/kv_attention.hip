@@ -2317,6 +2317,24 @@ int64_t kv_attention_workspace(const if4_kv_cache& c, const if4_kv_attention_arg
     return launches_of(c, a).workspace;
 }
 
+// What plan_of's choices stay within, as a function that grows with each size: splits by the
+// keys that one has at the least, rows of the partial sums by the tokens or, in a
+// launch of sequences with few rows, by a tile of each.
+int64_t kv_attention_workspace_most(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    const int64_t keys = a.max_len < kMaxKeys ? a.max_len : kMaxKeys;
+    const int64_t by_keys = (keys + kUnit * kWaves - 1) / (kUnit * kWaves);
+    const int64_t splits = by_keys < kMaxSplits ? by_keys : kMaxSplits;
+    if (splits <= 1) return 0;
+    const auto rows = [&](bool few, int64_t n) {
+        const int64_t most = most_partial_rows(c, few);
+        return n < most / splits ? n * splits : most;
+    };
+    const int64_t all = a.total_q * a.heads, tiles = a.batch * c.kv_heads * 32;
+    const int64_t few = rows(true, all > tiles ? all : tiles);
+    const int64_t many = a.max_q * (a.heads / c.kv_heads) > 32 ? rows(false, all) : 0;
+    return (few > many ? few : many) * (c.head_dim * 4 + 8);
+}
+
 hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_args& a,
                                void* workspace, hipStream_t stream) {
     Args p;

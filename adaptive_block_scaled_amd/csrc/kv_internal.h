@@ -20,6 +20,7 @@ hipError_t launch_kv_attention(const if4_kv_cache& c, const if4_kv_attention_arg
                                void* workspace, hipStream_t stream);
 
 int64_t kv_attention_workspace(const if4_kv_cache& c, const if4_kv_attention_args& a);
+int64_t kv_attention_workspace_most(const if4_kv_cache& c, const if4_kv_attention_args& a);
 
 // A divisor fixed for a call: m / n = m * magic >> shift for m < 2^31.  magic =
 // ceil(2^shift / n) with shift = 31 + ceil(log2 n) exceeds 2^shift / n by less than

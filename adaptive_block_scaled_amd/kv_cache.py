@@ -28,7 +28,8 @@ except ImportError as e:
     raise ImportError(f"the KV cache's C++ calls ({if4.HERE}/_kv_call.so) do not load ({e}); build them "
                       "with `python -m adaptive_block_scaled_amd.build`") from e
 
-EXPORTS = ("if4_kv_append", "if4_kv_read", "if4_kv_attention", "if4_kv_attention_workspace")
+EXPORTS = ("if4_kv_append", "if4_kv_read", "if4_kv_attention", "if4_kv_attention_workspace",
+           "if4_kv_attention_workspace_most")
 HEAD_DIMS = (64, 128, 256)
 
 
@@ -65,12 +66,13 @@ def _declare():
     lib.if4_kv_read.argtypes = [cache, vp, i64, vp, vp, ci, vp]
     lib.if4_kv_attention.restype = ci
     lib.if4_kv_attention.argtypes = [cache, args, vp, i64, vp]
-    lib.if4_kv_attention_workspace.restype = i64
-    lib.if4_kv_attention_workspace.argtypes = [cache, args]
+    for f in (lib.if4_kv_attention_workspace, lib.if4_kv_attention_workspace_most):
+        f.restype = i64
+        f.argtypes = [cache, args]
 
 
 _declare()
-_kv_call.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS))
+_kv_call.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS[:4]))
 
 
 class KVCache(NamedTuple):
@@ -287,13 +289,14 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_len
 
 def workspace_bytes(cache: KVCache, *, total_q: int, heads: int, batch: int, max_q: int,
                     max_len: int, window: int = 0, sinks: int = 0) -> int:
-    """Bytes that attention() needs for these sizes: a program that captures
-    calls in a graph, or makes many, allocates them once."""
+    """Bytes that are enough for every attention() of such a cache with no more of
+    these sizes, whatever its window: a program that captures calls in a graph, or
+    makes many, allocates them once."""
     c, _ = _cache(cache, 0, 0)
     sizes = dict(batch=batch, total_q=total_q, heads=heads, max_q=max_q, max_len=max_len,
                  window=window, sinks=sinks)
     a = _Attention(scale=1.0, causal=1, **{name: _held(n, 64) for name, n in sizes.items()})
-    need = lib.if4_kv_attention_workspace(c, a)
+    need = lib.if4_kv_attention_workspace_most(c, a)
     if need < 0:
-        _check("if4_kv_attention_workspace", -need)
+        _check("if4_kv_attention_workspace_most", -need)
     return need

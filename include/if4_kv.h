@@ -123,8 +123,14 @@ int if4_kv_attention(const if4_kv_cache* cache, const if4_kv_attention_args* arg
                      int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace that if4_kv_attention needs for these arguments (pointers
- * are not looked at), or a negative status code. */
+ * are not looked at), or a negative status code.  The keys are split to fill the
+ * chip, so a smaller batch or shorter contexts can need more. */
 int64_t if4_kv_attention_workspace(const if4_kv_cache* cache, const if4_kv_attention_args* args);
+
+/* Bytes that are enough for every call with this cache's heads and head_dim, these query
+ * heads, and no more of batch, total_q, max_q and max_len than here, whatever the
+ * window: for a workspace that is allocated once.  A negative status code as above. */
+int64_t if4_kv_attention_workspace_most(const if4_kv_cache* cache, const if4_kv_attention_args* args);
 
 #ifdef __cplusplus
 }

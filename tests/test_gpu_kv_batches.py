@@ -107,3 +107,20 @@ def test_a_hint_of_no_keys(kvc, heads, kv_heads, dim):
         table, seq_lens, starts = b.device()
         out = kvc.attention(b.q.cuda(), b.cache, table[:, :0].contiguous(), seq_lens, starts, max_q=max(chunks), **b.exps)
         assert bool((out == 0).all())
+
+
+def test_one_workspace_serves_a_batch_that_shrinks(kvc):
+    # sized once for the most; of these, 40 sequences fill the chip without splits and the
+    # fewer the more splits
+    b = Batch(kvc, [600 - i for i in range(40)], [1] * 40, 8, 8, 128, 16, 36)
+    table, lens, starts = b.device()
+    q = b.q.cuda()
+    need = kvc.workspace_bytes(b.cache, total_q=40, heads=8, batch=40, max_q=1, max_len=600)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = b.check(kvc, max_len=600)
+    for n in (40, 30, 11, 4, 1):
+        kw = dict(max_q=1, max_len=600, **b.exps)
+        got = kvc.attention(q[:n], b.cache, table[:n], lens[:n], starts[:n + 1], workspace=ws, **kw)
+        assert torch.equal(got, kvc.attention(q[:n], b.cache, table[:n], lens[:n], starts[:n + 1], **kw))
+        # (other splits: the rounding to bf16 and the arithmetic within, of values below 4)
+        assert np.abs(got.cpu().double().numpy() - want[:n]).max() < 2.0 ** -5
