@@ -1532,7 +1532,7 @@ __global__ void __launch_bounds__(kPairThreads, D == 64 ? 4 : 2) prompt_kernel(c
 }
 
 // ---------------------------------------------------------------------------
-// Wide heads (D = 256, more than 16 rows): tiles of 128 rows, 8 waves.
+// Wide heads (D = 256, more than 32 rows): tiles of 128 rows, 8 waves.
 //
 // Here the registers of one wave do not hold Q, O and the operands in flight, so
 // two waves of a SIMD, w and w + 4, share 32 rows: each has half of O's dims (the

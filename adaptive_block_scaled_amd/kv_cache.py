@@ -12,6 +12,9 @@ all work runs in the HIP kernels of libif4.so, on torch's current stream.  A
 call whose arguments are in order is marshalled in C++ (csrc/kv_call.cpp: 3 to
 5 us less than here, of calls that take 5 to 10); what that turns down comes to
 the checks below, which say what is wrong.
+
+These are operators of serving: none records a gradient, whatever its inputs
+require (as the rest of the binding does not).
 """
 import ctypes
 import math

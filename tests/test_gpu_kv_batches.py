@@ -124,3 +124,35 @@ def test_one_workspace_serves_a_batch_that_shrinks(kvc):
         assert torch.equal(got, kvc.attention(q[:n], b.cache, table[:n], lens[:n], starts[:n + 1], **kw))
         # (other splits: the rounding to bf16 and the arithmetic within, of values below 4)
         assert np.abs(got.cpu().double().numpy() - want[:n]).max() < 2.0 ** -5
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,chunks", [
+    (8, 1, 64, [16, 3, 11]), (8, 1, 128, [16, 3, 11]), (8, 2, 128, [150, 3, 90]), (8, 2, 64, [150, 3, 90]),
+    (6, 1, 256, [40, 3, 90]), (16, 2, 128, [1, 1, 1, 1, 2, 1, 1, 120, 1]),
+])
+def test_chunks_in_a_graph(kvc, heads, kv_heads, dim, chunks):
+    # every kernel and the join, replayed with other queries and lengths between eager calls
+    lens = [2100, 700, 900, 1, 64, 333, 40, 1700, 500][:len(chunks)]
+    b = Batch(kvc, lens, chunks, heads, kv_heads, dim, 16, 37)
+    table, seq_lens, starts = b.device()
+    q = b.q.cuda()
+    out = torch.empty_like(q)
+    sizes = dict(max_q=max(chunks), max_len=2100)
+    need = kvc.workspace_bytes(b.cache, total_q=len(q), heads=heads, batch=len(lens), **sizes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def step(out):
+        return kvc.attention(q, b.cache, table, seq_lens, starts, out=out, workspace=ws, **sizes, **b.exps)
+
+    step(out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out)
+    for i in range(4):
+        q.copy_(torch.randn_like(q.float()).bfloat16())
+        seq_lens.copy_((seq_lens - 1).clamp(min=0))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), step(torch.empty_like(q)).view(torch.int16)), i
+        torch.cuda.synchronize()
