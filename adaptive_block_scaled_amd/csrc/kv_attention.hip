@@ -438,8 +438,8 @@ __device__ __forceinline__ int larger(int a, int b) { return a > b ? a : b; }
 // waves' results are joined in LDS.
 //
 // Bound by memory while the rows are few: 64 sequences of 3001 to 12289 keys, 64
-// heads, D = 128 (566 MB): 117 us = 4.8 TB/s of a copy's 5.2; 4 of 100003 to 131071
-// (533 MB): 108 us = 4.9 TB/s.  One sequence of 4097 keys is latency: 7 us for a
+// heads, D = 128 (566 MB): 119 us = 4.8 TB/s of a copy's 5.2; 4 of 100003 to 131071
+// (533 MB): 111 us = 4.8 TB/s.  One sequence of 4097 keys is latency: 7 us for a
 // launch, the lengths, the page table, the codes, one after another.  With 32 rows per
 // tile two waves of a SIMD hide less of it: 16 chunks of 4 tokens over 8192 keys, 64
 // heads: 56 us, 2.8 TB/s.
@@ -943,9 +943,10 @@ __device__ __forceinline__ void store_row(const Args& p, const Sequence& s, int 
 //
 // Steps of 32 keys are pipelined: while the matrix cores compute the scores of
 // step k + 1, the VALU turns those of step k into probabilities, and while
-// they add step k to O, it decodes the next tile.  Bound by instruction issue, the
-// decode's and the softmax's beside the products': 4 chunks of 16 tokens over 16384
-// keys, 64 heads, D = 128 (128 rows each): 71 us, 483 TFLOP/s, 1.1 TB/s.
+// they add step k to O, it decodes the next tile.  4 chunks of 16 tokens over 16384
+// keys, 64 heads, D = 128 (128 rows each): 72 us with the join, 478 TFLOP/s, 1.1
+// TB/s.  No pipe is full: the matrix cores are busy 30% of the time and the VALU 44%, and
+// of a wave's time 36% go into waiting to issue and 26% into barriers, LDS and loads.
 template <int D>
 struct ManyRows {
     static constexpr int kTile = 64 * D * 2;  // bytes of K or V of 64 keys
@@ -1183,12 +1184,15 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 2) many_rows_kernel(co
 // into even slices of about four instructions behind each product: with a group's
 // unpacking in one piece, D = 128 was 1% slower, D = 256 3%.
 //
-// 2048 new of 16384 tokens, 64 heads, D = 128: 974 us, 1058 TFLOP/s (with all waves
-// in step, as in many_rows_kernel, 1161 us); D = 64: 587 us, 878 TFLOP/s.  Bound by
-// instruction issue at a power-limited clock of about 2 GHz: the matrix cores are
-// busy half of the time, 6.5 other VALU instructions per product (decode 2, softmax
-// 3) share the issue of two waves, and a workgroup's start (lengths, pages, codes
-// and q one after another, then code that no cache holds yet) takes about 5 us.
+// 2048 new of 16384 tokens, 64 heads, D = 128: 975 us, 1057 TFLOP/s (with all waves
+// in step, as in many_rows_kernel, 1161 us); D = 64: 611 us, 844 TFLOP/s, at a
+// power-limited clock of about 2 GHz.  No pipe is full: the matrix cores are busy 53% of the
+// time, and the VALU issues in 57%, with the products and 6.5 other instructions for each
+// (decode 2, softmax 3); of a wave's time 44% are issue, 36% waiting to issue and 20%
+// waiting at barriers and for LDS.  The phases are not alike, a tile's decode lies in
+// two of four, and each ends for all waves with its longest.  A workgroup's start (lengths,
+// pages, codes and q one after another, then code that no cache holds yet) takes about
+// 5 us.
 constexpr int kPairWaves = 8, kPairThreads = 64 * kPairWaves;
 
 template <int D>
@@ -1563,8 +1567,8 @@ __global__ void __launch_bounds__(kPairThreads, D == 64 ? 4 : 2) prompt_kernel(c
 // (Two workgroups per 256 rows that take half of O's dims each and both compute
 // all scores took 1.5 times the products and twice the softmax.)
 //
-// 2048 new of 16384 tokens, 32 heads: 990 us, 1041 TFLOP/s (the two workgroups:
-// 727).  Bound as prompt_rows is, with more decode per product, 128 rows sharing it
+// 2048 new of 16384 tokens, 32 heads: 995 to 1010 us, 1020 to 1036 TFLOP/s (the two
+// workgroups: 727).  Bound as prompt_rows is, with more decode per product, 128 rows sharing it
 // instead of 256.
 struct WideTile {
     static constexpr int D = 256, kRows = 128, kTile = 64 * D * 2;

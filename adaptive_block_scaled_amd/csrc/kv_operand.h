@@ -7,7 +7,10 @@
 // v_perm_b32 puts two such bytes into a pair of fp16 numbers, and one packed
 // multiply by the group's multiplier -- s' * 2^5 for FP4, fl16(6 s'/7 * 2^7)
 // for INT4 -- leaves every operand as (decoded value) * 2^-9: FP4 exactly,
-// INT4 with one fp16 rounding of |q| * fl16(6 s'/7).
+// INT4 with one fp16 rounding of |q| * fl16(6 s'/7): 2^-11 of the value, and not finer
+// than 2^-15 2^E, where the operand is subnormal (values below 2^-5 2^E; E is set so that a
+// tensor's largest reach some 2^11).  The matrix cores take fp16 and bf16 at the same
+// rate, and bf16 would keep three bits less of the INT4 values.
 #pragma once
 
 #include <hip/hip_runtime.h>

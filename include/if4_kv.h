@@ -102,8 +102,10 @@ int if4_kv_read(const if4_kv_cache* cache, const int64_t* slots, int64_t tokens,
  * Arithmetic: K and V are decoded to fp16 with 2^-9 as if4_gemm decodes its
  * operands, q is taken as fp16 after an exact power of two per row and head,
  * products are summed in fp32, probabilities are rounded to fp16 for the
- * second product (their sum is that of the rounded ones), the maximum, the sum and
- * the output are fp32 up to the one rounding of out to bf16.  Results do not depend on timing.
+ * second product (their sum is that of the rounded ones; the largest of a row in a split
+ * of its keys is 1 or more, and what is below 2^-25 of that counts for nothing), the
+ * maximum, the sum and the output are fp32 up to the one rounding of out to bf16.
+ * Results do not depend on timing.
  */
 typedef struct if4_kv_attention_args {
     const void* q;
