@@ -5,13 +5,19 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "../../include/if4_fp8.h"
 #include "../../include/if4_kv.h"
+#include "fp8_internal.h"
 #include "if4_internal.h"
 #include "kv_internal.h"
 
 namespace {
 
 constexpr int kMaxExp = 64;
+
+// Largest sizes of the FP8 entry points.
+constexpr int64_t kMaxSize = (int64_t)1 << 31, kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxK = (int64_t)1 << 22;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -44,6 +50,31 @@ int check_quantize_t(const void* x, int x_dtype, int64_t rows, int64_t cols, int
     if (rows == 0 || cols == 0) return IF4_OK;
     if (!x || !codes || !scales) return IF4_ERR_NULL;
     if (!aligned(x, elem_size(x_dtype)) || !aligned(codes, 8)) return IF4_ERR_ALIGN;
+    return IF4_OK;
+}
+
+// The contraction dimension, `along`, holds whole groups of 16; blocks (of one row or
+// square) are a grid dimension.
+int check_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                       int64_t along, int64_t others, int square, const uint8_t* codes,
+                       const uint8_t* scales) {
+    if (x_dtype != IF4_F32 && x_dtype != IF4_BF16) return IF4_ERR_DTYPE;
+    if (square != 0 && square != 1) return IF4_ERR_DTYPE;
+    if (rows < 0 || cols < 0 || along % 16 != 0 || ld_x < cols) return IF4_ERR_SHAPE;
+    if (rows > kMaxSize || cols > kMaxSize || ld_x > kMaxStride) return IF4_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return IF4_OK;
+    const int64_t blocks = (along + IF4_FP8_BLOCK - 1) / IF4_FP8_BLOCK;
+    if (others > 0x7FFFFFFF / blocks) return IF4_ERR_SHAPE;
+    if (!x || !codes || !scales) return IF4_ERR_NULL;
+    if (!aligned(x, 16) || (ld_x * elem_size(x_dtype)) % 16 != 0 || !aligned(codes, 16))
+        return IF4_ERR_ALIGN;
+    return IF4_OK;
+}
+
+// Sizes that the FP8 product's kernels index: rows of a tile by K in 31 bits.
+int check_fp8_gemm_sizes(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || K % 16 != 0) return IF4_ERR_SHAPE;
+    if (M > kMaxSize || N > kMaxSize || K > kMaxK) return IF4_ERR_SHAPE;
     return IF4_OK;
 }
 
@@ -206,6 +237,51 @@ int if4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_exp,
         return IF4_ERR_ALIGN;
     return hip_status(if4::launch_gemm(a_codes, a_scales, a_exp, w_codes, w_scales, w_exp, M,
                                        N, K, c, ldc, (hipStream_t)stream));
+}
+
+int if4_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                     int square, uint8_t* codes, uint8_t* scales, void* stream) {
+    const int st = check_fp8_quantize(x, x_dtype, rows, cols, ld_x, cols, rows, square, codes, scales);
+    if (st != IF4_OK || rows == 0 || cols == 0) return st;
+    return hip_status(if4::launch_fp8_quantize(x, x_dtype == IF4_BF16, rows, cols, ld_x, square,
+                                               codes, scales, (hipStream_t)stream));
+}
+
+int if4_fp8_quantize_t(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ld_x,
+                       int square, uint8_t* codes, uint8_t* scales, void* stream) {
+    const int st = check_fp8_quantize(x, x_dtype, rows, cols, ld_x, rows, cols, square, codes, scales);
+    if (st != IF4_OK || rows == 0 || cols == 0) return st;
+    return hip_status(if4::launch_fp8_quantize_t(x, x_dtype == IF4_BF16, rows, cols, ld_x, square,
+                                                 codes, scales, (hipStream_t)stream));
+}
+
+int64_t if4_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
+    const int st = check_fp8_gemm_sizes(M, N, K);
+    if (st != IF4_OK) return -st;
+    return M == 0 || N == 0 || K == 0 ? 0 : if4::fp8_gemm_workspace(M, N, K);
+}
+
+int if4_fp8_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                 const uint8_t* w_scales, int w_square, int64_t M, int64_t N, int64_t K, void* c,
+                 int c_dtype, int64_t ldc, void* workspace, int64_t workspace_bytes,
+                 void* stream) {
+    if (c_dtype != IF4_F32 && c_dtype != IF4_BF16) return IF4_ERR_DTYPE;
+    if (w_square != 0 && w_square != 1) return IF4_ERR_DTYPE;
+    const int st = check_fp8_gemm_sizes(M, N, K);
+    if (st != IF4_OK) return st;
+    if (ldc < N || ldc > kMaxStride) return IF4_ERR_SHAPE;
+    if (M == 0 || N == 0) return IF4_OK;
+    if (!c || (K > 0 && (!a_codes || !a_scales || !w_codes || !w_scales))) return IF4_ERR_NULL;
+    if (!aligned(c, elem_size(c_dtype)) ||
+        (K > 0 && (!aligned(a_codes, 16) || !aligned(w_codes, 16))))
+        return IF4_ERR_ALIGN;
+    const int64_t need = K > 0 ? if4::fp8_gemm_workspace(M, N, K) : 0;
+    if (need > 0 && !workspace) return IF4_ERR_NULL;
+    if (need > workspace_bytes) return IF4_ERR_SHAPE;
+    if (need > 0 && !aligned(workspace, 16)) return IF4_ERR_ALIGN;
+    return hip_status(if4::launch_fp8_gemm({a_codes, a_scales, w_codes, w_scales, w_square, M, N, K,
+                                            c, c_dtype == IF4_BF16, ldc, workspace},
+                                           (hipStream_t)stream));
 }
 
 int if4_kv_append(const if4_kv_cache* cache, const void* k, const void* v, int dtype,
