@@ -10,14 +10,17 @@
 #include "fp8_internal.h"
 #include "if4_internal.h"
 #include "kv_internal.h"
+#include "qk_internal.h"
 
 namespace {
 
 constexpr int kMaxExp = 64;
 
-// Largest sizes of the FP8 entry points.
+// Largest sizes of the FP8 entry points and of if4_norm_rotate.
 constexpr int64_t kMaxSize = (int64_t)1 << 31, kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxK = (int64_t)1 << 22;
+// Most heads of one kind that if4_norm_rotate takes.
+constexpr int64_t kMaxHeads = 65535;
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -68,6 +71,48 @@ int check_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, i
     if (!x || !codes || !scales) return IF4_ERR_NULL;
     if (!aligned(x, 16) || (ld_x * elem_size(x_dtype)) % 16 != 0 || !aligned(codes, 16))
         return IF4_ERR_ALIGN;
+    return IF4_OK;
+}
+
+int check_qk_part(const if4_qk_part& p, int64_t tokens, int size, int out_size, bool backward) {
+    if (p.heads == 0) return IF4_OK;
+    if (tokens > 0 && (!p.x || !p.y || (backward && !p.g))) return IF4_ERR_NULL;
+    if (!p.weight || (backward && !p.d_weight)) return IF4_ERR_NULL;
+    const int y_size = backward ? size : out_size;
+    if (!aligned(p.x, 16) || !aligned(p.y, 16) || !aligned(p.weight, 16)) return IF4_ERR_ALIGN;
+    if (backward && (!aligned(p.g, 16) || !aligned(p.d_weight, 4))) return IF4_ERR_ALIGN;
+    if (p.x_stride_token * size % 16 || p.x_stride_head * size % 16 ||
+        p.y_stride_token * y_size % 16 || p.y_stride_head * y_size % 16)
+        return IF4_ERR_ALIGN;
+    if (backward && (p.g_stride_token * out_size % 16 || p.g_stride_head * out_size % 16))
+        return IF4_ERR_ALIGN;
+    return IF4_OK;
+}
+
+int check_qk_sizes(const if4_qk_args& a) {
+    for (int t : {a.dtype, a.out_dtype})
+        if (t != IF4_F32 && t != IF4_BF16) return IF4_ERR_DTYPE;
+    if (a.interleaved != 0 && a.interleaved != 1) return IF4_ERR_DTYPE;
+    if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % 8) return IF4_ERR_SHAPE;
+    if (a.rotary < 0 || a.rotary > a.head_dim || a.rotary % 8) return IF4_ERR_SHAPE;
+    if (a.tokens < 0 || a.tokens > kMaxSize || a.table_rows < 0 || a.table_rows > kMaxSize)
+        return IF4_ERR_SHAPE;
+    for (int64_t h : {a.q.heads, a.k.heads})
+        if (h < 0 || h > kMaxHeads) return IF4_ERR_SHAPE;
+    if (!isfinite(a.eps) || a.eps < 0.0f) return IF4_ERR_RANGE;
+    return IF4_OK;
+}
+
+int check_qk(const if4_qk_args& a, bool backward) {
+    int st = check_qk_sizes(a);
+    if (st != IF4_OK) return st;
+    const int size = elem_size(a.dtype), out_size = elem_size(a.out_dtype);
+    for (const if4_qk_part* p : {&a.q, &a.k})
+        if ((st = check_qk_part(*p, a.tokens, size, out_size, backward)) != IF4_OK) return st;
+    if (a.tokens > 0 && a.q.heads + a.k.heads > 0) {
+        if (!a.positions || (a.rotary > 0 && a.table_rows > 0 && !a.table)) return IF4_ERR_NULL;
+        if (!aligned(a.positions, 8) || !aligned(a.table, 16)) return IF4_ERR_ALIGN;
+    }
     return IF4_OK;
 }
 
@@ -282,6 +327,30 @@ int if4_fp8_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t*
     return hip_status(if4::launch_fp8_gemm({a_codes, a_scales, w_codes, w_scales, w_square, M, N, K,
                                             c, c_dtype == IF4_BF16, ldc, workspace},
                                            (hipStream_t)stream));
+}
+
+int if4_norm_rotate(const if4_qk_args* args, void* stream) {
+    if (!args) return IF4_ERR_NULL;
+    const int st = check_qk(*args, false);
+    if (st != IF4_OK || args->tokens == 0 || args->q.heads + args->k.heads == 0) return st;
+    return hip_status(if4::launch_norm_rotate(*args, (hipStream_t)stream));
+}
+
+int64_t if4_norm_rotate_backward_workspace(const if4_qk_args* args) {
+    if (!args) return -IF4_ERR_NULL;
+    const int st = check_qk_sizes(*args);
+    return st != IF4_OK ? -st : if4::norm_rotate_backward_workspace(*args);
+}
+
+int if4_norm_rotate_backward(const if4_qk_args* args, void* workspace, int64_t workspace_bytes,
+                             void* stream) {
+    if (!args) return IF4_ERR_NULL;
+    const int st = check_qk(*args, true);
+    if (st != IF4_OK || args->q.heads + args->k.heads == 0) return st;
+    if (!workspace) return IF4_ERR_NULL;
+    if (workspace_bytes < if4::norm_rotate_backward_workspace(*args)) return IF4_ERR_SHAPE;
+    if (!aligned(workspace, 16)) return IF4_ERR_ALIGN;
+    return hip_status(if4::launch_norm_rotate_backward(*args, workspace, (hipStream_t)stream));
 }
 
 int if4_kv_append(const if4_kv_cache* cache, const void* k, const void* v, int dtype,
