@@ -29,7 +29,8 @@ CALLS = os.path.join(HERE, "_kv_call.so")
 CLANGXX = "/opt/rocm/llvm/bin/clang++"
 
 SOURCES = ["api.cpp", "quantize.hip", "dequantize.hip", "gemm.hip", "ifn.hip",
-           "fp8_quantize.hip", "fp8_gemm.hip", "qk.hip", "kv_cache.hip", "kv_attention.hip"]
+           "fp8_quantize.hip", "fp8_gemm.hip", "qk.hip", "kv_cache.hip",
+           "kv_attention.hip", "kv_weights.hip", "kv_evict.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

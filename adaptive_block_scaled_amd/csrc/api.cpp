@@ -7,8 +7,10 @@
 
 #include "../../include/if4_fp8.h"
 #include "../../include/if4_kv.h"
+#include "../../include/if4_kv_evict.h"
 #include "fp8_internal.h"
 #include "if4_internal.h"
+#include "kv_evict_internal.h"
 #include "kv_internal.h"
 #include "qk_internal.h"
 
@@ -163,6 +165,17 @@ int check_attention(const if4_kv_cache* cache, const if4_kv_attention_args* a) {
     if (a->window < 0 || a->sinks < 0 || (!a->causal && (a->window || a->sinks)))
         return IF4_ERR_RANGE;
     if (!isfinite(a->scale) || a->scale < 0.0f) return IF4_ERR_RANGE;
+    return IF4_OK;
+}
+
+// The sums of a call: `in` is read, `out` written where it is not NULL.
+int check_mass(const if4_kv_mass& m, int64_t batch, bool out_needed) {
+    if (m.mass_rows < 0 || m.mass_rows > kMaxIndex || m.width < 0 || m.width > kMaxIndex)
+        return IF4_ERR_SHAPE;
+    if (!m.rows && m.mass_rows < batch) return IF4_ERR_SHAPE;
+    if (m.mass_rows == 0 || m.width == 0) return IF4_OK;
+    if (!m.in || (out_needed && !m.out)) return IF4_ERR_NULL;
+    if (!aligned(m.in, 4) || !aligned(m.out, 4) || !aligned(m.rows, 4)) return IF4_ERR_ALIGN;
     return IF4_OK;
 }
 
@@ -429,6 +442,87 @@ int if4_kv_attention(const if4_kv_cache* cache, const if4_kv_attention_args* arg
     if (need > workspace_bytes) return IF4_ERR_SHAPE;
     if (!aligned(workspace, 16)) return IF4_ERR_ALIGN;
     return hip_status(if4::launch_kv_attention(*cache, a, workspace, (hipStream_t)stream));
+}
+
+int64_t if4_kv_weights_workspace(const if4_kv_cache* cache, const if4_kv_attention_args* args) {
+    const int st = check_attention(cache, args);
+    if (st != IF4_OK) return -st;
+    const if4_kv_attention_args a = bounded(*args);
+    return a.batch == 0 || a.max_q == 0 ? 0 : if4::kv_weights_workspace(*cache, a);
+}
+
+int64_t if4_kv_weights_workspace_most(const if4_kv_cache* cache, const if4_kv_attention_args* args) {
+    const int st = check_attention(cache, args);
+    if (st != IF4_OK) return -st;
+    const if4_kv_attention_args a = bounded(*args);
+    return a.batch == 0 || a.max_q == 0 ? 0 : if4::kv_weights_workspace_most(*cache, a);
+}
+
+int if4_kv_weights(const if4_kv_cache* cache, const if4_kv_attention_args* args,
+                   const if4_kv_mass* mass, void* workspace, int64_t workspace_bytes,
+                   void* stream) {
+    int st = check_attention(cache, args);
+    if (st != IF4_OK) return st;
+    if (!mass) return IF4_ERR_NULL;
+    const if4_kv_attention_args a = bounded(*args);
+    st = check_mass(*mass, a.batch, true);
+    if (st != IF4_OK) return st;
+    if (a.batch == 0 || a.max_q == 0) return IF4_OK;
+    if (!a.q || !a.seq_lens || !a.q_starts) return IF4_ERR_NULL;
+    if (a.table_stride > 0 && !a.page_table) return IF4_ERR_NULL;
+    st = check_cache_pointers(*cache);
+    if (st != IF4_OK) return st;
+    if (!aligned(a.q, 16) || !aligned(a.page_table, 4) || !aligned(a.seq_lens, 4) ||
+        !aligned(a.q_starts, 4) || a.q_stride_token % 8 || a.q_stride_head % 8)
+        return IF4_ERR_ALIGN;
+    const int64_t need = if4::kv_weights_workspace(*cache, a);
+    if (!workspace) return IF4_ERR_NULL;
+    if (need > workspace_bytes) return IF4_ERR_SHAPE;
+    if (!aligned(workspace, 16)) return IF4_ERR_ALIGN;
+    // no token has a place
+    if (cache->pages == 0 || a.table_stride == 0 || mass->mass_rows == 0 || mass->width == 0)
+        return IF4_OK;
+    return hip_status(if4::launch_kv_weights(*cache, a, *mass, workspace, (hipStream_t)stream));
+}
+
+int if4_kv_select(const if4_kv_mass* mass, const int32_t* seq_lens, int64_t batch,
+                  int64_t kv_heads, int64_t keep, int64_t recent, int64_t sinks, int32_t* kept,
+                  void* stream) {
+    if (!mass) return IF4_ERR_NULL;
+    if (batch < 0 || kv_heads <= 0 || kv_heads > kMaxKvHeads || batch > 0x7FFFFFFF / kv_heads)
+        return IF4_ERR_SHAPE;
+    if (keep < 0 || keep > kMaxIndex) return IF4_ERR_SHAPE;
+    if (recent < 0 || sinks < 0 || recent > keep || sinks > keep - recent) return IF4_ERR_RANGE;
+    const int st = check_mass(*mass, batch, false);
+    if (st != IF4_OK) return st;
+    if (batch == 0 || keep == 0) return IF4_OK;
+    if (!seq_lens || !kept) return IF4_ERR_NULL;
+    if (!aligned(seq_lens, 4) || !aligned(kept, 4)) return IF4_ERR_ALIGN;
+    return hip_status(if4::launch_kv_select(*mass, seq_lens, batch, kv_heads, keep, recent, sinks,
+                                            kept, (hipStream_t)stream));
+}
+
+int if4_kv_compact(const if4_kv_cache* cache, const int32_t* page_table, int64_t table_stride,
+                   const int32_t* kept, int64_t batch, int64_t keep, const int32_t* new_table,
+                   int64_t new_stride, void* stream) {
+    if (!cache) return IF4_ERR_NULL;
+    int st = check_cache(*cache);
+    if (st != IF4_OK) return st;
+    if (batch < 0 || keep < 0 || keep > kMaxIndex || table_stride < 0 || table_stride > kMaxIndex ||
+        new_stride < 0 || new_stride > kMaxIndex)
+        return IF4_ERR_SHAPE;
+    // workgroups, one for 16 tokens of a kv head, are a grid dimension
+    if (batch > 0x7FFFFFFF / cache->kv_heads ||
+        (batch > 0 && (keep + 15) / 16 > 0x7FFFFFFF / (batch * cache->kv_heads)))
+        return IF4_ERR_SHAPE;
+    if (batch == 0 || keep == 0 || table_stride == 0 || new_stride == 0 || cache->pages == 0)
+        return IF4_OK;
+    if (!page_table || !kept || !new_table) return IF4_ERR_NULL;
+    st = check_cache_pointers(*cache);
+    if (st != IF4_OK) return st;
+    if (!aligned(page_table, 4) || !aligned(kept, 4) || !aligned(new_table, 4)) return IF4_ERR_ALIGN;
+    return hip_status(if4::launch_kv_compact(*cache, page_table, table_stride, kept, batch, keep,
+                                             new_table, new_stride, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,511 @@
+// Attention weights added up per cached token, for gfx950 (definition in
+// include/if4_kv_evict.h).
+//
+// Two passes over the scores S^T = K Q^T, rows of a tile being (token, query head of one kv
+// head's group) pairs as in attention.  stats_kernel finds each row's maximum and sum over
+// the keys, by key splits; columns_kernel computes the scores again and adds
+// exp2(s - max - log2 sum) over the rows of every key, which it owns alone: no atomics, and
+// no order that depends on timing.
+//
+// A lane holds scores of one query row (matrix-core column) and 16 keys, so that a row's
+// maximum and sum, and a key's sum over row tiles, stay in registers until the end.
+//
+// K enters as 7 times its values: FP4's 7 c s' and INT4's 6 q s' have at most 9 bits, which
+// fp16 holds, so that nothing is rounded before the fp32 sums (decoded to its own value, an
+// INT4 code would be off by up to 2^-11 of it, more than the fp32 results allow).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kv_evict_internal.h"
+#include "kv_internal.h"
+#include "kv_operand.h"
+
+namespace if4 {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kUnit = 32;            // keys of a tile
+constexpr float kLowest = -3.0e38f;  // running maximum before any key
+constexpr float kSlack = 64.0f;      // how far scores may exceed the running maximum
+constexpr int kMaxLen = 0x3FFFFF00;  // keys of a sequence
+
+struct Args {
+    const uint8_t *k_codes, *k_scales;
+    const uint16_t* q;
+    int64_t q_st, q_sh;
+    const int32_t *page_table, *seq_lens, *q_starts;
+    int64_t table_stride;
+    if4_kv_mass mass;
+    f32x2* stats;  // [splits][rows of q x heads] maximum (in powers of two) and sum
+    int64_t stat_rows;
+    int total_q, max_q, pages, kv_heads, heads, batch_heads, row_blocks, splits;
+    int causal, window, sinks;
+    Divisor tiles;  // of 16 tokens in a page
+    Divisor group;  // query heads of a kv head
+    float q_scale;  // scale * log2(e) / 7
+    int k_exp;      // E of K plus the 12 of its operands
+};
+
+struct Sequence {
+    int first_row, rows;  // rows of q
+    int used;             // the first max_q of them
+    int len, pos0;        // keys, position of the first row
+    const int32_t* table;
+    int64_t mass_row;
+    bool there;
+};
+
+__device__ __forceinline__ Sequence sequence_of(const Args& p, int b) {
+    Sequence s;
+    int q0 = p.q_starts[b], q1 = p.q_starts[b + 1];
+    q0 = q0 < 0 ? 0 : q0 > p.total_q ? p.total_q : q0;
+    q1 = q1 < q0 ? q0 : q1 > p.total_q ? p.total_q : q1;
+    s.first_row = q0;
+    s.rows = q1 - q0;
+    s.used = s.rows < p.max_q ? s.rows : p.max_q;
+    int64_t room = p.table_stride * p.tiles.n * 16;
+    room = room < kMaxLen ? room : kMaxLen;
+    const int64_t len = p.seq_lens[b];
+    s.len = (int)(len < 0 ? 0 : len > room ? room : len);
+    s.pos0 = s.len - s.rows;
+    s.table = p.page_table + b * p.table_stride;
+    s.mass_row = p.mass.rows ? p.mass.rows[b] : b;
+    s.there = s.rows > 0 && s.mass_row >= 0 && s.mass_row < p.mass.mass_rows;
+    return s;
+}
+
+// Row of the cache (token of one kv head) that holds key j; j past the last key gives a
+// row of the last tile.
+__device__ __forceinline__ int64_t cache_row(const Args& p, const Sequence& s, int head, int j) {
+    const int last = s.len > 0 ? (s.len - 1) >> 4 : 0;
+    const uint32_t t = (uint32_t)((j >> 4) < last ? j >> 4 : last), i = p.tiles.into(t);
+    int page = s.table[i];
+    page = page < p.pages - 1 ? page : p.pages - 1;
+    page = page > 0 ? page : 0;
+    return ((int64_t)(page * p.kv_heads + head) * p.tiles.n + (t - i * p.tiles.n)) * 16 + (j & 15);
+}
+
+// The multipliers of 7 K 2^-12 2^-E, one per scale byte (see GroupScale).
+__device__ __forceinline__ void fill_table(uint2* table, int tid) {
+    const float sp = __builtin_amdgcn_cvt_scalef32_f32_fp8((uint32_t)tid & 0x7Fu, 1.0f, 0);
+    const bool int4 = (tid & 0x80) != 0;
+    const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)(sp * (int4 ? 96.0f : 28.0f)));
+    table[tid] = make_uint2(h | h << 16, int4 ? 0u : 0x00010001u);
+}
+
+// One key's half row: lane l has key l % 32 of a tile, dims D/2 * (l / 32) on.
+template <int D>
+struct KeyCodes {
+    uint32_t w[D / 16];  // 8 codes each
+    uint32_t s[D == 256 ? 2 : 1];
+    __device__ __forceinline__ void load(const Args& p, int64_t row, int h) {
+        const uint8_t* const c = p.k_codes + row * (D / 2) + h * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 64; i++) {
+            const uint4 v = reinterpret_cast<const uint4*>(c)[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+        const uint8_t* const b = p.k_scales + row * (D / 16) + h * (D / 32);
+        if constexpr (D == 64) {
+            s[0] = *reinterpret_cast<const uint16_t*>(b);
+        } else if constexpr (D == 128) {
+            s[0] = *reinterpret_cast<const uint32_t*>(b);
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(b);
+            s[0] = v.x, s[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void decode(const uint2* table, uint32_t four, half8 (&k)[D / 16]) const {
+#pragma unroll
+        for (int g = 0; g < D / 32; g++) {
+            KGroup u;
+            u.unpack(w[2 * g], w[2 * g + 1], k_scale(table, (s[g / 4] >> (8 * (g % 4))) & 0xFFu), four);
+            k[2 * g] = u.template operand<0>();
+            k[2 * g + 1] = u.template operand<1>();
+        }
+    }
+};
+
+// q of tile row r for lane half h, in fp16 after division by the power of two that brings
+// the row's largest magnitude into [1, 2); returns the factor of its scores.  A row
+// with an infinity or NaN becomes NaN as a whole.
+template <int D>
+__device__ __forceinline__ float load_q(const Args& p, const Sequence& s, int kv_head, int r, int h,
+                                        half8 (&q)[D / 16]) {
+    const int token = (int)p.group.into(r), m = r - token * (int)p.group.n;
+    const uint16_t* const x = p.q + (s.first_row + token) * p.q_st +
+                              (kv_head * (int)p.group.n + m) * p.q_sh + h * (D / 2);
+    uint4 v[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) v[i] = reinterpret_cast<const uint4*>(x)[i];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
+            top = top > lo ? top : lo;
+            top = top > hi ? top : hi;
+        }
+    }
+    const uint32_t other = (uint32_t)__shfl_xor((int)top, 32);
+    top = top > other ? top : other;
+    const int e = top == 0 ? 0 : (int)(top >> 7) - 127;
+    const float by = top < 0x7F80u ? __builtin_ldexpf(1.0f, -e) : __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            q[i][2 * j] = (_Float16)(__uint_as_float(w[j] << 16) * by);
+            q[i][2 * j + 1] = (_Float16)(__uint_as_float(w[j] & 0xFFFF0000u) * by);
+        }
+    }
+    // finite and above zero, so that a hidden key's -inf stays -inf
+    const float c = __builtin_ldexpf(p.q_scale, p.k_exp + e);
+    return __builtin_fminf(__builtin_fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
+}
+
+template <int D>
+__device__ __forceinline__ f32x16 scores(const half8 (&k)[D / 16], const half8 (&q)[D / 16]) {
+    f32x16 x = {};
+#pragma unroll
+    for (int t = 0; t < D / 16; t++) x = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[t], q[t], x, 0, 0, 0);
+    return x;
+}
+
+// Whether rows at positions lo .. hi all see keys first .. first + 31, and whether any of
+// them may see any.
+__device__ __forceinline__ bool all_seen(const Args& p, int len, int lo, int hi, int first) {
+    const int end = first + kUnit - 1;
+    return end < len && (!p.causal || end <= lo) && (!p.window || first > hi - p.window || end < p.sinks);
+}
+__device__ __forceinline__ bool any_seen(const Args& p, int len, int lo, int hi, int first) {
+    return first < len && (!p.causal || first <= hi) &&
+           (!p.window || first + kUnit - 1 > lo - p.window || first < p.sinks);
+}
+
+// Scores of keys that the row at `pos` does not see become -inf.  x[i] is that of key
+// first + 4 h + 8 (i / 4) + i % 4.
+__device__ __forceinline__ void hide(const Args& p, int len, int pos, int first, f32x16& x) {
+    const int last = p.causal && pos < len - 1 ? pos : len - 1;
+    const int lo = p.window ? pos - p.window : -1;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const int j = first + 8 * (i >> 2) + (i & 3);
+        x[i] = j <= last && (j > lo || j < p.sinks) ? x[i] : -__builtin_inff();
+    }
+}
+
+// The tiles of keys that rows at positions lo .. hi see: the first `sink`, then those from
+// `start` on.
+struct KeyTiles {
+    int sink, start, n;
+    __device__ __forceinline__ KeyTiles(const Args& p, int len, int lo, int hi) {
+        const int end = p.causal ? (hi + 1 < len ? hi + 1 : len) : len;
+        sink = start = n = 0;
+        if (end <= 0) return;
+        int first = p.window ? lo - p.window + 1 : 0;
+        first = first < 0 ? 0 : first;
+        start = first / kUnit;
+        const int s = p.sinks < first ? p.sinks : first;
+        sink = (s + kUnit - 1) / kUnit;
+        sink = sink < start ? sink : start;
+        n = sink + (end + kUnit - 1) / kUnit - start;
+    }
+    __device__ __forceinline__ int operator()(int i) const { return i < sink ? i : i - sink + start; }
+};
+
+// Rows 32 kTiles per workgroup and a split of the keys that they see; its waves take the
+// key tiles in turn, each for all these rows, and join at the end.
+template <int D, int kTiles>
+__global__ void __launch_bounds__(kThreads) stats_kernel(const Args p) {
+    __shared__ uint2 table[256];
+    __shared__ f32x2 part[kWaves][kTiles * 32];
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
+    const int block = rest % p.row_blocks, split = rest / p.row_blocks;
+    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+    const Sequence s = sequence_of(p, b);
+    const int rows = s.used * (int)p.group.n, row0 = block * kTiles * 32;
+    if (!s.there || row0 >= rows) return;
+    const uint32_t four = 4u + ((uint32_t)p.total_q >> 31);  // not foldable (see HighBytes)
+    fill_table(table, tid);
+    half8 q[kTiles][D / 16];
+    float factor[kTiles], m[kTiles], l[kTiles];
+    int pos[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; i++) {
+        const int r = row0 + 32 * i + (lane & 31), rc = r < rows ? r : rows - 1;
+        factor[i] = load_q<D>(p, s, head, rc, h, q[i]);
+        pos[i] = s.pos0 + (int)p.group.into(rc);
+        m[i] = kLowest;
+        l[i] = 0.0f;
+    }
+    __syncthreads();
+    const int end_row = row0 + kTiles * 32 < rows ? row0 + kTiles * 32 : rows;
+    const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(end_row - 1);
+    const KeyTiles tiles(p, s.len, pos_lo, pos_hi);
+    const int share = (tiles.n + p.splits - 1) / p.splits;
+    const int from = split * share, to = from + share < tiles.n ? from + share : tiles.n;
+    KeyCodes<D> next;
+    if (from + wave < to) next.load(p, cache_row(p, s, head, tiles(from + wave) * kUnit + (lane & 31)), h);
+    for (int t = from + wave; t < to; t += kWaves) {
+        const KeyCodes<D> codes = next;
+        if (t + kWaves < to) next.load(p, cache_row(p, s, head, tiles(t + kWaves) * kUnit + (lane & 31)), h);
+        const int first = tiles(t) * kUnit;
+        half8 k[D / 16];
+        codes.decode(table, four, k);
+        const bool whole = all_seen(p, s.len, pos_lo, pos_hi, first);
+#pragma unroll
+        for (int i = 0; i < kTiles; i++) {
+            f32x16 x = scores<D>(k, q[i]);
+            if (!whole) hide(p, s.len, pos[i], first + 4 * h, x);
+            float top = x[0];
+#pragma unroll
+            for (int j = 1; j < 16; j++) top = __builtin_fmaxf(top, x[j]);
+            top *= factor[i];
+            if (top > m[i] + kSlack) {
+                l[i] *= __builtin_amdgcn_exp2f(m[i] - top);
+                m[i] = top;
+            }
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; j++) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], factor[i], -m[i]));
+            l[i] += sum;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTiles; i++) {
+        const float om = __shfl_xor(m[i], 32), ol = __shfl_xor(l[i], 32);
+        const float top = __builtin_fmaxf(m[i], om);
+        const float sum = l[i] * __builtin_amdgcn_exp2f(m[i] - top) + ol * __builtin_amdgcn_exp2f(om - top);
+        if (h == 0) part[wave][32 * i + lane] = f32x2{top, sum};
+    }
+    __syncthreads();
+    for (int r = tid; r < kTiles * 32 && row0 + r < rows; r += kThreads) {
+        float top = kLowest, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) top = __builtin_fmaxf(top, part[w][r][0]);
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) sum += part[w][r][1] * __builtin_amdgcn_exp2f(part[w][r][0] - top);
+        const int token = (int)p.group.into(row0 + r), mm = row0 + r - token * (int)p.group.n;
+        p.stats[split * p.stat_rows + (int64_t)(s.first_row + token) * p.heads + head * (int)p.group.n + mm] =
+            f32x2{top, sum};
+    }
+}
+
+// The exponent that a row's scores are taken from: log2 of its sum over all keys.  A row
+// that sees none adds nothing to any key.
+__device__ __forceinline__ float log_sum(const Args& p, const Sequence& s, int kv_head, int r) {
+    const int token = (int)p.group.into(r), m = r - token * (int)p.group.n;
+    const f32x2* at = p.stats + (int64_t)(s.first_row + token) * p.heads + kv_head * (int)p.group.n + m;
+    float top = kLowest, sum = 0.0f;
+    for (int i = 0; i < p.splits; i++) {
+        const f32x2 v = at[i * p.stat_rows];
+        const float t = __builtin_fmaxf(top, v[0]);
+        sum = sum * __builtin_amdgcn_exp2f(top - t) + v[1] * __builtin_amdgcn_exp2f(v[0] - t);
+        top = t;
+    }
+    return sum == 0.0f ? __builtin_inff() : top + __builtin_amdgcn_logf(sum);
+}
+
+// kTiles tiles of 32 keys per wave, decoded once; the workgroup goes through the rows that
+// may see any of its keys, four tiles of 32 rows at a time, each of which one wave brings
+// into LDS in operand order.
+template <int D, int kTiles>
+__global__ void __launch_bounds__(kThreads) columns_kernel(const Args p) {
+    constexpr int kKeys = kWaves * kTiles * kUnit;
+    __shared__ uint2 table[256];
+    __shared__ __attribute__((aligned(16))) half8 rows_q[kWaves][D / 16][64];
+    __shared__ float row_factor[kWaves][32], row_log[kWaves][32];
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int bh = blockIdx.x % p.batch_heads, block0 = blockIdx.x / p.batch_heads;
+    const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
+    const Sequence s = sequence_of(p, b);
+    if (!s.there) return;
+    const uint32_t four = 4u + ((uint32_t)p.total_q >> 31);
+    const int rows = s.used * (int)p.group.n;
+    const int old = s.pos0 > 0 ? s.pos0 : 0;  // keys that had sums before
+    const int width = p.mass.width < s.len ? (int)p.mass.width : s.len;
+    const float* const in = p.mass.in + s.mass_row * p.mass.in_stride_row + head * p.mass.in_stride_head;
+    float* const out = p.mass.out + s.mass_row * p.mass.out_stride_row + head * p.mass.out_stride_head;
+    fill_table(table, tid);
+    __syncthreads();
+    const int stride = gridDim.x / p.batch_heads;
+    for (int64_t key0 = (int64_t)block0 * kKeys; key0 < width; key0 += (int64_t)stride * kKeys) {
+        const int first = (int)key0 + wave * kTiles * kUnit;
+        half8 k[kTiles][D / 16];
+#pragma unroll
+        for (int i = 0; i < kTiles; i++) {
+            KeyCodes<D> codes;
+            codes.load(p, cache_row(p, s, head, first + i * kUnit + (lane & 31)), h);
+            codes.decode(table, four, k[i]);
+        }
+        float acc[kTiles][16] = {};
+        // rows that may see keys key0 .. key0 + kKeys - 1: from the one at key0, to the last
+        // one whose window reaches back
+        int lo = 0, hi = rows;
+        if (p.causal) {
+            const int64_t t = key0 - s.pos0;
+            lo = t <= 0 ? 0 : t >= s.used ? rows : (int)t * (int)p.group.n;
+        }
+        if (p.window && key0 >= p.sinks) {
+            const int64_t t = key0 + kKeys - 1 + p.window - s.pos0;  // first token past
+            hi = t <= 0 ? 0 : t >= s.used ? rows : (int)t * (int)p.group.n;
+        }
+        for (int r0 = lo & ~31; r0 < hi; r0 += 32 * kWaves) {
+            {
+                const int r = r0 + 32 * wave + (lane & 31), rc = r < rows ? r : rows - 1;
+                half8 q[D / 16];
+                const float f = load_q<D>(p, s, head, rc, h, q);
+#pragma unroll
+                for (int t = 0; t < D / 16; t++) rows_q[wave][t][lane] = q[t];
+                if (h == 0) {
+                    row_factor[wave][lane] = f;
+                    row_log[wave][lane] = r < rows ? log_sum(p, s, head, rc) : __builtin_inff();
+                }
+            }
+            __syncthreads();
+            for (int w = 0; w < kWaves && r0 + 32 * w < hi; w++) {
+                const int ra = r0 + 32 * w, rz = ra + 31 < rows ? ra + 31 : rows - 1;
+                const int pos_lo = s.pos0 + (int)p.group.into(ra), pos_hi = s.pos0 + (int)p.group.into(rz);
+                half8 q[D / 16];
+#pragma unroll
+                for (int t = 0; t < D / 16; t++) q[t] = rows_q[w][t][lane];
+                const float f = row_factor[w][lane & 31], from = row_log[w][lane & 31];
+                const int r = ra + (lane & 31);
+                const int pos = s.pos0 + (int)p.group.into(r < rows ? r : rows - 1);
+#pragma unroll
+                for (int i = 0; i < kTiles; i++) {
+                    const int key = first + i * kUnit;
+                    if (!any_seen(p, s.len, pos_lo, pos_hi, key)) continue;
+                    f32x16 x = scores<D>(k[i], q);
+                    if (!all_seen(p, s.len, pos_lo, pos_hi, key)) hide(p, s.len, pos, key + 4 * h, x);
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        acc[i][j] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], f, -from));
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles; i++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                float v = acc[i][j];
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) v += __shfl_xor(v, d);
+                const int key = first + i * kUnit + 4 * h + 8 * (j >> 2) + (j & 3);
+                if ((lane & 31) == j && key < width) out[key] = key < old ? in[key] + v : v;
+            }
+    }
+}
+
+struct Plan {
+    int row_tiles;  // 32-row tiles of a workgroup of the first pass
+    int key_tiles;  // 32-key tiles of a wave of the second
+    int64_t row_blocks, splits, key_blocks;
+};
+
+constexpr int kFull = 1024;  // workgroups that fill the chip: four on a CU
+
+// Few rows take one tile of 32 and are split over the keys; many take four, which share a
+// tile's decode.  Splits and key blocks fill the chip.
+Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    Plan p;
+    const int64_t rows = a.max_q * (a.heads / c.kv_heads), pairs = a.batch * c.kv_heads;
+    const int64_t units = (a.max_len < kMaxLen ? a.max_len : kMaxLen) / kUnit + 1;
+    const bool few = rows <= 32 || c.head_dim == 256;
+    p.row_tiles = few ? 1 : 4;
+    p.row_blocks = (rows + 32 * p.row_tiles - 1) / (32 * p.row_tiles);
+    const int64_t most = (units + 2 * kWaves - 1) / (2 * kWaves);
+    p.splits = kFull / (pairs * p.row_blocks > kFull ? kFull : pairs * p.row_blocks);
+    p.splits = p.splits < most ? p.splits : most;
+    p.splits = p.splits < 1 ? 1 : p.splits > 32 ? 32 : p.splits;
+    p.key_tiles = rows <= 32 || c.head_dim == 256 ? 1 : 2;
+    const int64_t keys = kWaves * p.key_tiles;
+    p.key_blocks = (units + keys - 1) / keys;
+    const int64_t limit = 0x7FFFFFFF / pairs;
+    p.key_blocks = p.key_blocks < limit ? p.key_blocks : limit;
+    return p;
+}
+
+template <int D, int kTiles>
+void launch_stats(const Args& p, unsigned groups, hipStream_t stream) {
+    hipLaunchKernelGGL((stats_kernel<D, kTiles>), dim3(groups), dim3(kThreads), 0, stream, p);
+}
+template <int D, int kTiles>
+void launch_columns(const Args& p, unsigned groups, hipStream_t stream) {
+    hipLaunchKernelGGL((columns_kernel<D, kTiles>), dim3(groups), dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace
+
+int64_t kv_weights_workspace(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    return plan_of(c, a).splits * a.total_q * a.heads * 8;
+}
+
+int64_t kv_weights_workspace_most(const if4_kv_cache&, const if4_kv_attention_args& a) {
+    return 32 * a.total_q * a.heads * 8;
+}
+
+hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args& a,
+                             const if4_kv_mass& m, void* workspace, hipStream_t stream) {
+    const Plan plan = plan_of(c, a);
+    Args p;
+    p.k_codes = c.k_codes;
+    p.k_scales = c.k_scales;
+    p.q = reinterpret_cast<const uint16_t*>(a.q);
+    p.q_st = a.q_stride_token;
+    p.q_sh = a.q_stride_head;
+    p.page_table = a.page_table;
+    p.seq_lens = a.seq_lens;
+    p.q_starts = a.q_starts;
+    p.table_stride = a.table_stride;
+    p.mass = m;
+    p.stats = reinterpret_cast<f32x2*>(workspace);
+    p.stat_rows = a.total_q * a.heads;
+    p.total_q = (int)a.total_q;
+    p.max_q = (int)a.max_q;
+    p.pages = (int)c.pages;
+    p.kv_heads = (int)c.kv_heads;
+    p.heads = (int)a.heads;
+    const int64_t pairs = a.batch * c.kv_heads;
+    p.batch_heads = (int)pairs;
+    p.row_blocks = (int)plan.row_blocks;
+    p.splits = (int)plan.splits;
+    p.causal = a.causal;
+    p.window = (int)(a.window < kMaxLen ? a.window : 0);
+    p.sinks = (int)(a.sinks < kMaxLen ? a.sinks : kMaxLen);
+    p.tiles = Divisor(c.page_size / 16);
+    p.group = Divisor(a.heads / c.kv_heads);
+    p.q_scale = a.scale * 1.4426950408889634f / 7.0f;
+    p.k_exp = c.k_exp + 12;
+    const int64_t stat_groups = pairs * plan.row_blocks * plan.splits;
+    if (stat_groups > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const unsigned groups = (unsigned)stat_groups, columns = (unsigned)(pairs * plan.key_blocks);
+    if (c.head_dim == 64)
+        plan.row_tiles == 1 ? launch_stats<64, 1>(p, groups, stream) : launch_stats<64, 4>(p, groups, stream);
+    else if (c.head_dim == 128)
+        plan.row_tiles == 1 ? launch_stats<128, 1>(p, groups, stream) : launch_stats<128, 4>(p, groups, stream);
+    else
+        launch_stats<256, 1>(p, groups, stream);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    if (c.head_dim == 64)
+        plan.key_tiles == 1 ? launch_columns<64, 1>(p, columns, stream) : launch_columns<64, 2>(p, columns, stream);
+    else if (c.head_dim == 128)
+        plan.key_tiles == 1 ? launch_columns<128, 1>(p, columns, stream) : launch_columns<128, 2>(p, columns, stream);
+    else
+        launch_columns<256, 1>(p, columns, stream);
+    return hipGetLastError();
+}
+
+}  // namespace if4
