@@ -220,6 +220,226 @@ struct KeyTiles {
     __device__ __forceinline__ int operator()(int i) const { return i < sink ? i : i - sink + start; }
 };
 
+// ---------------------------------------------------------------------------
+// Few rows: those of a sequence and kv head fill no more than one tile.  Here rows lie in
+// the accumulators' registers and keys in the lanes (S = Q K^T), so that R <= 8 rows take
+// 4 of 16 registers through exp2, and a key's sum over rows is its lane's own.  A
+// workgroup takes a split of the keys, its waves one tile of 32 each in turn; the page
+// table's entry is on its way two tiles ahead, the codes one.
+
+// A lane's key on its way: the page table's entry, then the codes.
+template <int D>
+struct KeyAhead {
+    int page;
+    uint32_t tile, rest;
+    KeyCodes<D> codes;
+    __device__ __forceinline__ void look_up(const Args& p, const Sequence& s, int j) {
+        const int last = (s.len - 1) >> 4;
+        const uint32_t t = (uint32_t)((j >> 4) < last ? j >> 4 : last), i = p.tiles.into(t);
+        page = s.table[i];
+        tile = t - i * p.tiles.n;
+    }
+    __device__ __forceinline__ void load(const Args& p, int head, int lane) {
+        int at = page < p.pages - 1 ? page : p.pages - 1;
+        at = at > 0 ? at : 0;
+        codes.load(p, ((int64_t)(at * p.kv_heads + head) * p.tiles.n + tile) * 16 + (lane & 15), lane >> 5);
+    }
+};
+
+// Row of register r for lane half h.
+__device__ __forceinline__ int row_of(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
+
+// Scores of key j that its lane's rows do not see become -inf.
+template <int R>
+__device__ __forceinline__ void hide_rows(const Args& p, const Sequence& s, int rows, int h, int j, float (&x)[R / 2]) {
+#pragma unroll
+    for (int r = 0; r < R / 2; r++) {
+        const int row = row_of(r, h), pos = s.pos0 + (int)p.group.into(row < rows ? row : rows - 1);
+        const bool seen = j < s.len && (!p.causal || j <= pos) && (!p.window || j > pos - p.window || j < p.sinks);
+        x[r] = seen ? x[r] : -__builtin_inff();
+    }
+}
+
+// What both passes over few rows share: the rows' q, and the tiles of keys in turn.
+template <int D, int R>
+struct FewRows {
+    const Args& p;
+    Sequence s;
+    int head, lane, h, wave, rows, pos_lo, pos_hi;
+    uint32_t four;
+    half8 q[D / 16];
+    float f[R / 2];
+
+    __device__ __forceinline__ FewRows(const Args& args, int bh, uint2* table) : p(args) {
+        const int b = bh / p.kv_heads;
+        head = bh - b * p.kv_heads;
+        s = sequence_of(p, b);
+        lane = threadIdx.x & 63;
+        h = lane >> 5;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        rows = s.used * (int)p.group.n;
+        four = 4u + ((uint32_t)p.total_q >> 31);
+        fill_table(table, threadIdx.x);
+    }
+    __device__ __forceinline__ void load_rows() {
+        const int r = lane & 31;
+        const float own = load_q<D>(p, s, head, r < rows ? r : rows - 1, h, q);
+        spread(own, f);
+        pos_lo = s.pos0;
+        pos_hi = s.pos0 + s.used - 1;
+    }
+    // lane r's value into the registers of row r
+    __device__ __forceinline__ void spread(float own, float (&to)[R / 2]) const {
+#pragma unroll
+        for (int r = 0; r < R / 2; r++) to[r] = __shfl(own, row_of(r, h));
+    }
+    // each(first key, scores, whole) for the wave's tiles t of `count`, in order; tile(t) is
+    // the tile's place
+    template <class Tile, class Each>
+    __device__ __forceinline__ void go(const uint2* table, int from, int to, Tile&& tile, Each&& each) {
+        int t = from + wave;
+        if (t >= to) return;
+        KeyAhead<D> next;
+        const int j = lane & 31;
+        next.look_up(p, s, tile(t) * kUnit + j);
+        next.load(p, head, lane);
+        if (t + kWaves < to) next.look_up(p, s, tile(t + kWaves) * kUnit + j);
+        for (; t < to; t += kWaves) {
+            const KeyCodes<D> codes = next.codes;
+            const int first = tile(t) * kUnit;
+            if (t + kWaves < to) next.load(p, head, lane);
+            if (t + 2 * kWaves < to) next.look_up(p, s, tile(t + 2 * kWaves) * kUnit + j);
+            half8 k[D / 16];
+            codes.decode(table, four, k);
+            const f32x16 all = scores<D>(q, k);
+            float x[R / 2];
+#pragma unroll
+            for (int r = 0; r < R / 2; r++) x[r] = all[r];
+            if (!all_seen(p, s.len, pos_lo, pos_hi, first)) hide_rows<R>(p, s, rows, h, first + j, x);
+            each(first, x);
+        }
+    }
+};
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) few_stats_kernel(const Args p) {
+    __shared__ uint2 table[256];
+    __shared__ f32x2 part[kWaves][R];
+    FewRows<D, R> few(p, blockIdx.x % p.batch_heads, table);
+    const Sequence& s = few.s;
+    if (!s.there) return;
+    few.load_rows();
+    __syncthreads();
+    const KeyTiles tiles(p, s.len, few.pos_lo, few.pos_hi);
+    const int split = blockIdx.x / p.batch_heads, share = (tiles.n + p.splits - 1) / p.splits;
+    const int from = split * share, to = from + share < tiles.n ? from + share : tiles.n;
+    float m[R / 2], l[R / 2];
+#pragma unroll
+    for (int r = 0; r < R / 2; r++) m[r] = kLowest, l[r] = 0.0f;
+    few.go(table, from, to, [&](int t) { return tiles(t); }, [&](int, const float (&x)[R / 2]) {
+#pragma unroll
+        for (int r = 0; r < R / 2; r++) {
+            const float y = x[r] * few.f[r];
+            if (y > m[r] + kSlack) {
+                l[r] *= __builtin_amdgcn_exp2f(m[r] - y);
+                m[r] = y;
+            }
+            l[r] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], few.f[r], -m[r]));
+        }
+    });
+#pragma unroll
+    for (int r = 0; r < R / 2; r++) {
+        float top = m[r];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+        float sum = l[r] * __builtin_amdgcn_exp2f(m[r] - top);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) sum += __shfl_xor(sum, d);
+        if ((few.lane & 31) == 0) part[few.wave][row_of(r, few.h)] = f32x2{top, sum};
+    }
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r >= few.rows) return;
+    float top = kLowest, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) top = __builtin_fmaxf(top, part[w][r][0]);
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) sum += part[w][r][1] * __builtin_amdgcn_exp2f(part[w][r][0] - top);
+    const int token = (int)p.group.into(r), mm = r - token * (int)p.group.n;
+    p.stats[split * p.stat_rows + (int64_t)(s.first_row + token) * p.heads + few.head * (int)p.group.n + mm] =
+        f32x2{top, sum};
+}
+
+// The exponent that a row's scores are taken from: log2 of its sum over all keys.  A row
+// that sees none adds nothing to any key.
+__device__ __forceinline__ float log_sum(const Args& p, const Sequence& s, int kv_head, int r) {
+    const int token = (int)p.group.into(r), m = r - token * (int)p.group.n;
+    const f32x2* at = p.stats + (int64_t)(s.first_row + token) * p.heads + kv_head * (int)p.group.n + m;
+    float top = kLowest, sum = 0.0f;
+    for (int i = 0; i < p.splits; i++) {
+        const f32x2 v = at[i * p.stat_rows];
+        const float t = __builtin_fmaxf(top, v[0]);
+        sum = sum * __builtin_amdgcn_exp2f(top - t) + v[1] * __builtin_amdgcn_exp2f(v[0] - t);
+        top = t;
+    }
+    return sum == 0.0f ? __builtin_inff() : top + __builtin_amdgcn_logf(sum);
+}
+
+// Where a sequence's sums of one kv head are read and written.
+struct Sums {
+    const float* in;
+    float* out;
+    int old, width;  // keys that had sums before; keys that have a place
+    __device__ __forceinline__ Sums(const Args& p, const Sequence& s, int head) {
+        in = p.mass.in + s.mass_row * p.mass.in_stride_row + head * p.mass.in_stride_head;
+        out = p.mass.out + s.mass_row * p.mass.out_stride_row + head * p.mass.out_stride_head;
+        old = s.pos0 > 0 ? s.pos0 : 0;
+        width = p.mass.width < s.len ? (int)p.mass.width : s.len;
+    }
+};
+
+// The workgroups go through the keys the other way round than those of the first pass did,
+// whose last keys are still in the caches.
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) few_columns_kernel(const Args p) {
+    __shared__ uint2 table[256];
+    const int index = gridDim.x - 1 - blockIdx.x;
+    FewRows<D, R> few(p, index % p.batch_heads, table);
+    const Sequence& s = few.s;
+    if (!s.there) return;
+    const Sums sums(p, s, few.head);
+    const int tiles = (sums.width + kUnit - 1) / kUnit, share = (tiles + p.splits - 1) / p.splits;
+    const int from = index / p.batch_heads * share, to = from + share < tiles ? from + share : tiles;
+    if (from >= to) return;
+    few.load_rows();
+    float log[R / 2];
+    const int r = few.lane & 31;
+    few.spread(r < few.rows ? log_sum(p, s, few.head, r) : __builtin_inff(), log);
+    __syncthreads();
+    // tiles that some row sees: the others' sums are only copied, or start at zero
+    const KeyTiles seen(p, s.len, few.pos_lo, few.pos_hi);
+    const int sink = seen.n > 0 ? seen.sink : 0, start = seen.n > 0 ? seen.start : tiles;
+    const auto write = [&](int first, float v) {
+        const int key = first + r;
+        if (few.h == 0 && key < sums.width) sums.out[key] = key < sums.old ? sums.in[key] + v : v;
+    };
+    const auto add = [&](int first, const float (&x)[R / 2]) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < R / 2; i++) v += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], few.f[i], -log[i]));
+        write(first, v + __shfl_xor(v, 32));
+    };
+    const auto same = [](int t) { return t; };
+    const int a = from < sink ? (to < sink ? to : sink) : from;  // tiles from .. a are sinks,
+    const int z = a < start ? (to < start ? to : start) : a;     // a .. z hidden, z .. to seen
+    few.go(table, from, a, same, add);
+    for (int t = a + few.wave; t < z; t += kWaves) write(t * kUnit, 0.0f);
+    few.go(table, z, to, same, add);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows.
+
 // Rows 32 kTiles per workgroup and a split of the keys that they see; its waves take the
 // key tiles in turn, each for all these rows, and join at the end.
 template <int D, int kTiles>
@@ -300,21 +520,6 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Args p) {
     }
 }
 
-// The exponent that a row's scores are taken from: log2 of its sum over all keys.  A row
-// that sees none adds nothing to any key.
-__device__ __forceinline__ float log_sum(const Args& p, const Sequence& s, int kv_head, int r) {
-    const int token = (int)p.group.into(r), m = r - token * (int)p.group.n;
-    const f32x2* at = p.stats + (int64_t)(s.first_row + token) * p.heads + kv_head * (int)p.group.n + m;
-    float top = kLowest, sum = 0.0f;
-    for (int i = 0; i < p.splits; i++) {
-        const f32x2 v = at[i * p.stat_rows];
-        const float t = __builtin_fmaxf(top, v[0]);
-        sum = sum * __builtin_amdgcn_exp2f(top - t) + v[1] * __builtin_amdgcn_exp2f(v[0] - t);
-        top = t;
-    }
-    return sum == 0.0f ? __builtin_inff() : top + __builtin_amdgcn_logf(sum);
-}
-
 // kTiles tiles of 32 keys per wave, decoded once; the workgroup goes through the rows that
 // may see any of its keys, four tiles of 32 rows at a time, each of which one wave brings
 // into LDS in operand order.
@@ -332,14 +537,11 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const Args p) {
     if (!s.there) return;
     const uint32_t four = 4u + ((uint32_t)p.total_q >> 31);
     const int rows = s.used * (int)p.group.n;
-    const int old = s.pos0 > 0 ? s.pos0 : 0;  // keys that had sums before
-    const int width = p.mass.width < s.len ? (int)p.mass.width : s.len;
-    const float* const in = p.mass.in + s.mass_row * p.mass.in_stride_row + head * p.mass.in_stride_head;
-    float* const out = p.mass.out + s.mass_row * p.mass.out_stride_row + head * p.mass.out_stride_head;
+    const Sums sums(p, s, head);
     fill_table(table, tid);
     __syncthreads();
     const int stride = gridDim.x / p.batch_heads;
-    for (int64_t key0 = (int64_t)block0 * kKeys; key0 < width; key0 += (int64_t)stride * kKeys) {
+    for (int64_t key0 = (int64_t)block0 * kKeys; key0 < sums.width; key0 += (int64_t)stride * kKeys) {
         const int first = (int)key0 + wave * kTiles * kUnit;
         half8 k[kTiles][D / 16];
 #pragma unroll
@@ -403,33 +605,37 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const Args p) {
 #pragma unroll
                 for (int d = 1; d < 32; d *= 2) v += __shfl_xor(v, d);
                 const int key = first + i * kUnit + 4 * h + 8 * (j >> 2) + (j & 3);
-                if ((lane & 31) == j && key < width) out[key] = key < old ? in[key] + v : v;
+                if ((lane & 31) == j && key < sums.width) sums.out[key] = key < sums.old ? sums.in[key] + v : v;
             }
     }
 }
 
 struct Plan {
-    int row_tiles;  // 32-row tiles of a workgroup of the first pass
-    int key_tiles;  // 32-key tiles of a wave of the second
+    int few;        // rows of a tile where they fill no more than one, else 0
+    int row_tiles;  // many: 32-row tiles of a workgroup of the first pass
+    int key_tiles;  // many: 32-key tiles of a wave of the second
     int64_t row_blocks, splits, key_blocks;
 };
 
-constexpr int kFull = 1024;  // workgroups that fill the chip: four on a CU
+constexpr int kMostSplits = 64;
 
-// Few rows take one tile of 32 and are split over the keys; many take four, which share a
-// tile's decode.  Splits and key blocks fill the chip.
+// Key splits and key blocks fill the chip: few rows with kFew workgroups, eight to a CU (a
+// split has two tiles for each of its waves at least), many with kMany.
+constexpr int kFew = 2048, kMany = 1024;
+
 Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     Plan p;
     const int64_t rows = a.max_q * (a.heads / c.kv_heads), pairs = a.batch * c.kv_heads;
     const int64_t units = (a.max_len < kMaxLen ? a.max_len : kMaxLen) / kUnit + 1;
-    const bool few = rows <= 32 || c.head_dim == 256;
-    p.row_tiles = few ? 1 : 4;
-    p.row_blocks = (rows + 32 * p.row_tiles - 1) / (32 * p.row_tiles);
+    p.few = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+    p.row_tiles = c.head_dim == 256 ? 1 : 4;
+    p.row_blocks = p.few ? 1 : (rows + 32 * p.row_tiles - 1) / (32 * p.row_tiles);
+    const int64_t groups = pairs * p.row_blocks, full = p.few ? kFew : kMany;
     const int64_t most = (units + 2 * kWaves - 1) / (2 * kWaves);
-    p.splits = kFull / (pairs * p.row_blocks > kFull ? kFull : pairs * p.row_blocks);
+    p.splits = groups >= full ? 1 : (full + groups - 1) / groups;
     p.splits = p.splits < most ? p.splits : most;
-    p.splits = p.splits < 1 ? 1 : p.splits > 32 ? 32 : p.splits;
-    p.key_tiles = rows <= 32 || c.head_dim == 256 ? 1 : 2;
+    p.splits = p.splits < kMostSplits ? p.splits : kMostSplits;
+    p.key_tiles = c.head_dim == 256 ? 1 : 2;
     const int64_t keys = kWaves * p.key_tiles;
     p.key_blocks = (units + keys - 1) / keys;
     const int64_t limit = 0x7FFFFFFF / pairs;
@@ -437,13 +643,35 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     return p;
 }
 
-template <int D, int kTiles>
-void launch_stats(const Args& p, unsigned groups, hipStream_t stream) {
-    hipLaunchKernelGGL((stats_kernel<D, kTiles>), dim3(groups), dim3(kThreads), 0, stream, p);
+template <int D, int R>
+hipError_t launch_few(const Args& p, unsigned groups, hipStream_t stream) {
+    hipLaunchKernelGGL((few_stats_kernel<D, R>), dim3(groups), dim3(kThreads), 0, stream, p);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((few_columns_kernel<D, R>), dim3(groups), dim3(kThreads), 0, stream, p);
+    return hipGetLastError();
 }
-template <int D, int kTiles>
-void launch_columns(const Args& p, unsigned groups, hipStream_t stream) {
-    hipLaunchKernelGGL((columns_kernel<D, kTiles>), dim3(groups), dim3(kThreads), 0, stream, p);
+
+template <int D, int kRows, int kKeys>
+hipError_t launch_many(const Args& p, unsigned groups, unsigned columns, hipStream_t stream) {
+    hipLaunchKernelGGL((stats_kernel<D, kRows>), dim3(groups), dim3(kThreads), 0, stream, p);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((columns_kernel<D, kKeys>), dim3(columns), dim3(kThreads), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch(const Args& p, const Plan& plan, unsigned groups, unsigned columns, hipStream_t stream) {
+    switch (plan.few) {
+        case 8: return launch_few<D, 8>(p, groups, stream);
+        case 16: return launch_few<D, 16>(p, groups, stream);
+        case 32: return launch_few<D, 32>(p, groups, stream);
+    }
+    if constexpr (D == 256)
+        return launch_many<D, 1, 1>(p, groups, columns, stream);
+    else
+        return launch_many<D, 4, 2>(p, groups, columns, stream);
 }
 
 }  // namespace
@@ -453,7 +681,7 @@ int64_t kv_weights_workspace(const if4_kv_cache& c, const if4_kv_attention_args&
 }
 
 int64_t kv_weights_workspace_most(const if4_kv_cache&, const if4_kv_attention_args& a) {
-    return 32 * a.total_q * a.heads * 8;
+    return kMostSplits * a.total_q * a.heads * 8;
 }
 
 hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args& a,
@@ -491,21 +719,9 @@ hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args&
     const int64_t stat_groups = pairs * plan.row_blocks * plan.splits;
     if (stat_groups > 0x7FFFFFFF) return hipErrorInvalidValue;
     const unsigned groups = (unsigned)stat_groups, columns = (unsigned)(pairs * plan.key_blocks);
-    if (c.head_dim == 64)
-        plan.row_tiles == 1 ? launch_stats<64, 1>(p, groups, stream) : launch_stats<64, 4>(p, groups, stream);
-    else if (c.head_dim == 128)
-        plan.row_tiles == 1 ? launch_stats<128, 1>(p, groups, stream) : launch_stats<128, 4>(p, groups, stream);
-    else
-        launch_stats<256, 1>(p, groups, stream);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-    if (c.head_dim == 64)
-        plan.key_tiles == 1 ? launch_columns<64, 1>(p, columns, stream) : launch_columns<64, 2>(p, columns, stream);
-    else if (c.head_dim == 128)
-        plan.key_tiles == 1 ? launch_columns<128, 1>(p, columns, stream) : launch_columns<128, 2>(p, columns, stream);
-    else
-        launch_columns<256, 1>(p, columns, stream);
-    return hipGetLastError();
+    return c.head_dim == 64    ? launch<64>(p, plan, groups, columns, stream)
+           : c.head_dim == 128 ? launch<128>(p, plan, groups, columns, stream)
+                               : launch<256>(p, plan, groups, columns, stream);
 }
 
 }  // namespace if4
