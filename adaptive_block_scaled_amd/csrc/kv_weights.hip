@@ -41,6 +41,9 @@ struct Args {
     if4_kv_mass mass;
     f32x2* stats;  // [splits][rows of q x heads] maximum (in powers of two) and sum
     int64_t stat_rows;
+    half8* rows_q;      // many rows: tiles of 32 rows in operand order, see row_tile
+    float* row_factor;  // [..][32]
+    int64_t row_tiles;  // of one kv head
     int total_q, max_q, pages, kv_heads, heads, batch_heads, row_blocks, splits;
     int causal, window, sinks;
     Divisor tiles;  // of 16 tokens in a page
@@ -440,10 +443,22 @@ __global__ void __launch_bounds__(kThreads) few_columns_kernel(const Args p) {
 // ---------------------------------------------------------------------------
 // Many rows.
 
+// Place of a sequence's tile t of 32 rows: sequences follow one another, each from the tile
+// after the one that its first row would share, so that none has the same.
+__device__ __forceinline__ int64_t row_tile(const Args& p, const Sequence& s, int b, int head, int t) {
+    return head * p.row_tiles + ((int64_t)s.first_row * p.group.n >> 5) + b + t;
+}
+
+// 16 bytes per lane from memory straight into LDS, lane l's at `lds` + 16 l.
+__device__ __forceinline__ void load_to_lds(const void* from, void* lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
 // Rows 32 kTiles per workgroup and a split of the keys that they see; its waves take the
 // key tiles in turn, each for all these rows, and join at the end.
 template <int D, int kTiles>
-__global__ void __launch_bounds__(kThreads) stats_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 2) stats_kernel(const Args p) {
     __shared__ uint2 table[256];
     __shared__ f32x2 part[kWaves][kTiles * 32];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
@@ -466,6 +481,14 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Args p) {
         pos[i] = s.pos0 + (int)p.group.into(rc);
         m[i] = kLowest;
         l[i] = 0.0f;
+        // the second pass takes them from here (each wave writes some, of the first split's
+        // workgroups)
+        if (split == 0 && (i & (kWaves - 1)) == (kTiles >= kWaves ? wave : 0) && row0 + 32 * i < rows) {
+            const int64_t at = row_tile(p, s, b, head, row0 / 32 + i);
+#pragma unroll
+            for (int t = 0; t < D / 16; t++) p.rows_q[(at * (D / 16) + t) * 64 + lane] = q[i][t];
+            if (h == 0) p.row_factor[at * 32 + lane] = factor[i];
+        }
     }
     __syncthreads();
     const int end_row = row0 + kTiles * 32 < rows ? row0 + kTiles * 32 : rows;
@@ -521,14 +544,16 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const Args p) {
 }
 
 // kTiles tiles of 32 keys per wave, decoded once; the workgroup goes through the rows that
-// may see any of its keys, four tiles of 32 rows at a time, each of which one wave brings
-// into LDS in operand order.
+// may see any of its keys, kRowTiles tiles of 32 at a time, which come into LDS in operand
+// order while those before are multiplied.
 template <int D, int kTiles>
-__global__ void __launch_bounds__(kThreads) columns_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
     constexpr int kKeys = kWaves * kTiles * kUnit;
+    constexpr int kRowTiles = D == 256 ? 2 : 4;
+    constexpr int kPieces = kRowTiles * (D / 16) / kWaves;  // 1 KB pieces that a wave brings
     __shared__ uint2 table[256];
-    __shared__ __attribute__((aligned(16))) half8 rows_q[kWaves][D / 16][64];
-    __shared__ float row_factor[kWaves][32], row_log[kWaves][32];
+    __shared__ float row_factor[2][kRowTiles * 32], row_log[2][kRowTiles * 32];
+    extern __shared__ __attribute__((aligned(16))) half8 rows_q[];  // [2][kRowTiles][D / 16][64]
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int bh = blockIdx.x % p.batch_heads, block0 = blockIdx.x / p.batch_heads;
@@ -543,14 +568,6 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const Args p) {
     const int stride = gridDim.x / p.batch_heads;
     for (int64_t key0 = (int64_t)block0 * kKeys; key0 < sums.width; key0 += (int64_t)stride * kKeys) {
         const int first = (int)key0 + wave * kTiles * kUnit;
-        half8 k[kTiles][D / 16];
-#pragma unroll
-        for (int i = 0; i < kTiles; i++) {
-            KeyCodes<D> codes;
-            codes.load(p, cache_row(p, s, head, first + i * kUnit + (lane & 31)), h);
-            codes.decode(table, four, k[i]);
-        }
-        float acc[kTiles][16] = {};
         // rows that may see keys key0 .. key0 + kKeys - 1: from the one at key0, to the last
         // one whose window reaches back
         int lo = 0, hi = rows;
@@ -562,41 +579,74 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const Args p) {
             const int64_t t = key0 + kKeys - 1 + p.window - s.pos0;  // first token past
             hi = t <= 0 ? 0 : t >= s.used ? rows : (int)t * (int)p.group.n;
         }
-        for (int r0 = lo & ~31; r0 < hi; r0 += 32 * kWaves) {
-            {
-                const int r = r0 + 32 * wave + (lane & 31), rc = r < rows ? r : rows - 1;
-                half8 q[D / 16];
-                const float f = load_q<D>(p, s, head, rc, h, q);
+        const int t0 = lo / 32, tiles = lo < hi ? (hi + 31) / 32 : t0;
+        const half8* const from = p.rows_q + row_tile(p, s, b, head, 0) * (D / 16 * 64);
+        const float* const factors = p.row_factor + row_tile(p, s, b, head, 0) * 32;
+        float f_next = 0.0f, log_next = 0.0f;
+        // (rows past the last one of a tile have an infinite log; tiles past the last are the
+        // last one again, and not used)
+        const auto fetch = [&](int t, int buffer) {
+            half8* const to = rows_q + buffer * (kRowTiles * (D / 16) * 64);
 #pragma unroll
-                for (int t = 0; t < D / 16; t++) rows_q[wave][t][lane] = q[t];
-                if (h == 0) {
-                    row_factor[wave][lane] = f;
-                    row_log[wave][lane] = r < rows ? log_sum(p, s, head, rc) : __builtin_inff();
-                }
+            for (int i = 0; i < kPieces; i++) {
+                const int piece = wave * kPieces + i, rt = t + piece / (D / 16);
+                load_to_lds(from + ((int64_t)(rt < tiles ? rt : tiles - 1) * (D / 16) + piece % (D / 16)) * 64 + lane,
+                            to + piece * 64);
             }
+            const int r = 32 * t + tid;
+            if (tid < kRowTiles * 32) {
+                f_next = r < rows ? factors[r] : 1.0f;
+                log_next = r < rows ? log_sum(p, s, head, r) : __builtin_inff();
+            }
+        };
+        const auto arrive = [&](int buffer) {
+            if (tid < kRowTiles * 32) {
+                row_factor[buffer][tid] = f_next;
+                row_log[buffer][tid] = log_next;
+            }
+            __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
             __syncthreads();
-            for (int w = 0; w < kWaves && r0 + 32 * w < hi; w++) {
-                const int ra = r0 + 32 * w, rz = ra + 31 < rows ? ra + 31 : rows - 1;
+        };
+        if (t0 < tiles) fetch(t0, 0);
+        half8 k[kTiles][D / 16];
+#pragma unroll
+        for (int i = 0; i < kTiles; i++) {
+            KeyCodes<D> codes;
+            codes.load(p, cache_row(p, s, head, first + i * kUnit + (lane & 31)), h);
+            codes.decode(table, four, k[i]);
+        }
+        float acc[kTiles][16] = {};
+        int buffer = 0;
+        if (t0 < tiles) arrive(0);
+        for (int t = t0; t < tiles; t += kRowTiles) {
+            if (t + kRowTiles < tiles) fetch(t + kRowTiles, buffer ^ 1);
+            for (int w = 0; w < kRowTiles && t + w < tiles; w++) {
+                const int ra = 32 * (t + w), rz = ra + 31 < rows ? ra + 31 : rows - 1;
                 const int pos_lo = s.pos0 + (int)p.group.into(ra), pos_hi = s.pos0 + (int)p.group.into(rz);
+                const half8* const at = rows_q + (buffer * kRowTiles + w) * (D / 16 * 64) + lane;
                 half8 q[D / 16];
 #pragma unroll
-                for (int t = 0; t < D / 16; t++) q[t] = rows_q[w][t][lane];
-                const float f = row_factor[w][lane & 31], from = row_log[w][lane & 31];
-                const int r = ra + (lane & 31);
-                const int pos = s.pos0 + (int)p.group.into(r < rows ? r : rows - 1);
+                for (int i = 0; i < D / 16; i++) q[i] = at[i * 64];
+                const float f = row_factor[buffer][32 * w + (lane & 31)];
+                const float log = row_log[buffer][32 * w + (lane & 31)];
 #pragma unroll
                 for (int i = 0; i < kTiles; i++) {
                     const int key = first + i * kUnit;
                     if (!any_seen(p, s.len, pos_lo, pos_hi, key)) continue;
                     f32x16 x = scores<D>(k[i], q);
-                    if (!all_seen(p, s.len, pos_lo, pos_hi, key)) hide(p, s.len, pos, key + 4 * h, x);
+                    if (!all_seen(p, s.len, pos_lo, pos_hi, key)) {
+                        const int r = ra + (lane & 31);
+                        hide(p, s.len, s.pos0 + (int)p.group.into(r < rows ? r : rows - 1), key + 4 * h, x);
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; j++)
-                        acc[i][j] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], f, -from));
+                        acc[i][j] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], f, -log));
                 }
             }
-            __syncthreads();
+            buffer ^= 1;
+            if (t + kRowTiles < tiles) arrive(buffer);
         }
+        __syncthreads();  // (the next keys' rows come into the same buffers)
 #pragma unroll
         for (int i = 0; i < kTiles; i++)
 #pragma unroll
@@ -657,7 +707,12 @@ hipError_t launch_many(const Args& p, unsigned groups, unsigned columns, hipStre
     hipLaunchKernelGGL((stats_kernel<D, kRows>), dim3(groups), dim3(kThreads), 0, stream, p);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((columns_kernel<D, kKeys>), dim3(columns), dim3(kThreads), 0, stream, p);
+    constexpr int kSmem = 2 * (D == 256 ? 2 : 4) * 32 * D * 2;
+    // dynamic LDS above 64 KB (with the static) must be allowed per kernel (idempotent, any device)
+    const hipError_t allowed = hipFuncSetAttribute((const void*)columns_kernel<D, kKeys>,
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (allowed != hipSuccess) return allowed;
+    hipLaunchKernelGGL((columns_kernel<D, kKeys>), dim3(columns), dim3(kThreads), kSmem, stream, p);
     return hipGetLastError();
 }
 
@@ -676,12 +731,27 @@ hipError_t launch(const Args& p, const Plan& plan, unsigned groups, unsigned col
 
 }  // namespace
 
+// Workspace: the splits' maxima and sums, and for many rows q in operand order.
+namespace {
+int64_t stat_bytes(int64_t splits, const if4_kv_attention_args& a) {
+    return (splits * a.total_q * a.heads * 8 + 15) & ~(int64_t)15;
+}
+int64_t row_tiles(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    return a.total_q * (a.heads / c.kv_heads) / 32 + a.batch + 1;
+}
+int64_t row_bytes(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    return row_tiles(c, a) * c.kv_heads * 32 * (2 * c.head_dim + 4);
+}
+}  // namespace
+
 int64_t kv_weights_workspace(const if4_kv_cache& c, const if4_kv_attention_args& a) {
-    return plan_of(c, a).splits * a.total_q * a.heads * 8;
+    const Plan p = plan_of(c, a);
+    return stat_bytes(p.splits, a) + (p.few ? 0 : row_bytes(c, a));
 }
 
-int64_t kv_weights_workspace_most(const if4_kv_cache&, const if4_kv_attention_args& a) {
-    return kMostSplits * a.total_q * a.heads * 8;
+// (no call has more splits, nor rows in more tiles)
+int64_t kv_weights_workspace_most(const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    return stat_bytes(kMostSplits, a) + row_bytes(c, a);
 }
 
 hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args& a,
@@ -700,6 +770,9 @@ hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args&
     p.mass = m;
     p.stats = reinterpret_cast<f32x2*>(workspace);
     p.stat_rows = a.total_q * a.heads;
+    p.row_tiles = row_tiles(c, a);
+    p.rows_q = reinterpret_cast<half8*>(reinterpret_cast<uint8_t*>(workspace) + stat_bytes(plan.splits, a));
+    p.row_factor = reinterpret_cast<float*>(p.rows_q + p.row_tiles * c.kv_heads * 32 * c.head_dim / 8);
     p.total_q = (int)a.total_q;
     p.max_q = (int)a.max_q;
     p.pages = (int)c.pages;
