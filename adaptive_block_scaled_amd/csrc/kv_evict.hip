@@ -11,11 +11,17 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Select.  One workgroup per sequence and kv head finds the sum that is the last to be kept,
-// eight bits of its order at a time (the numbers of sums with each next byte, in LDS),
-// then goes through the tokens in order once more and writes those above it, and of those
-// equal to it the first.
+// eleven (then eleven and ten) bits of its order at a time: the numbers of sums with each
+// next digit, in LDS.  Then it goes through the tokens in order once more and writes those
+// above it, and of those equal to it the first.
+//
+// Bound by the latency of one workgroup's passes over its sums: a thread asks for 8 at once
+// when it counts and 4 when it writes.  Sums of one size are many (zeros, above all), and
+// atomics on one place of LDS wait for one another: the lanes with the first lane's digit
+// add once.
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kDigits = 2048;
 
 // Bits that order sums as numbers do: zeros equal, NaN above all.
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -32,10 +38,28 @@ struct SelectArgs {
     int kv_heads, keep, recent, sinks;
 };
 
+__device__ __forceinline__ uint32_t rank_in(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
+
+// One more of `digit` for each lane with `on`.
+__device__ __forceinline__ void count_digit(uint32_t* count, uint32_t digit, bool on) {
+    const uint64_t live = __builtin_amdgcn_ballot_w64(on);
+    if (live == 0) return;
+    const int leader = __builtin_ctzll(live);
+    const uint32_t first = (uint32_t)__builtin_amdgcn_readlane((int)digit, leader);
+    const bool same = on && digit == first;
+    const uint64_t alike = __builtin_amdgcn_ballot_w64(same);
+    if ((int)(threadIdx.x & 63) == leader)
+        atomicAdd(&count[first], (uint32_t)__builtin_popcountll(alike));
+    else if (on && !same)
+        atomicAdd(&count[digit], 1u);
+}
+
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
-    __shared__ uint32_t count[256];
-    __shared__ uint32_t above[2][kWaves];
-    __shared__ uint32_t found[2];
+    __shared__ uint32_t count[kDigits];
+    __shared__ uint32_t sums[kWaves], found[2];
+    __shared__ uint32_t before[2][kWaves];  // above, and equal << 16, of each wave
     const int b = blockIdx.x / p.kv_heads, head = blockIdx.x - b * p.kv_heads;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = p.mass.rows ? p.mass.rows[b] : b;
@@ -57,69 +81,105 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
     const int first = p.sinks, last = n - p.recent;  // (sinks + recent <= keep < n)
     uint32_t need = (uint32_t)(p.keep - p.sinks - p.recent);  // of those between, fewer than they are
     uint32_t prefix = 0;
-    if (need) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) count[tid] = 0;
-            __syncthreads();
-            for (int i = first + tid; i < last; i += kThreads) {
-                const uint32_t o = order_of(in[i]);
-                if (shift == 24 || o >> (shift + 8) == prefix) atomicAdd(&count[(o >> shift) & 255u], 1u);
+    int shift = 32;
+    while (need && shift > 0) {
+        const int bits = shift > 11 ? 11 : shift, below = shift - bits;
+        for (int i = tid; i < kDigits; i += kThreads) count[i] = 0;
+        __syncthreads();
+        const uint32_t mask = (1u << bits) - 1;
+        for (int base = first; base < last; base += 8 * kThreads) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int i = base + j * kThreads + tid;
+                v[j] = i < last ? in[i] : 0.0f;
             }
-            __syncthreads();
-            if (tid < 64) {  // from the largest byte down, four to a lane
-                uint32_t c[4], sum = 0;
-                for (int j = 0; j < 4; j++) sum += c[j] = count[255 - 4 * tid - j];
-                uint32_t upto = sum;
-                for (int d = 1; d < 64; d *= 2) {
-                    const uint32_t o = (uint32_t)__shfl_up((int)upto, d);
-                    upto += lane >= d ? o : 0;
-                }
-                uint32_t before = upto - sum;
-                if (before < need && need <= upto) {
-                    int j = 0;
-                    while (before + c[j] < need) before += c[j++];
-                    found[0] = 255u - 4u * (uint32_t)tid - (uint32_t)j;
-                    found[1] = need - before;
-                }
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t o = order_of(v[j]);
+                const bool on = base + j * kThreads + tid < last && (shift == 32 || o >> shift == prefix);
+                count_digit(count, (o >> below) & mask, on);
             }
-            __syncthreads();
-            prefix = prefix << 8 | found[0];
-            need = found[1];  // of those with this prefix
-            __syncthreads();
         }
-    } else {
-        prefix = 0xFFFFFFFFu;  // none between, NaN neither (need is 0)
+        __syncthreads();
+        // digits from the largest down, two to a thread; sums of the waves before
+        uint32_t c[2], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 2; j++) sum += c[j] = count[kDigits - 1 - 2 * tid - j];
+        uint32_t upto = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const uint32_t o = (uint32_t)__shfl_up((int)upto, d);
+            upto += lane >= d ? o : 0;
+        }
+        if (lane == 63) sums[wave] = upto;
+        __syncthreads();
+        for (int w = 0; w < wave; w++) upto += sums[w];
+        const uint32_t above = upto - sum;
+        if (above < need && need <= upto) {
+            const int j = above + c[0] < need;
+            found[0] = (uint32_t)(kDigits - 1 - 2 * tid - j);
+            found[1] = need - above - (j ? c[0] : 0);
+        }
+        __syncthreads();
+        prefix = prefix << bits | found[0];
+        need = found[1];  // of those with this prefix
+        shift = below;
     }
-    // (a chunk's sums have been read before any of its outputs is written, and these lie no
-    // further than the chunk: `out` may be `in`)
-    uint32_t written = 0, equals = 0;
-    for (int base = 0; base < n; base += kThreads) {
-        const int i = base + tid;
-        const float v = i < n ? in[i] : 0.0f;
-        const uint32_t o = order_of(v);
-        const bool fixed = i < n && (i < first || i >= last), free = i < n && !fixed;
-        const bool equal = free && o == prefix;
-        const uint64_t lower = ((uint64_t)1 << lane) - 1;
-        const uint64_t em = __builtin_amdgcn_ballot_w64(equal);
-        if (lane == 0) above[0][wave] = (uint32_t)__builtin_popcountll(em);
-        __syncthreads();
-        uint32_t er = equals + (uint32_t)__builtin_popcountll(em & lower);
-        for (int w = 0; w < kWaves; w++) {
-            er += w < wave ? above[0][w] : 0;
-            equals += above[0][w];
+    if (shift == 32) prefix = 0xFFFFFFFFu;  // none between, NaN neither (need is 0)
+    // Position i goes to the number of those above before it, and of those equal as many as are
+    // kept.  (A chunk's sums have been read before any of its outputs is written, and these
+    // lie no further than the chunk: `out` may be `in`.)
+    uint32_t aboves = 0, equals = 0;
+    int turn = 0;
+    const auto load = [&](int base, float (&v)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = base + 4 * tid + j < n ? in[base + 4 * tid + j] : 0.0f;
+    };
+    float next[4];
+    load(0, next);
+    for (int base = 0; base < n; base += 4 * kThreads, turn ^= 1) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = next[j];
+        load(base + 4 * kThreads, next);
+        bool up[4], equal[4];
+        uint32_t a = 0, e = 0, wave_a = 0, wave_e = 0;  // before this thread's first, in the wave
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int i = base + 4 * tid + j;
+            const uint32_t o = order_of(v[j]);
+            const bool between = i >= first && i < last;
+            up[j] = i < n && (!between || o > prefix);
+            equal[j] = between && o == prefix;
+            const uint64_t am = __builtin_amdgcn_ballot_w64(up[j]), em = __builtin_amdgcn_ballot_w64(equal[j]);
+            a += rank_in(am);
+            e += rank_in(em);
+            wave_a += (uint32_t)__builtin_popcountll(am);
+            wave_e += (uint32_t)__builtin_popcountll(em);
         }
-        const bool take = fixed || (free && o > prefix) || (equal && er < need);
-        const uint64_t tm = __builtin_amdgcn_ballot_w64(take);
-        if (lane == 0) above[1][wave] = (uint32_t)__builtin_popcountll(tm);
+        if (lane == 0) before[turn][wave] = wave_a | wave_e << 16;
         __syncthreads();
-        uint32_t at = written + (uint32_t)__builtin_popcountll(tm & lower);
+        uint32_t of_waves = 0, all = 0;
+#pragma unroll
         for (int w = 0; w < kWaves; w++) {
-            at += w < wave ? above[1][w] : 0;
-            written += above[1][w];
+            const uint32_t c = before[turn][w];
+            of_waves += w < wave ? c : 0;
+            all += c;
         }
-        if (take) {
-            kept[at] = i;
-            if (out) out[at] = v;
+        a += aboves + (of_waves & 0xFFFFu);
+        e += equals + (of_waves >> 16);
+        aboves += all & 0xFFFFu;
+        equals += all >> 16;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (up[j] || (equal[j] && e < need)) {
+                const uint32_t at = a + (e < need ? e : need);
+                kept[at] = base + 4 * tid + j;
+                if (out) out[at] = v[j];
+            }
+            a += up[j];
+            e += equal[j];
         }
     }
 }

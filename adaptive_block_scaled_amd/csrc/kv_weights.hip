@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kv_evict_internal.h"
 #include "kv_internal.h"
 #include "kv_operand.h"
@@ -26,11 +28,28 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+// Workgroup barrier that orders LDS only (loads from memory stay in flight).
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// f(0), f(1) .. f(n - 1) with constants.
+template <int n, int i = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (i < n) {
+        f(std::integral_constant<int, i>{});
+        each<n, i + 1>(f);
+    }
+}
+
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kUnit = 32;            // keys of a tile
 constexpr float kLowest = -3.0e38f;  // running maximum before any key
 constexpr float kSlack = 64.0f;      // how far scores may exceed the running maximum
 constexpr int kMaxLen = 0x3FFFFF00;  // keys of a sequence
+constexpr int kRawBufferFlags = 0x00020000;  // word 3 of a buffer resource for plain bytes
 
 struct Args {
     const uint8_t *k_codes, *k_scales;
@@ -449,97 +468,160 @@ __device__ __forceinline__ int64_t row_tile(const Args& p, const Sequence& s, in
     return head * p.row_tiles + ((int64_t)s.first_row * p.group.n >> 5) + b + t;
 }
 
-// 16 bytes per lane from memory straight into LDS, lane l's at `lds` + 16 l.
-__device__ __forceinline__ void load_to_lds(const void* from, void* lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// Blocks (w, i), w < kOuter and i < kInner, i fastest: fetch(w) brings operands for w from
+// LDS, beside the last block of the w before; score(w, i) computes a block; f(w, i, x) takes
+// its scores, between the matrix products of the next block.
+template <int kOuter, int kInner, int kSteps, class Fetch, class Score, class F>
+__device__ __forceinline__ void in_turn(Fetch&& fetch, Score&& score, F&& f) {
+    constexpr int kBlocks = kOuter * kInner;
+    const auto outer = [](auto n) { return std::integral_constant<int, decltype(n)::value / kInner>{}; };
+    const auto inner = [](auto n) { return std::integral_constant<int, decltype(n)::value % kInner>{}; };
+    const auto first = std::integral_constant<int, 0>{};
+    fetch(first);
+    if constexpr (kInner == 1 && kOuter > 1) fetch(std::integral_constant<int, 1>{});
+    f32x16 x = score(first, first);
+    each<kBlocks>([&](auto n) {
+        constexpr int next = decltype(n)::value + 1, w = next / kInner + 1;
+        if constexpr (next < kBlocks) {
+            const auto m = std::integral_constant<int, next>{};
+            if constexpr (next % kInner == kInner - 1 && w < kOuter) fetch(std::integral_constant<int, w>{});
+            const f32x16 y = score(outer(m), inner(m));
+            f(outer(n), inner(n), x);
+            x = y;
+#pragma unroll
+            for (int j = 0; j < kSteps; j++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);            // MFMA
+                __builtin_amdgcn_sched_group_barrier(0x400, 16 / kSteps, 0);  // exp2
+                __builtin_amdgcn_sched_group_barrier(0x002, 48 / kSteps, 0);  // other VALU
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);            // LDS read
+            }
+        } else {
+            f(outer(n), inner(n), x);
+        }
+    });
 }
 
-// Rows 32 kTiles per workgroup and a split of the keys that they see; its waves take the
-// key tiles in turn, each for all these rows, and join at the end.
+// kTiles tiles of 32 rows per wave and a split of the keys that the workgroup's rows see.
+// The keys come in groups of four tiles, of which each wave decodes one into LDS, in
+// operand order, for all.
 template <int D, int kTiles>
-__global__ void __launch_bounds__(kThreads, 2) stats_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) stats_kernel(const Args p) {
+    constexpr int kRows = kWaves * kTiles * 32;
     __shared__ uint2 table[256];
-    __shared__ f32x2 part[kWaves][kTiles * 32];
+    __shared__ __attribute__((aligned(16))) half8 keys[2][kWaves][D / 16][64];
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
-    const int block = rest % p.row_blocks, split = rest / p.row_blocks;
+    const int block = p.row_blocks - 1 - rest % p.row_blocks, split = rest / p.row_blocks;
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
     const Sequence s = sequence_of(p, b);
-    const int rows = s.used * (int)p.group.n, row0 = block * kTiles * 32;
+    const int rows = s.used * (int)p.group.n, row0 = block * kRows;
     if (!s.there || row0 >= rows) return;
     const uint32_t four = 4u + ((uint32_t)p.total_q >> 31);  // not foldable (see HighBytes)
     fill_table(table, tid);
+    const int own0 = row0 + wave * kTiles * 32;  // this wave's rows
+    const auto row_at = [&](int i) {
+        const int r = own0 + 32 * i + (lane & 31);
+        return r < rows ? r : rows - 1;
+    };
     half8 q[kTiles][D / 16];
     float factor[kTiles], m[kTiles], l[kTiles];
-    int pos[kTiles];
 #pragma unroll
     for (int i = 0; i < kTiles; i++) {
-        const int r = row0 + 32 * i + (lane & 31), rc = r < rows ? r : rows - 1;
-        factor[i] = load_q<D>(p, s, head, rc, h, q[i]);
-        pos[i] = s.pos0 + (int)p.group.into(rc);
+        factor[i] = load_q<D>(p, s, head, row_at(i), h, q[i]);
         m[i] = kLowest;
         l[i] = 0.0f;
-        // the second pass takes them from here (each wave writes some, of the first split's
-        // workgroups)
-        if (split == 0 && (i & (kWaves - 1)) == (kTiles >= kWaves ? wave : 0) && row0 + 32 * i < rows) {
-            const int64_t at = row_tile(p, s, b, head, row0 / 32 + i);
+        // the second pass takes them from here
+        if (split == 0 && own0 + 32 * i < rows) {
+            const int64_t at = row_tile(p, s, b, head, own0 / 32 + i);
 #pragma unroll
             for (int t = 0; t < D / 16; t++) p.rows_q[(at * (D / 16) + t) * 64 + lane] = q[i][t];
             if (h == 0) p.row_factor[at * 32 + lane] = factor[i];
         }
     }
-    __syncthreads();
-    const int end_row = row0 + kTiles * 32 < rows ? row0 + kTiles * 32 : rows;
-    const int pos_lo = s.pos0 + (int)p.group.into(row0), pos_hi = s.pos0 + (int)p.group.into(end_row - 1);
-    const KeyTiles tiles(p, s.len, pos_lo, pos_hi);
+    const auto position = [&](int r) { return s.pos0 + (int)p.group.into(r < rows ? r : rows - 1); };
+    const int pos_lo = position(own0), pos_hi = position(own0 + kTiles * 32 - 1);
+    const KeyTiles tiles(p, s.len, position(row0), position(row0 + kRows - 1));
     const int share = (tiles.n + p.splits - 1) / p.splits;
     const int from = split * share, to = from + share < tiles.n ? from + share : tiles.n;
-    KeyCodes<D> next;
-    if (from + wave < to) next.load(p, cache_row(p, s, head, tiles(from + wave) * kUnit + (lane & 31)), h);
-    for (int t = from + wave; t < to; t += kWaves) {
-        const KeyCodes<D> codes = next;
-        if (t + kWaves < to) next.load(p, cache_row(p, s, head, tiles(t + kWaves) * kUnit + (lane & 31)), h);
-        const int first = tiles(t) * kUnit;
-        half8 k[D / 16];
-        codes.decode(table, four, k);
-        const bool whole = all_seen(p, s.len, pos_lo, pos_hi, first);
+    // (tiles past the last are the last one again, and not used)
+    const auto tile = [&](int t) { return tiles(t < to ? t : to - 1); };
+    KeyAhead<D> next;
+    if (from < to) {
+        next.look_up(p, s, tile(from + wave) * kUnit + (lane & 31));
+        next.load(p, head, lane);
+        next.look_up(p, s, tile(from + kWaves + wave) * kUnit + (lane & 31));
+    }
+    __syncthreads();
+    // one block's maximum and sum
+    const auto add = [&](int i, const f32x16& x) {
+        float top = x[0];
 #pragma unroll
-        for (int i = 0; i < kTiles; i++) {
-            f32x16 x = scores<D>(k, q[i]);
-            if (!whole) hide(p, s.len, pos[i], first + 4 * h, x);
-            float top = x[0];
-#pragma unroll
-            for (int j = 1; j < 16; j++) top = __builtin_fmaxf(top, x[j]);
-            top *= factor[i];
-            if (top > m[i] + kSlack) {
-                l[i] *= __builtin_amdgcn_exp2f(m[i] - top);
-                m[i] = top;
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 16; j++) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], factor[i], -m[i]));
-            l[i] += sum;
+        for (int j = 1; j < 16; j++) top = __builtin_fmaxf(top, x[j]);
+        top *= factor[i];
+        if (__builtin_amdgcn_ballot_w64(top > m[i] + kSlack)) {
+            const float to = top > m[i] + kSlack ? top : m[i];
+            l[i] *= __builtin_amdgcn_exp2f(m[i] - to);
+            m[i] = to;
         }
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 16; j++) sum[j & 1] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], factor[i], -m[i]));
+        l[i] += sum[0] + sum[1];
+    };
+    int buffer = 0;
+    for (int t = from; t < to; t += kWaves) {
+        {
+            half8 k[D / 16];
+            next.codes.decode(table, four, k);
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) keys[buffer][wave][i][lane] = k[i];
+        }
+        if (t + kWaves < to) {
+            next.load(p, head, lane);
+            next.look_up(p, s, tile(t + 2 * kWaves + wave) * kUnit + (lane & 31));
+        }
+        lds_barrier();
+        const int first = tile(t) * kUnit, last = tile(t + kWaves - 1) * kUnit;
+        const auto key = [&](int w, int i) { return keys[buffer][w][i][lane]; };
+        if (t + kWaves <= to && last - first == (kWaves - 1) * kUnit && all_seen(p, s.len, pos_lo, pos_hi, first) &&
+            all_seen(p, s.len, pos_lo, pos_hi, last)) {
+            half8 k[2][D / 16];
+            in_turn<kWaves, kTiles, D / 16>(
+                [&](auto w) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; j++) k[decltype(w)::value & 1][j] = key(decltype(w)::value, j);
+                },
+                [&](auto w, auto i) { return scores<D>(k[decltype(w)::value & 1], q[decltype(i)::value]); },
+                [&](auto, auto i, const f32x16& x) { add(decltype(i)::value, x); });
+        } else {
+            for (int w = 0; w < kWaves && t + w < to; w++) {
+                const int at = tile(t + w) * kUnit;
+                if (!any_seen(p, s.len, pos_lo, pos_hi, at)) continue;
+                half8 k[D / 16];
+#pragma unroll
+                for (int j = 0; j < D / 16; j++) k[j] = key(w, j);
+#pragma unroll
+                for (int i = 0; i < kTiles; i++) {
+                    f32x16 x = scores<D>(k, q[i]);
+                    hide(p, s.len, position(own0 + 32 * i + (lane & 31)), at + 4 * h, x);
+                    add(i, x);
+                }
+            }
+        }
+        buffer ^= 1;
     }
 #pragma unroll
     for (int i = 0; i < kTiles; i++) {
         const float om = __shfl_xor(m[i], 32), ol = __shfl_xor(l[i], 32);
         const float top = __builtin_fmaxf(m[i], om);
         const float sum = l[i] * __builtin_amdgcn_exp2f(m[i] - top) + ol * __builtin_amdgcn_exp2f(om - top);
-        if (h == 0) part[wave][32 * i + lane] = f32x2{top, sum};
-    }
-    __syncthreads();
-    for (int r = tid; r < kTiles * 32 && row0 + r < rows; r += kThreads) {
-        float top = kLowest, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) top = __builtin_fmaxf(top, part[w][r][0]);
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) sum += part[w][r][1] * __builtin_amdgcn_exp2f(part[w][r][0] - top);
-        const int token = (int)p.group.into(row0 + r), mm = row0 + r - token * (int)p.group.n;
-        p.stats[split * p.stat_rows + (int64_t)(s.first_row + token) * p.heads + head * (int)p.group.n + mm] =
-            f32x2{top, sum};
+        const int r = own0 + 32 * i + lane;
+        if (h == 0 && r < rows) {
+            const int token = (int)p.group.into(r), mm = r - token * (int)p.group.n;
+            p.stats[split * p.stat_rows + (int64_t)(s.first_row + token) * p.heads + head * (int)p.group.n + mm] =
+                f32x2{top, sum};
+        }
     }
 }
 
@@ -586,12 +668,16 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
         // (rows past the last one of a tile have an infinite log; tiles past the last are the
         // last one again, and not used)
         const auto fetch = [&](int t, int buffer) {
-            half8* const to = rows_q + buffer * (kRowTiles * (D / 16) * 64);
+            // 1 KB pieces, 16 bytes per lane, straight into LDS (scalar addresses but for the lane)
+            constexpr int kTileBytes = D / 16 * 1024;
+            const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(from + (int64_t)t * (D / 16 * 64)), 0, kRowTiles * kTileBytes, kRawBufferFlags);
 #pragma unroll
             for (int i = 0; i < kPieces; i++) {
-                const int piece = wave * kPieces + i, rt = t + piece / (D / 16);
-                load_to_lds(from + ((int64_t)(rt < tiles ? rt : tiles - 1) * (D / 16) + piece % (D / 16)) * 64 + lane,
-                            to + piece * 64);
+                const int piece = wave * kPieces + i, w = piece / (D / 16), last = tiles - 1 - t;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (__attribute__((address_space(3))) void*)(rows_q + (buffer * kRowTiles * (D / 16) + piece) * 64),
+                    16, lane * 16, (w < last ? w : last) * kTileBytes + piece % (D / 16) * 1024, 0, 0);
             }
             const int r = 32 * t + tid;
             if (tid < kRowTiles * 32) {
@@ -620,27 +706,45 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
         if (t0 < tiles) arrive(0);
         for (int t = t0; t < tiles; t += kRowTiles) {
             if (t + kRowTiles < tiles) fetch(t + kRowTiles, buffer ^ 1);
-            for (int w = 0; w < kRowTiles && t + w < tiles; w++) {
-                const int ra = 32 * (t + w), rz = ra + 31 < rows ? ra + 31 : rows - 1;
-                const int pos_lo = s.pos0 + (int)p.group.into(ra), pos_hi = s.pos0 + (int)p.group.into(rz);
-                const half8* const at = rows_q + (buffer * kRowTiles + w) * (D / 16 * 64) + lane;
-                half8 q[D / 16];
+            const auto operand = [&](int w, int i) { return rows_q[((buffer * kRowTiles + w) * (D / 16) + i) * 64 + lane]; };
+            const auto add = [&](int i, const f32x16& x, float f, float log) {
 #pragma unroll
-                for (int i = 0; i < D / 16; i++) q[i] = at[i * 64];
-                const float f = row_factor[buffer][32 * w + (lane & 31)];
-                const float log = row_log[buffer][32 * w + (lane & 31)];
+                for (int j = 0; j < 16; j++) acc[i][j] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], f, -log));
+            };
+            const auto position = [&](int r) { return s.pos0 + (int)p.group.into(r < rows ? r : rows - 1); };
+            const int pos_lo = position(32 * t), pos_hi = position(32 * (t + kRowTiles) - 1);
+            if (all_seen(p, s.len, pos_lo, pos_hi, first) &&
+                all_seen(p, s.len, pos_lo, pos_hi, first + (kTiles - 1) * kUnit)) {
+                half8 q[2][D / 16];
+                float f[2], log[2];
+                in_turn<kRowTiles, kTiles, D / 16>(
+                    [&](auto w) {
+                        constexpr int at = decltype(w)::value;
 #pragma unroll
-                for (int i = 0; i < kTiles; i++) {
-                    const int key = first + i * kUnit;
-                    if (!any_seen(p, s.len, pos_lo, pos_hi, key)) continue;
-                    f32x16 x = scores<D>(k[i], q);
-                    if (!all_seen(p, s.len, pos_lo, pos_hi, key)) {
-                        const int r = ra + (lane & 31);
-                        hide(p, s.len, s.pos0 + (int)p.group.into(r < rows ? r : rows - 1), key + 4 * h, x);
+                        for (int j = 0; j < D / 16; j++) q[at & 1][j] = operand(at, j);
+                        f[at & 1] = row_factor[buffer][32 * at + (lane & 31)];
+                        log[at & 1] = row_log[buffer][32 * at + (lane & 31)];
+                    },
+                    [&](auto w, auto i) { return scores<D>(k[decltype(i)::value], q[decltype(w)::value & 1]); },
+                    [&](auto w, auto i, const f32x16& x) {
+                        add(decltype(i)::value, x, f[decltype(w)::value & 1], log[decltype(w)::value & 1]);
+                    });
+            } else {
+                for (int w = 0; w < kRowTiles && t + w < tiles; w++) {
+                    const int r0 = 32 * (t + w), lo_w = position(r0), hi_w = position(r0 + 31);
+                    half8 q[D / 16];
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) q[i] = operand(w, i);
+                    const float f = row_factor[buffer][32 * w + (lane & 31)];
+                    const float log = row_log[buffer][32 * w + (lane & 31)];
+#pragma unroll
+                    for (int i = 0; i < kTiles; i++) {
+                        const int key = first + i * kUnit;
+                        if (!any_seen(p, s.len, lo_w, hi_w, key)) continue;
+                        f32x16 x = scores<D>(k[i], q);
+                        hide(p, s.len, position(r0 + (lane & 31)), key + 4 * h, x);
+                        add(i, x, f, log);
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        acc[i][j] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], f, -log));
                 }
             }
             buffer ^= 1;
@@ -662,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
 
 struct Plan {
     int few;        // rows of a tile where they fill no more than one, else 0
-    int row_tiles;  // many: 32-row tiles of a workgroup of the first pass
+    int row_tiles;  // many: 32-row tiles of a wave of the first pass
     int key_tiles;  // many: 32-key tiles of a wave of the second
     int64_t row_blocks, splits, key_blocks;
 };
@@ -678,8 +782,9 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     const int64_t rows = a.max_q * (a.heads / c.kv_heads), pairs = a.batch * c.kv_heads;
     const int64_t units = (a.max_len < kMaxLen ? a.max_len : kMaxLen) / kUnit + 1;
     p.few = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
-    p.row_tiles = c.head_dim == 256 ? 1 : 4;
-    p.row_blocks = p.few ? 1 : (rows + 32 * p.row_tiles - 1) / (32 * p.row_tiles);
+    p.row_tiles = c.head_dim == 256 ? 1 : 2;
+    const int64_t block = 32 * kWaves * p.row_tiles;
+    p.row_blocks = p.few ? 1 : (rows + block - 1) / block;
     const int64_t groups = pairs * p.row_blocks, full = p.few ? kFew : kMany;
     const int64_t most = (units + 2 * kWaves - 1) / (2 * kWaves);
     p.splits = groups >= full ? 1 : (full + groups - 1) / groups;
@@ -726,7 +831,7 @@ hipError_t launch(const Args& p, const Plan& plan, unsigned groups, unsigned col
     if constexpr (D == 256)
         return launch_many<D, 1, 1>(p, groups, columns, stream);
     else
-        return launch_many<D, 4, 2>(p, groups, columns, stream);
+        return launch_many<D, 2, 2>(p, groups, columns, stream);
 }
 
 }  // namespace
