@@ -14,6 +14,7 @@ typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int8v __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr int BK = IF4_FP8_BLOCK;  // one K step: a block, 128 bytes of each row
@@ -30,8 +31,13 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Wait for all vector memory operations (vmcnt 0, the other counters free).
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// Wait until no more than n vector memory operations are on their way (the other counters
+// free).
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(n < 64, "vmcnt has six bits");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | (n >> 4) << 14);
+}
 
 // 16 bytes per lane from the buffer straight into LDS, lane l's at `lds` + 16 l.
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff,
@@ -83,22 +89,26 @@ struct Scales {
     }
 };
 
-template <int BM, int BN, bool kBf16, bool kBytes>
-__global__ void __launch_bounds__(kThreads)
+template <int BM, int BN, int kWavesM, int kWavesN, int kStages, bool kBf16, bool kBytes>
+__global__ void __launch_bounds__(64 * kWavesM * kWavesN)
 tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales,
             const uint8_t* __restrict__ w_codes, const uint8_t* __restrict__ w_scales,
             int w_square, int64_t M, int64_t N, int64_t K, void* __restrict__ c,
-            int64_t ldc, int tiles_m, int tiles_n) {
-    constexpr int TM = BM / 64, TN = BN / 64;  // 32 x 32 blocks of a wave
-    constexpr int kBuffer = (BM + BN) * BK;    // bytes of one step
+            int64_t ldc, int tiles_m, int tiles_n, float* __restrict__ parts, int splits) {
+    constexpr int WM = BM / kWavesM, WN = BN / kWavesN;  // a wave's part of the tile
+    constexpr int TM = WM / 32, TN = WN / 32;            // its 32 x 32 blocks
+    constexpr int kWaves = kWavesM * kWavesN;
+    constexpr int kBuffer = (BM + BN) * BK;              // bytes of one step
+    constexpr int kStepLoads = (BM + BN) / 8 / kWaves;   // of a wave, 1 KB each
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / kWavesN, wn = wave % kWavesN;
 
     const int total = tiles_m * tiles_n;
-    int bid = blockIdx.x;
+    int bid = blockIdx.x % total;
+    const int split = blockIdx.x / total;
     if (total % 8 == 0) bid = (bid % 8) * (total / 8) + bid / 8;
     const int band = bid / (kBandM * tiles_n), first_m = band * kBandM;
     const int band_m = tiles_m - first_m < kBandM ? tiles_m - first_m : kBandM;
@@ -112,24 +122,30 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(w_codes + n0 * K), 0, (int)(w_rows * K), kRawBufferFlags);
     const int steps = (int)((K + BK - 1) / BK);  // 1 at least
+    // this split's steps, whole windows of scale bytes
+    const int share = splits == 1 ? steps : ((steps + splits - 1) / splits + kWindow - 1) & ~(kWindow - 1);
+    const int begin = split * share, end = begin + share < steps ? begin + share : steps;
 
-    // Loads: instruction i of a wave brings 8 rows (1 KB); lane l the piece that lies at
-    // place l % 8 of row l / 8, which is piece (l % 8) ^ (row / 2 % 8) of the row.
-    // Rows 8 (4 i + wave) ..: row / 2 % 8 = 4 (wave % 2) + l / 16.
+    // Loads: one of a wave brings 8 rows (1 KB).  The piece of 16 bytes that lies at place l
+    // of row r is piece l ^ (r / 2 % 8) of the row, so that the reads of 16 lanes, one piece of
+    // 16 rows, cover all banks.  (Rows 8 (kWaves i + wave) ..: r / 2 % 8 = 4 (wave % 2) + lane / 16.)
     const int piece = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
     const uint32_t voff = (uint32_t)(lane >> 3) * (uint32_t)K + 16 * piece;
-    auto load_step = [&](int s) {
-        // in a last step that is no whole block, pieces past K are outside
-        const uint32_t v = (int64_t)s * BK + 16 * piece < K ? voff : 0x80000000u;  // (and steps past the last)
-        uint8_t* const to = smem + (s & 1) * kBuffer;
+    const int64_t limit = (int64_t)end * BK < K ? (int64_t)end * BK : K;
+    auto load_step = [&](int s, int buffer) {
+        // in a last step that is no whole block, pieces past K are outside, and so are steps
+        // past the last
+        // (one test, or a branch parts the reads from the products)
+        const uint32_t v = (int64_t)s * BK + 16 * piece < limit ? voff : 0x80000000u;
+        uint8_t* const to = smem + buffer * kBuffer;
 #pragma unroll
-        for (int i = 0; i < BM / 32; i++) {
-            const int r = 8 * (4 * i + wave);
+        for (int i = 0; i < BM / 8 / kWaves; i++) {
+            const int r = 8 * (kWaves * i + wave);
             load_to_lds(ra, v, (uint32_t)r * (uint32_t)K + (uint32_t)s * BK, to + r * BK);
         }
 #pragma unroll
-        for (int i = 0; i < BN / 32; i++) {
-            const int r = 8 * (4 * i + wave);
+        for (int i = 0; i < BN / 8 / kWaves; i++) {
+            const int r = 8 * (kWaves * i + wave);
             load_to_lds(rw, v, (uint32_t)r * (uint32_t)K + (uint32_t)s * BK, to + (BM + r) * BK);
         }
     };
@@ -141,12 +157,12 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     int off_a[TM], off_w[TN];
 #pragma unroll
     for (int i = 0; i < TM; i++) {
-        const int r = wm * (BM / 2) + 32 * i + (lane & 31);
+        const int r = wm * WM + 32 * i + (lane & 31);
         off_a[i] = (r < a_rows ? r : a_rows - 1) * steps;
     }
 #pragma unroll
     for (int j = 0; j < TN; j++) {
-        int r = wn * (BN / 2) + 32 * j + (lane & 31);
+        int r = wn * WN + 32 * j + (lane & 31);
         r = r < w_rows ? r : w_rows - 1;
         off_w[j] = (w_square ? r / BK : r) * steps;
     }
@@ -175,19 +191,19 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     // Fragment of row block R (32 rows), half h of a step's 128: lane l holds row l % 32,
     // pieces 4 h + 2 (l / 32) and the next.
     const int frow = lane & 31, fsw = (lane >> 1) & 7;
-    const int fp[2] = {2 * (lane >> 5), 2 * (lane >> 5) + 1};
     auto fragment = [&](const uint8_t* block, int h) {
-        const int4v x = *reinterpret_cast<const int4v*>(block + frow * BK + 16 * ((4 * h + fp[0]) ^ fsw));
-        const int4v y = *reinterpret_cast<const int4v*>(block + frow * BK + 16 * ((4 * h + fp[1]) ^ fsw));
+        const int at = 4 * h + 2 * (lane >> 5);
+        const int4v x = *reinterpret_cast<const int4v*>(block + frow * BK + 16 * (at ^ fsw));
+        const int4v y = *reinterpret_cast<const int4v*>(block + frow * BK + 16 * ((at + 1) ^ fsw));
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     };
     int8v fa[2][TM], fw[2][TN];
-    auto read = [&](int s, int h) {
-        const uint8_t* b = smem + (s & 1) * kBuffer;
+    auto read = [&](int buffer, int h) {
+        const uint8_t* b = smem + buffer * kBuffer;
 #pragma unroll
-        for (int i = 0; i < TM; i++) fa[h][i] = fragment(b + (wm * (BM / 2) + 32 * i) * BK, h);
+        for (int i = 0; i < TM; i++) fa[h][i] = fragment(b + (wm * WM + 32 * i) * BK, h);
 #pragma unroll
-        for (int j = 0; j < TN; j++) fw[h][j] = fragment(b + (BM + wn * (BN / 2) + 32 * j) * BK, h);
+        for (int j = 0; j < TN; j++) fw[h][j] = fragment(b + (BM + wn * WN + 32 * j) * BK, h);
     };
     auto multiply = [&](int h, auto byte) {
         if constexpr (kBf16) {
@@ -215,27 +231,29 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
             }
         }
     };
-    constexpr int kProducts = kBf16 ? 1 : 4;
-    constexpr int kLoads = ((BM + BN) / 32 + TM * TN - 1) / (TM * TN);
-    constexpr int kReads = (2 * (TM + TN) + TM * TN - 1) / (TM * TN);
     // One step: the products of its two halves, each product beside reads of the half
     // after it.  The barrier in the middle says both that step s + 1 has arrived and that
-    // all waves have read step s, so that its buffer takes step s + 2.  (No branch inside:
-    // steps past the last load zeros.)
+    // all waves have read step s, so that its buffer takes step s + kStages.  (No branch
+    // inside: steps past the last load zeros.)
+    constexpr int kProducts = kBf16 ? 1 : 4;  // matrix instructions of a 32 x 32 x 64 product
+    constexpr int kLoads = (kStepLoads + TM * TN - 1) / (TM * TN);
+    constexpr int kReads = (2 * (TM + TN) + TM * TN - 1) / (TM * TN);
+    static_assert(kWindow % kStages == 0, "a step's buffer goes by its place in the window");
     auto step = [&](int s, auto byte) {
-        read(s, 1);
+        constexpr int buffer = decltype(byte)::value % kStages;
+        read(buffer, 1);
         multiply(0, byte);
 #pragma unroll
         for (int i = 0; i < TM * TN; i++) {
-            __builtin_amdgcn_sched_group_barrier(0x008, kProducts, 0);       // MFMA
-            __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);  // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, kProducts, 0);  // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);     // LDS read
         }
         __builtin_amdgcn_sched_barrier(0);
-        wait_loads();
+        wait_loads<(kStages - 2) * kStepLoads>();
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        load_step(s + 2);
-        read(s + 1, 0);
+        load_step(s + kStages, buffer);
+        read((buffer + 1) % kStages, 0);
         multiply(1, byte);
 #pragma unroll
         for (int i = 0; i < TM * TN; i++) {
@@ -246,23 +264,40 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    load_scales(0);
-    load_step(0);
-    wait_loads();
-    lds_barrier();
-    take_scales(0);
-    load_step(1);
-    read(0, 0);
-    for (int s = 0; s < steps; s += kWindow) {
-        load_scales(s + kWindow);
-        step(s, std::integral_constant<int, 0>{});
-        if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
-        if (s + 2 < steps) step(s + 2, std::integral_constant<int, 2>{});
-        if (s + 3 < steps) step(s + 3, std::integral_constant<int, 3>{});
-        take_scales(s + kWindow);
+    if (begin < end) {
+        load_scales(begin);
+#pragma unroll
+        for (int i = 0; i < kStages; i++) load_step(begin + i, i);
+        wait_loads<(kStages - 1) * kStepLoads>();
+        lds_barrier();
+        take_scales(begin);
+        read(0, 0);
+        for (int s = begin; s < end; s += kWindow) {
+            load_scales(s + kWindow);
+            step(s, std::integral_constant<int, 0>{});
+            if (s + 1 < end) step(s + 1, std::integral_constant<int, 1>{});
+            if (s + 2 < end) step(s + 2, std::integral_constant<int, 2>{});
+            if (s + 3 < end) step(s + 3, std::integral_constant<int, 3>{});
+            take_scales(s + kWindow);
+        }
+        wait_loads<0>();  // (the last steps' zeros: LDS is not given back before they have arrived)
     }
-    wait_loads();  // (the last steps' zeros: LDS is not given back before they have arrived)
 
+    if (splits > 1) {  // fp32 sums of this split, [M, N] of its own
+        float* const part = parts + (int64_t)split * M * N;
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+            for (int j = 0; j < TN; j++) {
+                const int col = wn * WN + 32 * j + (lane & 31);
+#pragma unroll
+                for (int r = 0; r < 16; r++) {
+                    const int row = wm * WM + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                    if (row < a_rows && col < w_rows) part[(m0 + row) * N + n0 + col] = acc[i][j][r];
+                }
+            }
+        return;
+    }
     // lane: column lane % 32 of a block, rows 8 (r / 4) + 4 (lane / 32) + r % 4.  The
     // stores go through a buffer resource over the tile's rows that exist: one
     // vector offset per lane, and a store past M is dropped.
@@ -275,13 +310,13 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
         const uint32_t vo = (uint32_t)(lane & 31) * kSize + (uint32_t)(4 * (lane >> 5)) * ld;
 #pragma unroll
         for (int j = 0; j < TN; j++) {
-            const int col = wn * (BN / 2) + 32 * j;
+            const int col = wn * WN + 32 * j;
             if (col + (lane & 31) >= w_rows) continue;
 #pragma unroll
             for (int i = 0; i < TM; i++)
 #pragma unroll
                 for (int r = 0; r < 16; r++) {
-                    const uint32_t so = (uint32_t)(wm * (BM / 2) + 32 * i + 8 * (r >> 2) + (r & 3)) * ld +
+                    const uint32_t so = (uint32_t)(wm * WM + 32 * i + 8 * (r >> 2) + (r & 3)) * ld +
                                         col * kSize;
                     if constexpr (kBf16)
                         __builtin_amdgcn_raw_buffer_store_b16(
@@ -297,10 +332,10 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     for (int i = 0; i < TM; i++)
 #pragma unroll
         for (int j = 0; j < TN; j++) {
-            const int64_t col = n0 + wn * (BN / 2) + 32 * j + (lane & 31);
+            const int64_t col = n0 + wn * WN + 32 * j + (lane & 31);
 #pragma unroll
             for (int r = 0; r < 16; r++) {
-                const int64_t row = m0 + wm * (BM / 2) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                const int64_t row = m0 + wm * WM + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
                 if (row < M && col < N) {
                     if constexpr (kBf16)
                         reinterpret_cast<__bf16*>(c)[row * ldc + col] = (__bf16)acc[i][j][r];
@@ -309,6 +344,154 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
                 }
             }
         }
+}
+
+// Few rows of A (M <= 16 kTiles): the bytes of W bound the call, and each is used by one
+// wave only, so that they go from memory to registers, kDepth blocks ahead, with no LDS.
+// A wave has 16 rows of W and all rows of A (16 x 16 x 128 products, W's rows in the
+// accumulators' registers); the workgroup's 8 waves are kRows groups of 16 rows of W by
+// 8 / kRows shares of K, whose sums are added up in LDS in their order.
+constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
+
+// The two pieces of 16 bytes of a lane's 32 codes of block s: row `row` of the resource,
+// zeros past K.
+__device__ __forceinline__ int8v load_codes(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, int k, int s,
+                                            int64_t K) {
+    const bool a = (int64_t)s * BK + k < K, b = (int64_t)s * BK + k + 16 < K;
+    const int4v x = __builtin_bit_cast(int4v, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  rsrc, a ? (int)voff : (int)0x80000000, s * BK, 0));
+    const int4v y = __builtin_bit_cast(int4v, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  rsrc, b ? (int)(voff + 16) : (int)0x80000000, s * BK, 0));
+    return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <int kTiles, int kRows, bool kBf16, bool kBytes>
+__global__ void __launch_bounds__(kFewThreads)
+few_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales,
+           const uint8_t* __restrict__ w_codes, const uint8_t* __restrict__ w_scales,
+           int w_square, int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc) {
+    constexpr int kShares = kFewWaves / kRows;
+    __shared__ float4v sums[kShares > 1 ? kFewWaves : 1][kTiles][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = wave / kShares, part = wave % kShares;
+    const int64_t n0 = ((int64_t)blockIdx.x * kRows + group) * 16;
+    const int w_rows = N - n0 < 16 ? (int)(N - n0 > 0 ? N - n0 : 0) : 16;
+    const int steps = (int)((K + BK - 1) / BK);
+    const int share = ((steps + kShares - 1) / kShares + kWindow - 1) & ~(kWindow - 1);
+    const int from = part * share, to = from + share < steps ? from + share : steps;
+
+    float4v acc[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; i++) acc[i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    if (w_rows > 0 && from < to) {
+        const int r = lane & 15, k = 32 * (lane >> 4);
+        const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(w_codes + n0 * K), 0, (int)(w_rows * K), kRawBufferFlags);
+        const __amdgpu_buffer_rsrc_t ra =
+            __builtin_amdgcn_make_buffer_rsrc((void*)a_codes, 0, (int)(M * K), kRawBufferFlags);
+        // (rows past M and N read as zeros or as the last row's, and are not stored)
+        const uint32_t vw = (uint32_t)r * (uint32_t)K + k;
+        const int64_t w_first = w_square ? n0 / BK : n0;
+        const Scales<kBytes> scales_w(w_scales, w_first, w_square ? (N + BK - 1) / BK : N, steps);
+        const Scales<kBytes> scales_a(a_scales, 0, M, steps);
+        const int off_w = (w_square ? 0 : r < w_rows ? r : w_rows - 1) * steps;
+        uint32_t va[kTiles];
+        int off_a[kTiles];
+#pragma unroll
+        for (int i = 0; i < kTiles; i++) {
+            const int m = 16 * i + r < M ? 16 * i + r : (int)M - 1;
+            va[i] = (uint32_t)m * (uint32_t)K + k;
+            off_a[i] = m * steps;
+        }
+        // W of four blocks at once, those of the next four on their way; A's block by block
+        int8v w[2][kWindow];
+        uint32_t ew[2], ea[2][kTiles];
+        const auto load = [&](int which, int s) {
+#pragma unroll
+            for (int u = 0; u < kWindow; u++) w[which][u] = load_codes(rw, vw, k, s + u, K);
+            ew[which] = scales_w.window(off_w + s);
+#pragma unroll
+            for (int i = 0; i < kTiles; i++) ea[which][i] = scales_a.window(off_a[i] + s);
+        };
+        const auto multiply = [&](auto which, int s) {
+            constexpr int b = decltype(which)::value;
+            const uint32_t sw = scales_w.take(ew[b], off_w + s);
+            uint32_t sa[kTiles];
+#pragma unroll
+            for (int i = 0; i < kTiles; i++) sa[i] = scales_a.take(ea[b][i], off_a[i] + s);
+            int8v a[kWindow][kTiles];
+#pragma unroll
+            for (int u = 0; u < kWindow; u++)
+#pragma unroll
+                for (int i = 0; i < kTiles; i++) a[u][i] = load_codes(ra, va[i], k, s + u, K);
+#pragma unroll
+            for (int u = 0; u < kWindow; u++) {
+                // (blocks past the last are zeros, and their bytes another row's: not NaN then)
+                const bool past = s + u >= steps;
+                const uint32_t eu = past ? 127u : sw >> (8 * u);
+                bf16x8 x[4], y[4];
+                if constexpr (!kBf16) widen(w[b][u], eu, x);
+#pragma unroll
+                for (int i = 0; i < kTiles; i++) {
+                    const uint32_t fu = past ? 127u : sa[i] >> (8 * u);
+                    if constexpr (kBf16) {
+                        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[b][u], a[u][i], acc[i], 0, 0, 0,
+                                                                                  (int)eu, 0, (int)fu);
+                    } else {
+                        widen(a[u][i], fu, y);
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], y[q], acc[i], 0, 0, 0);
+                    }
+                }
+            }
+        };
+        load(0, from);
+        for (int s = from; s < to; s += 2 * kWindow) {
+            load(1, s + kWindow);
+            multiply(std::integral_constant<int, 0>{}, s);
+            if (s + kWindow >= to) break;
+            load(0, s + 2 * kWindow);
+            multiply(std::integral_constant<int, 1>{}, s + kWindow);
+        }
+    }
+    if constexpr (kShares > 1) {
+#pragma unroll
+        for (int i = 0; i < kTiles; i++) sums[wave][i][lane] = acc[i];
+        __syncthreads();
+        if (part != 0) return;
+#pragma unroll
+        for (int i = 0; i < kTiles; i++)
+            for (int p = 1; p < kShares; p++) acc[i] += sums[wave + p][i][lane];
+    }
+    // lane: row lane % 16 of A's tile, columns n0 + 4 (lane / 16) .. + 3
+#pragma unroll
+    for (int i = 0; i < kTiles; i++) {
+        const int64_t row = 16 * i + (lane & 15), col = n0 + 4 * (lane >> 4);
+        if (row >= M) continue;
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            if (col + r >= N) continue;
+            if constexpr (kBf16)
+                reinterpret_cast<__bf16*>(c)[row * ldc + col + r] = (__bf16)acc[i][r];
+            else
+                reinterpret_cast<float*>(c)[row * ldc + col + r] = acc[i][r];
+        }
+    }
+}
+
+template <int kTiles, int kRows, bool kBf16, bool kBytes>
+hipError_t launch_few_rows(const Fp8Gemm& g, hipStream_t stream) {
+    const unsigned groups = (unsigned)((g.N + 16 * kRows - 1) / (16 * kRows));
+    hipLaunchKernelGGL((few_kernel<kTiles, kRows, kBf16, kBytes>), dim3(groups), dim3(kFewThreads), 0, stream,
+                       g.a_codes, g.a_scales, g.w_codes, g.w_scales, g.w_square, g.M, g.N, g.K, g.c, g.ldc);
+    return hipGetLastError();
+}
+
+template <bool kBf16, bool kBytes>
+hipError_t launch_few(const Fp8Gemm& g, hipStream_t stream) {
+    return launch_few_rows<1, 1, kBf16, kBytes>(g, stream);
 }
 
 template <bool kBf16>
@@ -325,23 +508,83 @@ zero_kernel(void* __restrict__ c, int64_t M, int64_t N, int64_t ldc) {
     }
 }
 
-template <int BM, int BN, bool kBf16, bool kBytes>
-hipError_t launch_tile(const Fp8Gemm& g, hipStream_t stream) {
-    constexpr int kSmem = 2 * (BM + BN) * BK;
+// The splits' sums, added in their order.
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads)
+join_kernel(const float* __restrict__ parts, int splits, int64_t M, int64_t N, void* __restrict__ c, int64_t ldc) {
+    const int64_t total = M * N;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+        float v = parts[i];
+        for (int p = 1; p < splits; p++) v += parts[p * total + i];
+        const int64_t at = i / N * ldc + i % N;
+        if constexpr (kBf16)
+            reinterpret_cast<__bf16*>(c)[at] = (__bf16)v;
+        else
+            reinterpret_cast<float*>(c)[at] = v;
+    }
+}
+
+// How a product is cut: the tile, and the splits of K.
+struct Plan {
+    int tile;  // 0: few_kernel; rows and columns of a tile else
+    int splits;
+};
+
+// (kTileStages: as many as leave room for two workgroups on a CU, for one of 256 x 256)
+constexpr int kCus = 256;
+
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+    const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
+    if (M <= 4 || (M <= 16 && tiles(64) < kCus)) return {0, 1};
+    Plan p;
+    p.tile = M <= 64 ? 64 : tiles(256) >= kCus ? 256 : 2 * tiles(128) >= kCus ? 128 : 64;
+    const int64_t steps = (K + BK - 1) / BK, count = tiles(p.tile);
+    int64_t splits = count >= kCus ? 1 : 2 * kCus / count;
+    splits = splits < steps / (2 * kWindow) ? splits : steps / (2 * kWindow);
+    p.splits = (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
+    return p;
+}
+
+template <int BM, int BN, int kWavesM, int kWavesN, int kStages, bool kBf16, bool kBytes>
+hipError_t launch_tile(const Fp8Gemm& g, int splits, hipStream_t stream) {
+    constexpr int kSmem = kStages * (BM + BN) * BK;
+    const auto kernel = tile_kernel<BM, BN, kWavesM, kWavesN, kStages, kBf16, kBytes>;
     const int64_t tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
+    if (tiles_m * tiles_n * splits > 0x7FFFFFFF) return hipErrorInvalidValue;
     // dynamic LDS above 64 KB must be allowed per kernel (idempotent, any device)
-    const hipError_t err = hipFuncSetAttribute((const void*)tile_kernel<BM, BN, kBf16, kBytes>,
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const hipError_t err =
+        hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((tile_kernel<BM, BN, kBf16, kBytes>), dim3((unsigned)(tiles_m * tiles_n)), dim3(kThreads),
-                       kSmem, stream, g.a_codes, g.a_scales, g.w_codes, g.w_scales, g.w_square,
-                       g.M, g.N, g.K, g.c, g.ldc, (int)tiles_m, (int)tiles_n);
+    float* const parts = reinterpret_cast<float*>(g.workspace);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles_m * tiles_n * splits)), dim3(64 * kWavesM * kWavesN), kSmem, stream, g.a_codes,
+                       g.a_scales, g.w_codes, g.w_scales, g.w_square, g.M, g.N, g.K, g.c, g.ldc, (int)tiles_m,
+                       (int)tiles_n, parts, splits);
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess || splits == 1) return st;
+    const int64_t blocks = (g.M * g.N + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL(join_kernel<kBf16>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0, stream,
+                       parts, splits, g.M, g.N, g.c, g.ldc);
     return hipGetLastError();
+}
+
+template <bool kBf16, bool kBytes>
+hipError_t launch_of(const Fp8Gemm& g, hipStream_t stream) {
+    const Plan p = plan_of(g.M, g.N, g.K);
+    if (p.tile == 0) return launch_few<kBf16, kBytes>(g, stream);
+    if (kBytes || p.tile == 64) return launch_tile<64, 64, 2, 2, 4, kBf16, kBytes>(g, p.splits, stream);
+    if constexpr (!kBytes) {
+        if (p.tile == 128) return launch_tile<128, 128, 2, 2, 2, kBf16, false>(g, p.splits, stream);
+        return launch_tile<256, 256, 2, 2, 2, kBf16, false>(g, p.splits, stream);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-int64_t fp8_gemm_workspace(int64_t, int64_t, int64_t) { return 0; }
+int64_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
+    const Plan p = plan_of(M, N, K);
+    return p.splits > 1 ? p.splits * M * N * 4 : 0;
+}
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t stream) {
     if (g.K == 0) {
@@ -354,14 +597,8 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t stream) {
     const int64_t steps = (g.K + BK - 1) / BK;
     const int64_t w_scales = (g.w_square ? (g.N + BK - 1) / BK : g.N) * steps;
     const bool bytes = g.M * steps < 4 || w_scales < 4;
-    const int64_t wide = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-    if (g.c_bf16)
-        return bytes         ? launch_tile<128, 128, true, true>(g, stream)
-               : wide >= 256 ? launch_tile<256, 256, true, false>(g, stream)
-                             : launch_tile<128, 128, true, false>(g, stream);
-    return bytes         ? launch_tile<128, 128, false, true>(g, stream)
-           : wide >= 256 ? launch_tile<256, 256, false, false>(g, stream)
-                         : launch_tile<128, 128, false, false>(g, stream);
+    if (g.c_bf16) return bytes ? launch_of<true, true>(g, stream) : launch_of<true, false>(g, stream);
+    return bytes ? launch_of<false, true>(g, stream) : launch_of<false, false>(g, stream);
 }
 
 }  // namespace if4
