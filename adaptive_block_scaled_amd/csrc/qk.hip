@@ -223,17 +223,26 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p, float*
     }
 }
 
-// Adds `rows` rows of 2 dim sums: 16 columns per workgroup, 16 threads each.
-__global__ void __launch_bounds__(kThreads)
+// Adds `rows` rows (kRows at most) of 2 dim sums: 16 columns per workgroup, 64 threads each,
+// so that a thread's few loads are on their way at once (16 threads of 64 loads each: 20 us).
+constexpr int kRows = 1024;
+constexpr int kJoinThreads = 1024, kJoinParts = kJoinThreads / 16;
+__global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const float* __restrict__ sums, int rows, int dim, float* dq, float* dk) {
-    __shared__ float shared[16][17];
-    const int col = blockIdx.x * 16 + threadIdx.x % 16, part = threadIdx.x / 16;
-    float t = 0.0f;
-    for (int r = part; r < rows; r += 16) t += sums[(int64_t)r * 2 * dim + col];
-    shared[part][threadIdx.x % 16] = t;
+    __shared__ float shared[kJoinParts][17];
+    const int c = threadIdx.x % 16, col = blockIdx.x * 16 + c, part = threadIdx.x / 16;
+    float v[kRows / kJoinParts], t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows / kJoinParts; i++) {
+        const int r = part + i * kJoinParts;
+        v[i] = r < rows ? sums[(int64_t)r * 2 * dim + col] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows / kJoinParts; i++) t += v[i];
+    shared[part][c] = t;
     __syncthreads();
     if (part == 0) {
-        for (int q = 1; q < 16; q++) t += shared[q][threadIdx.x];
+        for (int q = 1; q < kJoinParts; q++) t += shared[q][c];
         float* const to = col < dim ? dq : dk;
         if (to) to[col < dim ? col : col - dim] = t;
     }
@@ -242,7 +251,6 @@ join_kernel(const float* __restrict__ sums, int rows, int dim, float* dq, float*
 // Vectors of a lane: as many as leave this many waves, for the chip to be full; the
 // backward pass has no more workgroups than kRows rows of sums.
 constexpr int kFullWaves = 256 * 16;
-constexpr int kRows = 1024;
 
 Args make_args(const if4_qk_args& a, int lanes) {
     Args p;
@@ -290,7 +298,7 @@ hipError_t backward(const if4_qk_args& a, float* sums, hipStream_t stream) {
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(2 * a.head_dim / 16)), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(2 * a.head_dim / 16)), dim3(kJoinThreads), 0, stream,
                        sums, rows, (int)a.head_dim, a.q.heads ? a.q.d_weight : nullptr,
                        a.k.heads ? a.k.d_weight : nullptr);
     return hipGetLastError();

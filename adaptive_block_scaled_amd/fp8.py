@@ -22,7 +22,14 @@ import ctypes
 
 import torch
 
+from . import if4
 from .if4 import _check, _dtype_code, _input, _need, lib
+
+try:
+    from . import _op_call
+except ImportError as e:
+    raise ImportError(f"the C++ calls ({if4.HERE}/_op_call.so) do not load ({e}); build them with "
+                      "`python -m adaptive_block_scaled_amd.build`") from e
 
 EXPORTS = ("if4_fp8_quantize", "if4_fp8_quantize_t", "if4_fp8_gemm", "if4_fp8_gemm_workspace")
 BLOCK = 128
@@ -43,6 +50,7 @@ def _declare():
 
 
 _declare()
+_op_call.bind_fp8(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS))
 
 
 def _blocks(n: int) -> int:
@@ -69,12 +77,24 @@ def quantize(x: torch.Tensor, square: bool = False, out=None):
     16-byte aligned rows, K a multiple of 16).  Returns (codes uint8 [rows, K], scales
     uint8 [rows, ceil(K/128)], or [ceil(rows/128), ceil(K/128)] with `square`); `out`
     may pass preallocated (codes, scales)."""
+    if out is None:
+        q = _op_call.quantize(x, bool(square), False)
+        if type(q) is tuple:
+            return q
+        if q:
+            _check("if4_fp8_quantize", q)
     _input(x)
     return _quantize(lib.if4_fp8_quantize, "if4_fp8_quantize", x, x.shape[0], x.shape[1], square, out)
 
 
 def quantize_t(x: torch.Tensor, square: bool = False, out=None):
     """quantize(x.T) without the transposed copy, for x [K, rows], K a multiple of 16."""
+    if out is None:
+        q = _op_call.quantize(x, bool(square), True)
+        if type(q) is tuple:
+            return q
+        if q:
+            _check("if4_fp8_quantize_t", q)
     _input(x)
     return _quantize(lib.if4_fp8_quantize_t, "if4_fp8_quantize_t", x, x.shape[1], x.shape[0], square, out)
 
@@ -91,6 +111,12 @@ def gemm(a_codes, a_scales, w_codes, w_scales, dtype=torch.bfloat16, out=None, w
     """C[M, N] = A[M, K] W[N, K]^T, summed in fp32, of `dtype` (bf16 or fp32).  A has
     blocks of one row, W blocks of one row or squares, as its scales' shape says.
     `out` may pass C with a row stride, `workspace` a uint8 tensor of workspace_bytes()."""
+    if out is None and workspace is None and (dtype is torch.bfloat16 or dtype is torch.float32):
+        c = _op_call.gemm(a_codes, a_scales, w_codes, w_scales, dtype is torch.bfloat16)
+        if type(c) is int:
+            _check("if4_fp8_gemm", c)
+        elif c is not None:
+            return c
     for name, t in (("a_codes", a_codes), ("w_codes", w_codes), ("w_scales", w_scales)):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise ValueError(f"{name} must be a 2-D tensor")

@@ -14,6 +14,7 @@ import math
 
 import torch
 
+from .fp8 import _op_call
 from .if4 import _check, _dtype_code, lib
 
 EXPORTS = ("if4_norm_rotate", "if4_norm_rotate_backward", "if4_norm_rotate_backward_workspace")
@@ -47,6 +48,7 @@ def _declare():
 
 
 _declare()
+_op_call.bind_qk(ctypes.cast(lib.if4_norm_rotate, ctypes.c_void_p).value)
 
 
 def rotation_table(rows: int, rotary: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -144,6 +146,13 @@ def norm_rotate(q, k, q_weight, k_weight, table, positions, *, eps: float = 1e-6
     Returns (q, k) of `dtype` (default: q's); `out` may pass them, the inputs themselves
     among them.  A token whose position is outside the table is skipped: its outputs keep
     what they hold, and are unset without `out`."""
+    if out is None and (dtype is None or dtype is torch.bfloat16 or dtype is torch.float32):
+        bf16 = (dtype or getattr(q, "dtype", None)) is torch.bfloat16
+        y = _op_call.norm_rotate(q, k, q_weight, k_weight, table, positions, eps, interleaved, bf16)
+        if type(y) is tuple:
+            return y
+        if y:
+            _check("if4_norm_rotate", y)
     if dtype is None:
         dtype = q.dtype if out is None and isinstance(q, torch.Tensor) else out[0].dtype
     a, dev = _args(q, k, q_weight, k_weight, table, positions, eps, interleaved, dtype)
