@@ -89,7 +89,7 @@ struct Scales {
     }
 };
 
-template <int BM, int BN, int kWavesM, int kWavesN, int kStagesA, int kStagesW, bool kBf16, bool kBytes>
+template <int BM, int BN, int kWavesM, int kWavesN, int kStages, bool kBf16, bool kBytes>
 __global__ void __launch_bounds__(64 * kWavesM * kWavesN)
 tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales,
             const uint8_t* __restrict__ w_codes, const uint8_t* __restrict__ w_scales,
@@ -98,9 +98,8 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     constexpr int WM = BM / kWavesM, WN = BN / kWavesN;  // a wave's part of the tile
     constexpr int TM = WM / 32, TN = WN / 32;            // its 32 x 32 blocks
     constexpr int kWaves = kWavesM * kWavesN;
-    // loads of a wave for a step, 1 KB each; bytes of a step; where W's buffers start
-    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = BN / 8 / kWaves;
-    constexpr int kBytesA = BM * BK, kBytesW = BN * BK, kW = kStagesA * kBytesA;
+    constexpr int kBuffer = (BM + BN) * BK;              // bytes of one step
+    constexpr int kStepLoads = (BM + BN) / 8 / kWaves;   // of a wave, 1 KB each
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -133,23 +132,21 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     const int piece = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
     const uint32_t voff = (uint32_t)(lane >> 3) * (uint32_t)K + 16 * piece;
     const int64_t limit = (int64_t)end * BK < K ? (int64_t)end * BK : K;
-    // in a last step that is no whole block, pieces past K are outside, and so are steps past
-    // the last (one test, or a branch parts the reads from the products)
-    auto voff_of = [&](int s) { return (int64_t)s * BK + 16 * piece < limit ? voff : 0x80000000u; };
-    auto load_a = [&](int s, int at) {
-        const uint32_t v = voff_of(s);
+    // (A's first: W's first is 8% slower where tiles are many, 1490 and 1610 us)
+    auto load_step = [&](int s, int buffer) {
+        // in a last step that is no whole block, pieces past K are outside, and so are steps
+        // past the last (one test, or a branch parts the reads from the products)
+        const uint32_t v = (int64_t)s * BK + 16 * piece < limit ? voff : 0x80000000u;
+        uint8_t* const to = smem + buffer * kBuffer;
 #pragma unroll
-        for (int i = 0; i < kLoadsA; i++) {
+        for (int i = 0; i < BM / 8 / kWaves; i++) {
             const int r = 8 * (kWaves * i + wave);
-            load_to_lds(ra, v, (uint32_t)r * (uint32_t)K + (uint32_t)s * BK, smem + at + r * BK);
+            load_to_lds(ra, v, (uint32_t)r * (uint32_t)K + (uint32_t)s * BK, to + r * BK);
         }
-    };
-    auto load_w = [&](int s, int at) {
-        const uint32_t v = voff_of(s);
 #pragma unroll
-        for (int i = 0; i < kLoadsW; i++) {
+        for (int i = 0; i < BN / 8 / kWaves; i++) {
             const int r = 8 * (kWaves * i + wave);
-            load_to_lds(rw, v, (uint32_t)r * (uint32_t)K + (uint32_t)s * BK, smem + kW + at + r * BK);
+            load_to_lds(rw, v, (uint32_t)r * (uint32_t)K + (uint32_t)s * BK, to + (BM + r) * BK);
         }
     };
 
@@ -201,11 +198,12 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
         return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     };
     int8v fa[2][TM], fw[2][TN];
-    auto read = [&](int at_a, int at_w, int h) {
+    auto read = [&](int buffer, int h) {
+        const uint8_t* b = smem + buffer * kBuffer;
 #pragma unroll
-        for (int i = 0; i < TM; i++) fa[h][i] = fragment(smem + at_a + (wm * WM + 32 * i) * BK, h);
+        for (int i = 0; i < TM; i++) fa[h][i] = fragment(b + (wm * WM + 32 * i) * BK, h);
 #pragma unroll
-        for (int j = 0; j < TN; j++) fw[h][j] = fragment(smem + kW + at_w + (wn * WN + 32 * j) * BK, h);
+        for (int j = 0; j < TN; j++) fw[h][j] = fragment(b + (BM + wn * WN + 32 * j) * BK, h);
     };
     auto multiply = [&](int h, auto byte) {
         if constexpr (kBf16) {
@@ -235,22 +233,15 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     };
     // One step: the products of its two halves, each product beside reads of the half
     // after it.  The barrier in the middle says both that step s + 1 has arrived and that
-    // all waves have read step s, so that its buffers take the steps kStagesA and kStagesW
-    // further on.  (No branch inside: steps past the last load zeros.)  W's loads come
-    // first: with one more stage of A, the barrier need not wait for A's last ones.
+    // all waves have read step s, so that its buffer takes step s + kStages.  (No branch
+    // inside: steps past the last load zeros.)
     constexpr int kProducts = kBf16 ? 1 : 4;  // matrix instructions of a 32 x 32 x 64 product
-    constexpr int kLoads = (kLoadsA + kLoadsW + TM * TN - 1) / (TM * TN);
+    constexpr int kLoads = (kStepLoads + TM * TN - 1) / (TM * TN);
     constexpr int kReads = (2 * (TM + TN) + TM * TN - 1) / (TM * TN);
-    constexpr int kOnTheWay = (kStagesW - 2) * (kLoadsA + kLoadsW) + (kStagesA - kStagesW) * kLoadsA;
-    static_assert(kWindow % kStagesW == 0, "a step's buffer of W goes by its place in the window");
-    int at_a = 0;
+    static_assert(kWindow % kStages == 0, "a step's buffer goes by its place in the window");
     auto step = [&](int s, auto byte) {
-        constexpr int w = decltype(byte)::value % kStagesW;
-        // (A's goes by it too where it has as many stages)
-        const int a = kStagesA == kStagesW ? w * kBytesA : at_a;
-        const int next = kStagesA == kStagesW ? (w + 1) % kStagesW * kBytesA
-                                              : (at_a == (kStagesA - 1) * kBytesA ? 0 : at_a + kBytesA);
-        read(a, w * kBytesW, 1);
+        constexpr int buffer = decltype(byte)::value % kStages;
+        read(buffer, 1);
         multiply(0, byte);
 #pragma unroll
         for (int i = 0; i < TM * TN; i++) {
@@ -258,12 +249,11 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
             __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);     // LDS read
         }
         __builtin_amdgcn_sched_barrier(0);
-        wait_loads<kOnTheWay>();
+        wait_loads<(kStages - 2) * kStepLoads>();
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        load_w(s + kStagesW, w * kBytesW);
-        load_a(s + kStagesA, a);
-        read(next, (w + 1) % kStagesW * kBytesW, 0);
+        load_step(s + kStages, buffer);
+        read((buffer + 1) % kStages, 0);
         multiply(1, byte);
 #pragma unroll
         for (int i = 0; i < TM * TN; i++) {
@@ -272,20 +262,16 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
             __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);  // loads
         }
         __builtin_amdgcn_sched_barrier(0);
-        at_a = next;
     };
 
     if (begin < end) {
         load_scales(begin);
 #pragma unroll
-        for (int i = 0; i < kStagesA; i++) {
-            if (i < kStagesW) load_w(begin + i, i * kBytesW);
-            load_a(begin + i, i * kBytesA);
-        }
-        wait_loads<(kStagesW - 1) * kLoadsW + (kStagesA - 1) * kLoadsA>();
+        for (int i = 0; i < kStages; i++) load_step(begin + i, i);
+        wait_loads<(kStages - 1) * kStepLoads>();
         lds_barrier();
         take_scales(begin);
-        read(0, 0, 0);
+        read(0, 0);
         for (int s = begin; s < end; s += kWindow) {
             load_scales(s + kWindow);
             step(s, std::integral_constant<int, 0>{});
@@ -559,10 +545,10 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
     return p;
 }
 
-template <int BM, int BN, int kWavesM, int kWavesN, int kStagesA, int kStagesW, bool kBf16, bool kBytes>
+template <int BM, int BN, int kWavesM, int kWavesN, int kStages, bool kBf16, bool kBytes>
 hipError_t launch_tile(const Fp8Gemm& g, int splits, hipStream_t stream) {
-    constexpr int kSmem = (kStagesA * BM + kStagesW * BN) * BK;
-    const auto kernel = tile_kernel<BM, BN, kWavesM, kWavesN, kStagesA, kStagesW, kBf16, kBytes>;
+    constexpr int kSmem = kStages * (BM + BN) * BK;
+    const auto kernel = tile_kernel<BM, BN, kWavesM, kWavesN, kStages, kBf16, kBytes>;
     const int64_t tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
     if (tiles_m * tiles_n * splits > 0x7FFFFFFF) return hipErrorInvalidValue;
     // dynamic LDS above 64 KB must be allowed per kernel (idempotent, any device)
@@ -585,10 +571,10 @@ template <bool kBf16, bool kBytes>
 hipError_t launch_of(const Fp8Gemm& g, hipStream_t stream) {
     const Plan p = plan_of(g.M, g.N, g.K);
     if (p.tile == 0) return launch_few<kBf16, kBytes>(g, stream);
-    if (kBytes || p.tile == 64) return launch_tile<64, 64, 2, 2, 4, 4, kBf16, kBytes>(g, p.splits, stream);
+    if (kBytes || p.tile == 64) return launch_tile<64, 64, 2, 2, 4, kBf16, kBytes>(g, p.splits, stream);
     if constexpr (!kBytes) {
-        if (p.tile == 128) return launch_tile<128, 128, 2, 2, 2, 2, kBf16, false>(g, p.splits, stream);
-        return launch_tile<256, 256, 2, 2, 3, 2, kBf16, false>(g, p.splits, stream);
+        if (p.tile == 128) return launch_tile<128, 128, 2, 2, 2, kBf16, false>(g, p.splits, stream);
+        return launch_tile<256, 256, 2, 2, 2, kBf16, false>(g, p.splits, stream);
     }
     return hipErrorInvalidValue;
 }
