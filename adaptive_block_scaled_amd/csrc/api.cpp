@@ -179,6 +179,14 @@ int check_mass(const if4_kv_mass& m, int64_t batch, bool out_needed) {
     return IF4_OK;
 }
 
+int check_select(const if4_kv_mass& m, int64_t batch, int64_t kv_heads, int64_t keep) {
+    if (m.mass_rows < 0 || m.mass_rows > kMaxIndex || m.width < 0 || m.width > kMaxIndex)
+        return IF4_ERR_SHAPE;
+    if (batch < 0 || kv_heads <= 0 || kv_heads > kMaxKvHeads || batch > 0x7FFFFFFF / kv_heads)
+        return IF4_ERR_SHAPE;
+    return keep < 0 || keep > kMaxIndex ? IF4_ERR_SHAPE : IF4_OK;
+}
+
 // No sequence can have more rows than there are.
 if4_kv_attention_args bounded(const if4_kv_attention_args& a) {
     if4_kv_attention_args r = a;
@@ -485,21 +493,32 @@ int if4_kv_weights(const if4_kv_cache* cache, const if4_kv_attention_args* args,
     return hip_status(if4::launch_kv_weights(*cache, a, *mass, workspace, (hipStream_t)stream));
 }
 
+int64_t if4_kv_select_workspace(const if4_kv_mass* mass, int64_t batch, int64_t kv_heads,
+                                int64_t keep) {
+    if (!mass) return -IF4_ERR_NULL;
+    const int st = check_select(*mass, batch, kv_heads, keep);
+    if (st != IF4_OK) return -st;
+    return batch == 0 || keep == 0 ? 0 : if4::kv_select_workspace(*mass, batch, kv_heads, keep);
+}
+
 int if4_kv_select(const if4_kv_mass* mass, const int32_t* seq_lens, int64_t batch,
                   int64_t kv_heads, int64_t keep, int64_t recent, int64_t sinks, int32_t* kept,
-                  void* stream) {
+                  void* workspace, int64_t workspace_bytes, void* stream) {
     if (!mass) return IF4_ERR_NULL;
-    if (batch < 0 || kv_heads <= 0 || kv_heads > kMaxKvHeads || batch > 0x7FFFFFFF / kv_heads)
-        return IF4_ERR_SHAPE;
-    if (keep < 0 || keep > kMaxIndex) return IF4_ERR_SHAPE;
+    int st = check_select(*mass, batch, kv_heads, keep);
+    if (st != IF4_OK) return st;
     if (recent < 0 || sinks < 0 || recent > keep || sinks > keep - recent) return IF4_ERR_RANGE;
-    const int st = check_mass(*mass, batch, false);
+    st = check_mass(*mass, batch, false);
     if (st != IF4_OK) return st;
     if (batch == 0 || keep == 0) return IF4_OK;
     if (!seq_lens || !kept) return IF4_ERR_NULL;
     if (!aligned(seq_lens, 4) || !aligned(kept, 4)) return IF4_ERR_ALIGN;
+    const int64_t need = if4::kv_select_workspace(*mass, batch, kv_heads, keep);
+    if (need > 0 && !workspace) return IF4_ERR_NULL;
+    if (need > workspace_bytes) return IF4_ERR_SHAPE;
+    if (need > 0 && !aligned(workspace, 16)) return IF4_ERR_ALIGN;
     return hip_status(if4::launch_kv_select(*mass, seq_lens, batch, kv_heads, keep, recent, sinks,
-                                            kept, (hipStream_t)stream));
+                                            kept, workspace, (hipStream_t)stream));
 }
 
 int if4_kv_compact(const if4_kv_cache* cache, const int32_t* page_table, int64_t table_stride,

@@ -10,15 +10,20 @@ namespace if4 {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Select.  One workgroup per sequence and kv head finds the sum that is the last to be kept,
-// eleven (then eleven and ten) bits of its order at a time: the numbers of sums with each
-// next digit, in LDS.  Then it goes through the tokens in order once more and writes those
-// above it, and of those equal to it the first.
+// Select.  The sum that is the last to be kept is found eleven (then eleven and ten) bits of
+// its order at a time: the numbers of sums with each next digit, in LDS.  Then the tokens
+// are gone through in order once more, and those above it are written, and of those equal to
+// it the first.
 //
-// Bound by the latency of one workgroup's passes over its sums: a thread asks for 8 at once
-// when it counts and 4 when it writes.  Sums of one size are many (zeros, above all), and
-// atomics on one place of LDS wait for one another: the lanes with the first lane's digit
-// add once.
+// One workgroup per sequence and kv head does all of it (select_kernel) where rows are
+// short, or are so many that they fill the chip.  Bound by the latency of its passes: a thread
+// asks for 8 sums at once when it counts and 4 when it writes.  Sums of one size are many
+// (zeros, above all), and atomics on one place of LDS wait for one another: the lanes
+// with the first lane's digit add once.
+//
+// Of long rows a workgroup takes a segment, and the passes are launches (segment kernels):
+// each leaves its digits' numbers in the workspace, and each workgroup of the next adds them
+// up itself.  131071 sums of 16 rows: 159 us in one workgroup each.
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kDigits = 2048;
@@ -56,89 +61,99 @@ __device__ __forceinline__ void count_digit(uint32_t* count, uint32_t digit, boo
         atomicAdd(&count[digit], 1u);
 }
 
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
-    __shared__ uint32_t count[kDigits];
-    __shared__ uint32_t sums[kWaves], found[2];
-    __shared__ uint32_t before[2][kWaves];  // above, and equal << 16, of each wave
-    const int b = blockIdx.x / p.kv_heads, head = blockIdx.x - b * p.kv_heads;
+// A row of sums, as its workgroups see it.
+struct Row {
+    int n, first, last;  // tokens; those first .. last - 1 are chosen from
+    const float* in;
+    float* out;
+    int32_t* kept;
+    __device__ __forceinline__ Row(const SelectArgs& p, int pair) {
+        const int b = pair / p.kv_heads, head = pair - b * p.kv_heads;
+        const int64_t row = p.mass.rows ? p.mass.rows[b] : b;
+        n = 0;
+        if (row >= 0 && row < p.mass.mass_rows) {
+            n = p.seq_lens[b];
+            n = n < 0 ? 0 : n > p.mass.width ? (int)p.mass.width : n;
+        }
+        first = p.sinks;  // (sinks + recent <= keep)
+        last = n - p.recent;
+        in = p.mass.in + row * p.mass.in_stride_row + head * p.mass.in_stride_head;
+        out = p.mass.out ? p.mass.out + row * p.mass.out_stride_row + head * p.mass.out_stride_head : nullptr;
+        kept = p.kept + (int64_t)pair * p.keep;
+    }
+};
+
+constexpr int bits_of(int level) { return level < 2 ? 11 : 10; }
+constexpr int below(int level) { return level == 0 ? 21 : level == 1 ? 10 : 0; }
+
+// Counts the digits of sums from .. to - 1 that have the prefix of the levels before.
+__device__ __forceinline__ void count_digits(uint32_t* count, const float* in, int from, int to, int level,
+                                             uint32_t prefix) {
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) count[i] = 0;
+    __syncthreads();
+    const int under = below(level), width = bits_of(level);
+    const uint32_t mask = (1u << width) - 1;
+    for (int base = from; base < to; base += 8 * kThreads) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int i = base + j * kThreads + threadIdx.x;
+            v[j] = i < to ? in[i] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const uint32_t o = order_of(v[j]);
+            const bool on = base + j * kThreads + (int)threadIdx.x < to && (level == 0 || o >> (under + width) == prefix);
+            count_digit(count, (o >> under) & mask, on);
+        }
+    }
+    __syncthreads();
+}
+
+// The digit that the sum number `need` from the largest has, of c[0] and c[1] sums with this
+// thread's digits kDigits - 1 - 2 t and the one below: found[0]; and its number among those
+// with the digit: found[1].
+struct Shared {
+    uint32_t sums[kWaves], found[2];
+};
+__device__ __forceinline__ void find_digit(Shared& sh, const uint32_t (&c)[2], uint32_t need) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t row = p.mass.rows ? p.mass.rows[b] : b;
-    int32_t* const kept = p.kept + (int64_t)blockIdx.x * p.keep;
-    int n = 0;
-    if (row >= 0 && row < p.mass.mass_rows) {
-        n = p.seq_lens[b];
-        n = n < 0 ? 0 : n > p.mass.width ? (int)p.mass.width : n;
+    const uint32_t sum = c[0] + c[1];
+    uint32_t upto = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = (uint32_t)__shfl_up((int)upto, d);
+        upto += lane >= d ? o : 0;
     }
-    const float* const in = p.mass.in + row * p.mass.in_stride_row + head * p.mass.in_stride_head;
-    float* const out = p.mass.out ? p.mass.out + row * p.mass.out_stride_row + head * p.mass.out_stride_head : nullptr;
-    if (n <= p.keep) {
-        for (int i = tid; i < p.keep; i += kThreads) {
-            kept[i] = i < n ? i : -1;
-            if (out && out != in && i < n) out[i] = in[i];
-        }
-        return;
+    if (lane == 63) sh.sums[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; w++) upto += sh.sums[w];
+    const uint32_t above = upto - sum;
+    if (above < need && need <= upto) {
+        const int j = above + c[0] < need;
+        sh.found[0] = (uint32_t)(kDigits - 1 - 2 * tid - j);
+        sh.found[1] = need - above - (j ? c[0] : 0);
     }
-    const int first = p.sinks, last = n - p.recent;  // (sinks + recent <= keep < n)
-    uint32_t need = (uint32_t)(p.keep - p.sinks - p.recent);  // of those between, fewer than they are
-    uint32_t prefix = 0;
-    int shift = 32;
-    while (need && shift > 0) {
-        const int bits = shift > 11 ? 11 : shift, below = shift - bits;
-        for (int i = tid; i < kDigits; i += kThreads) count[i] = 0;
-        __syncthreads();
-        const uint32_t mask = (1u << bits) - 1;
-        for (int base = first; base < last; base += 8 * kThreads) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int i = base + j * kThreads + tid;
-                v[j] = i < last ? in[i] : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const uint32_t o = order_of(v[j]);
-                const bool on = base + j * kThreads + tid < last && (shift == 32 || o >> shift == prefix);
-                count_digit(count, (o >> below) & mask, on);
-            }
-        }
-        __syncthreads();
-        // digits from the largest down, two to a thread; sums of the waves before
-        uint32_t c[2], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 2; j++) sum += c[j] = count[kDigits - 1 - 2 * tid - j];
-        uint32_t upto = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const uint32_t o = (uint32_t)__shfl_up((int)upto, d);
-            upto += lane >= d ? o : 0;
-        }
-        if (lane == 63) sums[wave] = upto;
-        __syncthreads();
-        for (int w = 0; w < wave; w++) upto += sums[w];
-        const uint32_t above = upto - sum;
-        if (above < need && need <= upto) {
-            const int j = above + c[0] < need;
-            found[0] = (uint32_t)(kDigits - 1 - 2 * tid - j);
-            found[1] = need - above - (j ? c[0] : 0);
-        }
-        __syncthreads();
-        prefix = prefix << bits | found[0];
-        need = found[1];  // of those with this prefix
-        shift = below;
-    }
-    if (shift == 32) prefix = 0xFFFFFFFFu;  // none between, NaN neither (need is 0)
-    // Position i goes to the number of those above before it, and of those equal as many as are
-    // kept.  (A chunk's sums have been read before any of its outputs is written, and these
-    // lie no further than the chunk: `out` may be `in`.)
-    uint32_t aboves = 0, equals = 0;
+    __syncthreads();
+}
+
+// Writes the tokens from .. to - 1 that stay: position i goes to the number of those above
+// before it, and of those equal as many as are kept; `aboves` (the first and last ones of a row
+// among them) and `equals` lie before `from`.  A chunk's sums have been read before any
+// of its outputs is written, and these lie no further than the chunk: `out` may be `in`
+// where one workgroup writes the row.
+__device__ __forceinline__ void write_kept(const Row& row, float* out, int from, int to, uint32_t prefix, uint32_t need,
+                                           uint32_t aboves, uint32_t equals) {
+    __shared__ uint32_t before[2][kWaves];  // above, and equal << 16, of each wave
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int turn = 0;
     const auto load = [&](int base, float (&v)[4]) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = base + 4 * tid + j < n ? in[base + 4 * tid + j] : 0.0f;
+        for (int j = 0; j < 4; j++) v[j] = base + 4 * tid + j < to ? row.in[base + 4 * tid + j] : 0.0f;
     };
     float next[4];
-    load(0, next);
-    for (int base = 0; base < n; base += 4 * kThreads, turn ^= 1) {
+    load(from, next);
+    for (int base = from; base < to; base += 4 * kThreads, turn ^= 1) {
         float v[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) v[j] = next[j];
@@ -149,9 +164,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
         for (int j = 0; j < 4; j++) {
             const int i = base + 4 * tid + j;
             const uint32_t o = order_of(v[j]);
-            const bool between = i >= first && i < last;
-            up[j] = i < n && (!between || o > prefix);
-            equal[j] = between && o == prefix;
+            const bool between = i >= row.first && i < row.last;
+            up[j] = i < to && (!between || o > prefix);
+            equal[j] = i < to && between && o == prefix;
             const uint64_t am = __builtin_amdgcn_ballot_w64(up[j]), em = __builtin_amdgcn_ballot_w64(equal[j]);
             a += rank_in(am);
             e += rank_in(em);
@@ -175,13 +190,150 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
         for (int j = 0; j < 4; j++) {
             if (up[j] || (equal[j] && e < need)) {
                 const uint32_t at = a + (e < need ? e : need);
-                kept[at] = base + 4 * tid + j;
+                row.kept[at] = base + 4 * tid + j;
                 if (out) out[at] = v[j];
             }
             a += up[j];
             e += equal[j];
         }
     }
+}
+
+// A prefix that no sum between has above or at it: none of them stays.
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
+    __shared__ uint32_t count[kDigits];
+    __shared__ Shared sh;
+    const Row row(p, blockIdx.x);
+    if (row.n <= p.keep) {
+        for (int i = threadIdx.x; i < p.keep; i += kThreads) {
+            row.kept[i] = i < row.n ? i : -1;
+            if (row.out && row.out != row.in && i < row.n) row.out[i] = row.in[i];
+        }
+        return;
+    }
+    uint32_t need = (uint32_t)(p.keep - p.sinks - p.recent);  // of those between, fewer than they are
+    uint32_t prefix = need ? 0 : kNone;
+    for (int level = 0; level < 3 && need; level++) {
+        count_digits(count, row.in, row.first, row.last, level, prefix);
+        const uint32_t c[2] = {count[kDigits - 1 - 2 * threadIdx.x], count[kDigits - 2 - 2 * threadIdx.x]};
+        find_digit(sh, c, need);
+        prefix = prefix << bits_of(level) | sh.found[0];
+        need = sh.found[1];  // of those with this prefix
+    }
+    write_kept(row, row.out, 0, row.n, prefix, need, 0, 0);
+}
+
+// Workspace of the segment kernels: [3][rows][segments][kDigits] numbers, then [rows][segments]
+// States, then the sums of rows that are written in place, [rows][keep].
+constexpr int kSegment = 8192;
+struct State {
+    uint32_t prefix, need;  // of the row, after the levels so far
+    uint32_t above;         // sums above it in the segments before this one
+    uint32_t unused;
+};
+struct SegmentArgs {
+    SelectArgs s;
+    uint32_t* counts;
+    State* states;
+    float* moved;  // NULL: out is another tensor
+    int rows, segments;
+};
+
+// What the levels before `level` say, from their numbers; `equals` are the sums equal to
+// the prefix in the segments before.
+__device__ __forceinline__ State resolve(const SegmentArgs& p, Shared& sh, int pair, int segment, int level,
+                                         uint32_t& equals) {
+    __shared__ uint32_t part[2];
+    State st = {0, (uint32_t)(p.s.keep - p.s.sinks - p.s.recent), 0, 0};
+    equals = 0;
+    if (level == 0) return st;
+    State* const own = p.states + (int64_t)pair * p.segments + segment;
+    if (level > 1) st = *own;
+    const int tid = threadIdx.x;
+    const uint32_t* const at = p.counts + (((int64_t)(level - 1) * p.rows + pair) * p.segments) * kDigits;
+    uint32_t c[2] = {0, 0}, mine[2] = {0, 0};
+    for (int g = 0; g < p.segments; g++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const uint32_t v = at[(int64_t)g * kDigits + kDigits - 1 - 2 * tid - j];
+            c[j] += v;
+            mine[j] += g < segment ? v : 0;
+        }
+    if (tid < 2) part[tid] = 0;
+    find_digit(sh, c, st.need);
+    const uint32_t digit = sh.found[0];
+    uint32_t up = 0;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const uint32_t d = (uint32_t)(kDigits - 1 - 2 * tid - j);
+        up += d > digit ? mine[j] : 0;
+        if (d == digit) part[1] = mine[j];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) up += (uint32_t)__shfl_xor((int)up, d);
+    if ((tid & 63) == 0 && up) atomicAdd(&part[0], up);
+    __syncthreads();
+    st.prefix = st.prefix << bits_of(level - 1) | digit;
+    st.need = sh.found[1];
+    st.above += part[0];
+    equals = part[1];
+    if (tid == 0) *own = st;
+    return st;
+}
+
+// (a segment's part of the tokens that are chosen from)
+template <int kLevel>
+__global__ void __launch_bounds__(kThreads) segment_count_kernel(const SegmentArgs p) {
+    __shared__ uint32_t count[kDigits];
+    __shared__ Shared sh;
+    const int pair = blockIdx.x / p.segments, segment = blockIdx.x - pair * p.segments;
+    const Row row(p.s, pair);
+    if (row.n <= p.s.keep || p.s.keep == p.s.sinks + p.s.recent) return;
+    uint32_t equals;
+    const State st = resolve(p, sh, pair, segment, kLevel, equals);
+    const int from = segment * kSegment, to = from + kSegment;
+    count_digits(count, row.in, from > row.first ? from : row.first, to < row.last ? to : row.last, kLevel, st.prefix);
+    uint32_t* const at = p.counts + (((int64_t)kLevel * p.rows + pair) * p.segments + segment) * kDigits;
+    for (int i = threadIdx.x; i < kDigits; i += kThreads) at[i] = count[i];
+}
+
+__global__ void __launch_bounds__(kThreads) segment_write_kernel(const SegmentArgs p) {
+    __shared__ Shared sh;
+    const int pair = blockIdx.x / p.segments, segment = blockIdx.x - pair * p.segments;
+    const Row row(p.s, pair);
+    const int from = segment * kSegment, to = from + kSegment < row.n ? from + kSegment : row.n;
+    if (row.n <= p.s.keep) {
+        for (int i = from + threadIdx.x; i < from + kSegment && i < p.s.keep; i += kThreads) {
+            row.kept[i] = i < row.n ? i : -1;
+            if (row.out && row.out != row.in && i < row.n) row.out[i] = row.in[i];
+        }
+        return;
+    }
+    State st = {kNone, 0, 0, 0};
+    uint32_t equals = 0;
+    if (p.s.keep > p.s.sinks + p.s.recent) st = resolve(p, sh, pair, segment, 3, equals);
+    const int fixed = (from < row.first ? from : row.first) + (from > row.last ? from - row.last : 0);
+    write_kept(row, p.moved ? p.moved + (int64_t)pair * p.s.keep : row.out, from, to, st.prefix, st.need,
+               st.above + (uint32_t)fixed, equals);
+}
+
+// The sums of rows that are written in place, once all of them have been read.
+__global__ void __launch_bounds__(kThreads) segment_move_kernel(const SegmentArgs p) {
+    const int pair = blockIdx.x / p.segments, segment = blockIdx.x - pair * p.segments;
+    const Row row(p.s, pair);
+    if (row.n <= p.s.keep) return;
+    const int from = segment * kSegment;
+    for (int i = from + threadIdx.x; i < from + kSegment && i < p.s.keep; i += kThreads)
+        row.out[i] = p.moved[(int64_t)pair * p.s.keep + i];
+}
+
+// Segments of a row, 0 where one workgroup takes it: rows of up to two segments, and those
+// that fill the chip without being parted.
+int64_t segments_of(const if4_kv_mass& m, int64_t rows, int64_t keep) {
+    if (m.width <= 2 * kSegment || rows >= 512 || keep >= m.width) return 0;
+    return (m.width + kSegment - 1) / kSegment;
 }
 
 // ---------------------------------------------------------------------------
@@ -263,11 +415,33 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const CompactArgs
 
 }  // namespace
 
+int64_t kv_select_workspace(const if4_kv_mass& m, int64_t batch, int64_t kv_heads, int64_t keep) {
+    const int64_t rows = batch * kv_heads, segments = segments_of(m, rows, keep);
+    return segments ? rows * (segments * (3 * kDigits * 4 + (int64_t)sizeof(State)) + keep * 4) : 0;
+}
+
 hipError_t launch_kv_select(const if4_kv_mass& m, const int32_t* seq_lens, int64_t batch,
                             int64_t kv_heads, int64_t keep, int64_t recent, int64_t sinks,
-                            int32_t* kept, hipStream_t stream) {
-    const SelectArgs p = {m, seq_lens, kept, (int)kv_heads, (int)keep, (int)recent, (int)sinks};
-    hipLaunchKernelGGL(select_kernel, dim3((unsigned)(batch * kv_heads)), dim3(kThreads), 0, stream, p);
+                            int32_t* kept, void* workspace, hipStream_t stream) {
+    const SelectArgs s = {m, seq_lens, kept, (int)kv_heads, (int)keep, (int)recent, (int)sinks};
+    const int64_t rows = batch * kv_heads, segments = segments_of(m, rows, keep);
+    if (segments == 0) {
+        hipLaunchKernelGGL(select_kernel, dim3((unsigned)rows), dim3(kThreads), 0, stream, s);
+        return hipGetLastError();
+    }
+    SegmentArgs p;
+    p.s = s;
+    p.rows = (int)rows;
+    p.segments = (int)segments;
+    p.counts = reinterpret_cast<uint32_t*>(workspace);
+    p.states = reinterpret_cast<State*>(p.counts + 3 * rows * segments * kDigits);
+    p.moved = m.out == m.in ? reinterpret_cast<float*>(p.states + rows * segments) : nullptr;
+    const dim3 grid((unsigned)(rows * segments));
+    hipLaunchKernelGGL(segment_count_kernel<0>, grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL(segment_count_kernel<1>, grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL(segment_count_kernel<2>, grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL(segment_write_kernel, grid, dim3(kThreads), 0, stream, p);
+    if (p.moved) hipLaunchKernelGGL(segment_move_kernel, grid, dim3(kThreads), 0, stream, p);
     return hipGetLastError();
 }
 

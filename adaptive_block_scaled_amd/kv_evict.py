@@ -21,7 +21,7 @@ from .if4 import _check, lib
 from .kv_cache import KVCache, _Attention, _Cache, _cache, _held, _plain, _raw_stream, _vectors
 
 EXPORTS = ("if4_kv_weights", "if4_kv_weights_workspace", "if4_kv_weights_workspace_most", "if4_kv_select",
-           "if4_kv_compact")
+           "if4_kv_select_workspace", "if4_kv_compact")
 
 
 class _Mass(ctypes.Structure):
@@ -39,7 +39,9 @@ def _declare():
         f.restype = i64
         f.argtypes = [cache, args]
     lib.if4_kv_select.restype = ci
-    lib.if4_kv_select.argtypes = [mass, vp, i64, i64, i64, i64, i64, vp, vp]
+    lib.if4_kv_select.argtypes = [mass, vp, i64, i64, i64, i64, i64, vp, vp, i64, vp]
+    lib.if4_kv_select_workspace.restype = i64
+    lib.if4_kv_select_workspace.argtypes = [mass, i64, i64, i64]
     lib.if4_kv_compact.restype = ci
     lib.if4_kv_compact.argtypes = [cache, vp, i64, vp, i64, i64, vp, i64, vp]
 
@@ -146,13 +148,14 @@ def workspace_bytes(cache: KVCache, *, total_q: int, heads: int, batch: int, max
 
 
 def select(mass: torch.Tensor, seq_lens: torch.Tensor, keep: int, *, recent: int = 0, sinks: int = 0, rows=None,
-           out=None, mass_out=None) -> torch.Tensor:
+           out=None, mass_out=None, workspace=None) -> torch.Tensor:
     """Positions of the `keep` tokens of each sequence and kv head to keep, int32 [batch,
     kv_heads, keep], ascending: the first `sinks`, the last `recent`, and the ones with the
     largest sums between them (equal ones: the earlier); all of a sequence that has no more,
     then -1.  Row rows[b] of mass belongs to sequence b, as in accumulate; seq_lens counts
     its tokens.  `mass_out` (mass itself is fine) gets the kept tokens' sums in
-    places 0, 1, ..; `out` may pass the positions preallocated."""
+    places 0, 1, ..; `out` may pass the positions preallocated, `workspace` a uint8 tensor of
+    select_workspace_bytes()."""
     if not isinstance(mass, torch.Tensor) or mass.dim() != 3 or not mass.is_cuda:
         raise ValueError("mass must be a CUDA tensor [sequences, kv_heads, width]")
     kv_heads, dev = mass.shape[1], mass.device
@@ -172,11 +175,30 @@ def select(mass: torch.Tensor, seq_lens: torch.Tensor, keep: int, *, recent: int
         out = torch.empty((batch, kv_heads, keep), dtype=torch.int32, device=dev)
     else:
         _plain(out, "out", (batch, kv_heads, keep), torch.int32, dev.index)
-    st = lib.if4_kv_select(_mass(mass, mass_out, rows, batch, dev), seq_lens.data_ptr(), batch, kv_heads, keep,
-                           recent, sinks, out.data_ptr(), _raw_stream(dev.index))
+    m = _mass(mass, mass_out, rows, batch, dev)
+    need = lib.if4_kv_select_workspace(m, batch, kv_heads, keep)
+    if need < 0:
+        _check("if4_kv_select", -need)
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != dev or workspace.dtype != torch.uint8 or \
+                not workspace.is_contiguous() or workspace.numel() < need:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = lib.if4_kv_select(m, seq_lens.data_ptr(), batch, kv_heads, keep, recent, sinks, out.data_ptr(),
+                           workspace.data_ptr() if need else None, need, _raw_stream(dev.index))
     if st:
         _check("if4_kv_select", st)
     return out
+
+
+def select_workspace_bytes(mass: torch.Tensor, batch: int, keep: int) -> int:
+    """Bytes of workspace that select() takes for such sums (0 unless they are long)."""
+    m = _Mass(mass_rows=mass.shape[0], width=mass.shape[2])
+    need = lib.if4_kv_select_workspace(m, batch, mass.shape[1], keep)
+    if need < 0:
+        _check("if4_kv_select_workspace", -need)
+    return need
 
 
 def compact(cache: KVCache, page_table: torch.Tensor, kept: torch.Tensor, new_table: torch.Tensor) -> KVCache:

@@ -69,10 +69,17 @@ int64_t if4_kv_weights_workspace_most(const if4_kv_cache* cache, const if4_kv_at
  *   mass     out (NULL: not wanted) gets their sums at 0, 1, ..; its width is keep or more;
  *            what lies behind stays.  It may be `in`.
  *   recent + sinks <= keep
+ *   workspace  device, 16-byte aligned, of if4_kv_select_workspace() bytes (NULL where that
+ *              is 0); holds nothing between calls
  */
 int if4_kv_select(const if4_kv_mass* mass, const int32_t* seq_lens, int64_t batch,
                   int64_t kv_heads, int64_t keep, int64_t recent, int64_t sinks, int32_t* kept,
-                  void* stream);
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for these arguments (of `mass` the sizes count, no pointer), or a
+ * negative status code. */
+int64_t if4_kv_select_workspace(const if4_kv_mass* mass, int64_t batch, int64_t kv_heads,
+                                int64_t keep);
 
 /*
  * Copy K and V of the kept tokens: position kept[b, h, i] of sequence b and kv head h, by

@@ -216,7 +216,9 @@ def chosen(row, n, keep, recent, sinks):
 SELECTS = [  # lens, width, keep, recent, sinks
     ([1], 1, 1, 0, 0), ([10, 3, 0], 12, 4, 1, 1), ([100, 64, 65], 100, 64, 0, 0), ([1000, 999], 1100, 333, 20, 4),
     ([5000, 1024, 1025], 5000, 1024, 256, 64), ([40], 30, 20, 5, 5), ([70], 70, 20, 10, 10), ([70], 70, 20, 20, 0),
-    ([9000], 9000, 8999, 0, 0), ([9000], 9000, 1, 0, 0), ([50], 50, 90, 3, 3), ([70000], 70000, 30000, 100, 4)]
+    ([9000], 9000, 8999, 0, 0), ([9000], 9000, 1, 0, 0), ([50], 50, 90, 3, 3), ([70000], 70000, 30000, 100, 4),
+    ([16385, 20000, 100], 20001, 1500, 30, 2), ([50000], 50000, 49999, 9000, 8500), ([40000, 40000], 40000, 20000, 20000, 0),
+    ([33000], 33000, 33000, 5, 5), ([25000, 24000], 25000, 24500, 0, 0)]
 
 
 @pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
@@ -371,6 +373,10 @@ def test_refusals(kvc, ev):
                dict(out=mass[:1].expand(2, 2, 40)), dict(workspace=torch.zeros(1, dtype=torch.uint8, device="cuda"))):
         with pytest.raises((ValueError, RuntimeError)):
             ev.accumulate(**{**ok, **kw})
+    wide = torch.zeros(1, 2, 40000, device="cuda")
+    assert ev.select_workspace_bytes(wide, 1, 10) > 0 and ev.select_workspace_bytes(mass, 2, 10) == 0
+    with pytest.raises(ValueError, match="workspace"):
+        ev.select(wide, lens[:1], 10, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     for kw in (dict(keep=-1), dict(keep=3, recent=4), dict(keep=5, recent=3, sinks=3), dict(sinks=-1), dict(recent=-1),
                dict(seq_lens=lens.long()), dict(mass_out=mass[:, :, :3]), dict(out=torch.zeros(2, 2, 3, device="cuda")),
                dict(mass=mass.cpu())):

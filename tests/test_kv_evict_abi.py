@@ -83,8 +83,8 @@ def test_weights_refusals(kvc, ev):
 
 
 def test_select_refusals(ev):
-    def call(m=None, lens=FAKE, batch=2, kv=2, keep=10, recent=2, sinks=1, kept=FAKE):
-        return ev.lib.if4_kv_select(mass(ev) if m is None else m, lens, batch, kv, keep, recent, sinks, kept, None)
+    def call(m=None, lens=FAKE, batch=2, kv=2, keep=10, recent=2, sinks=1, kept=FAKE, ws=None, size=0):
+        return ev.lib.if4_kv_select(mass(ev) if m is None else m, lens, batch, kv, keep, recent, sinks, kept, ws, size, None)
     for kw, st in BAD_MASS:
         assert call(mass(ev, **kw)) == st, kw
     for kw in (dict(batch=-1), dict(kv=0), dict(kv=1 << 17), dict(batch=1 << 31), dict(keep=-1), dict(keep=1 << 31)):
@@ -93,7 +93,16 @@ def test_select_refusals(ev):
         assert call(**kw) == RANGE, kw
     assert call(lens=None) == NULL and call(kept=None) == NULL
     assert call(lens=FAKE + 2) == ALIGN and call(kept=FAKE + 1) == ALIGN
-    assert ev.lib.if4_kv_select(None, FAKE, 2, 2, 10, 0, 0, FAKE, None) == NULL
+    assert ev.lib.if4_kv_select(None, FAKE, 2, 2, 10, 0, 0, FAKE, None, 0, None) == NULL
+    f = ev.lib.if4_kv_select_workspace
+    for kw in (dict(batch=-1), dict(kv_heads=0), dict(keep=-1), dict(keep=1 << 31)):
+        assert f(mass(ev), *{**dict(batch=2, kv_heads=2, keep=10), **kw}.values()) == -SHAPE
+    assert f(None, 2, 2, 10) == -NULL and f(mass(ev, width=-1), 2, 2, 10) == -SHAPE and f(mass(ev), 2, 2, 10) == 0
+    wide = dict(width=100000, in_stride_row=200000, in_stride_head=100000, out_stride_row=200000, out_stride_head=100000)
+    need = f(mass(ev, **wide), 2, 2, 10)
+    assert 0 < need <= 8 << 20
+    assert call(mass(ev, **wide), size=need) == NULL and call(mass(ev, **wide), ws=FAKE, size=need - 1) == SHAPE
+    assert call(mass(ev, **wide), ws=FAKE + 8, size=need) == ALIGN
     assert call(batch=0, lens=None) == OK and call(keep=0, recent=0, sinks=0, kept=None) == OK
 
 
