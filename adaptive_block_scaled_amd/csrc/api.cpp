@@ -96,7 +96,8 @@ int check_qk_sizes(const if4_qk_args& a) {
         if (t != IF4_F32 && t != IF4_BF16) return IF4_ERR_DTYPE;
     if (a.interleaved != 0 && a.interleaved != 1) return IF4_ERR_DTYPE;
     if (a.head_dim < 8 || a.head_dim > 256 || a.head_dim % 8) return IF4_ERR_SHAPE;
-    if (a.rotary < 0 || a.rotary > a.head_dim || a.rotary % 8) return IF4_ERR_SHAPE;
+    if (a.rotary < 0 || a.rotary > a.head_dim || a.rotary % (a.interleaved ? 8 : 16))
+        return IF4_ERR_SHAPE;
     if (a.tokens < 0 || a.tokens > kMaxSize || a.table_rows < 0 || a.table_rows > kMaxSize)
         return IF4_ERR_SHAPE;
     for (int64_t h : {a.q.heads, a.k.heads})

@@ -20,6 +20,8 @@ decltype(&if4_fp8_quantize_t) fp8_quantize_t;
 decltype(&if4_fp8_gemm) fp8_gemm;
 decltype(&if4_fp8_gemm_workspace) fp8_gemm_workspace;
 decltype(&if4_norm_rotate) qk_norm_rotate;
+decltype(&if4_norm_rotate_backward) qk_backward;
+decltype(&if4_norm_rotate_backward_workspace) qk_backward_workspace;
 
 bool tensor(PyObject* o, at::Tensor& t) {
     if (!THPVariable_Check(o)) return false;
@@ -124,34 +126,29 @@ bool vectors(PyObject* o, if4_qk_part& p, at::Tensor& x, at::ScalarType type, in
     return true;
 }
 
-// norm_rotate(q, k, q_weight, k_weight, table, positions, eps, interleaved, bf16) -> (q, k) | status | None
-PyObject* norm_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded([&]() -> PyObject* {
-        at::Tensor q, k, qw, kw, table, positions;
-        if4_qk_args p = {};
+// What the forward and the backward pass are both given, and the tensors that hold it.
+struct Rotation {
+    if4_qk_args p = {};
+    at::Tensor q, k, qw, kw, table, positions;
+    int64_t device;
+
+    // a: q, k, q_weight, k_weight, table, positions, eps, interleaved
+    bool from(PyObject* const* a) {
         int dtype;
-        if (n != 9 || !tensor(a[0], q) || q.dim() != 3 || !value_type(q.scalar_type(), dtype) ||
-            !tensor(a[4], table) || table.dim() != 2 || !PyFloat_Check(a[6]) || !PyBool_Check(a[7]) ||
-            !PyBool_Check(a[8]))
-            Py_RETURN_NONE;
-        const int64_t tokens = q.size(0), dim = q.size(2), device = q.device().index();
+        if (!tensor(a[0], q) || q.dim() != 3 || !value_type(q.scalar_type(), dtype) || !tensor(a[4], table) ||
+            table.dim() != 2 || !PyFloat_Check(a[6]) || !PyBool_Check(a[7]))
+            return false;
+        const int64_t tokens = q.size(0), dim = q.size(2);
+        device = q.device().index();
         const double eps = PyFloat_AS_DOUBLE(a[6]);
         if (!vectors(a[0], p.q, q, q.scalar_type(), device, tokens, dim) ||
             !vectors(a[1], p.k, k, q.scalar_type(), device, tokens, dim) ||
             !plain(a[2], qw, at::kFloat, device, {dim}) || !plain(a[3], kw, at::kFloat, device, {dim}) ||
             !plain(a[4], table, at::kFloat, device, table.sizes()) ||
             !plain(a[5], positions, at::kLong, device, {tokens}) || !(eps >= 0.0 && eps < 3e38))
-            Py_RETURN_NONE;
-        const bool bf16 = a[8] == Py_True;
-        const auto like = q.options().dtype(bf16 ? at::kBFloat16 : at::kFloat);
-        const at::Tensor qo = at::empty(q.sizes(), like), ko = at::empty(k.sizes(), like);
+            return false;
         p.q.weight = (const float*)qw.data_ptr();
         p.k.weight = (const float*)kw.data_ptr();
-        p.q.y = qo.data_ptr();
-        p.k.y = ko.data_ptr();
-        p.q.y_stride_token = p.q.heads * dim;
-        p.k.y_stride_token = p.k.heads * dim;
-        p.q.y_stride_head = p.k.y_stride_head = dim;
         p.table = (const float*)table.data_ptr();
         p.positions = (const int64_t*)positions.data_ptr();
         p.tokens = tokens;
@@ -161,10 +158,69 @@ PyObject* norm_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
         p.eps = (float)eps;
         p.interleaved = a[7] == Py_True;
         p.dtype = dtype;
-        p.out_dtype = bf16 ? IF4_BF16 : IF4_F32;
-        const int st = qk_norm_rotate(&p, stream_of(device));
+        return true;
+    }
+    // results of q's and k's shapes
+    void into(if4_qk_part& part, const at::Tensor& y) {
+        part.y = y.data_ptr();
+        part.y_stride_token = part.heads * p.head_dim;
+        part.y_stride_head = p.head_dim;
+    }
+};
+
+// norm_rotate(q, k, q_weight, k_weight, table, positions, eps, interleaved, bf16) -> (q, k) | status | None
+PyObject* norm_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Rotation r;
+        if (n != 9 || !PyBool_Check(a[8]) || !r.from(a)) Py_RETURN_NONE;
+        const bool bf16 = a[8] == Py_True;
+        const auto like = r.q.options().dtype(bf16 ? at::kBFloat16 : at::kFloat);
+        const at::Tensor qo = at::empty(r.q.sizes(), like), ko = at::empty(r.k.sizes(), like);
+        r.into(r.p.q, qo);
+        r.into(r.p.k, ko);
+        r.p.out_dtype = bf16 ? IF4_BF16 : IF4_F32;
+        const int st = qk_norm_rotate(&r.p, stream_of(r.device));
         if (st != IF4_OK) return PyLong_FromLong(st);
         return pair(qo, ko);
+    });
+}
+
+// norm_rotate_backward(dq, dk, q, k, q_weight, k_weight, table, positions, eps, interleaved)
+//     -> (q's, k's, q_weight's, k_weight's gradients) | status | None
+PyObject* norm_rotate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Rotation r;
+        at::Tensor g[2];
+        if (n != 10 || !r.from(a + 2) || !tensor(a[0], g[0]) || g[0].dim() != 3 ||
+            !value_type(g[0].scalar_type(), r.p.out_dtype) || r.p.q.heads == 0 || r.p.k.heads == 0)
+            Py_RETURN_NONE;
+        if4_qk_part* const parts[2] = {&r.p.q, &r.p.k};
+        for (int i = 0; i < 2; i++) {
+            if4_qk_part like = {};
+            if (!vectors(a[i], like, g[i], g[0].scalar_type(), r.device, r.p.tokens, r.p.head_dim) ||
+                like.heads != parts[i]->heads)
+                Py_RETURN_NONE;
+            parts[i]->g = like.x;
+            parts[i]->g_stride_token = like.x_stride_token;
+            parts[i]->g_stride_head = like.x_stride_head;
+        }
+        const at::Tensor dq = at::empty(r.q.sizes(), r.q.options()), dk = at::empty(r.k.sizes(), r.k.options());
+        const auto floats = r.q.options().dtype(at::kFloat);
+        const at::Tensor dqw = at::empty({r.p.head_dim}, floats), dkw = at::empty({r.p.head_dim}, floats);
+        r.into(r.p.q, dq);
+        r.into(r.p.k, dk);
+        r.p.q.d_weight = (float*)dqw.data_ptr();
+        r.p.k.d_weight = (float*)dkw.data_ptr();
+        const int64_t need = qk_backward_workspace(&r.p);
+        if (need < 0) return PyLong_FromLong(-need);
+        const at::Tensor work = at::empty({need}, r.q.options().dtype(at::kByte));
+        const int st = qk_backward(&r.p, work.data_ptr(), need, stream_of(r.device));
+        if (st != IF4_OK) return PyLong_FromLong(st);
+        PyObject* t = PyTuple_New(4);
+        if (!t) return nullptr;
+        const at::Tensor* const results[4] = {&dq, &dk, &dqw, &dkw};
+        for (int i = 0; i < 4; i++) PyTuple_SET_ITEM(t, i, THPVariable_Wrap(*results[i]));
+        return t;
     });
 }
 
@@ -195,11 +251,13 @@ PyObject* bind_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// bind_qk(norm_rotate)
+// bind_qk(norm_rotate, norm_rotate_backward, its workspace)
 PyObject* bind_qk(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* f[1];
-    if (!addresses(a, n, f, 1)) return nullptr;
+    void* f[3];
+    if (!addresses(a, n, f, 3)) return nullptr;
     qk_norm_rotate = (decltype(qk_norm_rotate))f[0];
+    qk_backward = (decltype(qk_backward))f[1];
+    qk_backward_workspace = (decltype(qk_backward_workspace))f[2];
     Py_RETURN_NONE;
 }
 
@@ -207,6 +265,7 @@ PyMethodDef methods[] = {
     {"quantize", (PyCFunction)(void*)quantize, METH_FASTCALL, nullptr},
     {"gemm", (PyCFunction)(void*)gemm, METH_FASTCALL, nullptr},
     {"norm_rotate", (PyCFunction)(void*)norm_rotate, METH_FASTCALL, nullptr},
+    {"norm_rotate_backward", (PyCFunction)(void*)norm_rotate_backward, METH_FASTCALL, nullptr},
     {"bind_fp8", (PyCFunction)(void*)bind_fp8, METH_FASTCALL, nullptr},
     {"bind_qk", (PyCFunction)(void*)bind_qk, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},

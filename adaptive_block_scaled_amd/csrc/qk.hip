@@ -1,11 +1,12 @@
 // Norm and rotation of queries and keys in one pass, and its gradients, for gfx950.
 // The formulas are those of include/if4_qk.h.
 //
-// A vector of D values lies in L = D/8 lanes (rounded up to a power of two), 8 values in
-// each: two runs of 4, chosen so that both members of a rotated pair are in one lane.
-// The mean of the squares is then three to five exchanges between lanes, and the rotation
-// none.  Bound by memory: each value is read and written once; a wave keeps its token's
-// cosines and sines while it goes through several heads.
+// A vector of D values lies in L = D/8 lanes (rounded up to a power of two), 8 neighbours in
+// each, so that a lane's 16 (or 32) bytes are one access.  The mean of the squares is three
+// to five exchanges between lanes, in registers; pairs of two halves lie in two lanes, which
+// trade their values, and neighbouring pairs in one.  Bound by memory: each value is read and
+// written once; a wave keeps its token's cosines and sines while it goes through several
+// heads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,64 +19,132 @@ namespace {
 
 constexpr int kThreads = 256;
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 template <bool kBf16>
-__device__ __forceinline__ void load4(const void* p, int64_t at, float* v) {
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
     if constexpr (kBf16) {
-        const bf16x4 w = *reinterpret_cast<const bf16x4*>(reinterpret_cast<const uint16_t*>(p) + at);
+        const bf16x8 w = *reinterpret_cast<const bf16x8*>(reinterpret_cast<const uint16_t*>(p) + at);
 #pragma unroll
-        for (int i = 0; i < 4; i++) v[i] = (float)w[i];
+        for (int i = 0; i < 8; i++) v[i] = (float)w[i];
     } else {
-        const float4 w = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
-        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float4 w = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at)[i];
+            v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
+        }
     }
 }
 
+// Keeps the compiler from making one store of the two kinds, which would be the ordinary.
+__device__ __forceinline__ void apart() { asm volatile(""); }
+
+// `past`: past the caches.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <bool kBf16>
-__device__ __forceinline__ void store4(void* p, int64_t at, const float* v) {
+__device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8], bool past) {
     if constexpr (kBf16) {
-        bf16x4 w;
+        bf16x8 w;
 #pragma unroll
-        for (int i = 0; i < 4; i++) w[i] = (__bf16)v[i];
-        *reinterpret_cast<bf16x4*>(reinterpret_cast<uint16_t*>(p) + at) = w;
+        for (int i = 0; i < 8; i++) w[i] = (__bf16)v[i];
+        bf16x8* const to = reinterpret_cast<bf16x8*>(reinterpret_cast<uint16_t*>(p) + at);
+        if (past) {
+            apart();
+            __builtin_nontemporal_store(w, to);
+            apart();
+        } else {
+            *to = w;
+        }
     } else {
-        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        f32x4* const to = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + at);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const f32x4 w = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            if (past) {
+                apart();
+                __builtin_nontemporal_store(w, to + i);
+                apart();
+            } else {
+                to[i] = w;
+            }
+        }
     }
+}
+
+// v of the lane that a DPP control names.
+template <int kControl>
+__device__ __forceinline__ float moved(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kControl, 0xF, 0xF, true));
 }
 
 // Sum over L neighbouring lanes, the same bits in all of them.
 template <int L>
 __device__ __forceinline__ float sum_lanes(float v) {
-#pragma unroll
-    for (int d = 1; d < L; d *= 2) v += __shfl_xor(v, d);
+    v += moved<0xB1>(v);   // quad_perm 1,0,3,2
+    v += moved<0x4E>(v);   // quad_perm 2,3,0,1
+    v += moved<0x141>(v);  // half row mirrored
+    if constexpr (L >= 16) v += moved<0x140>(v);  // row mirrored
+    if constexpr (L >= 32) v += __shfl_xor(v, 16);
     return v;
 }
 
-// What a lane holds of every vector: values at[0] .. + 3 and at[1] .. + 3, which are pairs
-// 4 i .. 4 i + 3 where i < rotary / 8.
+// What lane i of a vector's holds: values 8 i .. 8 i + 7.  Of pairs of two halves (a, b)
+// lanes below rotary / 16 hold the a's of pairs 8 i .., as many after them the b's; of
+// neighbouring pairs lane i holds pairs 4 i ...
+template <bool kInterleaved>
 struct Place {
-    int at[2];
+    int at;         // its first value
+    int pair;       // its first pair
     bool in, turned;
-    __device__ __forceinline__ Place(int i, int dim, int rotary, bool interleaved) {
-        in = 8 * i < dim;
-        turned = 8 * i < rotary;
-        at[0] = turned && !interleaved ? 4 * i : 8 * i;
-        at[1] = turned && !interleaved ? rotary / 2 + 4 * i : 8 * i + 4;
+    bool second;    // holds b's
+    int partner;    // lane of the wave with the other members
+    __device__ __forceinline__ Place(int lane, int i, int dim, int rotary) {
+        at = 8 * i;
+        in = at < dim;
+        turned = at < rotary;
+        const int half = rotary / 16;
+        second = i >= half;
+        pair = kInterleaved ? 4 * i : 8 * (second ? i - half : i);
+        partner = turned ? lane + (second ? -half : half) : lane;
     }
 };
 
-// (a, b) -> (a c - b s, a s + b c) for the lane's four pairs.
+// Cosines and sines of a lane's pairs.
 template <bool kInterleaved>
-__device__ __forceinline__ void turn(float (&v)[8], const float (&c)[4], const float (&s)[4]) {
+struct Turn {
+    static constexpr int kPairs = kInterleaved ? 4 : 8;
+    float c[kPairs], s[kPairs];
+    // (`sign` -1: the other way round.  Of pairs of two halves the b's sine is the other one.)
+    __device__ __forceinline__ void load(const float* row, int rotary, const Place<kInterleaved>& at, float sign) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const int x = kInterleaved ? 2 * j : j, y = kInterleaved ? 2 * j + 1 : 4 + j;
-        const float a = v[x], b = v[y];
-        v[x] = fmaf(a, c[j], -(b * s[j]));
-        v[y] = fmaf(a, s[j], b * c[j]);
+        for (int i = 0; i < kPairs; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(row + at.pair + i);
+            const float4 y = *reinterpret_cast<const float4*>(row + rotary / 2 + at.pair + i);
+            c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+            s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+        }
+        if (!kInterleaved && !at.second) sign = -sign;
+#pragma unroll
+        for (int i = 0; i < kPairs; i++) s[i] *= sign;
     }
-}
+    // (a, b) -> (a c - b s, a s + b c)
+    __device__ __forceinline__ void operator()(float (&v)[8], const Place<kInterleaved>& at) const {
+        if constexpr (kInterleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float a = v[2 * j], b = v[2 * j + 1];
+                v[2 * j] = at.turned ? fmaf(a, c[j], -(b * s[j])) : a;
+                v[2 * j + 1] = at.turned ? fmaf(a, s[j], b * c[j]) : b;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float other = __shfl(v[j], at.partner);  // (all lanes take part)
+                v[j] = at.turned ? fmaf(v[j], c[j], other * s[j]) : v[j];
+            }
+        }
+    }
+};
 
 struct Args {
     if4_qk_part part[2];
@@ -85,21 +154,36 @@ struct Args {
     int dim, rotary, heads;  // heads: of both parts
     int per, chunks;         // vectors of a lane, and waves of a token
     float eps;
+    int past;  // whether results go past the caches
 };
 
-// Cosines and sines of a token for this lane; false: the token is skipped.
-__device__ __forceinline__ bool load_turn(const Args& p, int64_t token, int i, const Place& at,
-                                          float (&c)[4], float (&s)[4]) {
-    const int64_t pos = p.positions[token];
-    if (pos < 0 || pos >= p.table_rows) return false;
-    if (at.turned) {
-        load4<false>(p.table, pos * p.rotary + 4 * i, c);
-        load4<false>(p.table, pos * p.rotary + p.rotary / 2 + 4 * i, s);
+// One lane's part of a vector: which kind it is, and its values.
+struct Vector {
+    int kind, head;
+    bool there;
+    __device__ __forceinline__ Vector(const Args& p, int h) {
+        there = h < p.heads;
+        kind = h < (int)p.part[0].heads ? 0 : 1;
+        head = kind ? h - (int)p.part[0].heads : h;
     }
-    return true;
-}
+};
 
-// A wave per token and chunk of its heads; its 64 / L lane groups take them in turn.
+// The two weights' values of a lane.
+struct Weights {
+    float w[2][8] = {};
+    __device__ __forceinline__ Weights(const Args& p, int at, bool in) {
+#pragma unroll
+        for (int kind = 0; kind < 2; kind++)
+            if (p.part[kind].heads && in) load8<false>(p.part[kind].weight, at, w[kind]);
+    }
+    __device__ __forceinline__ float operator()(int kind, int j) const { return kind ? w[1][j] : w[0][j]; }
+};
+
+// A wave per token and chunk of its heads; its 64 / L lane groups take them in turn.  8192
+// tokens of 72 vectors of 128 in bf16 (304 MB moved) 52.5 us, 5.8 TB/s, with up to 8 vectors
+// to a lane and stores past the caches; up to 4, 18: 57, 59; ordinary stores 69 (what they leave
+// in the caches has to be written back from there); two vectors at once 76; waves that
+// stay for many tokens 61.
 template <int L, bool kIn, bool kOut, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
     constexpr int G = 64 / L;
@@ -107,36 +191,28 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
     const int64_t wave = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
     const int64_t token = wave / p.chunks;
     if (token >= p.tokens) return;
-    const Place at(i, p.dim, p.rotary, kInterleaved);
-    float c[4], s[4];
-    if (!load_turn(p, token, i, at, c, s)) return;
-    int h = (int)(wave - token * p.chunks) * p.per * G + lane / L;
+    const int64_t pos = p.positions[token];
+    if (pos < 0 || pos >= p.table_rows) return;
+    const Place<kInterleaved> at(lane, i, p.dim, p.rotary);
+    Turn<kInterleaved> turn = {};
+    if (at.turned) turn.load(p.table + pos * p.rotary, p.rotary, at, 1.0f);
+    const Weights w(p, at.at, at.in);
     const float inv = 1.0f / (float)p.dim;
+    int h = (int)(wave - token * p.chunks) * p.per * G + lane / L;
     for (int n = 0; n < p.per; n++, h += G) {
-        const bool there = h < p.heads && at.in;
-        const int kind = h < p.part[0].heads ? 0 : 1;
-        const if4_qk_part& part = p.part[kind];
-        const int head = kind ? h - (int)p.part[0].heads : h;
-        float v[8] = {}, w[8] = {};
-        if (there) {
-            const int64_t x = token * part.x_stride_token + head * part.x_stride_head;
-            load4<kIn>(part.x, x + at.at[0], v);
-            load4<kIn>(part.x, x + at.at[1], v + 4);
-            load4<false>(part.weight, at.at[0], w);
-            load4<false>(part.weight, at.at[1], w + 4);
-        }
+        const Vector x(p, h);
+        const if4_qk_part& part = p.part[x.kind];
+        float v[8] = {};
+        if (x.there && at.in) load8<kIn>(part.x, token * part.x_stride_token + x.head * part.x_stride_head + at.at, v);
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(v[j], v[j], ss);
         const float r = rsqrtf(fmaf(sum_lanes<L>(ss), inv, p.eps));
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = v[j] * r * w[j];
-        if (at.turned) turn<kInterleaved>(v, c, s);
-        if (there) {
-            const int64_t y = token * part.y_stride_token + head * part.y_stride_head;
-            store4<kOut>(part.y, y + at.at[0], v);
-            store4<kOut>(part.y, y + at.at[1], v + 4);
-        }
+        for (int j = 0; j < 8; j++) v[j] = v[j] * r * w(x.kind, j);
+        turn(v, at);
+        if (x.there && at.in)
+            store8<kOut>(part.y, token * part.y_stride_token + x.head * part.y_stride_head + at.at, v, p.past);
     }
 }
 
@@ -149,44 +225,32 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p, float*
     constexpr int G = 64 / L, kWaves = kThreads / 64;
     __shared__ float shared[kWaves * G][2][8 * L];
     const int lane = threadIdx.x & 63, i = lane % L;
-    const Place at(i, p.dim, p.rotary, kInterleaved);
-    float w[2][8] = {}, dw[2][8] = {};
-#pragma unroll
-    for (int kind = 0; kind < 2; kind++)
-        if (p.part[kind].heads && at.in) {
-            load4<false>(p.part[kind].weight, at.at[0], w[kind]);
-            load4<false>(p.part[kind].weight, at.at[1], w[kind] + 4);
-        }
+    const Place<kInterleaved> at(lane, i, p.dim, p.rotary);
+    const Weights w(p, at.at, at.in);
+    float dw[2][8] = {};
     const float inv = 1.0f / (float)p.dim;
     const int64_t waves = (int64_t)gridDim.x * kWaves;
     for (int64_t unit = (int64_t)blockIdx.x * kWaves + threadIdx.x / 64; unit < p.tokens * p.chunks; unit += waves) {
         const int64_t token = unit / p.chunks;
-        float c[4] = {}, s[4] = {};
-        const bool live = load_turn(p, token, i, at, c, s);
+        const int64_t pos = p.positions[token];
+        const bool live = pos >= 0 && pos < p.table_rows;
+        Turn<kInterleaved> back = {};
+        if (live && at.turned) back.load(p.table + pos * p.rotary, p.rotary, at, -1.0f);
         int h = (int)(unit - token * p.chunks) * p.per * G + lane / L;
         for (int n = 0; n < p.per; n++, h += G) {
-            const bool there = h < p.heads && at.in;
-            const int kind = h < p.part[0].heads ? 0 : 1;
-            const if4_qk_part& part = p.part[kind];
-            const int head = kind ? h - (int)p.part[0].heads : h;
+            const Vector v(p, h);
+            const if4_qk_part& part = p.part[v.kind];
+            const bool there = v.there && at.in;
             float x[8] = {}, g[8] = {};
             if (there && live) {
-                const int64_t xo = token * part.x_stride_token + head * part.x_stride_head;
-                const int64_t go = token * part.g_stride_token + head * part.g_stride_head;
-                load4<kIn>(part.x, xo + at.at[0], x);
-                load4<kIn>(part.x, xo + at.at[1], x + 4);
-                load4<kOut>(part.g, go + at.at[0], g);
-                load4<kOut>(part.g, go + at.at[1], g + 4);
+                load8<kIn>(part.x, token * part.x_stride_token + v.head * part.x_stride_head + at.at, x);
+                load8<kOut>(part.g, token * part.g_stride_token + v.head * part.g_stride_head + at.at, g);
             }
-            if (at.turned) {
-                const float back[4] = {-s[0], -s[1], -s[2], -s[3]};
-                turn<kInterleaved>(g, c, back);
-            }
-            float ss = 0.0f, dot = 0.0f;
-            float gw[8];
+            back(g, at);
+            float ss = 0.0f, dot = 0.0f, gw[8];
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                gw[j] = g[j] * (kind ? w[1][j] : w[0][j]);
+                gw[j] = g[j] * w(v.kind, j);
                 ss = fmaf(x[j], x[j], ss);
                 dot = fmaf(gw[j], x[j], dot);
             }
@@ -196,15 +260,11 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p, float*
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const float d = there && live ? g[j] * x[j] * r : 0.0f;
-                dw[0][j] += kind ? 0.0f : d;
-                dw[1][j] += kind ? d : 0.0f;
+                dw[0][j] += v.kind ? 0.0f : d;
+                dw[1][j] += v.kind ? d : 0.0f;
                 dx[j] = live ? r * fmaf(-x[j], mean, gw[j]) : 0.0f;
             }
-            if (there) {
-                const int64_t y = token * part.y_stride_token + head * part.y_stride_head;
-                store4<kIn>(part.y, y + at.at[0], dx);
-                store4<kIn>(part.y, y + at.at[1], dx + 4);
-            }
+            if (there) store8<kIn>(part.y, token * part.y_stride_token + v.head * part.y_stride_head + at.at, dx, p.past);
         }
     }
     const int row = threadIdx.x / L;
@@ -212,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p, float*
 #pragma unroll
         for (int kind = 0; kind < 2; kind++)
 #pragma unroll
-            for (int j = 0; j < 8; j++) shared[row][kind][at.at[j / 4] + j % 4] = dw[kind][j];
+            for (int j = 0; j < 8; j++) shared[row][kind][at.at + j] = dw[kind][j];
     }
     __syncthreads();
     for (int d = threadIdx.x; d < 2 * p.dim; d += kThreads) {
@@ -248,11 +308,13 @@ join_kernel(const float* __restrict__ sums, int rows, int dim, float* dq, float*
     }
 }
 
-// Vectors of a lane: as many as leave this many waves, for the chip to be full; the
-// backward pass has no more workgroups than kRows rows of sums.
-constexpr int kFullWaves = 256 * 16;
+// Vectors of a lane: as many as leave this many waves, for the chip to be full, and no more
+// than kMostTurns; the backward pass has no more workgroups than kRows rows of sums.
+constexpr int kFullWaves = 256 * 16, kMostTurns = 8;
+// Results of more bytes than the caches of the chip's eight parts hold go past them.
+constexpr int64_t kCaches = (int64_t)32 << 20;
 
-Args make_args(const if4_qk_args& a, int lanes) {
+Args make_args(const if4_qk_args& a, int lanes, int y_size) {
     Args p;
     p.part[0] = a.q;
     p.part[1] = a.k;
@@ -265,10 +327,11 @@ Args make_args(const if4_qk_args& a, int lanes) {
     p.heads = (int)(a.q.heads + a.k.heads);
     const int groups = 64 / lanes, turns = (p.heads + groups - 1) / groups;
     const int64_t each = a.tokens * turns / kFullWaves;
-    p.per = each < 1 ? 1 : each > turns ? turns : (int)each;
+    p.per = each < 1 ? 1 : each > kMostTurns ? kMostTurns : (int)each;
     p.chunks = (turns + p.per - 1) / p.per;
     p.per = (turns + p.chunks - 1) / p.chunks;  // even shares
     p.eps = a.eps;
+    p.past = a.tokens * p.heads * p.dim * y_size > kCaches;
     return p;
 }
 
@@ -276,7 +339,7 @@ int lanes_of(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
 template <int L, bool kIn, bool kOut, bool kInterleaved>
 hipError_t forward(const if4_qk_args& a, hipStream_t stream) {
-    const Args p = make_args(a, L);
+    const Args p = make_args(a, L, kOut ? 2 : 4);
     const int64_t groups = (a.tokens * p.chunks + kThreads / 64 - 1) / (kThreads / 64);
     hipLaunchKernelGGL((forward_kernel<L, kIn, kOut, kInterleaved>), dim3((unsigned)groups),
                        dim3(kThreads), 0, stream, p);
@@ -284,7 +347,7 @@ hipError_t forward(const if4_qk_args& a, hipStream_t stream) {
 }
 
 int backward_rows(const if4_qk_args& a) {
-    const Args p = make_args(a, lanes_of(a.head_dim));
+    const Args p = make_args(a, lanes_of(a.head_dim), 4);
     const int64_t groups = (a.tokens * p.chunks + kThreads / 64 - 1) / (kThreads / 64);
     return (int)(groups < kRows ? groups : kRows);
 }
@@ -294,7 +357,7 @@ hipError_t backward(const if4_qk_args& a, float* sums, hipStream_t stream) {
     const int rows = backward_rows(a);
     if (rows) {
         hipLaunchKernelGGL((backward_kernel<L, kIn, kOut, kInterleaved>), dim3(rows), dim3(kThreads),
-                           0, stream, make_args(a, L), sums);
+                           0, stream, make_args(a, L, kIn ? 2 : 4), sums);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }

@@ -18,7 +18,7 @@ import math
 import torch
 
 from .if4 import _check, lib
-from .kv_cache import KVCache, _Attention, _Cache, _cache, _held, _plain, _raw_stream, _vectors
+from .kv_cache import KVCache, _Attention, _Cache, _cache, _held, _kv_call, _plain, _raw_stream, _vectors
 
 EXPORTS = ("if4_kv_weights", "if4_kv_weights_workspace", "if4_kv_weights_workspace_most", "if4_kv_select",
            "if4_kv_select_workspace", "if4_kv_compact")
@@ -47,6 +47,8 @@ def _declare():
 
 
 _declare()
+_kv_call.bind_evict(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+    "if4_kv_weights", "if4_kv_weights_workspace", "if4_kv_select", "if4_kv_select_workspace", "if4_kv_compact")))
 
 
 def _sums(t, name, kv_heads, device, rows=None, width=None):
@@ -69,8 +71,7 @@ def _mass(mass, out, rows, batch, device):
         _plain(rows, "rows", (batch,), torch.int32, device.index)
     elif mass.shape[0] < batch:
         raise ValueError(f"mass must have a row for each of {batch} sequences, or rows be given")
-    if out is not None and out is not mass and (out.stride(0) < 0 or any(
-            s < out.shape[2] for n, s in zip(out.shape[:2], out.stride()) if n > 1)):
+    if out is not None and any(s < out.shape[2] for n, s in zip(out.shape[:2], out.stride()) if n > 1):
         raise ValueError("the sums' rows must not overlap")
     return _Mass(mass.data_ptr(), mass.stride(0), mass.stride(1), None if out is None else out.data_ptr(),
                  0 if out is None else out.stride(0), 0 if out is None else out.stride(1),
@@ -91,6 +92,14 @@ def accumulate(mass: torch.Tensor, q: torch.Tensor, cache: KVCache, page_table: 
     default mass itself, written in place; a new `out` of mass's shape gets the sums of the
     call's sequences and keeps the rest.  `workspace` may pass a uint8 tensor of
     workspace_bytes()."""
+    if workspace is None:
+        to = mass if out is None else out
+        st = _kv_call.weights(mass, to, rows, q, cache, page_table, seq_lens, q_starts, max_q, max_len, scale, k_exp,
+                              causal, window, sinks)
+        if st == 0:
+            return to
+        if st:
+            _check("if4_kv_weights", st)
     c, index = _cache(cache, k_exp, 0)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D tensor [total_q, heads, D]")
@@ -156,6 +165,12 @@ def select(mass: torch.Tensor, seq_lens: torch.Tensor, keep: int, *, recent: int
     its tokens.  `mass_out` (mass itself is fine) gets the kept tokens' sums in
     places 0, 1, ..; `out` may pass the positions preallocated, `workspace` a uint8 tensor of
     select_workspace_bytes()."""
+    if out is None and workspace is None:
+        kept = _kv_call.select(mass, seq_lens, keep, recent, sinks, rows, mass_out)
+        if type(kept) is int:
+            _check("if4_kv_select", kept)
+        elif kept is not None:
+            return kept
     if not isinstance(mass, torch.Tensor) or mass.dim() != 3 or not mass.is_cuda:
         raise ValueError("mass must be a CUDA tensor [sequences, kv_heads, width]")
     kv_heads, dev = mass.shape[1], mass.device
@@ -205,6 +220,11 @@ def compact(cache: KVCache, page_table: torch.Tensor, kept: torch.Tensor, new_ta
     """Copy K and V of the kept tokens (select's result) from the pages of page_table (int32
     [batch, pages]) to places 0, 1, .. of new_table's (int32 [batch, pages]), which must
     be other ones.  Returns the cache, which is written in place."""
+    st = _kv_call.compact(cache, page_table, kept, new_table, 0)
+    if st == 0:
+        return cache
+    if st:
+        _check("if4_kv_compact", st)
     c, index = _cache(cache, 0, 0)
     for t, name, dims in ((page_table, "page_table", 2), (kept, "kept", 3), (new_table, "new_table", 2)):
         if not isinstance(t, torch.Tensor) or t.dim() != dims:

@@ -48,7 +48,7 @@ def _declare():
 
 
 _declare()
-_op_call.bind_qk(ctypes.cast(lib.if4_norm_rotate, ctypes.c_void_p).value)
+_op_call.bind_qk(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS))
 
 
 def rotation_table(rows: int, rotary: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -141,7 +141,7 @@ def norm_rotate(q, k, q_weight, k_weight, table, positions, *, eps: float = 1e-6
     D, other strides multiples of 16 bytes), each vector divided by the root of its mean
     square, times its weight (fp32 [D]), and its first table.shape[1] values rotated by the
     token's position (int64 [tokens]): pairs (i, i + rotary/2), or (2i, 2i + 1) where
-    `interleaved`.  D is a multiple of 8 up to 256, rotary one of 8 up to D.
+    `interleaved`.  D is a multiple of 8 up to 256, rotary one of 16 (interleaved: 8) up to D.
 
     Returns (q, k) of `dtype` (default: q's); `out` may pass them, the inputs themselves
     among them.  A token whose position is outside the table is skipped: its outputs keep
@@ -176,6 +176,12 @@ def norm_rotate_backward(dq, dk, q, k, q_weight, k_weight, table, positions, *, 
     or bf16, both alike).  Returns (q's, k's, q_weight's, k_weight's): the first two of q's
     dtype (`out` may pass them), the weights' fp32 [D].  Skipped tokens have zero gradients
     and add nothing.  `workspace` may pass a uint8 tensor of workspace_bytes()."""
+    if out is None and workspace is None:
+        grads = _op_call.norm_rotate_backward(dq, dk, q, k, q_weight, k_weight, table, positions, eps, interleaved)
+        if type(grads) is tuple:
+            return grads
+        if grads:
+            _check("if4_norm_rotate_backward", grads)
     if not isinstance(dq, torch.Tensor):
         raise ValueError("dq must be a 3-D CUDA tensor [tokens, heads, D]")
     a, dev = _args(q, k, q_weight, k_weight, table, positions, eps, interleaved, dq.dtype)

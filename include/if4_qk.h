@@ -44,7 +44,7 @@ typedef struct if4_qk_args {
     const float* table;       /* device [table_rows, rotary], 16-byte aligned */
     const int64_t* positions; /* device [tokens] */
     int64_t tokens, head_dim; /* head_dim a multiple of 8 in [8, 256] */
-    int64_t rotary;           /* a multiple of 8 in [0, head_dim] */
+    int64_t rotary;           /* a multiple of 16, or of 8 where interleaved, in [0, head_dim] */
     int64_t table_rows;
     float eps; /* finite, >= 0 */
     int32_t interleaved;

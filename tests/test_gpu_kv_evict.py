@@ -370,7 +370,7 @@ def test_refusals(kvc, ev):
                dict(mass=mass[:, :, ::2]), dict(out=mass[:, :, :39]), dict(q=b.q), dict(q=ok["q"][:, :3]), dict(window=-1),
                dict(causal=False, window=3), dict(scale=-1.0), dict(scale=float("nan")), dict(seq_lens=lens.long()),
                dict(rows=lens.long()), dict(rows=lens[:1]), dict(k_exp=65), dict(max_q=-1), dict(max_len=-1),
-               dict(out=mass[:1].expand(2, 2, 40)), dict(workspace=torch.zeros(1, dtype=torch.uint8, device="cuda"))):
+               dict(out=mass[:1].expand(2, 2, 40)), dict(mass=mass[:1].expand(2, 2, 40)), dict(workspace=torch.zeros(1, dtype=torch.uint8, device="cuda"))):
         with pytest.raises((ValueError, RuntimeError)):
             ev.accumulate(**{**ok, **kw})
     wide = torch.zeros(1, 2, 40000, device="cuda")
@@ -378,7 +378,7 @@ def test_refusals(kvc, ev):
     with pytest.raises(ValueError, match="workspace"):
         ev.select(wide, lens[:1], 10, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     for kw in (dict(keep=-1), dict(keep=3, recent=4), dict(keep=5, recent=3, sinks=3), dict(sinks=-1), dict(recent=-1),
-               dict(seq_lens=lens.long()), dict(mass_out=mass[:, :, :3]), dict(out=torch.zeros(2, 2, 3, device="cuda")),
+               dict(seq_lens=lens.long()), dict(mass_out=mass[:, :, :3]), dict(mass_out=mass[:1].expand(2, 2, 40)), dict(out=torch.zeros(2, 2, 3, device="cuda")),
                dict(mass=mass.cpu())):
         with pytest.raises((ValueError, RuntimeError)):
             ev.select(**{**dict(mass=mass, seq_lens=lens, keep=10), **kw})

@@ -88,13 +88,14 @@ def rounded(bound, want, dtype):
 
 # every lane count, dims that leave lanes empty, part of the dims turned, none, one token and many
 SHAPES = [(1, 1, 1, 64, 64), (3, 4, 2, 128, 128), (5, 6, 3, 256, 256), (17, 7, 1, 80, 32), (9, 5, 5, 96, 96),
-          (33, 32, 8, 128, 64), (2, 3, 1, 8, 8), (4, 2, 2, 72, 24), (6, 8, 4, 128, 0), (700, 16, 4, 64, 64)]
+          (33, 32, 8, 128, 64), (2, 3, 1, 8, 8), (4, 2, 2, 72, 24), (4, 2, 2, 72, 48), (2, 3, 1, 16, 16), (3, 2, 1, 176, 112), (6, 8, 4, 128, 0), (700, 16, 4, 64, 64)]
+# (pairs of two halves: rotary is a multiple of 16)
+KINDS = [(*s, il) for s in SHAPES for il in (False, True) if il or s[4] % 16 == 0]
 TYPES = [(BF16, BF16), (F32, BF16), (F32, F32), (BF16, F32)]
 
 
-@pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dtype,out", TYPES)
-@pytest.mark.parametrize("tokens,heads,kv,dim,rotary", SHAPES)
+@pytest.mark.parametrize("tokens,heads,kv,dim,rotary,interleaved", KINDS)
 def test_forward(qk, tokens, heads, kv, dim, rotary, dtype, out, interleaved):
     q, k, w, table, pos, _ = inputs(tokens, heads, kv, dim, rotary, dtype, out)
     got = qk.norm_rotate(q, k, *w, table, pos, eps=1e-5, interleaved=interleaved, dtype=out)
@@ -104,9 +105,8 @@ def test_forward(qk, tokens, heads, kv, dim, rotary, dtype, out, interleaved):
         near(y.double(), want, rounded(bound, want, out))
 
 
-@pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dtype,out", TYPES)
-@pytest.mark.parametrize("tokens,heads,kv,dim,rotary", SHAPES)
+@pytest.mark.parametrize("tokens,heads,kv,dim,rotary,interleaved", KINDS)
 def test_backward(qk, tokens, heads, kv, dim, rotary, dtype, out, interleaved):
     q, k, w, table, pos, dy = inputs(tokens, heads, kv, dim, rotary, dtype, out, 1)
     got = qk.norm_rotate_backward(*dy, q, k, *w, table, pos, eps=1e-5, interleaved=interleaved)
@@ -119,11 +119,11 @@ def test_backward(qk, tokens, heads, kv, dim, rotary, dtype, out, interleaved):
 
 def test_gradients_against_differences(qk):
     """<dy, y> as a function of one value at a time, by central differences in 64 bits."""
-    q, k, w, table, pos, dy = inputs(2, 2, 1, 16, 8, F32, F32, 2)
+    q, k, w, table, pos, dy = inputs(2, 2, 1, 24, 16, F32, F32, 2)
     got = qk.norm_rotate_backward(*dy, q, k, *w, table, pos, eps=1e-3)
 
     def value(x, wt, d):
-        return float((forward(x, wt, table, pos, 1e-3, 8, False)[0] * d.double().cpu()).sum())
+        return float((forward(x, wt, table, pos, 1e-3, 16, False)[0] * d.double().cpu()).sum())
     for i, (x, wt, d) in enumerate(zip((q, k), w, dy)):
         x, wt = x.double().cpu(), wt.double().cpu()
         for of, grad in ((x, got[i]), (wt, got[2 + i])):
@@ -247,7 +247,7 @@ def test_refusals(qk):
     q, k, w, table, pos, dy = inputs(4, 4, 2, 64, 64, BF16, BF16, 9)
     ok = dict(q=q, k=k, q_weight=w[0], k_weight=w[1], table=table, positions=pos)
     bad = [dict(q=q.half()), dict(q=q.cpu()), dict(k=k.float()), dict(k=k[:3]), dict(k=k[..., :32]), dict(q=q[0]),
-           dict(q_weight=w[0].bfloat16()), dict(k_weight=w[1][:32]), dict(table=table[:, :60]), dict(table=table[:, ::2]),
+           dict(q_weight=w[0].bfloat16()), dict(k_weight=w[1][:32]), dict(table=table[:, :60]), dict(table=table[:, :24].contiguous()), dict(table=table[:, ::2]),
            dict(table=table.double()), dict(positions=pos.int()), dict(positions=pos[:3]), dict(eps=-1.0),
            dict(eps=float("nan")), dict(dtype=torch.float16), dict(out=(q.float(), k)), dict(q=q.transpose(1, 2)),
            dict(out=(q[:, :1].expand(4, 4, 64), k)), dict(table=qk.rotation_table(10, 128))]

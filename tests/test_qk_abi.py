@@ -43,7 +43,7 @@ def args(qk, part="q", **kw):
 
 
 SIZES = [(dict(head_dim=0), SHAPE), (dict(head_dim=60), SHAPE), (dict(head_dim=264), SHAPE), (dict(rotary=-8), SHAPE),
-         (dict(rotary=72), SHAPE), (dict(rotary=12), SHAPE), (dict(tokens=-1), SHAPE), (dict(tokens=1 << 32), SHAPE),
+         (dict(rotary=72), SHAPE), (dict(rotary=12), SHAPE), (dict(rotary=24), SHAPE), (dict(rotary=20, interleaved=1), SHAPE), (dict(tokens=-1), SHAPE), (dict(tokens=1 << 32), SHAPE),
          (dict(table_rows=-1), SHAPE), (dict(heads=-1), SHAPE), (dict(heads=1 << 17), SHAPE), (dict(eps=-1.0), RANGE),
          (dict(eps=float("inf")), RANGE), (dict(eps=float("nan")), RANGE), (dict(dtype=2), DTYPE),
          (dict(out_dtype=-1), DTYPE), (dict(interleaved=2), DTYPE)]
