@@ -300,7 +300,9 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     }
     // lane: column lane % 32 of a block, rows 8 (r / 4) + 4 (lane / 32) + r % 4.  The
     // stores go through a buffer resource over the tile's rows that exist: one
-    // vector offset per lane, and a store past M is dropped.
+    // vector offset per lane, and a store past M is dropped.  C of the largest tiles is more
+    // than the caches hold, and goes past them (non-temporal).
+    constexpr int kStorePolicy = BM == 256 ? 2 : 0;
     constexpr int kSize = kBf16 ? 2 : 4;
     if ((uint64_t)ldc * (kSize * BM) < (1ull << 31)) {
         const uint32_t ld = (uint32_t)ldc * kSize;
@@ -320,10 +322,10 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
                                         col * kSize;
                     if constexpr (kBf16)
                         __builtin_amdgcn_raw_buffer_store_b16(
-                            __builtin_bit_cast(short, (__bf16)acc[i][j][r]), rc, (int)vo, (int)so, 0);
+                            __builtin_bit_cast(short, (__bf16)acc[i][j][r]), rc, (int)vo, (int)so, kStorePolicy);
                     else
                         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), rc,
-                                                              (int)vo, (int)so, 0);
+                                                              (int)vo, (int)so, kStorePolicy);
                 }
         }
         return;

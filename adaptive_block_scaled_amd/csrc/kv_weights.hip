@@ -359,15 +359,19 @@ __global__ void __launch_bounds__(kThreads) few_stats_kernel(const Args p) {
 #pragma unroll
     for (int r = 0; r < R / 2; r++) m[r] = kLowest, l[r] = 0.0f;
     few.go(table, from, to, [&](int t) { return tiles(t); }, [&](int, const float (&x)[R / 2]) {
+        bool raise = false;
 #pragma unroll
-        for (int r = 0; r < R / 2; r++) {
-            const float y = x[r] * few.f[r];
-            if (y > m[r] + kSlack) {
-                l[r] *= __builtin_amdgcn_exp2f(m[r] - y);
-                m[r] = y;
+        for (int r = 0; r < R / 2; r++) raise |= x[r] * few.f[r] > m[r] + kSlack;
+        if (__builtin_amdgcn_ballot_w64(raise)) {
+#pragma unroll
+            for (int r = 0; r < R / 2; r++) {
+                const float y = x[r] * few.f[r], to = y > m[r] + kSlack ? y : m[r];
+                l[r] *= __builtin_amdgcn_exp2f(m[r] - to);
+                m[r] = to;
             }
-            l[r] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], few.f[r], -m[r]));
         }
+#pragma unroll
+        for (int r = 0; r < R / 2; r++) l[r] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], few.f[r], -m[r]));
     });
 #pragma unroll
     for (int r = 0; r < R / 2; r++) {
