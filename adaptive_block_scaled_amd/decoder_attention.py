@@ -196,10 +196,13 @@ class AttentionBlock:
         since they came.  Sequences that have no more stay as they are."""
         if not self.weights_of:
             raise ValueError("the block keeps no attention weights (weights_of)")
+        seqs = list(seqs)
+        if len(set(seqs)) != len(seqs):
+            raise ValueError("a sequence comes twice")
+        if keep <= 0 or recent < 0 or sinks < 0 or recent + sinks > keep:
+            raise ValueError("keep must be positive, recent and sinks not negative, nor more than keep together")
         long = [s for s in seqs if self.pages.lens[s] > keep]
-        if not long or keep <= 0:
-            if keep <= 0:
-                raise ValueError(f"keep must be positive, not {keep}")
+        if not long:
             return
         table, lens = self.pages.table(long)
         fresh = self.pages.fresh([keep] * len(long))

@@ -137,9 +137,13 @@ def test_refusals():
         b.forward(torch.zeros(2, 250, device="cuda").bfloat16(), ["a"], [2])
     assert b.pages.lens == {"a": 3} and b.pages.seen == {"a": 3}
     b = block(da, weights_of=10)
-    with pytest.raises(ValueError, match="keep"):
-        b.forward(torch.zeros(3, 256, device="cuda").bfloat16(), ["a"], [3])
-        b.evict(["a"], 0)
+    b.forward(torch.zeros(6, 256, device="cuda").bfloat16(), ["a"], [6])
+    owned, free = dict(b.pages.owned), list(b.pages.free)
+    for args, kw in (((["a"], 0), {}), ((["a"], 2), dict(recent=2, sinks=1)), ((["a"], 2), dict(sinks=-1)),
+                     ((["a", "a"], 2), {})):
+        with pytest.raises(ValueError, match="keep|twice"):
+            b.evict(*args, **kw)
+    assert b.pages.owned == owned and b.pages.free == free and b.pages.lens == {"a": 6}
 
 
 def test_command(capsys):

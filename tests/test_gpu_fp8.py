@@ -209,6 +209,39 @@ def test_other_stream_and_graph(fp8):
         assert torch.equal(out, fp8.gemm(*fp8.quantize(b), *qw))
 
 
+@pytest.mark.parametrize("m,n,k,square,dtype", [(1, 512, 4096, True, BF16), (40, 200, 4224, False, F32), (200, 260, 2048, True, BF16),
+                                                (2048, 2100, 512, True, BF16), (4096, 4100, 256, False, F32)])
+def test_every_kind_of_tile_in_a_graph(fp8, m, n, k, square, dtype):
+    # one row, K split over workgroups, each tile size; replayed beside eager calls
+    qw = fp8.quantize(spread((n, k), 2, BF16).cuda(), square)
+    a = spread((m, k), 1, BF16).cuda()
+    b = a.clone()
+    work = torch.empty(fp8.workspace_bytes(m, n, k), dtype=torch.uint8, device="cuda")
+    out = torch.empty(m, n, dtype=dtype, device="cuda")
+    fp8.gemm(*fp8.quantize(b), *qw, out=out, workspace=work)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fp8.gemm(*fp8.quantize(b), *qw, out=out, workspace=work)
+    for i in range(3):
+        b.copy_(a.roll(i + 1, 0))
+        graph.replay()
+        want = fp8.gemm(*fp8.quantize(b), *qw, dtype=dtype)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_the_same_row_in_every_tile_size(fp8):
+    """A row's products lie within the bound whatever its neighbours, and fp32 sums of one
+    row agree between tiles up to their order."""
+    a, w = spread((300, 1040), 1, BF16), spread((700, 1040), 2, BF16, 0.1)
+    qw = fp8.quantize(w.cuda())
+    whole = fp8.gemm(*fp8.quantize(a.cuda()), *qw, dtype=F32)
+    for rows in (1, 5, 40, 90):
+        part = fp8.gemm(*fp8.quantize(a[:rows].cuda()), *qw, dtype=F32)
+        size = a[:rows].double().abs().cuda() @ w.double().abs().cuda().T
+        assert bool(((part - whole[:rows]).abs().double() <= 1.2 * size * 2 * 1041 * 2.0 ** -24).all())
+
+
 def test_refusals(fp8):
     u8 = dict(dtype=torch.uint8, device="cuda")
     x = torch.zeros(32, 64, dtype=BF16, device="cuda")

@@ -361,6 +361,47 @@ def test_other_stream_and_graph(kvc, ev):
         assert torch.equal(out, want) and torch.equal(kept, ev.select(want, args[3], 50, recent=5))
 
 
+def test_many_rows_and_long_sums_in_a_graph(kvc, ev):
+    # the passes of many rows and the segments of long sums, replayed beside eager calls
+    b = Batch(kvc, [400, 90], [70, 90], 8, 2, 128, 16, 19)
+    q = b.q.cuda()
+    args = (b.cache, *b.device())
+    kw = dict(max_q=90, max_len=400, k_exp=b.exps["k_exp"])
+    long = torch.rand(2, 2, 30000, device="cuda")
+    n32 = torch.tensor([30000, 17000], dtype=torch.int32, device="cuda")
+    work = torch.empty(ev.workspace_bytes(b.cache, total_q=160, heads=8, batch=2, max_q=90, max_len=400), dtype=torch.uint8,
+                       device="cuda")
+    space = torch.empty(ev.select_workspace_bytes(long, 2, 5000), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(2, 2, 400, device="cuda")
+    kept = ev.select(long, n32, 5000, recent=64, workspace=space)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ev.accumulate(out, q, *args, workspace=work, **kw)
+        ev.select(long, n32, 5000, recent=64, out=kept, workspace=space)
+    for i in range(3):
+        q.mul_(1.1)
+        long.copy_(long.roll(1000, 2))
+        out.zero_()
+        graph.replay()
+        want = ev.accumulate(torch.zeros_like(out), q, *args, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(kept, ev.select(long, n32, 5000, recent=64))
+
+
+def test_padded_batches(kvc, ev):
+    # rows of q before the first sequence and behind the last, and sequences without rows
+    b = Batch(kvc, [80, 50, 33], [5, 0, 40], 4, 2, 64, 16, 20)
+    table, lens, _ = b.device()
+    q = torch.randn(60, 4, 64, device="cuda").bfloat16()
+    starts = torch.tensor([7, 12, 12, 52], dtype=torch.int32, device="cuda")
+    mass = torch.rand(3, 2, 100, device="cuda")
+    got = ev.accumulate(mass.clone(), q, b.cache, table, lens, starts, max_q=40, k_exp=b.exps["k_exp"])
+    close = torch.cat([q[7:12], q[12:52]])
+    want = ev.accumulate(mass.clone(), close, b.cache, table, lens,
+                         torch.tensor([0, 5, 5, 45], dtype=torch.int32, device="cuda"), max_q=40, k_exp=b.exps["k_exp"])
+    assert torch.equal(got, want) and torch.equal(got[1], mass[1])
+
+
 def test_refusals(kvc, ev):
     b = Batch(kvc, [40, 20], [1, 1], 4, 2, 64, 16, 18)
     mass = torch.zeros(2, 2, 40, device="cuda")
