@@ -1,5 +1,14 @@
 // FP8 x FP8 product for gfx950: C[M,N] = A[M,K] * W[N,K]^T, E4M3 codes with a power
 // of two per block of 128 along K (include/if4_fp8.h), fp32 sums.
+//
+// The block of 128 is a matrix instruction's K (or twice it), so that a block's byte goes into
+// the instruction as its scale and costs nothing.  But the scaled FP8 instructions do not add
+// products one by one: of 8 neighbouring k they bring the products to the largest one's
+// exponent and cut them 13 bits below it.  That is within what rounding a result to bf16
+// loses, so results in bf16 take them.  Results in fp32 take the bf16 instructions, in
+// which every product and every sum of fp32 is whole: E4M3 times a power of two is exact in
+// bf16, and the conversion (v_cvt_scalef32) applies the byte too.  That is at half the rate, for
+// gradients of weights: 4096 x 8192 x 4096 190 us, 1440 TFLOP/s, and 104 with a result in bf16 (2650).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -89,6 +98,29 @@ struct Scales {
     }
 };
 
+// A tile of BM x BN results per workgroup, and (splits > 1) a share of K.
+//
+// A step is one block of K: BM + BN lines of 128 bytes, brought into LDS without a stop in
+// registers, kStages steps ahead.  Its two halves of 64 are the operands of 32 x 32 x 64
+// products, read one half ahead of the products that need them, a few reads beside each
+// product.  In the loop nothing branches (a branch parts the reads from the products, which
+// cost 8 to 15% wherever one was): what lies past K, M or N is outside the buffer resource and
+// arrives as zeros, and a step's buffer is known when compiled.
+//
+// 256 x 256 with four waves of 128 x 128: 256 accumulators each, and the fewest LDS bytes a
+// product (a wave reads 256 rows for 16 products a half; of 64 x 128 parts, 8 waves, 1.5 times
+// as many, and slower).  One workgroup and one wave per SIMD fit, so that products wait
+// wherever the wave waits: 8192 x 28672 x 8192 1470 us, 2620 TFLOP/s, with the matrix units busy
+// 63% of the time (of no step but products 3830 are reached by one wave a SIMD and 4490 by
+// two), 840 MB read and written once being 170 us.  Three stages or prefetch by half steps:
+// slower.  Tiles of 128 (64 KB of LDS, two workgroups on a CU, each covering the other's
+// waits) with two stages: 2048 x 4096 x 4096 44 us, four stages and one workgroup 60.  Tiles
+// of 64 with four stages: 64 x 28672 x 8192, 239 MB, 64.6 us, 3.7 TB/s; two stages 66.5 (256 x
+// 6144 x 4096: 23.9, 26.6).
+//
+// Tiles are gone through in bands of kBandM rows of tiles, and workgroups that follow one
+// another on one XCD have tiles that follow one another, so that its L2 has their A and W
+// (bands of 2, 8 and 16 were slower).
 template <int BM, int BN, int kWavesM, int kWavesN, int kStages, bool kBf16, bool kBytes>
 __global__ void __launch_bounds__(64 * kWavesM * kWavesN)
 tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales,
@@ -348,11 +380,12 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
         }
 }
 
-// Few rows of A (M <= 16 kTiles): the bytes of W bound the call, and each is used by one
-// wave only, so that they go from memory to registers, kDepth blocks ahead, with no LDS.
-// A wave has 16 rows of W and all rows of A (16 x 16 x 128 products, W's rows in the
-// accumulators' registers); the workgroup's 8 waves are kRows groups of 16 rows of W by
-// 8 / kRows shares of K, whose sums are added up in LDS in their order.
+// Few rows of A (M <= 16): the bytes of W bound the call, and each is used by one wave only, so
+// that they go from memory to registers, four blocks ahead, with no LDS.  A workgroup has 16
+// rows of W and all rows of A (16 x 16 x 128 products, W's rows in the accumulators'
+// registers); its 8 waves take shares of K, whose sums are added up in LDS in their order.
+// M = 1, N = 6144, K = 4096 (25 MB): 7.5 us, 3.4 TB/s, of which the launch and the first
+// answer from memory are about half.
 constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 
 // The two pieces of 16 bytes of a lane's 32 codes of block s: row `row` of the resource,
@@ -367,26 +400,22 @@ __device__ __forceinline__ int8v load_codes(__amdgpu_buffer_rsrc_t rsrc, uint32_
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int kTiles, int kRows, bool kBf16, bool kBytes>
+template <bool kBf16, bool kBytes>
 __global__ void __launch_bounds__(kFewThreads)
 few_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales,
            const uint8_t* __restrict__ w_codes, const uint8_t* __restrict__ w_scales,
            int w_square, int64_t M, int64_t N, int64_t K, void* __restrict__ c, int64_t ldc) {
-    constexpr int kShares = kFewWaves / kRows;
-    __shared__ float4v sums[kShares > 1 ? kFewWaves : 1][kTiles][64];
+    __shared__ float4v sums[kFewWaves][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int group = wave / kShares, part = wave % kShares;
-    const int64_t n0 = ((int64_t)blockIdx.x * kRows + group) * 16;
-    const int w_rows = N - n0 < 16 ? (int)(N - n0 > 0 ? N - n0 : 0) : 16;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int w_rows = N - n0 < 16 ? (int)(N - n0) : 16;
     const int steps = (int)((K + BK - 1) / BK);
-    const int share = ((steps + kShares - 1) / kShares + kWindow - 1) & ~(kWindow - 1);
-    const int from = part * share, to = from + share < steps ? from + share : steps;
+    const int share = ((steps + kFewWaves - 1) / kFewWaves + kWindow - 1) & ~(kWindow - 1);
+    const int from = wave * share, to = from + share < steps ? from + share : steps;
 
-    float4v acc[kTiles];
-#pragma unroll
-    for (int i = 0; i < kTiles; i++) acc[i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    if (w_rows > 0 && from < to) {
+    float4v acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (from < to) {
         const int r = lane & 15, k = 32 * (lane >> 4);
         const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
             (void*)(w_codes + n0 * K), 0, (int)(w_rows * K), kRawBufferFlags);
@@ -398,54 +427,38 @@ few_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_sc
         const Scales<kBytes> scales_w(w_scales, w_first, w_square ? (N + BK - 1) / BK : N, steps);
         const Scales<kBytes> scales_a(a_scales, 0, M, steps);
         const int off_w = (w_square ? 0 : r < w_rows ? r : w_rows - 1) * steps;
-        uint32_t va[kTiles];
-        int off_a[kTiles];
-#pragma unroll
-        for (int i = 0; i < kTiles; i++) {
-            const int m = 16 * i + r < M ? 16 * i + r : (int)M - 1;
-            va[i] = (uint32_t)m * (uint32_t)K + k;
-            off_a[i] = m * steps;
-        }
-        // W of four blocks at once, those of the next four on their way; A's block by block
+        const int m = r < M ? r : (int)M - 1;
+        const uint32_t va = (uint32_t)m * (uint32_t)K + k;
+        const int off_a = m * steps;
+        // W of four blocks at once, those of the next four on their way
         int8v w[2][kWindow];
-        uint32_t ew[2], ea[2][kTiles];
+        uint32_t ew[2], ea[2];
         const auto load = [&](int which, int s) {
 #pragma unroll
             for (int u = 0; u < kWindow; u++) w[which][u] = load_codes(rw, vw, k, s + u, K);
             ew[which] = scales_w.window(off_w + s);
-#pragma unroll
-            for (int i = 0; i < kTiles; i++) ea[which][i] = scales_a.window(off_a[i] + s);
+            ea[which] = scales_a.window(off_a + s);
         };
         const auto multiply = [&](auto which, int s) {
             constexpr int b = decltype(which)::value;
-            const uint32_t sw = scales_w.take(ew[b], off_w + s);
-            uint32_t sa[kTiles];
+            const uint32_t sw = scales_w.take(ew[b], off_w + s), sa = scales_a.take(ea[b], off_a + s);
+            int8v a[kWindow];
 #pragma unroll
-            for (int i = 0; i < kTiles; i++) sa[i] = scales_a.take(ea[b][i], off_a[i] + s);
-            int8v a[kWindow][kTiles];
-#pragma unroll
-            for (int u = 0; u < kWindow; u++)
-#pragma unroll
-                for (int i = 0; i < kTiles; i++) a[u][i] = load_codes(ra, va[i], k, s + u, K);
+            for (int u = 0; u < kWindow; u++) a[u] = load_codes(ra, va, k, s + u, K);
 #pragma unroll
             for (int u = 0; u < kWindow; u++) {
                 // (blocks past the last are zeros, and their bytes another row's: not NaN then)
                 const bool past = s + u >= steps;
-                const uint32_t eu = past ? 127u : sw >> (8 * u);
-                bf16x8 x[4], y[4];
-                if constexpr (!kBf16) widen(w[b][u], eu, x);
+                const uint32_t eu = past ? 127u : sw >> (8 * u), fu = past ? 127u : sa >> (8 * u);
+                if constexpr (kBf16) {
+                    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[b][u], a[u], acc, 0, 0, 0, (int)eu, 0,
+                                                                           (int)fu);
+                } else {
+                    bf16x8 x[4], y[4];
+                    widen(w[b][u], eu, x);
+                    widen(a[u], fu, y);
 #pragma unroll
-                for (int i = 0; i < kTiles; i++) {
-                    const uint32_t fu = past ? 127u : sa[i] >> (8 * u);
-                    if constexpr (kBf16) {
-                        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[b][u], a[u][i], acc[i], 0, 0, 0,
-                                                                                  (int)eu, 0, (int)fu);
-                    } else {
-                        widen(a[u][i], fu, y);
-#pragma unroll
-                        for (int q = 0; q < 4; q++)
-                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], y[q], acc[i], 0, 0, 0);
-                    }
+                    for (int q = 0; q < 4; q++) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[q], y[q], acc, 0, 0, 0);
                 }
             }
         };
@@ -458,42 +471,28 @@ few_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_sc
             multiply(std::integral_constant<int, 1>{}, s + kWindow);
         }
     }
-    if constexpr (kShares > 1) {
+    sums[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+    for (int p = 1; p < kFewWaves; p++) acc += sums[p][lane];
+    // lane: row lane % 16 of A, columns n0 + 4 (lane / 16) .. + 3
+    const int64_t row = lane & 15, col = n0 + 4 * (lane >> 4);
+    if (row >= M) return;
 #pragma unroll
-        for (int i = 0; i < kTiles; i++) sums[wave][i][lane] = acc[i];
-        __syncthreads();
-        if (part != 0) return;
-#pragma unroll
-        for (int i = 0; i < kTiles; i++)
-            for (int p = 1; p < kShares; p++) acc[i] += sums[wave + p][i][lane];
+    for (int r = 0; r < 4; r++) {
+        if (col + r >= N) continue;
+        if constexpr (kBf16)
+            reinterpret_cast<__bf16*>(c)[row * ldc + col + r] = (__bf16)acc[r];
+        else
+            reinterpret_cast<float*>(c)[row * ldc + col + r] = acc[r];
     }
-    // lane: row lane % 16 of A's tile, columns n0 + 4 (lane / 16) .. + 3
-#pragma unroll
-    for (int i = 0; i < kTiles; i++) {
-        const int64_t row = 16 * i + (lane & 15), col = n0 + 4 * (lane >> 4);
-        if (row >= M) continue;
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            if (col + r >= N) continue;
-            if constexpr (kBf16)
-                reinterpret_cast<__bf16*>(c)[row * ldc + col + r] = (__bf16)acc[i][r];
-            else
-                reinterpret_cast<float*>(c)[row * ldc + col + r] = acc[i][r];
-        }
-    }
-}
-
-template <int kTiles, int kRows, bool kBf16, bool kBytes>
-hipError_t launch_few_rows(const Fp8Gemm& g, hipStream_t stream) {
-    const unsigned groups = (unsigned)((g.N + 16 * kRows - 1) / (16 * kRows));
-    hipLaunchKernelGGL((few_kernel<kTiles, kRows, kBf16, kBytes>), dim3(groups), dim3(kFewThreads), 0, stream,
-                       g.a_codes, g.a_scales, g.w_codes, g.w_scales, g.w_square, g.M, g.N, g.K, g.c, g.ldc);
-    return hipGetLastError();
 }
 
 template <bool kBf16, bool kBytes>
 hipError_t launch_few(const Fp8Gemm& g, hipStream_t stream) {
-    return launch_few_rows<1, 1, kBf16, kBytes>(g, stream);
+    hipLaunchKernelGGL((few_kernel<kBf16, kBytes>), dim3((unsigned)((g.N + 15) / 16)), dim3(kFewThreads), 0, stream,
+                       g.a_codes, g.a_scales, g.w_codes, g.w_scales, g.w_square, g.M, g.N, g.K, g.c, g.ldc);
+    return hipGetLastError();
 }
 
 template <bool kBf16>
@@ -532,7 +531,15 @@ struct Plan {
     int splits;
 };
 
-// (kTileStages: as many as leave room for two workgroups on a CU, for one of 256 x 256)
+// The largest tile whose tiles fill the CUs (128: half of them, for what two parts of K then
+// bring), and few_kernel for few rows.  In us, results in bf16, W from memory:
+//   few_kernel and tiles of 64:  1 x 6144 x 4096  8.4, 10.7;  4  9.0, 10.8;  16  10.9, 11.2;
+//                                16 x 28672 x 8192  72, 53 (W's tiles fill the CUs)
+//   64 and 128:   256 x 6144 x 4096  24, 27;  512  38, 36;  1024 x 4096 x 4096  35, 27
+//   128 and 256:  2048 x 4096 x 4096  44, 100;  4096 x 4096 x 4096  82, 68
+// K is parted where tiles leave CUs free, so that there are up to two workgroups on each, of 8
+// steps at least; parted and whole:  64 x 6144 x 4096  16.0, 22.8;  300 x 1024 x 16384  26,
+// 78;  512 x 6144 x 4096  36, 34 (its results are many for what is gained).
 constexpr int kCus = 256;
 
 Plan plan_of(int64_t M, int64_t N, int64_t K) {

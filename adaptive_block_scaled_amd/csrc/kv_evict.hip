@@ -16,14 +16,15 @@ namespace {
 // it the first.
 //
 // One workgroup per sequence and kv head does all of it (select_kernel) where rows are
-// short, or are so many that they fill the chip.  Bound by the latency of its passes: a thread
-// asks for 8 sums at once when it counts and 4 when it writes.  Sums of one size are many
-// (zeros, above all), and atomics on one place of LDS wait for one another: the lanes
+// short, or are many.  Bound by the latency of its four passes, with one workgroup on a CU: a
+// thread asks for 8 sums at once when it counts and 4 when it writes (256 rows of 16384 sums
+// 28 us, of which the first pass reads memory and the others the caches).  Sums of one size
+// are many (zeros, above all), and atomics on one place of LDS wait for one another: the lanes
 // with the first lane's digit add once.
 //
 // Of long rows a workgroup takes a segment, and the passes are launches (segment kernels):
 // each leaves its digits' numbers in the workspace, and each workgroup of the next adds them
-// up itself.  131071 sums of 16 rows: 159 us in one workgroup each.
+// up itself.  16 rows of 131071 sums: 43 us, 159 in one workgroup each.
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kDigits = 2048;
@@ -329,10 +330,12 @@ __global__ void __launch_bounds__(kThreads) segment_move_kernel(const SegmentArg
         row.out[i] = p.moved[(int64_t)pair * p.s.keep + i];
 }
 
-// Segments of a row, 0 where one workgroup takes it: rows of up to two segments, and those
-// that fill the chip without being parted.
+// Segments of a row, 0 where one workgroup takes it: rows of up to two segments, and so many
+// that they keep the chip busy without being parted.  In us, one workgroup a row and
+// segments:  8 rows of 16384 sums 25, 26, of 24000 34, 27, of 131071 153, 41;  64 rows of 16384
+// 26, 28, of 24000 35, 31, of 131071 159, 114;  256 rows of 24000 37, 66, of 131071 169, 413.
 int64_t segments_of(const if4_kv_mass& m, int64_t rows, int64_t keep) {
-    if (m.width <= 2 * kSegment || rows >= 512 || keep >= m.width) return 0;
+    if (m.width <= 2 * kSegment || rows > 64 || keep >= m.width) return 0;
     return (m.width + kSegment - 1) / kSegment;
 }
 
@@ -340,7 +343,10 @@ int64_t segments_of(const if4_kv_mass& m, int64_t rows, int64_t keep) {
 // Compact.  A workgroup fills one tile of 16 tokens of one sequence and kv head: V's 16
 // pieces of each token lie 16 tokens apart, so that a whole tile is written in one piece
 // of 8 D bytes, and what is read of a source tile is read by one workgroup and its
-// neighbours.
+// neighbours.  Bound by memory, and by how it is laid out: of a source tile with any token
+// kept, V's every 64-byte line is read, whichever of its 16 tokens stay.  32 sequences of about 7100
+// tokens and 8 kv heads of 128, of which 2048 stay (so that nearly every tile has one; 240
+// MB read and written): 65 us, 3.7 TB/s.
 
 constexpr int kCopyThreads = 256;
 

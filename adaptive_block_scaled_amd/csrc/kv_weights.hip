@@ -13,6 +13,12 @@
 // K enters as 7 times its values: FP4's 7 c s' and INT4's 6 q s' have at most 9 bits, which
 // fp16 holds, so that nothing is rounded before the fp32 sums (decoded to its own value, an
 // INT4 code would be off by up to 2^-11 of it, more than the fp32 results allow).
+//
+// Few rows (8 of each kv head; 64 sequences of 7600 tokens, 282 MB of K): 77 us and 85, 3.5
+// TB/s, each pass bound by the decoding of 72 bytes a key beside their loads.  Many rows
+// (16384 of each of 8 kv heads over 16384 keys, heads of 128): 585 us and 630, about 640
+// cycles of a SIMD for a block of 32 x 32 scores, whose matrix products take 256, exponentials
+// 256 and other operations 200 that partly run beside the products; two waves share a SIMD.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

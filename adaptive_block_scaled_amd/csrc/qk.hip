@@ -180,10 +180,11 @@ struct Weights {
 };
 
 // A wave per token and chunk of its heads; its 64 / L lane groups take them in turn.  8192
-// tokens of 72 vectors of 128 in bf16 (304 MB moved) 52.5 us, 5.8 TB/s, with up to 8 vectors
-// to a lane and stores past the caches; up to 4, 18: 57, 59; ordinary stores 69 (what they leave
-// in the caches has to be written back from there); two vectors at once 76; waves that
-// stay for many tokens 61.
+// tokens of 72 vectors of 128 in bf16 (304 MB moved), other ones in each call: 72.7 us, 4.2
+// TB/s, with up to 8 vectors to a lane and stores past the caches; up to 2, 3, 4, 12, 18: 81,
+// 75, 77, 79, 93; ordinary stores 73.2; the next vector on its way while one is turned
+// 77.  The same tensors in each call, which the caches hold in part: 52.5, up to 4 57, up to 18
+// 59, ordinary stores 69.  64 tokens: 4.2 us, the time of a launch.
 template <int L, bool kIn, bool kOut, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
     constexpr int G = 64 / L;
@@ -219,7 +220,8 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args p) {
 // dz = the rotation undone on g, r = 1 / sqrt(mean x^2 + eps):
 //     dx = r (dz w - x r^2 mean(dz w x)),   dw = sum dz x r.
 // Each lane keeps its sums of dw over all vectors that it sees; a workgroup joins them
-// through LDS and writes one row of the workspace, and join_kernel adds the rows.
+// through LDS and writes one row of the workspace, and join_kernel adds the rows.  4099 tokens
+// of 40 vectors of 128 in bf16 (126 MB): 28 us and 4.7 of the join, 3.9 TB/s.
 template <int L, bool kIn, bool kOut, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const Args p, float* __restrict__ sums) {
     constexpr int G = 64 / L, kWaves = kThreads / 64;
