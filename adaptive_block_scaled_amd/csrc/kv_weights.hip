@@ -270,7 +270,8 @@ struct KeyAhead {
     __device__ __forceinline__ void load(const Args& p, int head, int lane) {
         int at = page < p.pages - 1 ? page : p.pages - 1;
         at = at > 0 ? at : 0;
-        codes.load(p, ((int64_t)(at * p.kv_heads + head) * p.tiles.n + tile) * 16 + (lane & 15), lane >> 5);
+        const uint32_t group = (uint32_t)at * (uint32_t)p.kv_heads + (uint32_t)head;
+        codes.load(p, (int64_t)((uint64_t)group * p.tiles.n + tile) * 16 + (lane & 15), lane >> 5);
     }
 };
 
@@ -287,6 +288,21 @@ __device__ __forceinline__ void hide_rows(const Args& p, const Sequence& s, int 
         x[r] = seen ? x[r] : -__builtin_inff();
     }
 }
+
+// The split and the (sequence, kv head) pair of a workgroup.  A CU gets every 256th workgroup:
+// each split's pairs begin further on by the golden section of all, so that one CU's are of
+// many sequences, and CUs have as much to do as one another where lengths differ (8 sequences
+// of 2000 to 20000 tokens: 48 us without, 43).
+struct Work {
+    int split, pair;
+    __device__ __forceinline__ Work(const Args& p, int index) {
+        split = index / p.batch_heads;
+        const uint32_t n = (uint32_t)p.batch_heads;
+        const uint32_t on = (uint32_t)((uint64_t)((uint32_t)split * 0x9E3779B9u) * n >> 32);
+        const uint32_t at = (uint32_t)index - (uint32_t)split * n + on;
+        pair = (int)(at < n ? at : at - n);
+    }
+};
 
 // What both passes over few rows share: the rows' q, and the tiles of keys in turn.
 template <int D, int R>
@@ -333,12 +349,11 @@ struct FewRows {
         next.load(p, head, lane);
         if (t + kWaves < to) next.look_up(p, s, tile(t + kWaves) * kUnit + j);
         for (; t < to; t += kWaves) {
-            const KeyCodes<D> codes = next.codes;
             const int first = tile(t) * kUnit;
+            half8 k[D / 16];
+            next.codes.decode(table, four, k);
             if (t + kWaves < to) next.load(p, head, lane);
             if (t + 2 * kWaves < to) next.look_up(p, s, tile(t + 2 * kWaves) * kUnit + j);
-            half8 k[D / 16];
-            codes.decode(table, four, k);
             const f32x16 all = scores<D>(q, k);
             float x[R / 2];
 #pragma unroll
@@ -350,34 +365,39 @@ struct FewRows {
 };
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads) few_stats_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 2) few_stats_kernel(const Args p) {
     __shared__ uint2 table[256];
     __shared__ f32x2 part[kWaves][R];
-    FewRows<D, R> few(p, blockIdx.x % p.batch_heads, table);
+    const Work work(p, blockIdx.x);
+    FewRows<D, R> few(p, work.pair, table);
     const Sequence& s = few.s;
     if (!s.there) return;
     few.load_rows();
     __syncthreads();
     const KeyTiles tiles(p, s.len, few.pos_lo, few.pos_hi);
-    const int split = blockIdx.x / p.batch_heads, share = (tiles.n + p.splits - 1) / p.splits;
-    const int from = split * share, to = from + share < tiles.n ? from + share : tiles.n;
+    const int share = (tiles.n + p.splits - 1) / p.splits;
+    const int from = work.split * share, to = from + share < tiles.n ? from + share : tiles.n;
     float m[R / 2], l[R / 2];
 #pragma unroll
     for (int r = 0; r < R / 2; r++) m[r] = kLowest, l[r] = 0.0f;
     few.go(table, from, to, [&](int t) { return tiles(t); }, [&](int, const float (&x)[R / 2]) {
-        bool raise = false;
+        float y[R / 2], top = -__builtin_inff();
 #pragma unroll
-        for (int r = 0; r < R / 2; r++) raise |= x[r] * few.f[r] > m[r] + kSlack;
-        if (__builtin_amdgcn_ballot_w64(raise)) {
+        for (int r = 0; r < R / 2; r++) {
+            y[r] = __builtin_fmaf(x[r], few.f[r], -m[r]);
+            top = __builtin_fmaxf(top, y[r]);
+        }
+        if (__builtin_amdgcn_ballot_w64(top > kSlack)) {
 #pragma unroll
             for (int r = 0; r < R / 2; r++) {
-                const float y = x[r] * few.f[r], to = y > m[r] + kSlack ? y : m[r];
+                const float to = y[r] > kSlack ? x[r] * few.f[r] : m[r];
                 l[r] *= __builtin_amdgcn_exp2f(m[r] - to);
                 m[r] = to;
+                y[r] = __builtin_fmaf(x[r], few.f[r], -to);
             }
         }
 #pragma unroll
-        for (int r = 0; r < R / 2; r++) l[r] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], few.f[r], -m[r]));
+        for (int r = 0; r < R / 2; r++) l[r] += __builtin_amdgcn_exp2f(y[r]);
     });
 #pragma unroll
     for (int r = 0; r < R / 2; r++) {
@@ -398,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) few_stats_kernel(const Args p) {
 #pragma unroll
     for (int w = 0; w < kWaves; w++) sum += part[w][r][1] * __builtin_amdgcn_exp2f(part[w][r][0] - top);
     const int token = (int)p.group.into(r), mm = r - token * (int)p.group.n;
-    p.stats[split * p.stat_rows + (int64_t)(s.first_row + token) * p.heads + few.head * (int)p.group.n + mm] =
+    p.stats[work.split * p.stat_rows + (int64_t)(s.first_row + token) * p.heads + few.head * (int)p.group.n + mm] =
         f32x2{top, sum};
 }
 
@@ -433,15 +453,15 @@ struct Sums {
 // The workgroups go through the keys the other way round than those of the first pass did,
 // whose last keys are still in the caches.
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads) few_columns_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 2) few_columns_kernel(const Args p) {
     __shared__ uint2 table[256];
-    const int index = gridDim.x - 1 - blockIdx.x;
-    FewRows<D, R> few(p, index % p.batch_heads, table);
+    const Work work(p, gridDim.x - 1 - blockIdx.x);
+    FewRows<D, R> few(p, work.pair, table);
     const Sequence& s = few.s;
     if (!s.there) return;
     const Sums sums(p, s, few.head);
     const int tiles = (sums.width + kUnit - 1) / kUnit, share = (tiles + p.splits - 1) / p.splits;
-    const int from = index / p.batch_heads * share, to = from + share < tiles ? from + share : tiles;
+    const int from = work.split * share, to = from + share < tiles ? from + share : tiles;
     if (from >= to) return;
     few.load_rows();
     float log[R / 2];
@@ -783,9 +803,13 @@ struct Plan {
 
 constexpr int kMostSplits = 64;
 
-// Key splits and key blocks fill the chip: few rows with kFew workgroups, eight to a CU (a
-// split has two tiles for each of its waves at least), many with kMany.
-constexpr int kFew = 2048, kMany = 1024;
+// Key splits fill the chip: kFull workgroups, four to a CU (a split has two tiles for each of
+// its waves at least).  Few rows of so many pairs that fewer than two splits of each would do
+// that take twice as many, so that workgroups that are done early have others after them.  In
+// us, 1024 workgroups and 2048:  8 sequences of 2000 to 20000 tokens, 8 kv heads, 43, 61;  32
+// of 3001 to 12289 88, 95;  4 of 100003 to 131071 137, 169;  64 of 3001 to 12289 158, 157;  100
+// of 100 to 9000 160, 153.
+constexpr int kFull = 1024;
 
 Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     Plan p;
@@ -795,7 +819,7 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     p.row_tiles = c.head_dim == 256 ? 1 : 2;
     const int64_t block = 32 * kWaves * p.row_tiles;
     p.row_blocks = p.few ? 1 : (rows + block - 1) / block;
-    const int64_t groups = pairs * p.row_blocks, full = p.few ? kFew : kMany;
+    const int64_t groups = pairs * p.row_blocks, full = p.few && 2 * pairs > kFull ? 2 * kFull : kFull;
     const int64_t most = (units + 2 * kWaves - 1) / (2 * kWaves);
     p.splits = groups >= full ? 1 : (full + groups - 1) / groups;
     p.splits = p.splits < most ? p.splits : most;
