@@ -24,7 +24,7 @@ namespace {
 //
 // Of long rows a workgroup takes a segment, and the passes are launches (segment kernels):
 // each leaves its digits' numbers in the workspace, and each workgroup of the next adds them
-// up itself.  16 rows of 131071 sums: 43 us, 159 in one workgroup each.
+// up itself.  16 rows of 131071 sums: 41 us, 155 in one workgroup each.
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kDigits = 2048;
@@ -228,7 +228,6 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
 
 // Workspace of the segment kernels: [3][rows][segments][kDigits] numbers, then [rows][segments]
 // States, then the sums of rows that are written in place, [rows][keep].
-constexpr int kSegment = 8192;
 struct State {
     uint32_t prefix, need;  // of the row, after the levels so far
     uint32_t above;         // sums above it in the segments before this one
@@ -239,7 +238,7 @@ struct SegmentArgs {
     uint32_t* counts;
     State* states;
     float* moved;  // NULL: out is another tensor
-    int rows, segments;
+    int rows, segments, segment;  // segments of a row, sums of each
 };
 
 // What the levels before `level` say, from their numbers; `equals` are the sums equal to
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) segment_count_kernel(const SegmentAr
     if (row.n <= p.s.keep || p.s.keep == p.s.sinks + p.s.recent) return;
     uint32_t equals;
     const State st = resolve(p, sh, pair, segment, kLevel, equals);
-    const int from = segment * kSegment, to = from + kSegment;
+    const int from = segment * p.segment, to = from + p.segment;
     count_digits(count, row.in, from > row.first ? from : row.first, to < row.last ? to : row.last, kLevel, st.prefix);
     uint32_t* const at = p.counts + (((int64_t)kLevel * p.rows + pair) * p.segments + segment) * kDigits;
     for (int i = threadIdx.x; i < kDigits; i += kThreads) at[i] = count[i];
@@ -304,9 +303,9 @@ __global__ void __launch_bounds__(kThreads) segment_write_kernel(const SegmentAr
     __shared__ Shared sh;
     const int pair = blockIdx.x / p.segments, segment = blockIdx.x - pair * p.segments;
     const Row row(p.s, pair);
-    const int from = segment * kSegment, to = from + kSegment < row.n ? from + kSegment : row.n;
+    const int from = segment * p.segment, to = from + p.segment < row.n ? from + p.segment : row.n;
     if (row.n <= p.s.keep) {
-        for (int i = from + threadIdx.x; i < from + kSegment && i < p.s.keep; i += kThreads) {
+        for (int i = from + threadIdx.x; i < from + p.segment && i < p.s.keep; i += kThreads) {
             row.kept[i] = i < row.n ? i : -1;
             if (row.out && row.out != row.in && i < row.n) row.out[i] = row.in[i];
         }
@@ -325,18 +324,24 @@ __global__ void __launch_bounds__(kThreads) segment_move_kernel(const SegmentArg
     const int pair = blockIdx.x / p.segments, segment = blockIdx.x - pair * p.segments;
     const Row row(p.s, pair);
     if (row.n <= p.s.keep) return;
-    const int from = segment * kSegment;
-    for (int i = from + threadIdx.x; i < from + kSegment && i < p.s.keep; i += kThreads)
+    const int from = segment * p.segment;
+    for (int i = from + threadIdx.x; i < from + p.segment && i < p.s.keep; i += kThreads)
         row.out[i] = p.moved[(int64_t)pair * p.s.keep + i];
 }
 
-// Segments of a row, 0 where one workgroup takes it: rows of up to two segments, and so many
-// that they keep the chip busy without being parted.  In us, one workgroup a row and
-// segments:  8 rows of 16384 sums 25, 26, of 24000 34, 27, of 131071 153, 41;  64 rows of 16384
-// 26, 28, of 24000 35, 31, of 131071 159, 114;  256 rows of 24000 37, 66, of 131071 169, 413.
-int64_t segments_of(const if4_kv_mass& m, int64_t rows, int64_t keep) {
-    if (m.width <= 2 * kSegment || rows > 64 || keep >= m.width) return 0;
-    return (m.width + kSegment - 1) / kSegment;
+// Sums of a segment, 0 where one workgroup takes a row: rows that are short, or so many that
+// they keep the chip busy without being parted.  A workgroup for each CU, and 16 segments of a
+// row at most, because each workgroup reads the numbers of all segments of its row (64 rows of
+// 131071 sums in segments of 8192: 113 us).  In us, one workgroup a row and segments:
+//   8 rows of 16384 sums 25, 26, of 24000 34, 27, of 131071 153, 41, of 300000 347, 57;
+//   64 rows of 16384 26, 28, of 24000 35, 31, of 131071 159, 64;
+//   128 rows of 24000 35, 39, of 40000 54, 49, of 131071 168, 103;  256 of 24000 37, 66.
+int64_t segment_of(const if4_kv_mass& m, int64_t rows, int64_t keep) {
+    constexpr int64_t kUnit = 8 * kThreads;
+    if (m.width <= (rows > 64 ? 4 : 2) * kUnit || rows > 128 || keep >= m.width) return 0;
+    const int64_t each = (m.width * (rows > 16 ? rows : 16) + 255) / 256;
+    const int64_t segment = (each + kUnit - 1) / kUnit * kUnit;
+    return segment < m.width ? segment : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -422,22 +427,26 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const CompactArgs
 }  // namespace
 
 int64_t kv_select_workspace(const if4_kv_mass& m, int64_t batch, int64_t kv_heads, int64_t keep) {
-    const int64_t rows = batch * kv_heads, segments = segments_of(m, rows, keep);
-    return segments ? rows * (segments * (3 * kDigits * 4 + (int64_t)sizeof(State)) + keep * 4) : 0;
+    const int64_t rows = batch * kv_heads, segment = segment_of(m, rows, keep);
+    if (!segment) return 0;
+    const int64_t segments = (m.width + segment - 1) / segment;
+    return rows * (segments * (3 * kDigits * 4 + (int64_t)sizeof(State)) + keep * 4);
 }
 
 hipError_t launch_kv_select(const if4_kv_mass& m, const int32_t* seq_lens, int64_t batch,
                             int64_t kv_heads, int64_t keep, int64_t recent, int64_t sinks,
                             int32_t* kept, void* workspace, hipStream_t stream) {
     const SelectArgs s = {m, seq_lens, kept, (int)kv_heads, (int)keep, (int)recent, (int)sinks};
-    const int64_t rows = batch * kv_heads, segments = segments_of(m, rows, keep);
-    if (segments == 0) {
+    const int64_t rows = batch * kv_heads, segment = segment_of(m, rows, keep);
+    if (segment == 0) {
         hipLaunchKernelGGL(select_kernel, dim3((unsigned)rows), dim3(kThreads), 0, stream, s);
         return hipGetLastError();
     }
+    const int64_t segments = (m.width + segment - 1) / segment;
     SegmentArgs p;
     p.s = s;
     p.rows = (int)rows;
+    p.segment = (int)segment;
     p.segments = (int)segments;
     p.counts = reinterpret_cast<uint32_t*>(workspace);
     p.states = reinterpret_cast<State*>(p.counts + 3 * rows * segments * kDigits);

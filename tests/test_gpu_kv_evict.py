@@ -218,7 +218,8 @@ SELECTS = [  # lens, width, keep, recent, sinks
     ([5000, 1024, 1025], 5000, 1024, 256, 64), ([40], 30, 20, 5, 5), ([70], 70, 20, 10, 10), ([70], 70, 20, 20, 0),
     ([9000], 9000, 8999, 0, 0), ([9000], 9000, 1, 0, 0), ([50], 50, 90, 3, 3), ([70000], 70000, 30000, 100, 4),
     ([16385, 20000, 100], 20001, 1500, 30, 2), ([50000], 50000, 49999, 9000, 8500), ([40000, 40000], 40000, 20000, 20000, 0),
-    ([33000], 33000, 33000, 5, 5), ([25000, 24000], 25000, 24500, 0, 0)]
+    ([33000], 33000, 33000, 5, 5), ([25000, 24000], 25000, 24500, 0, 0),
+    ([140000, 20, 16385, 0, 33000, 600], 140000, 700, 30, 2), ([40000, 17, 16384, 300] + 18 * [9], 40000, 16500, 7, 3)]
 
 
 @pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
