@@ -69,6 +69,8 @@ struct Args {
     half8* rows_q;      // many rows: tiles of 32 rows in operand order, see row_tile
     float* row_factor;  // [..][32]
     int64_t row_tiles;  // of one kv head
+    float* part_sums;   // many rows: [parts][pairs][key_blocks][keys of a block]
+    int key_blocks, parts;
     int total_q, max_q, pages, kv_heads, heads, batch_heads, row_blocks, splits;
     int causal, window, sinks;
     Divisor tiles;  // of 16 tokens in a page
@@ -657,7 +659,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) stats_kernel(const
 
 // kTiles tiles of 32 keys per wave, decoded once; the workgroup goes through the rows that
 // may see any of its keys, kRowTiles tiles of 32 at a time, which come into LDS in operand
-// order while those before are multiplied.
+// order while those before are multiplied.  Where blocks of keys are few, a block's rows are
+// parted over workgroups, and join_kernel adds the parts in their order.  (Blocks past the
+// planned ones, of sequences longer than they were said to be, are not parted.)
 template <int D, int kTiles>
 __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
     constexpr int kKeys = kWaves * kTiles * kUnit;
@@ -668,7 +672,8 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
     extern __shared__ __attribute__((aligned(16))) half8 rows_q[];  // [2][kRowTiles][D / 16][64]
     const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int bh = blockIdx.x % p.batch_heads, block0 = blockIdx.x / p.batch_heads;
+    const int bh = blockIdx.x % p.batch_heads, rest = blockIdx.x / p.batch_heads;
+    const int part = rest / p.key_blocks, block0 = rest - part * p.key_blocks;
     const int b = bh / p.kv_heads, head = bh - b * p.kv_heads;
     const Sequence s = sequence_of(p, b);
     if (!s.there) return;
@@ -677,8 +682,10 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
     const Sums sums(p, s, head);
     fill_table(table, tid);
     __syncthreads();
-    const int stride = gridDim.x / p.batch_heads;
-    for (int64_t key0 = (int64_t)block0 * kKeys; key0 < sums.width; key0 += (int64_t)stride * kKeys) {
+    const int64_t stride = (int64_t)p.key_blocks * kKeys;
+    for (int64_t key0 = (int64_t)block0 * kKeys; key0 < sums.width; key0 += stride) {
+        const bool parted = p.parts > 1 && key0 < stride;
+        if (part > 0 && !parted) break;
         const int first = (int)key0 + wave * kTiles * kUnit;
         // rows that may see keys key0 .. key0 + kKeys - 1: from the one at key0, to the last
         // one whose window reaches back
@@ -691,7 +698,12 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
             const int64_t t = key0 + kKeys - 1 + p.window - s.pos0;  // first token past
             hi = t <= 0 ? 0 : t >= s.used ? rows : (int)t * (int)p.group.n;
         }
-        const int t0 = lo / 32, tiles = lo < hi ? (hi + 31) / 32 : t0;
+        int t0 = lo / 32, tiles = lo < hi ? (hi + 31) / 32 : t0;
+        if (parted) {  // whole steps of kRowTiles, so that only a last part has fewer
+            const int share = ((tiles - t0 + p.parts - 1) / p.parts + kRowTiles - 1) / kRowTiles * kRowTiles;
+            t0 = t0 + part * share < tiles ? t0 + part * share : tiles;
+            tiles = t0 + share < tiles ? t0 + share : tiles;
+        }
         const half8* const from = p.rows_q + row_tile(p, s, b, head, 0) * (D / 16 * 64);
         const float* const factors = p.row_factor + row_tile(p, s, b, head, 0) * 32;
         float f_next = 0.0f, log_next = 0.0f;
@@ -789,9 +801,28 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
 #pragma unroll
                 for (int d = 1; d < 32; d *= 2) v += __shfl_xor(v, d);
                 const int key = first + i * kUnit + 4 * h + 8 * (j >> 2) + (j & 3);
-                if ((lane & 31) == j && key < sums.width) sums.out[key] = key < sums.old ? sums.in[key] + v : v;
+                if ((lane & 31) == j && key < sums.width) {
+                    if (parted)
+                        p.part_sums[((int64_t)part * p.batch_heads + bh) * stride + key] = v;
+                    else
+                        sums.out[key] = key < sums.old ? sums.in[key] + v : v;
+                }
             }
     }
+}
+
+// The parts' sums of a block of keys, one to a thread, added in their order.
+__global__ void join_kernel(const Args p) {
+    const int bh = blockIdx.x % p.batch_heads, b = bh / p.kv_heads;
+    const int key = blockIdx.x / p.batch_heads * blockDim.x + threadIdx.x;
+    const Sequence s = sequence_of(p, b);
+    if (!s.there) return;
+    const Sums sums(p, s, bh - b * p.kv_heads);
+    if (key >= sums.width) return;
+    const int64_t stride = (int64_t)p.key_blocks * blockDim.x;
+    float v = 0.0f;
+    for (int i = 0; i < p.parts; i++) v += p.part_sums[((int64_t)i * p.batch_heads + bh) * stride + key];
+    sums.out[key] = key < sums.old ? sums.in[key] + v : v;
 }
 
 struct Plan {
@@ -799,6 +830,7 @@ struct Plan {
     int row_tiles;  // many: 32-row tiles of a wave of the first pass
     int key_tiles;  // many: 32-key tiles of a wave of the second
     int64_t row_blocks, splits, key_blocks;
+    int64_t parts;  // many: of a key block's rows
 };
 
 constexpr int kMostSplits = 64;
@@ -829,8 +861,18 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     p.key_blocks = (units + keys - 1) / keys;
     const int64_t limit = 0x7FFFFFFF / pairs;
     p.key_blocks = p.key_blocks < limit ? p.key_blocks : limit;
+    // (a part has 8 tiles of rows at least)
+    const int64_t blocks = pairs * p.key_blocks, tiles = (rows + 31) / 32;
+    p.parts = p.few || blocks >= kFull / 2 ? 1 : (kFull + blocks - 1) / blocks;
+    p.parts = p.parts < tiles / 8 ? p.parts : tiles / 8 > 1 ? tiles / 8 : 1;
     return p;
 }
+
+// Sums of the parts, and the most that any call has: fewer than kFull + kFull / 2 workgroups.
+int64_t part_bytes(const Plan& p, const if4_kv_cache& c, const if4_kv_attention_args& a) {
+    return p.parts > 1 ? p.parts * a.batch * c.kv_heads * p.key_blocks * kWaves * p.key_tiles * kUnit * 4 : 0;
+}
+constexpr int64_t kMostPartBytes = (int64_t)(kFull + kFull / 2) * kWaves * 2 * kUnit * 4;
 
 template <int D, int R>
 hipError_t launch_few(const Args& p, unsigned groups, hipStream_t stream) {
@@ -851,7 +893,10 @@ hipError_t launch_many(const Args& p, unsigned groups, unsigned columns, hipStre
     const hipError_t allowed = hipFuncSetAttribute((const void*)columns_kernel<D, kKeys>,
                                                    hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (allowed != hipSuccess) return allowed;
-    hipLaunchKernelGGL((columns_kernel<D, kKeys>), dim3(columns), dim3(kThreads), kSmem, stream, p);
+    hipLaunchKernelGGL((columns_kernel<D, kKeys>), dim3(columns * p.parts), dim3(kThreads), kSmem, stream, p);
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess || p.parts == 1) return st;
+    hipLaunchKernelGGL(join_kernel, dim3(columns), dim3(kWaves * kKeys * kUnit), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -870,7 +915,7 @@ hipError_t launch(const Args& p, const Plan& plan, unsigned groups, unsigned col
 
 }  // namespace
 
-// Workspace: the splits' maxima and sums, and for many rows q in operand order.
+// Workspace: the splits' maxima and sums, and for many rows q in operand order and the parts' sums.
 namespace {
 int64_t stat_bytes(int64_t splits, const if4_kv_attention_args& a) {
     return (splits * a.total_q * a.heads * 8 + 15) & ~(int64_t)15;
@@ -885,12 +930,12 @@ int64_t row_bytes(const if4_kv_cache& c, const if4_kv_attention_args& a) {
 
 int64_t kv_weights_workspace(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     const Plan p = plan_of(c, a);
-    return stat_bytes(p.splits, a) + (p.few ? 0 : row_bytes(c, a));
+    return stat_bytes(p.splits, a) + (p.few ? 0 : row_bytes(c, a) + part_bytes(p, c, a));
 }
 
-// (no call has more splits, nor rows in more tiles)
+// (no call has more splits, nor rows in more tiles, nor more parts)
 int64_t kv_weights_workspace_most(const if4_kv_cache& c, const if4_kv_attention_args& a) {
-    return stat_bytes(kMostSplits, a) + row_bytes(c, a);
+    return stat_bytes(kMostSplits, a) + row_bytes(c, a) + kMostPartBytes;
 }
 
 hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args& a,
@@ -912,6 +957,9 @@ hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args&
     p.row_tiles = row_tiles(c, a);
     p.rows_q = reinterpret_cast<half8*>(reinterpret_cast<uint8_t*>(workspace) + stat_bytes(plan.splits, a));
     p.row_factor = reinterpret_cast<float*>(p.rows_q + p.row_tiles * c.kv_heads * 32 * c.head_dim / 8);
+    p.part_sums = p.row_factor + p.row_tiles * c.kv_heads * 32;
+    p.key_blocks = (int)plan.key_blocks;
+    p.parts = (int)plan.parts;
     p.total_q = (int)a.total_q;
     p.max_q = (int)a.max_q;
     p.pages = (int)c.pages;
