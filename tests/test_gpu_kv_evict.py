@@ -129,6 +129,19 @@ def test_fewer_sums_than_tokens(kvc, ev):
     run(kvc, ev, [150, 40], [2, 40], 4, 2, 64, 16, 7, width=1)
 
 
+PARTED = [  # so many rows, and so few blocks of keys, that a block's rows are parted
+    ([300, 40], [300, 7], 16, 2, 128, 16), ([700], [200], 8, 1, 64, 32), ([520, 300], [150, 300], 8, 2, 256, 64),
+    ([530], [66], 8, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("kw", [{}, dict(window=20, sinks=3), dict(window=200), dict(causal=False), dict(max_q=70),
+                                dict(width=130), dict(max_len=0), dict(max_len=257), dict(max_len=1 << 20)],
+                         ids=lambda kw: "-".join("%s_%s" % i for i in kw.items()) or "plain")
+@pytest.mark.parametrize("lens,chunks,heads,kv,dim,page", PARTED)
+def test_parted_rows(kvc, ev, lens, chunks, heads, kv, dim, page, kw):
+    run(kvc, ev, lens, chunks, heads, kv, dim, page, 14, **kw)
+
+
 def test_weights_of_a_row_sum_to_one(kvc, ev):
     b, got = run(kvc, ev, [3000, 1500], [40, 1], 8, 2, 128, 64, 8)
     mass = torch.zeros(2, 2, 3000, device="cuda")
@@ -362,15 +375,16 @@ def test_other_stream_and_graph(kvc, ev):
         assert torch.equal(out, want) and torch.equal(kept, ev.select(want, args[3], 50, recent=5))
 
 
-def test_many_rows_and_long_sums_in_a_graph(kvc, ev):
+@pytest.mark.parametrize("heads", [8, 32])  # rows of 32 are parted
+def test_many_rows_and_long_sums_in_a_graph(kvc, ev, heads):
     # the passes of many rows and the segments of long sums, replayed beside eager calls
-    b = Batch(kvc, [400, 90], [70, 90], 8, 2, 128, 16, 19)
+    b = Batch(kvc, [400, 90], [70, 90], heads, 2, 128, 16, 19)
     q = b.q.cuda()
     args = (b.cache, *b.device())
     kw = dict(max_q=90, max_len=400, k_exp=b.exps["k_exp"])
     long = torch.rand(2, 2, 30000, device="cuda")
     n32 = torch.tensor([30000, 17000], dtype=torch.int32, device="cuda")
-    work = torch.empty(ev.workspace_bytes(b.cache, total_q=160, heads=8, batch=2, max_q=90, max_len=400), dtype=torch.uint8,
+    work = torch.empty(ev.workspace_bytes(b.cache, total_q=160, heads=heads, batch=2, max_q=90, max_len=400), dtype=torch.uint8,
                        device="cuda")
     space = torch.empty(ev.select_workspace_bytes(long, 2, 5000), dtype=torch.uint8, device="cuda")
     out = torch.zeros(2, 2, 400, device="cuda")
