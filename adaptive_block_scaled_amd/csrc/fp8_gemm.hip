@@ -333,8 +333,8 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
     // lane: column lane % 32 of a block, rows 8 (r / 4) + 4 (lane / 32) + r % 4.  The
     // stores go through a buffer resource over the tile's rows that exist: one
     // vector offset per lane, and a store past M is dropped.  C of the largest tiles is more
-    // than the caches hold, and goes past them (non-temporal).
-    constexpr int kStorePolicy = BM == 256 ? 2 : 0;
+    // than the caches hold, and goes past them (non-temporal) where its rows are whole lines (5000 x
+    // 5000 x 512 58 us past them, 43 through them; 8192 x 28672 x 8192 1470, 1495).
     constexpr int kSize = kBf16 ? 2 : 4;
     if ((uint64_t)ldc * (kSize * BM) < (1ull << 31)) {
         const uint32_t ld = (uint32_t)ldc * kSize;
@@ -342,24 +342,31 @@ tile_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_s
             reinterpret_cast<uint8_t*>(c) + (m0 * ldc + n0) * kSize, 0, (int)((uint32_t)a_rows * ld),
             kRawBufferFlags);
         const uint32_t vo = (uint32_t)(lane & 31) * kSize + (uint32_t)(4 * (lane >> 5)) * ld;
+        const auto store = [&](auto policy) {
+            constexpr int kPolicy = decltype(policy)::value;
 #pragma unroll
-        for (int j = 0; j < TN; j++) {
-            const int col = wn * WN + 32 * j;
-            if (col + (lane & 31) >= w_rows) continue;
+            for (int j = 0; j < TN; j++) {
+                const int col = wn * WN + 32 * j;
+                if (col + (lane & 31) >= w_rows) continue;
 #pragma unroll
-            for (int i = 0; i < TM; i++)
+                for (int i = 0; i < TM; i++)
 #pragma unroll
-                for (int r = 0; r < 16; r++) {
-                    const uint32_t so = (uint32_t)(wm * WM + 32 * i + 8 * (r >> 2) + (r & 3)) * ld +
-                                        col * kSize;
-                    if constexpr (kBf16)
-                        __builtin_amdgcn_raw_buffer_store_b16(
-                            __builtin_bit_cast(short, (__bf16)acc[i][j][r]), rc, (int)vo, (int)so, kStorePolicy);
-                    else
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), rc,
-                                                              (int)vo, (int)so, kStorePolicy);
-                }
-        }
+                    for (int r = 0; r < 16; r++) {
+                        const uint32_t so = (uint32_t)(wm * WM + 32 * i + 8 * (r >> 2) + (r & 3)) * ld +
+                                            col * kSize;
+                        if constexpr (kBf16)
+                            __builtin_amdgcn_raw_buffer_store_b16(
+                                __builtin_bit_cast(short, (__bf16)acc[i][j][r]), rc, (int)vo, (int)so, kPolicy);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), rc,
+                                                                  (int)vo, (int)so, kPolicy);
+                    }
+            }
+        };
+        if (BM == 256 && ((reinterpret_cast<uintptr_t>(c) | ld) & 127) == 0)
+            store(std::integral_constant<int, 2>{});
+        else
+            store(std::integral_constant<int, 0>{});
         return;
     }
 #pragma unroll
@@ -531,23 +538,40 @@ struct Plan {
     int splits;
 };
 
-// The largest tile whose tiles fill the CUs (128: half of them, for what two parts of K then
+// Tiles whose workgroups fill the CUs (128: half of them, for what two parts of K then
 // bring), and few_kernel for few rows.  In us, results in bf16, W from memory:
 //   few_kernel and tiles of 64:  1 x 6144 x 4096  8.4, 10.7;  4  9.0, 10.8;  16  10.9, 11.2;
 //                                16 x 28672 x 8192  72, 53 (W's tiles fill the CUs)
 //   64 and 128:   256 x 6144 x 4096  24, 27;  512  38, 36;  1024 x 4096 x 4096  35, 27
 //   128 and 256:  2048 x 4096 x 4096  44, 100;  4096 x 4096 x 4096  82, 68
+// Where tiles of 256 fill the CUs too, an estimate of the time decides: rounds of 256 of
+// them, or of 512 of the smaller, times steps and what a tile has besides, its results above
+// all (more where rows of C are no whole lines), from fits to measured times.  128 and 256 in
+// bf16 and fp32:  4096 x 5004 x 2048  66, 77 and 93, 121;  1929 x 25702 x 2320  199, 201 and 261,
+// 304;  8192 x 8192 x 1024  118, 89 and 151, 146;  1024 x 28672 x 8192  286, 216 and 393, 375.
 // K is parted where tiles leave CUs free, so that there are up to two workgroups on each, of 8
 // steps at least; parted and whole:  64 x 6144 x 4096  16.0, 22.8;  300 x 1024 x 16384  26,
 // 78;  512 x 6144 x 4096  36, 34 (its results are many for what is gained).
 constexpr int kCus = 256;
 
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
+bool wide_tiles(int64_t M, int64_t N, int64_t steps, bool bf16, bool whole_lines) {
+    const int64_t wide = ((M + 255) / 256) * ((N + 255) / 256), narrow = ((M + 127) / 128) * ((N + 127) / 128);
+    if (wide < kCus) return false;
+    // ns of a step, and of a tile's start and end
+    const int64_t a = bf16 ? 1600 : 3000, b = bf16 ? 1100 : 1710;
+    const int64_t ea = (bf16 ? 9000 : 12000) + (whole_lines ? 0 : 8000), eb = bf16 ? 5600 : 5200;
+    return (wide + kCus - 1) / kCus * (a * steps + ea) <= (narrow + 2 * kCus - 1) / (2 * kCus) * (b * steps + eb);
+}
+
+// (results' type and lines choose between tiles that both leave K whole: no workspace depends
+// on them)
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool bf16, bool whole_lines) {
     const auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
     if (M <= 4 || (M <= 16 && tiles(64) < kCus)) return {0, 1};
     Plan p;
-    p.tile = M <= 64 ? 64 : tiles(256) >= kCus ? 256 : 2 * tiles(128) >= kCus ? 128 : 64;
-    const int64_t steps = (K + BK - 1) / BK, count = tiles(p.tile);
+    const int64_t steps = (K + BK - 1) / BK;
+    p.tile = M <= 64 || 2 * tiles(128) < kCus ? 64 : wide_tiles(M, N, steps, bf16, whole_lines) ? 256 : 128;
+    const int64_t count = tiles(p.tile);
     int64_t splits = count >= kCus ? 1 : 2 * kCus / count;
     splits = splits < steps / (2 * kWindow) ? splits : steps / (2 * kWindow);
     p.splits = (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
@@ -576,9 +600,14 @@ hipError_t launch_tile(const Fp8Gemm& g, int splits, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Whether rows of C are whole lines of the caches.
+bool whole_lines(const Fp8Gemm& g) {
+    return ((reinterpret_cast<uintptr_t>(g.c) | (uintptr_t)(g.ldc * (g.c_bf16 ? 2 : 4))) & 127) == 0;
+}
+
 template <bool kBf16, bool kBytes>
 hipError_t launch_of(const Fp8Gemm& g, hipStream_t stream) {
-    const Plan p = plan_of(g.M, g.N, g.K);
+    const Plan p = plan_of(g.M, g.N, g.K, kBf16, whole_lines(g));
     if (p.tile == 0) return launch_few<kBf16, kBytes>(g, stream);
     if (kBytes || p.tile == 64) return launch_tile<64, 64, 2, 2, 4, kBf16, kBytes>(g, p.splits, stream);
     if constexpr (!kBytes) {
@@ -591,7 +620,7 @@ hipError_t launch_of(const Fp8Gemm& g, hipStream_t stream) {
 }  // namespace
 
 int64_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
-    const Plan p = plan_of(M, N, K);
+    const Plan p = plan_of(M, N, K, true, true);
     return p.splits > 1 ? p.splits * M * N * 4 : 0;
 }
 

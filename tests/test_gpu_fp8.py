@@ -123,6 +123,24 @@ def test_gemm_of_many_tiles(fp8):
     bounded(*product(fp8, 4100, 4300, 784, False, F32))
 
 
+@pytest.mark.parametrize("m,n,k,square,dtype", [(3970, 4090, 1296, True, BF16), (3970, 4090, 2976, False, F32),
+                                                (4096, 4096, 272, False, F32), (2100, 4100, 400, True, BF16)])
+def test_gemm_of_large_tiles(fp8, m, n, k, square, dtype):
+    bounded(*product(fp8, m, n, k, square, dtype))
+
+
+def test_rows_of_whole_lines_and_their_neighbours(fp8):
+    # the largest tiles' stores, with columns of the buffer behind the product's last
+    qa, qw = fp8.quantize(spread((3970, 1296), 1, BF16).cuda()), fp8.quantize(spread((4090, 1296), 2, BF16, 0.1).cuda(), True)
+    want = fp8.gemm(*qa, *qw)
+    for dtype in (BF16, F32):
+        buffer = torch.full((3971, 4160), -3.0, dtype=dtype, device="cuda")
+        fp8.gemm(*qa, *qw, dtype=dtype, out=buffer[:3970, :4090])
+        assert bool((buffer[3970:] == -3).all()) and bool((buffer[:, 4090:] == -3).all())
+        if dtype is BF16:
+            assert torch.equal(buffer[:3970, :4090], want)
+
+
 def test_gemm_exact_with_small_whole_numbers(fp8):
     # sums of whole numbers below 2^24 have one value whatever the order: layouts and blocks
     g = np.random.default_rng(3)
