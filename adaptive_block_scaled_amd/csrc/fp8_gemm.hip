@@ -557,10 +557,11 @@ constexpr int kCus = 256;
 bool wide_tiles(int64_t M, int64_t N, int64_t steps, bool bf16, bool whole_lines) {
     const int64_t wide = ((M + 255) / 256) * ((N + 255) / 256), narrow = ((M + 127) / 128) * ((N + 127) / 128);
     if (wide < kCus) return false;
-    // ns of a step, and of a tile's start and end
-    const int64_t a = bf16 ? 1600 : 3000, b = bf16 ? 1100 : 1710;
-    const int64_t ea = (bf16 ? 9000 : 12000) + (whole_lines ? 0 : 8000), eb = bf16 ? 5600 : 5200;
-    return (wide + kCus - 1) / kCus * (a * steps + ea) <= (narrow + 2 * kCus - 1) / (2 * kCus) * (b * steps + eb);
+    // us of a step, and of a tile's start and end (no sizes overflow)
+    const double a = bf16 ? 1.6 : 3.0, b = bf16 ? 1.1 : 1.71;
+    const double ea = (bf16 ? 9.0 : 12.0) + (whole_lines ? 0.0 : 8.0), eb = bf16 ? 5.6 : 5.2;
+    return (double)((wide + kCus - 1) / kCus) * (a * (double)steps + ea) <=
+           (double)((narrow + 2 * kCus - 1) / (2 * kCus)) * (b * (double)steps + eb);
 }
 
 // (results' type and lines choose between tiles that both leave K whole: no workspace depends

@@ -17,8 +17,9 @@
 // Few rows (8 of each kv head; 64 sequences of 7600 tokens, 282 MB of K): 67 us and 82, 4.2
 // and 3.6 TB/s (the second reads and writes 31 MB of sums too), each pass bound by the decoding
 // of 72 bytes a key beside their loads.  Many rows (16384 of each of 8 kv heads over 16384
-// keys, heads of 128): 555 us and 605, about 600 cycles of a SIMD for a block of 32 x 32 scores, whose matrix products take 256, exponentials
-// 256 and other operations 200 that partly run beside the products; two waves share a SIMD.
+// keys, heads of 128): 555 us and 605, about 600 cycles of a SIMD for a block of 32 x 32
+// scores, whose matrix products take 256, exponentials 256 and other operations 200 that
+// partly run beside the products; two waves share a SIMD.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -78,6 +78,7 @@ def test_workspace(fp8):
             assert fp8.lib.if4_fp8_gemm(*args, None, need, None) == NULL
             assert fp8.lib.if4_fp8_gemm(*args, FAKE, need - 1, None) == SHAPE
             assert fp8.lib.if4_fp8_gemm(*args, FAKE + 8, need, None) == ALIGN
+    assert f(1 << 31, 1 << 31, 1 << 22) == 0 and f(1 << 31, 1, 1 << 22) >= 0  # the largest sizes
 
 
 def test_binding_needs_gpu_tensors(fp8):
