@@ -209,10 +209,11 @@ __device__ __forceinline__ f32x16 scores(const half8 (&k)[D / 16], const half8 (
     return x;
 }
 
-// Whether rows at positions lo .. hi all see keys first .. first + 31, and whether any of
-// them may see any.
-__device__ __forceinline__ bool all_seen(const Args& p, int len, int lo, int hi, int first) {
-    const int end = first + kUnit - 1;
+// Whether rows at positions lo .. hi all see the keys of `tiles` tiles from key `first` on
+// (all of them in the window or all of them first tokens: between these two lie hidden keys),
+// and whether any of them may see any of keys first .. first + 31.
+__device__ __forceinline__ bool all_seen(const Args& p, int len, int lo, int hi, int first, int tiles = 1) {
+    const int end = first + tiles * kUnit - 1;
     return end < len && (!p.causal || end <= lo) && (!p.window || first > hi - p.window || end < p.sinks);
 }
 __device__ __forceinline__ bool any_seen(const Args& p, int len, int lo, int hi, int first) {
@@ -617,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) stats_kernel(const
         lds_barrier();
         const int first = tile(t) * kUnit, last = tile(t + kWaves - 1) * kUnit;
         const auto key = [&](int w, int i) { return keys[buffer][w][i][lane]; };
-        if (t + kWaves <= to && last - first == (kWaves - 1) * kUnit && all_seen(p, s.len, pos_lo, pos_hi, first) &&
-            all_seen(p, s.len, pos_lo, pos_hi, last)) {
+        if (t + kWaves <= to && last - first == (kWaves - 1) * kUnit &&
+            all_seen(p, s.len, pos_lo, pos_hi, first, kWaves)) {
             half8 k[2][D / 16];
             in_turn<kWaves, kTiles, D / 16>(
                 [&](auto w) {
@@ -756,8 +757,7 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
             };
             const auto position = [&](int r) { return s.pos0 + (int)p.group.into(r < rows ? r : rows - 1); };
             const int pos_lo = position(32 * t), pos_hi = position(32 * (t + kRowTiles) - 1);
-            if (all_seen(p, s.len, pos_lo, pos_hi, first) &&
-                all_seen(p, s.len, pos_lo, pos_hi, first + (kTiles - 1) * kUnit)) {
+            if (all_seen(p, s.len, pos_lo, pos_hi, first, kTiles)) {
                 half8 q[2][D / 16];
                 float f[2], log[2];
                 in_turn<kRowTiles, kTiles, D / 16>(

@@ -142,6 +142,20 @@ def test_parted_rows(kvc, ev, lens, chunks, heads, kv, dim, page, kw):
     run(kvc, ev, lens, chunks, heads, kv, dim, page, 14, **kw)
 
 
+NEXT_TO_SINKS = [  # lens, chunks, heads, kv_heads, windows and first tokens
+    ([300], [300], 4, 2, [(64, 32), (64, 64), (128, 48), (128, 130), (200, 32), (200, 48), (200, 64)]),
+    ([171], [171], 8, 1, [(100, 64), (40, 128)]), ([700], [150], 2, 1, [(512, 64), (512, 130), (600, 40)]),
+    ([330, 700, 90], [330, 100, 20], 4, 2, [(250, 64), (600, 48)])]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,chunks,heads,kv,window,sinks", [(*c[:4], *w) for c in NEXT_TO_SINKS for w in c[4]])
+def test_windows_that_leave_the_first_tokens(kvc, ev, lens, chunks, heads, kv, dim, window, sinks):
+    # rows whose window begins a little behind the first tokens: between the two lie hidden keys,
+    # in tiles whose neighbours on both sides are seen whole
+    run(kvc, ev, lens, chunks, heads, kv, dim, 16, 21, window=window, sinks=sinks)
+
+
 def test_weights_of_a_row_sum_to_one(kvc, ev):
     b, got = run(kvc, ev, [3000, 1500], [40, 1], 8, 2, 128, 64, 8)
     mass = torch.zeros(2, 2, 3000, device="cuda")
