@@ -28,7 +28,10 @@ bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
 int elem_size(int dtype) { return dtype == IF4_F32 ? 4 : 2; }
 
-int hip_status(hipError_t e) { return e == hipSuccess ? IF4_OK : IF4_ERR_HIP; }
+// (an invalid configuration: more workgroups than one launch holds, see launch_limit.h)
+int hip_status(hipError_t e) {
+    return e == hipSuccess ? IF4_OK : e == hipErrorInvalidConfiguration ? IF4_ERR_SHAPE : IF4_ERR_HIP;
+}
 
 int check_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols,
                    int64_t ld_x, const uint8_t* codes, const uint8_t* scales,
@@ -205,7 +208,7 @@ const char* if4_status_string(int status) {
     switch (status) {
         case IF4_OK: return "ok";
         case IF4_ERR_NULL: return "null pointer";
-        case IF4_ERR_SHAPE: return "bad shape (negative size, cols/K not a multiple of 16, or leading dimension too small)";
+        case IF4_ERR_SHAPE: return "bad shape (negative size, cols/K not a multiple of 16, or leading dimension too small, or more than one launch holds)";
         case IF4_ERR_ALIGN: return "misaligned pointer or leading dimension";
         case IF4_ERR_DTYPE: return "unknown dtype or mode";
         case IF4_ERR_RANGE: return "scale exponent outside [-64, 64]";

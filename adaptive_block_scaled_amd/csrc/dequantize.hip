@@ -15,6 +15,7 @@
 
 #include "if4_decode.h"
 #include "if4_internal.h"
+#include "launch_limit.h"
 #include "xcd_order.h"
 
 namespace if4 {
@@ -95,7 +96,7 @@ hipError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_
     const int64_t gpr = cols / 16;
     const int64_t ngroups = rows * gpr;
     const int64_t blocks = (ngroups + kThreads - 1) / kThreads;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(blocks, kThreads)) return hipErrorInvalidConfiguration;
     if (bf16)
         launch<true>(codes, scales, rows, gpr, y, ld_y, pow2f(scale_exp), (unsigned)blocks, stream);
     else

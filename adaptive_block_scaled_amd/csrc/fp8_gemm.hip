@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "fp8_internal.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -497,7 +498,9 @@ few_kernel(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_sc
 
 template <bool kBf16, bool kBytes>
 hipError_t launch_few(const Fp8Gemm& g, hipStream_t stream) {
-    hipLaunchKernelGGL((few_kernel<kBf16, kBytes>), dim3((unsigned)((g.N + 15) / 16)), dim3(kFewThreads), 0, stream,
+    const int64_t groups = (g.N + 15) / 16;
+    if (!launchable(groups, kFewThreads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((few_kernel<kBf16, kBytes>), dim3((unsigned)groups), dim3(kFewThreads), 0, stream,
                        g.a_codes, g.a_scales, g.w_codes, g.w_scales, g.w_square, g.M, g.N, g.K, g.c, g.ldc);
     return hipGetLastError();
 }
@@ -584,7 +587,7 @@ hipError_t launch_tile(const Fp8Gemm& g, int splits, hipStream_t stream) {
     constexpr int kSmem = kStages * (BM + BN) * BK;
     const auto kernel = tile_kernel<BM, BN, kWavesM, kWavesN, kStages, kBf16, kBytes>;
     const int64_t tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN;
-    if (tiles_m * tiles_n * splits > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(tiles_m * tiles_n * splits, 64 * kWavesM * kWavesN)) return hipErrorInvalidConfiguration;
     // dynamic LDS above 64 KB must be allowed per kernel (idempotent, any device)
     const hipError_t err =
         hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);

@@ -10,6 +10,7 @@
 
 #include "fp8_internal.h"
 #include "kv_internal.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -232,6 +233,8 @@ hipError_t launch_fp8_quantize(const void* x, int bf16, int64_t rows, int64_t co
     const int64_t across = blocks_of(cols);
     const int64_t count = (square ? blocks_of(rows) : rows) * across;
     const Divisor by(across);
+    if (!launchable(square ? count : (count + kThreads / 8 - 1) / (kThreads / 8), kThreads))
+        return hipErrorInvalidConfiguration;
     if (square) {
         const auto k = bf16 ? squares_kernel<true> : squares_kernel<false>;
         hipLaunchKernelGGL(k, dim3((unsigned)count), dim3(kThreads), 0, stream, x, rows, cols,
@@ -249,6 +252,7 @@ hipError_t launch_fp8_quantize_t(const void* x, int bf16, int64_t rows, int64_t 
                                  int64_t ld_x, int square, uint8_t* codes, uint8_t* scales,
                                  hipStream_t stream) {
     const int64_t count = blocks_of(rows) * blocks_of(cols);
+    if (!launchable(count, kThreads)) return hipErrorInvalidConfiguration;
     const Divisor by(blocks_of(rows));
     const auto k = bf16 ? (square ? transposed_kernel<true, true> : transposed_kernel<true, false>)
                         : (square ? transposed_kernel<false, true> : transposed_kernel<false, false>);

@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "if4_internal.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -725,7 +726,7 @@ hipError_t launch_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t 
         return hipGetLastError();
     }
     const int64_t tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
-    if (tiles_m * tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(tiles_m * tiles_n, kThreads)) return hipErrorInvalidConfiguration;
     // C = sum * 2^(a_exp + w_exp + 18): each decoded operand carries 2^-9.
     // The exponent lies in [-110, 146], so it is applied per output in the
     // kernel (ldexp), never as one fp32 factor, which would overflow.

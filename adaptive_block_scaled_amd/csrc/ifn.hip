@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "if4_internal.h"
+#include "launch_limit.h"
 #include "xcd_order.h"
 
 namespace if4 {
@@ -800,7 +801,7 @@ hipError_t launch_q(const void* x, int64_t rows, int64_t cols, int64_t ld_x, uin
     const int64_t gpr = cols / 16;
     if constexpr (kBits == 6 && kBf16) {
         const int64_t blocks = (rows * gpr + 2 * kQThreads - 1) / (2 * kQThreads);
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!launchable(blocks, kQThreads)) return hipErrorInvalidConfiguration;
         const uint16_t* xb = reinterpret_cast<const uint16_t*>(x);
         if (ld_x == cols)
             hipLaunchKernelGGL((quantize_if6_bf16_kernel<kMode, true>), dim3((unsigned)blocks),
@@ -813,7 +814,7 @@ hipError_t launch_q(const void* x, int64_t rows, int64_t cols, int64_t ld_x, uin
         return hipGetLastError();
     }
     const int64_t blocks = (rows * gpr + kQThreads - 1) / kQThreads;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(blocks, kQThreads)) return hipErrorInvalidConfiguration;
     if (ld_x == cols)
         hipLaunchKernelGGL((quantize_ifn_kernel<kBits, kMode, kBf16, true>), dim3((unsigned)blocks),
                            dim3(kQThreads), 0, stream, x, rows, gpr, ld_x, codes, scales,
@@ -848,7 +849,7 @@ hipError_t dispatch_dq(const uint8_t* codes, const uint8_t* scales, int64_t rows
     const bool contig = ld_y == cols;
     if constexpr (kBits == 3) {  // registers only
         const int64_t blocks = (rows * gpr + kD3Threads - 1) / kD3Threads;
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!launchable(blocks, kD3Threads)) return hipErrorInvalidConfiguration;
 #define IF4_DQ3(B, C)                                                                          \
         hipLaunchKernelGGL((dequantize_if3_kernel<B, C>), dim3((unsigned)blocks),              \
                            dim3(kD3Threads), 0, stream, codes, scales, rows, gpr, y, ld_y,     \
@@ -863,7 +864,7 @@ hipError_t dispatch_dq(const uint8_t* codes, const uint8_t* scales, int64_t rows
 #undef IF4_DQ3
     } else {  // per-workgroup LDS tables
         const int64_t blocks = (rows * gpr + kThreads - 1) / kThreads;
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!launchable(blocks, kThreads)) return hipErrorInvalidConfiguration;
 #define IF4_DQN(B, C)                                                                          \
         hipLaunchKernelGGL((dequantize_ifn_kernel<kBits, B, C>), dim3((unsigned)blocks),       \
                            dim3(kThreads), 0, stream, codes, scales, rows, gpr, y, ld_y,       \

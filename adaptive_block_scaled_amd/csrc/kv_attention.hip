@@ -29,6 +29,7 @@
 #include "if4_internal.h"
 #include "kv_internal.h"
 #include "kv_operand.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -2277,18 +2278,20 @@ Launches launches_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
 template <int D>
 hipError_t launch(void (*kernel)(Args), int threads, int lds, int64_t grid, const Args& p,
                   hipStream_t stream) {
+    const int64_t rows = p.rows_all;
+    const bool few = p.splits <= kFewSplits;
+    if (!launchable(grid, threads) ||
+        (p.splits > 1 && !launchable(few ? (rows + kWaves - 1) / kWaves : rows, kThreads)))
+        return hipErrorInvalidConfiguration;
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kernel,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t rows = p.rows_all;
-    if (rows > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (p.splits <= kFewSplits)
+    if (few)
         hipLaunchKernelGGL((join_few_kernel<D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
                            dim3(kThreads), 0, stream, p);
     else
@@ -2298,7 +2301,7 @@ hipError_t launch(void (*kernel)(Args), int threads, int lds, int64_t grid, cons
 
 template <int D>
 hipError_t dispatch(const Args& p, const Plan& pl, hipStream_t stream) {
-    if (pl.items > INT32_MAX) return hipErrorInvalidValue;
+    if (pl.items > INT32_MAX) return hipErrorInvalidConfiguration;
     const int64_t grid = pl.items * pl.splits;
     if constexpr (D <= 128) {
         if (pl.kind == Plan::kPrompt)

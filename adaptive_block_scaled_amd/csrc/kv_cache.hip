@@ -12,6 +12,7 @@
 #include "if4_encode.h"
 #include "if4_internal.h"
 #include "kv_internal.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -219,7 +220,7 @@ hipError_t append(const if4_kv_cache& c, const AppendArgs& p, int bf16, int mode
                   hipStream_t stream) {
     constexpr int per = kThreads / (D / 16);
     const int64_t runs = (p.tokens + per - 1) / per;
-    if (runs > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(runs, kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)runs, (unsigned)c.kv_heads, 2);
     if (bf16)
         append_mode<D, true>(p, mode, grid, stream);
@@ -232,7 +233,7 @@ template <int D>
 hipError_t read(const if4_kv_cache& c, const ReadArgs& p, int bf16, hipStream_t stream) {
     constexpr int per = kThreads / (D / 16);
     const int64_t runs = (p.tokens + per - 1) / per;
-    if (runs > 0x7FFFFFFF / c.kv_heads) return hipErrorInvalidValue;
+    if (!launchable(runs * c.kv_heads, kThreads)) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(runs * c.kv_heads), 1, 2);
     if (bf16)
         hipLaunchKernelGGL((read_kernel<D, true>), grid, dim3(kThreads), 0, stream, p);

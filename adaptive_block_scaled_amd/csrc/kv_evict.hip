@@ -5,6 +5,7 @@
 
 #include "kv_evict_internal.h"
 #include "kv_internal.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -439,6 +440,7 @@ hipError_t launch_kv_select(const if4_kv_mass& m, const int32_t* seq_lens, int64
     const SelectArgs s = {m, seq_lens, kept, (int)kv_heads, (int)keep, (int)recent, (int)sinks};
     const int64_t rows = batch * kv_heads, segment = segment_of(m, rows, keep);
     if (segment == 0) {
+        if (!launchable(rows, kThreads)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL(select_kernel, dim3((unsigned)rows), dim3(kThreads), 0, stream, s);
         return hipGetLastError();
     }
@@ -464,13 +466,20 @@ hipError_t launch_kv_compact(const if4_kv_cache& c, const int32_t* page_table,
                              int64_t table_stride, const int32_t* kept, int64_t batch,
                              int64_t keep, const int32_t* new_table, int64_t new_stride,
                              hipStream_t stream) {
-    const int64_t tiles = (keep + 15) / 16;
-    if (tiles > 0x7FFFFFFF / (batch * c.kv_heads)) return hipErrorInvalidValue;
-    const CompactArgs p = {c, page_table, kept, new_table, table_stride, new_stride, keep, (int)tiles, Divisor(c.page_size / 16)};
-    const dim3 grid((unsigned)(batch * c.kv_heads * tiles));
+    const int64_t tiles = (keep + 15) / 16, each = c.kv_heads * tiles;  // workgroups of a sequence
+    if (!launchable(each, kCopyThreads)) return hipErrorInvalidConfiguration;
     const auto k = c.head_dim == 64 ? compact_kernel<64> : c.head_dim == 128 ? compact_kernel<128> : compact_kernel<256>;
-    hipLaunchKernelGGL(k, grid, dim3(kCopyThreads), 0, stream, p);
-    return hipGetLastError();
+    // as many sequences at once as a launch holds
+    const int64_t most = most_groups(kCopyThreads) / each;
+    for (int64_t b = 0; b < batch; b += most) {
+        const CompactArgs p = {c, page_table + b * table_stride, kept + b * c.kv_heads * keep, new_table + b * new_stride,
+                               table_stride, new_stride, keep, (int)tiles, Divisor(c.page_size / 16)};
+        const dim3 grid((unsigned)((batch - b < most ? batch - b : most) * each));
+        hipLaunchKernelGGL(k, grid, dim3(kCopyThreads), 0, stream, p);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace if4

@@ -28,6 +28,7 @@
 #include "kv_evict_internal.h"
 #include "kv_internal.h"
 #include "kv_operand.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -860,8 +861,8 @@ Plan plan_of(const if4_kv_cache& c, const if4_kv_attention_args& a) {
     p.key_tiles = c.head_dim == 256 ? 1 : 2;
     const int64_t keys = kWaves * p.key_tiles;
     p.key_blocks = (units + keys - 1) / keys;
-    const int64_t limit = 0x7FFFFFFF / pairs;
-    p.key_blocks = p.key_blocks < limit ? p.key_blocks : limit;
+    const int64_t limit = most_groups(kThreads) / pairs;  // (the kernel goes on to what lies past them)
+    p.key_blocks = p.key_blocks < limit ? p.key_blocks : limit > 0 ? limit : 1;
     // (a part has 8 tiles of rows at least)
     const int64_t blocks = pairs * p.key_blocks, tiles = (rows + 31) / 32;
     p.parts = p.few || blocks >= kFull / 2 ? 1 : (kFull + blocks - 1) / blocks;
@@ -978,7 +979,7 @@ hipError_t launch_kv_weights(const if4_kv_cache& c, const if4_kv_attention_args&
     p.q_scale = a.scale * 1.4426950408889634f / 7.0f;
     p.k_exp = c.k_exp + 12;
     const int64_t stat_groups = pairs * plan.row_blocks * plan.splits;
-    if (stat_groups > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(stat_groups, kThreads)) return hipErrorInvalidConfiguration;
     const unsigned groups = (unsigned)stat_groups, columns = (unsigned)(pairs * plan.key_blocks);
     return c.head_dim == 64    ? launch<64>(p, plan, groups, columns, stream)
            : c.head_dim == 128 ? launch<128>(p, plan, groups, columns, stream)

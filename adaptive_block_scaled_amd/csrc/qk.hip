@@ -12,6 +12,7 @@
 
 #include <type_traits>
 
+#include "launch_limit.h"
 #include "qk_internal.h"
 
 namespace if4 {
@@ -343,6 +344,7 @@ template <int L, bool kIn, bool kOut, bool kInterleaved>
 hipError_t forward(const if4_qk_args& a, hipStream_t stream) {
     const Args p = make_args(a, L, kOut ? 2 : 4);
     const int64_t groups = (a.tokens * p.chunks + kThreads / 64 - 1) / (kThreads / 64);
+    if (!launchable(groups, kThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((forward_kernel<L, kIn, kOut, kInterleaved>), dim3((unsigned)groups),
                        dim3(kThreads), 0, stream, p);
     return hipGetLastError();

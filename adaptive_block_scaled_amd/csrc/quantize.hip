@@ -24,6 +24,7 @@
 
 #include "if4_encode.h"
 #include "if4_internal.h"
+#include "launch_limit.h"
 
 namespace if4 {
 namespace {
@@ -190,7 +191,7 @@ hipError_t launch(const void* x, int64_t rows, int64_t cols, int64_t ld_x, uint8
     const float pe = pow2f(scale_exp), pn = pow2f(-scale_exp);
     if constexpr (kBf16) {
         const int64_t blocks = (ngroups + kRowThreads * kGPT - 1) / (kRowThreads * kGPT);
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!launchable(blocks, kRowThreads)) return hipErrorInvalidConfiguration;
         const uint16_t* xb = reinterpret_cast<const uint16_t*>(x);
         if (ld_x == cols)
             hipLaunchKernelGGL((quantize_bf16_kernel<kMode, true, kRotate>),
@@ -423,7 +424,7 @@ hipError_t launch_t(const void* x, int64_t rows, int64_t cols, int64_t ld_x, uin
     // interior tiles address with 32-bit offsets)
     if ((uintptr_t)x % 16 == 0 && (ld_x * elem) % 16 == 0 && ld_x * elem < (1 << 24)) {
         const int64_t col_tiles = (cols + kTC - 1) / kTC, row_tiles = (rows + kTR - 1) / kTR;
-        if (col_tiles * row_tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!launchable(col_tiles * row_tiles, kThreads)) return hipErrorInvalidConfiguration;
         const int wide_out =
             rows % kTR == 0 && (uintptr_t)codes % 16 == 0 && (uintptr_t)scales % 8 == 0;
         hipLaunchKernelGGL((quantize_t_tile_kernel<kBf16, kMode>),
@@ -433,7 +434,7 @@ hipError_t launch_t(const void* x, int64_t rows, int64_t cols, int64_t ld_x, uin
     }
     const int64_t col_blocks = (cols + kThreads - 1) / kThreads;
     const int64_t chunks = (rows / 16 + kTChunk - 1) / kTChunk;
-    if (col_blocks * chunks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(col_blocks * chunks, kThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((quantize_t_kernel<kBf16, kMode>), dim3((unsigned)(col_blocks * chunks)),
                        dim3(kThreads), 0, stream, x, rows, cols, ld_x, codes, scales, pe, pn,
                        col_blocks);

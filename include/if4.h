@@ -57,7 +57,8 @@ extern "C" {
 enum {
     IF4_OK = 0,
     IF4_ERR_NULL = 1,  /* a required pointer is NULL                      */
-    IF4_ERR_SHAPE = 2, /* negative size, cols/K not a multiple of 16, ld too small */
+    IF4_ERR_SHAPE = 2, /* negative size, cols/K not a multiple of 16, ld too small,
+                          or more work than one launch holds (2^32 threads) */
     IF4_ERR_ALIGN = 3, /* pointer or leading dimension misaligned         */
     IF4_ERR_DTYPE = 4, /* unknown dtype or mode                           */
     IF4_ERR_RANGE = 5, /* |scale_exp| > 64                                */

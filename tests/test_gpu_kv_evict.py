@@ -337,6 +337,30 @@ def test_compact_skips_what_is_outside(kvc, ev):
     assert all(torch.equal(x, y) for x, y in zip(b.cache, before))
 
 
+def test_compact_of_more_sequences_than_a_launch_holds(kvc, ev):
+    # 2^24 tiles of 16 tokens: workgroups of 256 threads whose number takes more than 32 bits
+    batch, kv, keep, page = 1025, 8, 1 << 15, 1 << 12
+    cache = kvc.empty(4, page, kv, 64)
+    for t in cache:
+        t.copy_(torch.randint(0, 256, t.shape, dtype=torch.uint8, device="cuda"))
+    before = [t.clone() for t in cache]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kept = torch.full((batch, kv, keep), -1, **i32)
+    new = torch.full((batch, keep // page), -1, **i32)
+    for b, page_to in ((0, 1), (batch - 2, 2), (batch - 1, 3)):  # the last 16 places of each, from page 0
+        kept[b, :, -16:] = torch.arange(b % 7, b % 7 + 16, **i32)
+        new[b, -1] = page_to
+    ev.compact(cache, torch.zeros(batch, 1, **i32), kept, new)
+    for b, page_to in ((0, 1), (batch - 2, 2), (batch - 1, 3)):
+        at = slice(b % 7, b % 7 + 16)
+        for i in range(2):  # k
+            assert torch.equal(cache[i][page_to, :, -16:], before[i][0, :, at])
+            assert torch.equal(cache[i][page_to, :, :-16], before[i][page_to, :, :-16])
+        old = torch.cat([before[2][0, :, 0], before[2][0, :, 1]], 2)  # v: tiles of 16 tokens
+        assert torch.equal(cache[2][page_to, :, -1], old[:, :, at])
+        assert torch.equal(cache[2][page_to, :, :-1], before[2][page_to, :, :-1])
+
+
 def test_attention_after_eviction(kvc, ev):
     """The operators in a row: weights, the choice, the move, and attention over what is left,
     against attention over those tokens' values alone."""
