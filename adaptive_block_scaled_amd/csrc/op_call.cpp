@@ -79,8 +79,10 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto bytes = x.options().dtype(at::kByte);
         const at::Tensor codes = at::empty({rows, k}, bytes);
         const at::Tensor scales = at::empty({square ? blocks(rows) : rows, blocks(k)}, bytes);
+        // (one row is none apart from another: its stride has any value)
+        const int64_t ld = x.size(0) > 1 ? x.stride(0) : x.size(1);
         const int st = (t ? fp8_quantize_t : fp8_quantize)(
-            x.data_ptr(), dtype, x.size(0), x.size(1), x.stride(0), square, (uint8_t*)codes.data_ptr(),
+            x.data_ptr(), dtype, x.size(0), x.size(1), ld, square, (uint8_t*)codes.data_ptr(),
             (uint8_t*)scales.data_ptr(), stream_of(x.device().index()));
         if (st != IF4_OK) return PyLong_FromLong(st);
         return pair(codes, scales);

@@ -23,7 +23,7 @@ import ctypes
 import torch
 
 from . import if4
-from .if4 import _check, _dtype_code, _input, _need, lib
+from .if4 import _check, _dtype_code, _input, _ld, _need, lib
 
 try:
     from . import _op_call
@@ -66,7 +66,7 @@ def _quantize(fn, name, x, rows, k, square, out):
         codes, scales = out
         _need(codes, "codes", (rows, k), torch.uint8, x.device)
         _need(scales, "scales", shape, torch.uint8, x.device)
-    st = fn(x.data_ptr(), _dtype_code(x.dtype), *x.shape, x.stride(0), 1 if square else 0,
+    st = fn(x.data_ptr(), _dtype_code(x.dtype), *x.shape, _ld(x), 1 if square else 0,
             codes.data_ptr(), scales.data_ptr(), _raw_stream(x.get_device()))
     _check(name, st)
     return codes, scales
@@ -142,7 +142,7 @@ def gemm(a_codes, a_scales, w_codes, w_scales, dtype=torch.bfloat16, out=None, w
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     st = lib.if4_fp8_gemm(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
                           1 if square else 0, m, n, k, out.data_ptr(), _dtype_code(out.dtype),
-                          out.stride(0), workspace.data_ptr() if need else None, need,
+                          _ld(out), workspace.data_ptr() if need else None, need,
                           _raw_stream(a_codes.get_device()))
     _check("if4_fp8_gemm", st)
     return out

@@ -115,6 +115,12 @@ def _input(x):
         raise ValueError("x must be a 2-D CUDA tensor with unit stride along dim 1")
 
 
+def _ld(t) -> int:
+    """Elements between the rows of a 2-D tensor.  One row is none apart from another, and
+    torch gives its stride any value."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _outputs(out, device, codes_shape, scales_shape):
     if out is None:
         return (torch.empty(codes_shape, dtype=torch.uint8, device=device),
@@ -132,7 +138,7 @@ def quantize(x: torch.Tensor, scale_exp: int = 0, mode: int = MODE_ADAPTIVE, out
     _input(x)
     rows, cols = x.shape
     codes, scales = _outputs(out, x.device, (rows, cols // 2), (rows, cols // GROUP))
-    st = lib.if4_quantize_mode(x.data_ptr(), _dtype_code(x.dtype), rows, cols, x.stride(0),
+    st = lib.if4_quantize_mode(x.data_ptr(), _dtype_code(x.dtype), rows, cols, _ld(x),
                                codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode),
                                _stream(x.device))
     _check("if4_quantize_mode", st)
@@ -146,7 +152,7 @@ def quantize_t(x: torch.Tensor, scale_exp: int = 0, mode: int = MODE_ADAPTIVE, o
     _input(x)
     rows, cols = x.shape
     codes, scales = _outputs(out, x.device, (cols, rows // 2), (cols, rows // GROUP))
-    st = lib.if4_quantize_t(x.data_ptr(), _dtype_code(x.dtype), rows, cols, x.stride(0),
+    st = lib.if4_quantize_t(x.data_ptr(), _dtype_code(x.dtype), rows, cols, _ld(x),
                             codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode),
                             _stream(x.device))
     _check("if4_quantize_t", st)
@@ -162,7 +168,7 @@ def quantize_rht(x: torch.Tensor, sign_mask: int, scale_exp: int = 0, mode: int 
     _input(x)
     rows, cols = x.shape
     codes, scales = _outputs(out, x.device, (rows, cols // 2), (rows, cols // GROUP))
-    st = lib.if4_quantize_rht(x.data_ptr(), _dtype_code(x.dtype), rows, cols, x.stride(0),
+    st = lib.if4_quantize_rht(x.data_ptr(), _dtype_code(x.dtype), rows, cols, _ld(x),
                               int(sign_mask), codes.data_ptr(), scales.data_ptr(),
                               int(scale_exp), int(mode), _stream(x.device))
     _check("if4_quantize_rht", st)
@@ -179,7 +185,7 @@ def quantize_ifn(x: torch.Tensor, bits: int, scale_exp: int = 0, mode: int = MOD
     codes, scales = _outputs(out, x.device, (rows, cols // GROUP * 2 * bits),
                              (rows, cols // GROUP))
     st = lib.if4_quantize_ifn(int(bits), x.data_ptr(), _dtype_code(x.dtype), rows, cols,
-                              x.stride(0), codes.data_ptr(), scales.data_ptr(), int(scale_exp),
+                              _ld(x), codes.data_ptr(), scales.data_ptr(), int(scale_exp),
                               int(mode), _stream(x.device))
     _check("if4_quantize_ifn", st)
     return codes, scales
@@ -199,7 +205,7 @@ def dequantize_ifn(codes: torch.Tensor, scales: torch.Tensor, bits: int, scale_e
         y = out
         _need(y, "out", (rows, cols), y.dtype, codes.device, dense=False)
     st = lib.if4_dequantize_ifn(int(bits), codes.data_ptr(), scales.data_ptr(), rows, cols,
-                                int(scale_exp), y.data_ptr(), _dtype_code(y.dtype), y.stride(0),
+                                int(scale_exp), y.data_ptr(), _dtype_code(y.dtype), _ld(y),
                                 _stream(codes.device))
     _check("if4_dequantize_ifn", st)
     return y
@@ -219,7 +225,7 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, scale_exp: int = 0,
         y = out
         _need(y, "out", (rows, cols), y.dtype, codes.device, dense=False)
     st = lib.if4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, int(scale_exp),
-                            y.data_ptr(), _dtype_code(y.dtype), y.stride(0),
+                            y.data_ptr(), _dtype_code(y.dtype), _ld(y),
                             _stream(codes.device))
     _check("if4_dequantize", st)
     return y
@@ -245,7 +251,7 @@ def gemm(a_codes, a_scales, a_exp, w_codes, w_scales, w_exp, out=None) -> torch.
         c = out
         _need(c, "out", (M, N), torch.float32, dev, dense=False)
     st = lib.if4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), int(a_exp), w_codes.data_ptr(),
-                      w_scales.data_ptr(), int(w_exp), M, N, K, c.data_ptr(), c.stride(0),
+                      w_scales.data_ptr(), int(w_exp), M, N, K, c.data_ptr(), _ld(c),
                       _stream(a_codes.device))
     _check("if4_gemm", st)
     return c

@@ -112,3 +112,22 @@ def test_runs_on_the_callers_stream(if4, operands):
     flat = lambda r: [t for x in r for t in (x if isinstance(x, tuple) else (x,))]
     for g, w in zip(flat(got), flat(want)):
         assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("stride", [0, 1, 7, 1 << 20])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_row_of_any_stride(if4, dtype, stride):
+    # rows are apart by their stride; torch gives that of a single one any value
+    def one_row(t):
+        return torch.as_strided(t, t.shape, (stride, 1))
+    x = torch.randn(1, 96, device="cuda").to(dtype)
+    want = if4.quantize(x)
+    w = if4.quantize(torch.randn(40, 96, device="cuda").to(dtype))
+    for row in (x[0][:, None].T, one_row(x)):
+        for got, ref in ((if4.quantize(row), want), (if4.quantize_rht(row, 5), if4.quantize_rht(x, 5)),
+                         (if4.quantize_ifn(row, 6), if4.quantize_ifn(x, 6)), (if4.quantize_ifn(row, 3), if4.quantize_ifn(x, 3))):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    y, c = torch.zeros(1, 96, dtype=dtype, device="cuda"), torch.zeros(1, 40, device="cuda")
+    if4.dequantize(*want, out=one_row(y))
+    if4.gemm(*want, 0, *w, 0, out=one_row(c))
+    assert torch.equal(y, if4.dequantize(*want, 0, dtype)) and torch.equal(c, if4.gemm(*want, 0, *w, 0))

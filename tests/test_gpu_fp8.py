@@ -279,3 +279,27 @@ def test_refusals(fp8):
             fp8.gemm(*a, *a, **kw)
     with pytest.raises(ValueError, match="codes"):
         fp8.quantize(x, out=(torch.zeros(32, 63, **u8), torch.zeros(32, 1, **u8)))
+
+
+def one_row(v, stride):
+    """v [1, K] with any stride between its rows, as views of vectors have."""
+    return torch.as_strided(v.contiguous(), v.shape, (stride, 1))
+
+
+@pytest.mark.parametrize("stride", [0, 1, 7, 1 << 20])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_row_of_any_stride(fp8, dtype, stride):
+    x = spread((1, 144), 1, dtype)
+    rows = (x[0][:, None].cuda().T, one_row(x.cuda(), stride))
+    codes, scales = torch.empty(1, 144, dtype=torch.uint8, device="cuda"), torch.empty(1, 2, dtype=torch.uint8, device="cuda")
+    qw = fp8.quantize(spread((40, 144), 2, BF16).cuda())
+    want = fp8.gemm(*fp8.quantize(x.cuda()), *qw, dtype=dtype)
+    for row in rows:
+        check(fp8.quantize(row), x, False)
+        check(fp8.quantize(row, True), x, True)
+        check(fp8.quantize(row, out=(codes, scales)), x, False)
+        q = (one_row(codes, stride), scales)  # (what is contiguous whatever its stride)
+        out = torch.zeros(1, 40, dtype=dtype, device="cuda")
+        assert torch.equal(fp8.gemm(*q, *qw, dtype=dtype), want)
+        fp8.gemm(*q, *qw, out=one_row(out, stride))
+        assert torch.equal(out, want)
