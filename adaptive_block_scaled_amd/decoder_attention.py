@@ -193,7 +193,9 @@ class AttentionBlock:
     def evict(self, seqs, keep: int, recent: int = 0, sinks: int = 0):
         """Cut the caches of these sequences to `keep` tokens of each kv head: the first
         `sinks`, the latest `recent`, and those with the largest sums of attention weights
-        since they came.  Sequences that have no more stay as they are."""
+        since they came.  Sequences that have no more stay as they are.  What is kept goes to
+        other pages: there have to be free ones for `keep` tokens of one sequence, else
+        MemoryError and nothing is cut."""
         if not self.weights_of:
             raise ValueError("the block keeps no attention weights (weights_of)")
         seqs = list(seqs)
@@ -202,14 +204,21 @@ class AttentionBlock:
         if keep <= 0 or recent < 0 or sinks < 0 or recent + sinks > keep:
             raise ValueError("keep must be positive, recent and sinks not negative, nor more than keep together")
         long = [s for s in seqs if self.pages.lens[s] > keep]
-        if not long:
-            return
-        table, lens = self.pages.table(long)
-        fresh = self.pages.fresh([keep] * len(long))
-        kept = kv_evict.select(self.mass, lens, keep, recent=recent, sinks=sinks, rows=self._mass_rows(long),
+        # as many at once as the free pages allow, whose old pages, which are no fewer, are
+        # free for the next ones then
+        each = -(-keep // self.pages.size)
+        while long:
+            some = long[:max(1, len(self.pages.free) // each)]
+            self._cut(some, keep, recent, sinks)
+            long = long[len(some):]
+
+    def _cut(self, seqs, keep, recent, sinks):
+        table, lens = self.pages.table(seqs)
+        fresh = self.pages.fresh([keep] * len(seqs))
+        kept = kv_evict.select(self.mass, lens, keep, recent=recent, sinks=sinks, rows=self._mass_rows(seqs),
                                mass_out=self.mass)
         kv_evict.compact(self.cache, table, kept, self.pages.rows(fresh))
-        for s, pages in zip(long, fresh):
+        for s, pages in zip(seqs, fresh):
             self.pages.move(s, pages, keep)
 
     def release(self, seq):

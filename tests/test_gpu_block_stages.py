@@ -105,6 +105,28 @@ def test_eviction_keeps_the_tokens_that_matter():
         assert float((got[s] - want[0]).norm() / want.norm()) < 0.02
 
 
+@pytest.mark.parametrize("free", [4, 5, 8])
+def test_eviction_from_a_full_cache(free):
+    """Free pages for one sequence's kept tokens are enough for any number of sequences, and
+    the outcome is that of an eviction with room for all at once."""
+    from adaptive_block_scaled_amd import decoder_attention as da, kv_cache
+    prompts, keep = [200, 70, 90, 66], 64  # of pages of 16: 4 each are kept
+    roomy, full = block(da, weights_of=400, pages=60), block(da, weights_of=400, pages=60)
+    for b in (roomy, full):
+        da.serve(b, prompts, 0, 64, 256)
+    held = [full.pages.free.pop() for _ in range(len(full.pages.free) - free)]
+    for b in (roomy, full):
+        b.evict(range(4), keep, recent=8, sinks=2)
+    assert full.pages.lens == roomy.pages.lens == {s: 64 for s in range(4)}
+    owned = sum((full.pages.owned[s] for s in range(4)), [])
+    assert sorted(owned + full.pages.free + held) == list(range(60))
+    assert torch.equal(full.mass, roomy.mass)
+    for s in range(4):
+        kv = [kv_cache.read(b.cache, torch.tensor([b.pages.owned[s][j // 16] * 16 + j % 16 for j in range(64)],
+                                                  device="cuda"), **b.exps) for b in (full, roomy)]
+        assert all(torch.equal(x, y) for x, y in zip(*kv))
+
+
 def test_sums_of_released_sequences_are_used_again():
     from adaptive_block_scaled_amd import decoder_attention as da
     b = block(da, weights_of=100, pages=60)
