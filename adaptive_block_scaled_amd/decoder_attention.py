@@ -72,6 +72,10 @@ class Pages:
             raise MemoryError("the cache has too few free pages")
         return [[self.free.pop() for _ in range(n)] for n in need]
 
+    def give_back(self, pages):
+        """What fresh() gave is not used."""
+        self.free += sum(pages, [])[::-1]
+
     def move(self, seq, pages, tokens: int):
         """The sequence lives in these pages from now on, with its first `tokens` places."""
         self.free += self.owned[seq]
@@ -214,10 +218,15 @@ class AttentionBlock:
 
     def _cut(self, seqs, keep, recent, sinks):
         table, lens = self.pages.table(seqs)
+        rows = self._mass_rows(seqs)
         fresh = self.pages.fresh([keep] * len(seqs))
-        kept = kv_evict.select(self.mass, lens, keep, recent=recent, sinks=sinks, rows=self._mass_rows(seqs),
-                               mass_out=self.mass)
-        kv_evict.compact(self.cache, table, kept, self.pages.rows(fresh))
+        try:
+            new_table = self.pages.rows(fresh)
+            kept = kv_evict.select(self.mass, lens, keep, recent=recent, sinks=sinks, rows=rows, mass_out=self.mass)
+        except BaseException:  # (no memory for a result or a workspace: nothing has been launched)
+            self.pages.give_back(fresh)
+            raise
+        kv_evict.compact(self.cache, table, kept, new_table)
         for s, pages in zip(seqs, fresh):
             self.pages.move(s, pages, keep)
 

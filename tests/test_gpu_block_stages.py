@@ -127,6 +127,27 @@ def test_eviction_from_a_full_cache(free):
         assert all(torch.equal(x, y) for x, y in zip(*kv))
 
 
+def test_an_eviction_that_fails_takes_no_pages(monkeypatch):
+    # no memory for the choice of tokens: the block is as before, and the same call goes through later
+    from adaptive_block_scaled_amd import decoder_attention as da
+    b = block(da, weights_of=100)
+    b.forward(torch.randn(50, 256, device="cuda").bfloat16(), ["a"], [50])
+    before = (list(b.pages.free), {s: list(p) for s, p in b.pages.owned.items()}, dict(b.pages.lens), b.mass.clone())
+
+    def none(*a, **kw):
+        raise torch.OutOfMemoryError("none left")
+    for owner, name in ((da.kv_evict, "select"), (b.pages, "rows")):
+        with monkeypatch.context() as m:
+            calls = [getattr(owner, name)]
+            # (the first table is that of the pages the sequence has)
+            m.setattr(owner, name, none if name == "select" else lambda p: calls.pop()(p) if calls else none())
+            with pytest.raises(torch.OutOfMemoryError):
+                b.evict(["a"], 20, recent=4)
+        assert (b.pages.free, b.pages.owned, b.pages.lens) == before[:3] and torch.equal(b.mass, before[3])
+    b.evict(["a"], 20, recent=4)
+    assert b.pages.lens == {"a": 20} and len(b.pages.owned["a"]) == 2
+
+
 def test_sums_of_released_sequences_are_used_again():
     from adaptive_block_scaled_amd import decoder_attention as da
     b = block(da, weights_of=100, pages=60)
