@@ -228,11 +228,11 @@ bool sums(PyObject* o, at::Tensor& t, int64_t device) {
            t.stride(2) == 1;
 }
 
-// rows of sums that do not overlap
+// rows of sums that do not overlap: strides as of some order of sequences and heads
 bool apart(const at::Tensor& t) {
-    for (int i = 0; i < 2; i++)
-        if (t.size(i) > 1 && t.stride(i) < t.size(2)) return false;
-    return true;
+    const int64_t n = t.size(0), h = t.size(1), w = t.size(2), sn = t.stride(0), sh = t.stride(1);
+    return (n <= 1 || sn >= w) && (h <= 1 || sh >= w) &&
+           (n <= 1 || h <= 1 || sn >= sh * (h - 1) + w || sh >= sn * (n - 1) + w);
 }
 
 // mass, out | None and rows | None

@@ -66,12 +66,19 @@ def _sums(t, name, kv_heads, device, rows=None, width=None):
         raise ValueError(f"{name} must have unit stride along its last dim")
 
 
+def _apart(t):
+    """Whether rows along the last dim do not overlap: strides as of some order of the first two."""
+    (n, h, w), (sn, sh, _) = t.shape, t.stride()
+    return (n <= 1 or sn >= w) and (h <= 1 or sh >= w) and \
+        (n <= 1 or h <= 1 or sn >= sh * (h - 1) + w or sh >= sn * (n - 1) + w)
+
+
 def _mass(mass, out, rows, batch, device):
     if rows is not None:
         _plain(rows, "rows", (batch,), torch.int32, device.index)
     elif mass.shape[0] < batch:
         raise ValueError(f"mass must have a row for each of {batch} sequences, or rows be given")
-    if out is not None and any(s < out.shape[2] for n, s in zip(out.shape[:2], out.stride()) if n > 1):
+    if out is not None and not _apart(out):
         raise ValueError("the sums' rows must not overlap")
     return _Mass(mass.data_ptr(), mass.stride(0), mass.stride(1), None if out is None else out.data_ptr(),
                  0 if out is None else out.stride(0), 0 if out is None else out.stride(1),

@@ -481,3 +481,20 @@ def test_refusals(kvc, ev):
                  (table, kept, table.long()), (table.cpu(), kept, table), (table, kept, table[0])):
         with pytest.raises(ValueError):
             ev.compact(b.cache, *args)
+
+
+def test_sums_whose_rows_meet_are_refused(kvc, ev):
+    # strides that are wide enough each, and rows of two sequences in one place
+    b = Batch(kvc, [40, 20], [1, 1], 4, 2, 64, 16, 18)
+    args = (b.q.cuda(), b.cache, *b.device())
+    kw = dict(max_q=1, k_exp=b.exps["k_exp"])
+    buffer, mass = torch.zeros(200, device="cuda"), torch.zeros(2, 2, 40, device="cuda")
+    bad, good = (buffer.as_strided((2, 2, 40), (s, 40, 1)) for s in (40, 80))
+    for call in (lambda t: ev.accumulate(mass, *args, out=t, **kw), lambda t: ev.accumulate(t, *args, **kw),
+                 lambda t: ev.select(mass, args[3], 10, mass_out=t)):
+        with pytest.raises(ValueError, match="overlap"):
+            call(bad)
+        call(good)
+    # heads before sequences
+    turned = torch.zeros(2, 2, 40, device="cuda").transpose(0, 1)
+    assert torch.equal(ev.accumulate(mass, *args, out=turned, **kw), ev.accumulate(mass.clone(), *args, **kw))

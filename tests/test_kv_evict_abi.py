@@ -153,3 +153,18 @@ def test_binding_needs_gpu_tensors(kvc, ev):
         ev.select(m, i, 4)
     with pytest.raises(ValueError, match="CUDA"):
         ev.compact(c, i[None], i[None, None], i[None])
+
+
+def test_rows_of_sums_that_overlap(ev):
+    # [2 sequences, 3 heads, 40]: wide enough strides of each may still meet one another's rows
+    import torch
+    buffer = torch.zeros(1000)
+    mass = torch.zeros(2, 3, 40)
+    for strides in ((40, 40), (80, 40), (100, 40), (40, 60), (39, 200), (200, 39), (0, 40), (120, 0)):
+        with pytest.raises(ValueError, match="overlap"):
+            ev._mass(mass, buffer.as_strided((2, 3, 40), (*strides, 1)), None, 2, torch.device("cpu"))
+    for strides in ((120, 40), (40, 80), (150, 45), (50, 100)):
+        m = ev._mass(mass, buffer.as_strided((2, 3, 40), (*strides, 1)), None, 2, torch.device("cpu"))
+        assert (m.out_stride_row, m.out_stride_head) == strides
+    for shape in ((1, 3, 40), (2, 1, 40)):  # what nothing is apart by has any stride
+        ev._mass(mass[:shape[0], :shape[1]], buffer.as_strided(shape, (40, 40, 1)), None, shape[0], torch.device("cpu"))
