@@ -222,8 +222,8 @@ __device__ __forceinline__ bool any_seen(const Args& p, int len, int lo, int hi,
            (!p.window || first + kUnit - 1 > lo - p.window || first < p.sinks);
 }
 
-// Scores of keys that the row at `pos` does not see become -inf.  x[i] is that of key
-// first + 4 h + 8 (i / 4) + i % 4.
+// Scores (or what they are as exponents) of keys that the row at `pos` does not see become
+// -inf.  x[i] is that of key first + 4 h + 8 (i / 4) + i % 4.
 __device__ __forceinline__ void hide(const Args& p, int len, int pos, int first, f32x16& x) {
     const int last = p.causal && pos < len - 1 ? pos : len - 1;
     const int lo = p.window ? pos - p.window : -1;
@@ -283,7 +283,7 @@ struct KeyAhead {
 // Row of register r for lane half h.
 __device__ __forceinline__ int row_of(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
-// Scores of key j that its lane's rows do not see become -inf.
+// Scores (or what they are as exponents) of key j that its lane's rows do not see become -inf.
 template <int R>
 __device__ __forceinline__ void hide_rows(const Args& p, const Sequence& s, int rows, int h, int j, float (&x)[R / 2]) {
 #pragma unroll
@@ -342,8 +342,8 @@ struct FewRows {
 #pragma unroll
         for (int r = 0; r < R / 2; r++) to[r] = __shfl(own, row_of(r, h));
     }
-    // each(first key, scores, whole) for the wave's tiles t of `count`, in order; tile(t) is
-    // the tile's place
+    // each(first key, scores, whether all rows see all keys) for the wave's tiles from .. to - 1,
+    // in order; tile(t) is the tile's place
     template <class Tile, class Each>
     __device__ __forceinline__ void go(const uint2* table, int from, int to, Tile&& tile, Each&& each) {
         int t = from + wave;
@@ -363,9 +363,11 @@ struct FewRows {
             float x[R / 2];
 #pragma unroll
             for (int r = 0; r < R / 2; r++) x[r] = all[r];
-            if (!all_seen(p, s.len, pos_lo, pos_hi, first)) hide_rows<R>(p, s, rows, h, first + j, x);
-            each(first, x);
+            each(first, x, all_seen(p, s.len, pos_lo, pos_hi, first));
         }
+    }
+    __device__ __forceinline__ void hide(int first, float (&x)[R / 2]) const {
+        hide_rows<R>(p, s, rows, h, first + (lane & 31), x);
     }
 };
 
@@ -385,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_stats_kernel(const Args p) {
     float m[R / 2], l[R / 2];
 #pragma unroll
     for (int r = 0; r < R / 2; r++) m[r] = kLowest, l[r] = 0.0f;
-    few.go(table, from, to, [&](int t) { return tiles(t); }, [&](int, const float (&x)[R / 2]) {
+    few.go(table, from, to, [&](int t) { return tiles(t); }, [&](int first, float (&x)[R / 2], bool whole) {
+        if (!whole) few.hide(first, x);
         float y[R / 2], top = -__builtin_inff();
 #pragma unroll
         for (int r = 0; r < R / 2; r++) {
@@ -480,10 +483,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_columns_kernel(const Args p) 
         const int key = first + r;
         if (few.h == 0 && key < sums.width) sums.out[key] = key < sums.old ? sums.in[key] + v : v;
     };
-    const auto add = [&](int first, const float (&x)[R / 2]) {
+    // (hidden as exponents: of a row that is NaN, what it does not see gets nothing all the same)
+    const auto add = [&](int first, float (&x)[R / 2], bool whole) {
         float v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < R / 2; i++) v += __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], few.f[i], -log[i]));
+        for (int i = 0; i < R / 2; i++) x[i] = __builtin_fmaf(x[i], few.f[i], -log[i]);
+        if (!whole) few.hide(first, x);
+#pragma unroll
+        for (int i = 0; i < R / 2; i++) v += __builtin_amdgcn_exp2f(x[i]);
         write(first, v + __shfl_xor(v, 32));
     };
     const auto same = [](int t) { return t; };
@@ -786,8 +793,12 @@ __global__ void __launch_bounds__(kThreads, 2) columns_kernel(const Args p) {
                         const int key = first + i * kUnit;
                         if (!any_seen(p, s.len, lo_w, hi_w, key)) continue;
                         f32x16 x = scores<D>(k[i], q);
+                        // (hidden as exponents, as in few_columns_kernel)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) x[j] = __builtin_fmaf(x[j], f, -log);
                         hide(p, s.len, position(r0 + (lane & 31)), key + 4 * h, x);
-                        add(i, x, f, log);
+#pragma unroll
+                        for (int j = 0; j < 16; j++) acc[i][j] += __builtin_amdgcn_exp2f(x[j]);
                     }
                 }
             }

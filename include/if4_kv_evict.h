@@ -40,7 +40,8 @@ typedef struct if4_kv_mass {
  *     out[row, g, j] = (j < seq_lens[b] - T_b ? in[row, g, j] : 0) + sum_i sum_m P_imj
  * over the first max_q rows i and the query heads m of g.  The newest tokens start
  * from nothing: a slot that is used again needs no clearing.  Rows of q that see no
- * key add nothing.  Sequences without rows of q are left as they are, and so is what lies
+ * key add nothing.  A row that is NaN, or sees a key that is, makes the sums of the keys that
+ * it sees NaN and no others.  Sequences without rows of q are left as they are, and so is what lies
  * at and past a sequence's length.
  * Arithmetic: the cache's values enter exactly (as 7 times theirs, in fp16), q as in
  * if4_kv_attention; scores, maxima, sums and weights are fp32, in an order that does not

@@ -181,6 +181,28 @@ def test_hidden_nan_and_seen_nan(kvc, ev):
             assert abs(float(mass.double().sum()) - 4) < 1e-5 and not bool(mass[0, 0, 62:].any())
 
 
+@pytest.mark.parametrize("kw", [{}, dict(window=30, sinks=5), dict(causal=False)], ids=["plain", "window", "full"])
+@pytest.mark.parametrize("lens,chunks,heads,kv,dim", [([100], [6], 8, 2, 64), ([90, 40], [16, 3], 2, 1, 128),
+                                                      ([200, 70], [120, 5], 4, 2, 64), ([300], [200], 2, 1, 256)])
+def test_rows_that_are_nan_reach_what_they_see_only(kvc, ev, lens, chunks, heads, kv, dim, kw):
+    b = Batch(kvc, lens, chunks, heads, kv, dim, 16, 22)
+    g = np.random.default_rng(22)
+    for row, value in ((1, float("nan")), (chunks[0] // 2, float("inf"))):
+        b.q[row, 0, 3] = value
+    mass = g.exponential(size=(len(lens), kv, max(lens) + 3)).astype(np.float32)
+    scale = dim ** -0.5
+    got = ev.accumulate(torch.from_numpy(mass).cuda(), b.q.cuda(), b.cache, *b.device(), max_q=b.max_q, scale=scale,
+                        k_exp=b.exps["k_exp"], **kw).cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        nan = np.isnan(weights(b, mass, scale, **kw)[0])
+    # what no such row sees has nothing of it, whatever its values: the same as for any others
+    b.q[~b.q.isfinite()] = 1.0
+    want, bound = weights(b, mass, scale, **kw)
+    assert nan.any() and not nan[:, 1:].any() and (nan[0, 0, :lens[0]].all() == ("causal" in kw))
+    assert np.array_equal(np.isnan(got), nan)
+    assert (np.abs(got - want) <= bound)[~nan].all()
+
+
 def test_rows_of_a_pool_and_a_new_output(kvc, ev):
     b = Batch(kvc, [100, 30, 50], [1, 2, 3], 4, 2, 128, 16, 10)
     pool = torch.rand(6, 2, 120, device="cuda")
