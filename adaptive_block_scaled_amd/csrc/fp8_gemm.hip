@@ -7,8 +7,9 @@
 // exponent and cut them 13 bits below it.  That is within what rounding a result to bf16
 // loses, so results in bf16 take them.  Results in fp32 take the bf16 instructions, in
 // which every product and every sum of fp32 is whole: E4M3 times a power of two is exact in
-// bf16, and the conversion (v_cvt_scalef32) applies the byte too.  That is at half the rate, for
-// gradients of weights: 4096 x 8192 x 4096 190 us, 1440 TFLOP/s, and 104 with a result in bf16 (2650).
+// bf16 (for bytes 3 to 246; below, codes under bf16's least 2^-133 are rounded to a multiple of
+// it, above, what reaches 2^128 overflows), and the conversion (v_cvt_scalef32) applies the
+// byte too.  That is at half the rate, for gradients of weights: 4096 x 8192 x 4096 190 us, 1440 TFLOP/s, and 104 with a result in bf16 (2650).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -56,7 +57,8 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_
         rsrc, (__attribute__((address_space(3))) void*)lds, 16, (int)voff, (int)soff, 0, 0);
 }
 
-// 32 codes to bf16, exactly, times the power of two in the low byte of `scale`.
+// 32 codes to bf16, times the power of two in the low byte of `scale`: exactly for bytes 3 to
+// 246 (the conversion takes a byte of 0, which is no fp32 power, as 2^-127).
 __device__ __forceinline__ void widen(int8v codes, uint32_t scale, bf16x8 (&out)[4]) {
     const float s = __uint_as_float((scale & 0xFFu) << 23);
 #pragma unroll

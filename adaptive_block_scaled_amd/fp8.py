@@ -109,9 +109,9 @@ def workspace_bytes(m: int, n: int, k: int) -> int:
 
 def gemm(a_codes, a_scales, w_codes, w_scales, dtype=torch.bfloat16, out=None, workspace=None) -> torch.Tensor:
     """C[M, N] = A[M, K] W[N, K]^T, summed in fp32, of `dtype` (bf16 or fp32; products
-    enter an fp32 result whole, a bf16 one cut 13 bits below the largest of their 8
-    neighbours).  A has blocks of one row, W blocks of one row or squares, as its scales'
-    shape says.
+    enter an fp32 result whole, but for operands that bf16 does not hold, those of scale bytes
+    0, 1, 2 and from 247 on; a bf16 one cut 13 bits below the largest of their 8 neighbours).
+    A has blocks of one row, W blocks of one row or squares, as its scales' shape says.
     `out` may pass C with a row stride, `workspace` a uint8 tensor of workspace_bytes()."""
     if out is None and workspace is None and (dtype is torch.bfloat16 or dtype is torch.float32):
         c = _op_call.gemm(a_codes, a_scales, w_codes, w_scales, dtype is torch.bfloat16)

@@ -57,11 +57,14 @@ int if4_fp8_quantize_t(const void* x, int x_dtype, int64_t rows, int64_t cols, i
 /*
  * C = A W^T: A [M, K] with blocks of one row, W [N, K] with blocks of one row
  * (w_square 0) or squares (1).
- * Sums are fp32.  For a c of IF4_F32 every product enters them whole.  For one of IF4_BF16
- * the FP8 matrix instructions add them: of each 8 neighbouring k the products are brought
- * to the exponent of the largest one and cut 13 bits below it before they are added, so
- * that a result is off by up to 2^-10 of the sum of its products' magnitudes besides
- * its rounding.
+ * Sums are fp32.  For a c of IF4_F32 every product enters them whole, of values that bf16
+ * holds.  It holds all of bytes 3 to 246; of bytes 0, 1 and 2 (blocks of amax up to 448 *
+ * 2^-125) values that are no multiples of 2^-133 are rounded to one, and of bytes from 247
+ * on those of 2^128 and more are infinities (NaN times zero).  For a c of IF4_BF16, where
+ * bytes 0 to 254 are taken as they are, the FP8 matrix instructions add the products: of
+ * each 8 neighbouring k they are brought to the exponent of the largest one and cut 13
+ * bits below it before they are added, so that a result is off by up to 2^-10 of the sum
+ * of its products' magnitudes besides its rounding.
  *   codes    device, 16-byte aligned; scales device.
  *   c        device [M, N], IF4_F32 or IF4_BF16 (rounded to nearest even once), leading
  *            dimension ldc >= N (elements).

@@ -303,3 +303,31 @@ def test_one_row_of_any_stride(fp8, dtype, stride):
         assert torch.equal(fp8.gemm(*q, *qw, dtype=dtype), want)
         fp8.gemm(*q, *qw, out=one_row(out, stride))
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("m", [3, 70, 300])
+@pytest.mark.parametrize("ba,bw", [(0, 250), (1, 246), (2, 240), (3, 246), (4, 127), (246, 3), (246, 20), (127, 0), (200, 2)])
+def test_bytes_near_the_ends(fp8, m, ba, bw):
+    """Every code times one, of blocks of the least and the largest bytes.  bf16 results: the
+    product, rounded.  fp32 results: the product, whose operands bf16 holds down to multiples of
+    2^-133: below byte 3 each is off by half of that at the most."""
+    codes = np.array([c for c in range(256) if c & 127 != 127], np.uint8)
+    a, w = np.zeros((m, 256), np.uint8), np.zeros((256, 256), np.uint8)
+    a[:, :254] = np.roll(codes, 1)
+    w[np.arange(254), np.arange(254)] = 0x38  # one
+    sa, sw = np.full((m, 2), ba, np.uint8), np.full((256, 2), bw, np.uint8)
+    if bw < 3:  # the codes on W's side
+        a, w = np.zeros((m, 256), np.uint8), np.zeros((256, 256), np.uint8)
+        a[np.arange(m), np.arange(m) % 254], w[:, :254] = 0x38, np.roll(codes, 1)
+    va, vw = ref.values(a, sa), ref.values(w, sw)
+    want = va @ vw.T
+    q = [torch.from_numpy(t).cuda() for t in (a, sa, w, sw)]
+    half = torch.from_numpy(want).to(BF16)
+    assert torch.equal(fp8.gemm(*q).cpu(), half)
+    got = fp8.gemm(*q, dtype=F32).cpu().double().numpy()
+    off = np.zeros(want.shape)
+    for low, byte, other in ((va, ba, np.abs(vw).max()), (vw, bw, np.abs(va).max())):
+        if byte < 3:
+            off += 2.0 ** -134 * other
+    assert (np.abs(got - want) <= off + np.abs(want) * 2.0 ** -24).all()
+    assert (off > 0).any() == (min(ba, bw) < 3) and (np.isfinite(got)).all()
