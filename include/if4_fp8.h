@@ -10,7 +10,7 @@
  * weight and its transpose hold the same values).  Blocks at the end of a row or
  * column are as long as what is left.
  *   exponent  e = byte - 127, the least one >= -127 with amax * 2^-e <= 448 (amax: the
- *             block's largest magnitude); 0 in a block of zeros.
+ *             block's largest magnitude): -127, byte 0, in a block of zeros.
  *   code      E4M3 value nearest to x * 2^-e (ties to even), the sign of zeros kept.
  * Scaling by a power of two rounds nothing, so each value is rounded once, and the
  * matrix cores take the byte as it is.  A block that holds a NaN or an infinity has byte
