@@ -331,3 +331,66 @@ def test_bytes_near_the_ends(fp8, m, ba, bw):
             off += 2.0 ** -134 * other
     assert (np.abs(got - want) <= off + np.abs(want) * 2.0 ** -24).all()
     assert (off > 0).any() == (min(ba, bw) < 3) and (np.isfinite(got)).all()
+
+
+def operands(m, n, k, seed=0):
+    """Codes without NaN and bytes around one, as the product takes them."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def part(rows):
+        codes = torch.randint(0, 256, (rows, k), generator=g, device="cuda", dtype=torch.uint8)
+        scales = torch.randint(120, 131, (rows, ref.blocks(k)), generator=g, device="cuda", dtype=torch.uint8)
+        return torch.where(codes & 127 == 127, codes - 1, codes), scales
+    return (*part(m), *part(n))
+
+
+# one row, 16 rows, tiles of 64, 128 and 256
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 528), (5, 70, 256), (70, 130, 256), (1100, 1900, 144), (3970, 4090, 1296)])
+def test_nothing_is_written_behind_the_last_row_or_beside_it(fp8, m, n, k, dtype):
+    # as many rows and columns of another tensor's as a whole tile has
+    q = operands(m, n, k)
+    for shift in (0, 3):  # (rows of whole lines or not)
+        buffer = torch.full((m + 512, 2048 * (1 + (n + 515) // 2048)), -3.0, dtype=dtype, device="cuda")
+        out = buffer[256:256 + m, 256 + shift:256 + shift + n]
+        fp8.gemm(*q, out=out)
+        assert torch.equal(out, fp8.gemm(*q, dtype=dtype)) or n > 4000  # (tiles may go by whole lines)
+        assert bool(out.isfinite().all())
+        out.fill_(-3.0)
+        assert bool((buffer == -3.0).all())
+
+
+# the tile and, of each, a row stride at which its rows are 2^31 bytes apart
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("m,n,k,tile", [(20, 90, 400, 64), (66, 16390, 272, 128), (257, 32768, 1024, 256)])
+def test_rows_that_are_far_apart(fp8, m, n, k, tile, dtype):
+    q = operands(m, n, k, 1)
+    ld = (1 << 31) // tile // dtype.itemsize
+    buffer = torch.full((m * ld,), -3.0, dtype=dtype, device="cuda")
+    out = buffer.view(m, ld)[:, :n]
+    fp8.gemm(*q, out=out)
+    assert torch.equal(out, fp8.gemm(*q, dtype=dtype))
+    out.fill_(-3.0)
+    assert bool((buffer == -3.0).all())
+
+
+def test_gradients_against_differences_of_the_product(fp8):
+    """<dy, y> as a function of one value of x or w at a time, y by the product, against the products
+    that give the gradients.  Whole numbers that the codes hold: every sum has one value, and
+    central differences of what is linear are exact."""
+    m, n, k = 272, 400, 528
+    g = np.random.default_rng(7)
+    x, w, dy = (torch.from_numpy(g.integers(-8, 9, s)).float().cuda() for s in ((m, k), (n, k), (m, n)))
+
+    def value(x, w):
+        y = fp8.gemm(*fp8.quantize(x), *fp8.quantize(w, True), dtype=F32)
+        return float((dy.double() * y.double()).sum())
+    dx = fp8.gemm(*fp8.quantize(dy), *fp8.quantize_t(w, True), dtype=F32)
+    dw = fp8.gemm(*fp8.quantize_t(dy), *fp8.quantize_t(x), dtype=F32)
+    for of, grad in ((0, dx), (1, dw)):
+        assert bool(grad.any())
+        for i, j in ((0, 0), (7, 9), (131, 127), (200, 128), (271, 527)):
+            lo, hi = ([x, w][of].clone() for _ in range(2))
+            lo[i, j], hi[i, j] = -3, 5
+            a, b = ((t, w) if of == 0 else (x, t) for t in (hi, lo))
+            assert value(*a) - value(*b) == 8 * float(grad[i, j])
