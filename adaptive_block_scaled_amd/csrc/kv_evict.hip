@@ -143,9 +143,10 @@ __device__ __forceinline__ void find_digit(Shared& sh, const uint32_t (&c)[2], u
 // before it, and of those equal as many as are kept; `aboves` (the first and last ones of a row
 // among them) and `equals` lie before `from`.  A chunk's sums have been read before any
 // of its outputs is written, and these lie no further than the chunk: `out` may be `in`
-// where one workgroup writes the row.
-__device__ __forceinline__ void write_kept(const Row& row, float* out, int from, int to, uint32_t prefix, uint32_t need,
-                                           uint32_t aboves, uint32_t equals) {
+// where one workgroup writes the row.  (Two sequences of one row, written in place, count
+// each other's sums in between, and may come to more than `keep`: none goes past it.)
+__device__ __forceinline__ void write_kept(const Row& row, float* out, int keep, int from, int to, uint32_t prefix,
+                                           uint32_t need, uint32_t aboves, uint32_t equals) {
     __shared__ uint32_t before[2][kWaves];  // above, and equal << 16, of each wave
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int turn = 0;
@@ -192,8 +193,10 @@ __device__ __forceinline__ void write_kept(const Row& row, float* out, int from,
         for (int j = 0; j < 4; j++) {
             if (up[j] || (equal[j] && e < need)) {
                 const uint32_t at = a + (e < need ? e : need);
-                row.kept[at] = base + 4 * tid + j;
-                if (out) out[at] = v[j];
+                if (at < (uint32_t)keep) {
+                    row.kept[at] = base + 4 * tid + j;
+                    if (out) out[at] = v[j];
+                }
             }
             a += up[j];
             e += equal[j];
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
         prefix = prefix << bits_of(level) | sh.found[0];
         need = sh.found[1];  // of those with this prefix
     }
-    write_kept(row, row.out, 0, row.n, prefix, need, 0, 0);
+    write_kept(row, row.out, p.keep, 0, row.n, prefix, need, 0, 0);
 }
 
 // Workspace of the segment kernels: [3][rows][segments][kDigits] numbers, then [rows][segments]
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) segment_write_kernel(const SegmentAr
     uint32_t equals = 0;
     if (p.s.keep > p.s.sinks + p.s.recent) st = resolve(p, sh, pair, segment, 3, equals);
     const int fixed = (from < row.first ? from : row.first) + (from > row.last ? from - row.last : 0);
-    write_kept(row, p.moved ? p.moved + (int64_t)pair * p.s.keep : row.out, from, to, st.prefix, st.need,
+    write_kept(row, p.moved ? p.moved + (int64_t)pair * p.s.keep : row.out, p.s.keep, from, to, st.prefix, st.need,
                st.above + (uint32_t)fixed, equals);
 }
 

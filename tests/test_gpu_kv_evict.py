@@ -310,6 +310,20 @@ def test_select_rows_and_lengths(ev):
     assert bool((kept[1:] == -1).all())
 
 
+@pytest.mark.parametrize("width,keep", [(9000, 300), (40000, 300), (9000, 8800)])
+def test_select_of_sequences_with_one_row_in_place(ev, width, keep):
+    # each reads sums that others write: any choice, but nothing outside of the outputs
+    batch = 40 if width < 10000 else 4
+    mass = torch.rand(3, 2, width + 50, device="cuda")
+    before = mass.clone()
+    kept = torch.full((batch + 2, 2, keep), 7 - (1 << 31), dtype=torch.int32, device="cuda")
+    rows = torch.ones(batch, dtype=torch.int32, device="cuda")
+    lens = torch.full((batch,), width, dtype=torch.int32, device="cuda")
+    ev.select(mass[:, :, :width], lens, keep, recent=5, sinks=3, rows=rows, out=kept[1:-1], mass_out=mass[:, :, :width])
+    assert bool((kept[[0, -1]] == 7 - (1 << 31)).all())
+    assert torch.equal(mass[[0, 2]], before[[0, 2]]) and torch.equal(mass[1, :, keep:], before[1, :, keep:])
+
+
 @pytest.mark.parametrize("dim,page,kv", [(64, 16, 3), (128, 64, 2), (256, 32, 1)])
 def test_compact(kvc, ev, dim, page, kv):
     lens, keep = [200, 37, 5, 100], 45
