@@ -23,7 +23,8 @@
 extern "C" {
 #endif
 
-/* The sums, and where they go: `out` may be `in` (with its strides). */
+/* The sums, and where they go: `out` may be `in` (with its strides), and must not overlap it
+ * otherwise. */
 typedef struct if4_kv_mass {
     const float* in;
     int64_t in_stride_row, in_stride_head;
@@ -68,7 +69,8 @@ int64_t if4_kv_weights_workspace_most(const if4_kv_cache* cache, const if4_kv_at
  *   kept     device int32 [batch, kv_heads, keep] contiguous: their positions,
  *            ascending, then -1
  *   mass     out (NULL: not wanted) gets their sums at 0, 1, ..; its width is keep or more;
- *            what lies behind stays.  It may be `in`.
+ *            what lies behind stays.  It may be `in` (sequences that have one row then
+ *            get any positions, or unset ones).
  *   recent + sinks <= keep
  *   workspace  device, 16-byte aligned, of if4_kv_select_workspace() bytes (NULL where that
  *              is 0); holds nothing between calls
