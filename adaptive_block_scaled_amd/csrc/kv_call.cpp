@@ -7,9 +7,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <math.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
 
 #include "../../include/if4_kv.h"
 #include "../../include/if4_kv_evict.h"
@@ -57,6 +61,20 @@ bool exponent(PyObject* o, int32_t& v) {
     return true;
 }
 
+void* stream_of(int64_t device) {
+    return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
+}
+
+// The tensors' device is the current one for the time of a call: its default stream is a
+// null handle, which HIP takes as the default stream of the current device.
+struct On {
+    std::optional<c10::hip::HIPGuard> guard;
+    explicit On(int64_t device) {
+        static const bool one = c10::hip::device_count() == 1;
+        if (!one && c10::hip::current_device() != device) guard.emplace((c10::DeviceIndex)device);
+    }
+};
+
 struct Cache {
     if4_kv_cache c;
     int64_t device;
@@ -89,9 +107,7 @@ struct Cache {
         c.v_scales = (uint8_t*)t[3].data_ptr();
         return true;
     }
-    void* stream() const {
-        return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
-    }
+    void* stream() const { return stream_of(device); }
 };
 
 bool value_type(at::ScalarType s, int& dtype) {
@@ -126,6 +142,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             !vectors(a[2], v, k.scalar_type(), c.device, shape) ||
             !plain(a[3], slots, at::kLong, c.device, {shape[0]}))
             Py_RETURN_NONE;
+        const On on(c.device);
         return PyLong_FromLong(kv_append(&c.c, k.data_ptr(), v.data_ptr(), dtype, shape[0],
                                          k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                                          (const int64_t*)slots.data_ptr(), (int)mode, c.stream()));
@@ -144,6 +161,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor k = at::empty({slots.size(0), c.c.kv_heads, c.c.head_dim},
                                        slots.options().dtype(bf16 ? at::kBFloat16 : at::kFloat));
         const at::Tensor v = at::empty(k.sizes(), k.options());
+        const On on(c.device);
         const int st = kv_read(&c.c, (const int64_t*)slots.data_ptr(), slots.size(0), k.data_ptr(),
                                v.data_ptr(), bf16 ? IF4_BF16 : IF4_F32, c.stream());
         if (st != IF4_OK) return PyLong_FromLong(st);
@@ -215,6 +233,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (need < 0) return PyLong_FromLong(-need);
         at::Tensor ws;
         if (need > 0) ws = at::empty({need}, b.q.options().dtype(at::kByte));
+        const On on(b.c.device);
         const int st =
             kv_attention(&b.c.c, &p, need > 0 ? ws.data_ptr() : nullptr, need, b.c.stream());
         if (st != IF4_OK) return PyLong_FromLong(st);
@@ -275,6 +294,7 @@ PyObject* weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (need < 0) return PyLong_FromLong(-need);
         at::Tensor ws;
         if (need > 0) ws = at::empty({need}, b.q.options().dtype(at::kByte));
+        const On on(b.c.device);
         return PyLong_FromLong(
             kv_weights(&b.c.c, &b.p, &m.m, need > 0 ? ws.data_ptr() : nullptr, need, b.c.stream()));
     });
@@ -301,9 +321,10 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (need < 0) return PyLong_FromLong(-need);
         at::Tensor ws;
         if (need > 0) ws = at::empty({need}, lens.options().dtype(at::kByte));
+        const On on(device);
         const int st = kv_select(&m.m, (const int32_t*)lens.data_ptr(), batch, heads, keep, recent, sinks,
                                  (int32_t*)kept.data_ptr(), need > 0 ? ws.data_ptr() : nullptr, need,
-                                 c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream());
+                                 stream_of(device));
         if (st != IF4_OK) return PyLong_FromLong(st);
         return THPVariable_Wrap(kept);
     });
@@ -322,6 +343,7 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
             !plain(a[2], kept, at::kInt, c.device, {batch, c.c.kv_heads, keep}) ||
             !plain(a[3], fresh, at::kInt, c.device, {batch, fresh.size(1)}))
             Py_RETURN_NONE;
+        const On on(c.device);
         return PyLong_FromLong(kv_compact(&c.c, (const int32_t*)table.data_ptr(), table.size(1),
                                           (const int32_t*)kept.data_ptr(), batch, keep,
                                           (const int32_t*)fresh.data_ptr(), fresh.size(1), c.stream()));

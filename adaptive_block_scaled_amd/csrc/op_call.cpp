@@ -6,9 +6,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <math.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
 
 #include "../../include/if4_fp8.h"
 #include "../../include/if4_qk.h"
@@ -42,6 +46,16 @@ bool value_type(at::ScalarType s, int& dtype) {
 void* stream_of(int64_t device) {
     return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
 }
+
+// The tensors' device is the current one for the time of a call: its default stream is a
+// null handle, which HIP takes as the default stream of the current device.
+struct On {
+    std::optional<c10::hip::HIPGuard> guard;
+    explicit On(int64_t device) {
+        static const bool one = c10::hip::device_count() == 1;
+        if (!one && c10::hip::current_device() != device) guard.emplace((c10::DeviceIndex)device);
+    }
+};
 
 int64_t blocks(int64_t n) { return (n + IF4_FP8_BLOCK - 1) / IF4_FP8_BLOCK; }
 
@@ -81,6 +95,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor scales = at::empty({square ? blocks(rows) : rows, blocks(k)}, bytes);
         // (one row is none apart from another: its stride has any value)
         const int64_t ld = x.size(0) > 1 ? x.stride(0) : x.size(1);
+        const On on(x.device().index());
         const int st = (t ? fp8_quantize_t : fp8_quantize)(
             x.data_ptr(), dtype, x.size(0), x.size(1), ld, square, (uint8_t*)codes.data_ptr(),
             (uint8_t*)scales.data_ptr(), stream_of(x.device().index()));
@@ -107,6 +122,7 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor c = at::empty({m, rows}, ac.options().dtype(bf16 ? at::kBFloat16 : at::kFloat));
         at::Tensor work;
         if (need > 0) work = at::empty({need}, ac.options());
+        const On on(device);
         const int st = fp8_gemm((const uint8_t*)ac.data_ptr(), (const uint8_t*)as.data_ptr(),
                                 (const uint8_t*)wc.data_ptr(), (const uint8_t*)ws.data_ptr(), square, m, rows, k,
                                 c.data_ptr(), bf16 ? IF4_BF16 : IF4_F32, rows, need > 0 ? work.data_ptr() : nullptr,
@@ -181,6 +197,7 @@ PyObject* norm_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
         r.into(r.p.q, qo);
         r.into(r.p.k, ko);
         r.p.out_dtype = bf16 ? IF4_BF16 : IF4_F32;
+        const On on(r.device);
         const int st = qk_norm_rotate(&r.p, stream_of(r.device));
         if (st != IF4_OK) return PyLong_FromLong(st);
         return pair(qo, ko);
@@ -216,6 +233,7 @@ PyObject* norm_rotate_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t need = qk_backward_workspace(&r.p);
         if (need < 0) return PyLong_FromLong(-need);
         const at::Tensor work = at::empty({need}, r.q.options().dtype(at::kByte));
+        const On on(r.device);
         const int st = qk_backward(&r.p, work.data_ptr(), need, stream_of(r.device));
         if (st != IF4_OK) return PyLong_FromLong(st);
         PyObject* t = PyTuple_New(4);

@@ -23,7 +23,7 @@ import ctypes
 import torch
 
 from . import if4
-from .if4 import _check, _dtype_code, _input, _ld, _need, lib
+from .if4 import _check, _dtype_code, _input, _ld, _need, _on, lib
 
 try:
     from . import _op_call
@@ -66,8 +66,8 @@ def _quantize(fn, name, x, rows, k, square, out):
         codes, scales = out
         _need(codes, "codes", (rows, k), torch.uint8, x.device)
         _need(scales, "scales", shape, torch.uint8, x.device)
-    st = fn(x.data_ptr(), _dtype_code(x.dtype), *x.shape, _ld(x), 1 if square else 0,
-            codes.data_ptr(), scales.data_ptr(), _raw_stream(x.get_device()))
+    st = _on(x.get_device(), fn, x.data_ptr(), _dtype_code(x.dtype), *x.shape, _ld(x), 1 if square else 0,
+             codes.data_ptr(), scales.data_ptr(), _raw_stream(x.get_device()))
     _check(name, st)
     return codes, scales
 
@@ -140,9 +140,9 @@ def gemm(a_codes, a_scales, w_codes, w_scales, dtype=torch.bfloat16, out=None, w
             raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    st = lib.if4_fp8_gemm(a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
-                          1 if square else 0, m, n, k, out.data_ptr(), _dtype_code(out.dtype),
-                          _ld(out), workspace.data_ptr() if need else None, need,
-                          _raw_stream(a_codes.get_device()))
+    index = a_codes.get_device()
+    st = _on(index, lib.if4_fp8_gemm, a_codes.data_ptr(), a_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+             1 if square else 0, m, n, k, out.data_ptr(), _dtype_code(out.dtype), _ld(out),
+             workspace.data_ptr() if need else None, need, _raw_stream(index))
     _check("if4_fp8_gemm", st)
     return out

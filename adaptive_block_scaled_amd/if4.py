@@ -76,6 +76,15 @@ def _stream(dev) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+def _on(index: int, fn, *args):
+    """fn(*args) with CUDA device `index`, the tensors', current: its default stream is a null
+    handle, which HIP takes as the default stream of the current device."""
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
 def _check(fn, st):
     if st != IF4_OK:
         raise IF4Error(fn, st)
@@ -138,9 +147,8 @@ def quantize(x: torch.Tensor, scale_exp: int = 0, mode: int = MODE_ADAPTIVE, out
     _input(x)
     rows, cols = x.shape
     codes, scales = _outputs(out, x.device, (rows, cols // 2), (rows, cols // GROUP))
-    st = lib.if4_quantize_mode(x.data_ptr(), _dtype_code(x.dtype), rows, cols, _ld(x),
-                               codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode),
-                               _stream(x.device))
+    st = _on(x.get_device(), lib.if4_quantize_mode, x.data_ptr(), _dtype_code(x.dtype), rows, cols,
+             _ld(x), codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode), _stream(x.device))
     _check("if4_quantize_mode", st)
     return codes, scales
 
@@ -152,9 +160,8 @@ def quantize_t(x: torch.Tensor, scale_exp: int = 0, mode: int = MODE_ADAPTIVE, o
     _input(x)
     rows, cols = x.shape
     codes, scales = _outputs(out, x.device, (cols, rows // 2), (cols, rows // GROUP))
-    st = lib.if4_quantize_t(x.data_ptr(), _dtype_code(x.dtype), rows, cols, _ld(x),
-                            codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode),
-                            _stream(x.device))
+    st = _on(x.get_device(), lib.if4_quantize_t, x.data_ptr(), _dtype_code(x.dtype), rows, cols,
+             _ld(x), codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode), _stream(x.device))
     _check("if4_quantize_t", st)
     return codes, scales
 
@@ -168,9 +175,9 @@ def quantize_rht(x: torch.Tensor, sign_mask: int, scale_exp: int = 0, mode: int 
     _input(x)
     rows, cols = x.shape
     codes, scales = _outputs(out, x.device, (rows, cols // 2), (rows, cols // GROUP))
-    st = lib.if4_quantize_rht(x.data_ptr(), _dtype_code(x.dtype), rows, cols, _ld(x),
-                              int(sign_mask), codes.data_ptr(), scales.data_ptr(),
-                              int(scale_exp), int(mode), _stream(x.device))
+    st = _on(x.get_device(), lib.if4_quantize_rht, x.data_ptr(), _dtype_code(x.dtype), rows, cols,
+             _ld(x), int(sign_mask), codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode),
+             _stream(x.device))
     _check("if4_quantize_rht", st)
     return codes, scales
 
@@ -184,9 +191,8 @@ def quantize_ifn(x: torch.Tensor, bits: int, scale_exp: int = 0, mode: int = MOD
     rows, cols = x.shape
     codes, scales = _outputs(out, x.device, (rows, cols // GROUP * 2 * bits),
                              (rows, cols // GROUP))
-    st = lib.if4_quantize_ifn(int(bits), x.data_ptr(), _dtype_code(x.dtype), rows, cols,
-                              _ld(x), codes.data_ptr(), scales.data_ptr(), int(scale_exp),
-                              int(mode), _stream(x.device))
+    st = _on(x.get_device(), lib.if4_quantize_ifn, int(bits), x.data_ptr(), _dtype_code(x.dtype), rows,
+             cols, _ld(x), codes.data_ptr(), scales.data_ptr(), int(scale_exp), int(mode), _stream(x.device))
     _check("if4_quantize_ifn", st)
     return codes, scales
 
@@ -204,9 +210,8 @@ def dequantize_ifn(codes: torch.Tensor, scales: torch.Tensor, bits: int, scale_e
     else:
         y = out
         _need(y, "out", (rows, cols), y.dtype, codes.device, dense=False)
-    st = lib.if4_dequantize_ifn(int(bits), codes.data_ptr(), scales.data_ptr(), rows, cols,
-                                int(scale_exp), y.data_ptr(), _dtype_code(y.dtype), _ld(y),
-                                _stream(codes.device))
+    st = _on(codes.get_device(), lib.if4_dequantize_ifn, int(bits), codes.data_ptr(), scales.data_ptr(),
+             rows, cols, int(scale_exp), y.data_ptr(), _dtype_code(y.dtype), _ld(y), _stream(codes.device))
     _check("if4_dequantize_ifn", st)
     return y
 
@@ -224,9 +229,8 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, scale_exp: int = 0,
     else:
         y = out
         _need(y, "out", (rows, cols), y.dtype, codes.device, dense=False)
-    st = lib.if4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, int(scale_exp),
-                            y.data_ptr(), _dtype_code(y.dtype), _ld(y),
-                            _stream(codes.device))
+    st = _on(codes.get_device(), lib.if4_dequantize, codes.data_ptr(), scales.data_ptr(), rows, cols,
+             int(scale_exp), y.data_ptr(), _dtype_code(y.dtype), _ld(y), _stream(codes.device))
     _check("if4_dequantize", st)
     return y
 
@@ -250,8 +254,8 @@ def gemm(a_codes, a_scales, a_exp, w_codes, w_scales, w_exp, out=None) -> torch.
     else:
         c = out
         _need(c, "out", (M, N), torch.float32, dev, dense=False)
-    st = lib.if4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), int(a_exp), w_codes.data_ptr(),
-                      w_scales.data_ptr(), int(w_exp), M, N, K, c.data_ptr(), _ld(c),
-                      _stream(a_codes.device))
+    st = _on(a_codes.get_device(), lib.if4_gemm, a_codes.data_ptr(), a_scales.data_ptr(), int(a_exp),
+             w_codes.data_ptr(), w_scales.data_ptr(), int(w_exp), M, N, K, c.data_ptr(), _ld(c),
+             _stream(a_codes.device))
     _check("if4_gemm", st)
     return c

@@ -23,7 +23,7 @@ from typing import NamedTuple
 import torch
 
 from . import if4
-from .if4 import GROUP, MODE_ADAPTIVE, _check, _dtype_code, _need, lib
+from .if4 import GROUP, MODE_ADAPTIVE, _check, _dtype_code, _need, _on, lib
 
 try:
     from . import _kv_call
@@ -179,8 +179,8 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor
     _vectors(v, "v", shape, k.dtype, index)
     _plain(slots, "slots", shape[:1], torch.int64, index)
     (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
-    st = lib.if4_kv_append(c, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), shape[0], kt, kh,
-                           vt, vh, slots.data_ptr(), _held(mode, 32), _raw_stream(index))
+    st = _on(index, lib.if4_kv_append, c, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), shape[0], kt, kh,
+             vt, vh, slots.data_ptr(), _held(mode, 32), _raw_stream(index))
     if st:
         _check("if4_kv_append", st)
     return cache
@@ -211,8 +211,8 @@ def read(cache: KVCache, slots: torch.Tensor, k_exp: int = 0, v_exp: int = 0,
             raise ValueError("out must be two tensors (k, v)")
         _plain(k, "k", shape, k.dtype, index)
         _plain(v, "v", shape, k.dtype, index)
-    st = lib.if4_kv_read(c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-                         _dtype_code(k.dtype), _raw_stream(index))
+    st = _on(index, lib.if4_kv_read, c, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+             _dtype_code(k.dtype), _raw_stream(index))
     if st:
         _check("if4_kv_read", st)
     return k, v
@@ -283,8 +283,8 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_len
             raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {q.device}")
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = lib.if4_kv_attention(c, a, workspace.data_ptr() if need else None, need,
-                              _raw_stream(index))
+    st = _on(index, lib.if4_kv_attention, c, a, workspace.data_ptr() if need else None, need,
+             _raw_stream(index))
     if st:
         _check("if4_kv_attention", st)
     return out

@@ -17,7 +17,7 @@ import math
 
 import torch
 
-from .if4 import _check, lib
+from .if4 import _check, _on, lib
 from .kv_cache import KVCache, _Attention, _Cache, _cache, _held, _kv_call, _plain, _raw_stream, _vectors
 
 EXPORTS = ("if4_kv_weights", "if4_kv_weights_workspace", "if4_kv_weights_workspace_most", "if4_kv_select",
@@ -145,7 +145,7 @@ def accumulate(mass: torch.Tensor, q: torch.Tensor, cache: KVCache, page_table: 
             raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {q.device}")
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = lib.if4_kv_weights(c, a, m, workspace.data_ptr() if need else None, need, _raw_stream(index))
+    st = _on(index, lib.if4_kv_weights, c, a, m, workspace.data_ptr() if need else None, need, _raw_stream(index))
     if st:
         _check("if4_kv_weights", st)
     return out
@@ -207,8 +207,8 @@ def select(mass: torch.Tensor, seq_lens: torch.Tensor, keep: int, *, recent: int
             raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    st = lib.if4_kv_select(m, seq_lens.data_ptr(), batch, kv_heads, keep, recent, sinks, out.data_ptr(),
-                           workspace.data_ptr() if need else None, need, _raw_stream(dev.index))
+    st = _on(dev.index, lib.if4_kv_select, m, seq_lens.data_ptr(), batch, kv_heads, keep, recent, sinks, out.data_ptr(),
+             workspace.data_ptr() if need else None, need, _raw_stream(dev.index))
     if st:
         _check("if4_kv_select", st)
     return out
@@ -240,8 +240,8 @@ def compact(cache: KVCache, page_table: torch.Tensor, kept: torch.Tensor, new_ta
     _plain(page_table, "page_table", (batch, width), torch.int32, index)
     _plain(kept, "kept", (batch, c.kv_heads, kept.shape[2]), torch.int32, index)
     _plain(new_table, "new_table", (batch, new_table.shape[1]), torch.int32, index)
-    st = lib.if4_kv_compact(c, page_table.data_ptr(), width, kept.data_ptr(), batch, kept.shape[2],
-                            new_table.data_ptr(), new_table.shape[1], _raw_stream(index))
+    st = _on(index, lib.if4_kv_compact, c, page_table.data_ptr(), width, kept.data_ptr(), batch, kept.shape[2],
+             new_table.data_ptr(), new_table.shape[1], _raw_stream(index))
     if st:
         _check("if4_kv_compact", st)
     return cache

@@ -15,7 +15,7 @@ import math
 import torch
 
 from .fp8 import _op_call
-from .if4 import _check, _dtype_code, lib
+from .if4 import _check, _dtype_code, _on, lib
 
 EXPORTS = ("if4_norm_rotate", "if4_norm_rotate_backward", "if4_norm_rotate_backward_workspace")
 
@@ -157,7 +157,7 @@ def norm_rotate(q, k, q_weight, k_weight, table, positions, *, eps: float = 1e-6
         dtype = q.dtype if out is None and isinstance(q, torch.Tensor) else out[0].dtype
     a, dev = _args(q, k, q_weight, k_weight, table, positions, eps, interleaved, dtype)
     out = _results(a, (q.shape, k.shape), dtype, dev, out)
-    st = lib.if4_norm_rotate(a, _raw_stream(q.get_device()))
+    st = _on(q.get_device(), lib.if4_norm_rotate, a, _raw_stream(q.get_device()))
     _check("if4_norm_rotate", st)
     return out
 
@@ -203,6 +203,6 @@ def norm_rotate_backward(dq, dk, q, k, q_weight, k_weight, table, positions, *, 
         part.d_weight = row.data_ptr()
         if part.heads == 0:
             row.zero_()
-    st = lib.if4_norm_rotate_backward(a, workspace.data_ptr(), need, _raw_stream(q.get_device()))
+    st = _on(q.get_device(), lib.if4_norm_rotate_backward, a, workspace.data_ptr(), need, _raw_stream(q.get_device()))
     _check("if4_norm_rotate_backward", st)
     return (*dx, dw[0], dw[1])

@@ -37,9 +37,10 @@
  *   * All data pointers are DEVICE pointers owned by the caller; the library
  *     allocates no memory and keeps no state, and is safe to call from
  *     several threads.
- *   * `stream` is a hipStream_t (NULL = the default stream).  Work is only
- *     enqueued; the call returns before it runs.  Faults inside a kernel
- *     surface at the caller's next synchronisation.
+ *   * `stream` is a hipStream_t of the device that holds the data (NULL = the
+ *     default stream of the CURRENT device, which has to be that one).  Work
+ *     is only enqueued; the call returns before it runs.  Faults inside a
+ *     kernel surface at the caller's next synchronisation.
  *   * Arguments are validated on the host before anything is launched; a
  *     non-zero status means nothing was enqueued.  Zero rows (or zero
  *     M/N/K) is valid and enqueues nothing -- except if4_gemm with K == 0,
