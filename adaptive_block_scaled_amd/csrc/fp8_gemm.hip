@@ -11,8 +11,8 @@
 // take the bf16 instructions, in which every product and every sum of fp32 is whole: E4M3
 // times a power of two is exact in bf16 (for bytes 3 to 246; below, codes under bf16's least
 // 2^-133 are rounded to a multiple of it, above, what reaches 2^128 overflows), and the
-// conversion (v_cvt_scalef32) applies the byte too.  For gradients of weights, 4096 x 8192 x
-// 4096: 190 us, 1440 TFLOP/s, and 104 with a result in bf16 (2650).
+// conversion (v_cvt_scalef32) applies the byte too.  4096 x 8192 x 4096: 222 us in fp32 (1240
+// TFLOP/s), 118 in bf16 (2330).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

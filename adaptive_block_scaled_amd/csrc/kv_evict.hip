@@ -354,8 +354,8 @@ int64_t segment_of(const if4_kv_mass& m, int64_t rows, int64_t keep) {
 // of 8 D bytes, and what is read of a source tile is read by one workgroup and its
 // neighbours.  Bound by memory, and by how it is laid out: of a source tile with any token
 // kept, V's every 64-byte line is read, whichever of its 16 tokens stay.  32 sequences of about 7100
-// tokens and 8 kv heads of 128, of which 2048 stay (so that nearly every tile has one; 240
-// MB read and written): 65 us, 3.7 TB/s.
+// tokens and 8 kv heads of 128, of which 2048 stay (so that nearly every tile has one; 254
+// MB read and written, 130 of them V's tiles), other ones in each call: 69 us, 3.7 TB/s.
 
 constexpr int kCopyThreads = 256;
 
