@@ -143,8 +143,8 @@ def norm_rotate(q, k, q_weight, k_weight, table, positions, *, eps: float = 1e-6
     token's position (int64 [tokens]): pairs (i, i + rotary/2), or (2i, 2i + 1) where
     `interleaved`.  D is a multiple of 8 up to 256, rotary one of 16 (interleaved: 8) up to D.
 
-    Returns (q, k) of `dtype` (default: q's); `out` may pass them, the inputs themselves
-    among them.  A token whose position is outside the table is skipped: its outputs keep
+    Returns (q, k) of `dtype` (default: q's); `out` may pass them, q itself for q and k itself
+    for k among others, but nothing that overlaps an input otherwise.  A token whose position is outside the table is skipped: its outputs keep
     what they hold, and are unset without `out`."""
     if out is None and (dtype is None or dtype is torch.bfloat16 or dtype is torch.float32):
         bf16 = (dtype or getattr(q, "dtype", None)) is torch.bfloat16

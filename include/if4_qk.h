@@ -51,8 +51,8 @@ typedef struct if4_qk_args {
     int32_t dtype, out_dtype; /* IF4_F32 or IF4_BF16 */
 } if4_qk_args;
 
-/* y may be x where their types and strides are the same; it must not overlap it
- * otherwise. */
+/* A part's y may be its x where their types and strides are the same; otherwise no y may
+ * overlap an x or the other y. */
 int if4_norm_rotate(const if4_qk_args* args, void* stream);
 
 /*
